@@ -65,6 +65,8 @@ extern "C" {
 typedef uint16_t moe_bf16_t;
 /* IEEE binary16 (fp16) bit pattern. */
 typedef uint16_t moe_f16_t;
+/* 8-bit float, 4 exponent and 3 significand bits, no infinities (e4m3fn). */
+typedef uint8_t moe_e4m3_t;
 
 typedef enum {
     MOE_OK = 0,
@@ -460,6 +462,120 @@ moe_status_t moe_add_rmsnorm(const moe_bf16_t *x, moe_bf16_t *residual,
                              const moe_bf16_t *weight, int64_t N, int H,
                              float eps, int gemma, moe_bf16_t *normed,
                              cudaStream_t stream);
+
+/* -------------------------------------------------------------------------
+ * moe_add_rmsnorm_fp8 -- moe_add_rmsnorm with an 8-bit output and one scale a
+ * token: the input of an 8-bit product (moe_linear_fp8), and optionally the
+ * bf16 one next to it (the router's input).
+ *   r = bf16(x + residual), or x without a residual
+ *   y = r / sqrt(mean(r^2) + eps) * weight       (* (1 + weight) with gemma)
+ *   scale[n] = max(max_h |y[n, h]| / 448, 2^-100),  q = e4m3(y / scale[n])
+ *
+ *   x            [N, H] bf16 in
+ *   residual     [N, H] bf16 in, or NULL
+ *   weight       [H]    bf16
+ *   residual_out [N, H] bf16 out: r; may be residual itself; NULL: not stored
+ *   q            [N, H] e4m3 out     scale [N] fp32 out
+ *   normed       [N, H] bf16 out: bf16(y), or NULL
+ * No other outputs may overlap an input.  Every array 16-byte aligned (scale
+ * 4-byte).  Precision: sums and scales in fp32, one rounding of each output;
+ * q is the rounded product with the reciprocal of the scale (a value that
+ * lies on the border of two e4m3 values may go to either).  The sum of
+ * squares is an fp32 one: rows of magnitude 1e18 overflow it.  A row with a
+ * NaN or an infinity gets scale NaN.  Limits: H % 8 == 0, H <= 65536.
+ * ---------------------------------------------------------------------- */
+moe_status_t moe_add_rmsnorm_fp8(const moe_bf16_t *x, const moe_bf16_t *residual,
+                                 const moe_bf16_t *weight, int64_t N, int H, float eps,
+                                 int gemma, moe_bf16_t *residual_out, moe_e4m3_t *q,
+                                 float *scale, moe_bf16_t *normed, cudaStream_t stream);
+
+/* -------------------------------------------------------------------------
+ * moe_quantize_fp8 -- rows to e4m3 with one scale a row: the weights of an
+ * 8-bit product at load (a row an output), or activations between two of them.
+ *   scale[n] = max(max_h |x[n, h]| / 448, 2^-100),  q = e4m3(x / scale[n])
+ *   x [N, H] bf16, q [N, H] e4m3 out (both 16-byte aligned), scale [N] fp32 out
+ * Precision, NaN, infinities and limits as moe_add_rmsnorm_fp8 (a row with an
+ * infinity gets scale +inf, its infinities NaN and its other values 0).
+ * ---------------------------------------------------------------------- */
+moe_status_t moe_quantize_fp8(const moe_bf16_t *x, int64_t N, int H, moe_e4m3_t *q,
+                              float *scale, cudaStream_t stream);
+
+/* -------------------------------------------------------------------------
+ * moe_linear, moe_linear_fp8 -- a projection with its epilogue in one kernel:
+ *   out[n, o] = act(sum_k x[n, k] weight[o, k] (* x_scale[n] * w_scale[o])
+ *                   + bias[o]) + residual[n, o]
+ *
+ *   x        [N, K] bf16 (moe_linear) or e4m3 (moe_linear_fp8)
+ *   weight   [O, K] of the same type
+ *   x_scale  [N] fp32, w_scale [O] fp32 (moe_linear_fp8; what
+ *            moe_add_rmsnorm_fp8 and moe_quantize_fp8 write)
+ *   bias     [O] bf16 or NULL
+ *   residual [N, O] bf16 or NULL
+ *   act      a moe_activation_t
+ *   out      [N, O] bf16, or fp32 when out_fp32 != 0 (a router's logits); a
+ *            bf16 out may be residual itself, and overlaps nothing else
+ *   workspace >= moe_linear_workspace_bytes() bytes, or NULL (then device
+ *            failures are not recorded)
+ * Precision: products and sums in fp32 on the tensor cores, the epilogue in
+ * fp32, one rounding of out.  Every output element's value depends on its own
+ * row and N alone selects the tiling: other N may differ in the last bit of
+ * the fp32 sum.  Limits: K % 8 == 0 (bf16) or K % 16 == 0 (e4m3), any O >= 1;
+ * x, weight 16-byte aligned; bias, residual and out aligned to their type.
+ * ---------------------------------------------------------------------- */
+typedef enum {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_SILU = 1,       /* v / (1 + e^-v) */
+    MOE_ACT_GELU = 2,       /* v (1 + erf(v / sqrt 2)) / 2 */
+    MOE_ACT_GELU_TANH = 3,  /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */
+    MOE_ACT_RELU = 4        /* max(v, 0) */
+} moe_activation_t;
+
+size_t moe_linear_workspace_bytes(void);
+moe_status_t moe_linear(const moe_bf16_t *x, const moe_bf16_t *weight, const moe_bf16_t *bias,
+                        const moe_bf16_t *residual, int64_t N, int K, int O, int act, void *out,
+                        int out_fp32, void *workspace, size_t workspace_bytes,
+                        cudaStream_t stream);
+moe_status_t moe_linear_fp8(const moe_e4m3_t *x, const float *x_scale, const moe_e4m3_t *weight,
+                            const float *w_scale, const moe_bf16_t *bias,
+                            const moe_bf16_t *residual, int64_t N, int K, int O, int act,
+                            void *out, int out_fp32, void *workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+
+/* -------------------------------------------------------------------------
+ * moe_balance_loss, moe_balance_loss_backward -- the router's load statistics
+ * and losses, and their gradient with respect to the router logits:
+ *   p_n = softmax(logits_n), lse_n = log sum_e exp(logits_ne); T tokens that
+ *   the mask leaves in; counts_e = their slots with id e; f_e = counts_e/(k T)
+ *   losses[0] = E sum_e f_e (sum_n p_ne / T)      (balance: 1 when even)
+ *   losses[1] = sum_n lse_n^2 / T                 (the size of the logits)
+ *   dlogits   = grad[0] dlosses[0]/dlogits + grad[1] dlosses[1]/dlogits
+ * (the counts have no gradient).
+ *
+ *   logits   [N, E] fp32, or bf16 when logits_bf16 != 0
+ *   topk_ids [N, k] int32, as moe_route gives them; a negative id is a
+ *            dropped slot and counts nowhere; an id >= E does not either and
+ *            is recorded as MOE_ERR_DEVICE_CHECK
+ *   mask     [N] bytes or NULL: a token with 0 takes no part (its logits and
+ *            ids are not read, its gradient is 0)
+ *   losses   [2] fp32 out    counts [E] int32 out    tokens [1] int32 out: T
+ *   grad     [2] fp32 (device): the losses' incoming gradients
+ *   dlogits  [N, E] out, in the logits' type; may be logits itself
+ *   workspace >= moe_balance_loss_workspace_bytes(N, E), 256-byte aligned;
+ *            its status word as everywhere
+ * A token whose logits are all -inf has p = 0 and lse = 0, gradient 0, and
+ * counts in T.  Without tokens (T = 0, N = 0) the losses, counts and
+ * gradients are 0.  The sums over tokens have a fixed order: the same inputs
+ * give the same bits.  Limits: 1 <= E <= 256, k >= 1, N * k < 2^31.
+ * ---------------------------------------------------------------------- */
+size_t moe_balance_loss_workspace_bytes(int64_t N, int E);
+moe_status_t moe_balance_loss(const void *logits, int logits_bf16, const int32_t *topk_ids,
+                              const uint8_t *mask, int64_t N, int E, int k, float *losses,
+                              int32_t *counts, int32_t *tokens, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+moe_status_t moe_balance_loss_backward(const void *logits, int logits_bf16,
+                                       const int32_t *counts, const int32_t *tokens,
+                                       const uint8_t *mask, const float *grad, int64_t N, int E,
+                                       int k, void *dlogits, cudaStream_t stream);
 
 /* -------------------------------------------------------------------------
  * moe_dense_mlp -- the dense SwiGLU MLP of the non-MoE layers (Qwen3MLP of

@@ -85,6 +85,14 @@ def lib():
         "moe_align_noalloc": ([P, i64, i32, i32, i32, P, P, P, P, P, P, P], i32),
         "moe_dense_mlp_workspace_bytes": ([i64, i32, i32], sz),
         "moe_add_rmsnorm": ([P, P, P, i64, i32, ctypes.c_float, i32, P, P], i32),
+        "moe_add_rmsnorm_fp8": ([P, P, P, i64, i32, ctypes.c_float, i32, P, P, P, P, P], i32),
+        "moe_quantize_fp8": ([P, i64, i32, P, P, P], i32),
+        "moe_linear_workspace_bytes": ([], sz),
+        "moe_linear": ([P, P, P, P, i64, i32, i32, i32, P, i32, P, sz, P], i32),
+        "moe_linear_fp8": ([P, P, P, P, P, P, i64, i32, i32, i32, P, i32, P, sz, P], i32),
+        "moe_balance_loss_workspace_bytes": ([i64, i32], sz),
+        "moe_balance_loss": ([P, i32, P, P, i64, i32, i32, P, P, P, P, sz, P], i32),
+        "moe_balance_loss_backward": ([P, i32, P, P, P, P, i64, i32, i32, P, P], i32),
         "moe_dense_mlp": ([P, P, P, P, i64, i32, i32, P, P, sz, P], i32),
         "moe_dense_mlp_prepared": ([P, P, P, P, i64, i32, i32, P, P, sz, P], i32),
     }
@@ -285,6 +293,156 @@ def moe_add_rmsnorm(x, residual, weight, eps: float = 1e-6, gemma: bool = False,
     _check(lib().moe_add_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), N, H, float(eps),
                                  int(bool(gemma)), _ptr(normed), _stream()), "moe_add_rmsnorm")
     return normed
+
+
+def _typed(t, name, dtype, shape):
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.shape != shape:
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape "
+                         f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+def _typed_or_none(t, name, dtype, shape):
+    return None if t is None else _typed(t, name, dtype, shape)
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def moe_add_rmsnorm_fp8(x, residual, weight, eps: float = 1e-6, gemma: bool = False, q=None,
+                        scale=None, normed=None, residual_out=None, want_normed: bool = False):
+    """r = bf16(x + residual) (x without a residual), y = RMSNorm(r): returns
+    (q e4m3 [N, H], scale fp32 [N], normed bf16 [N, H] or None) with q * scale
+    = y.  r goes to ``residual_out``, or without one back to ``residual``."""
+    N, H = _matrix(x, "x")
+    bf16 = torch.bfloat16
+    if residual_out is None:
+        residual_out = residual
+    if q is None:
+        q = torch.empty((N, H), dtype=torch.float8_e4m3fn, device=x.device)
+    if scale is None:
+        scale = torch.empty(N, dtype=torch.float32, device=x.device)
+    if normed is None and want_normed:
+        normed = torch.empty((N, H), dtype=bf16, device=x.device)
+    _check(lib().moe_add_rmsnorm_fp8(
+        _typed(x, "x", bf16, (N, H)), _typed_or_none(residual, "residual", bf16, (N, H)),
+        _typed(weight, "weight", bf16, (H,)), N, H, eps, bool(gemma),
+        _typed_or_none(residual_out, "residual_out", bf16, (N, H)),
+        _typed(q, "q", torch.float8_e4m3fn, (N, H)), _typed(scale, "scale", torch.float32, (N,)),
+        _typed_or_none(normed, "normed", bf16, (N, H)), _stream()), "moe_add_rmsnorm_fp8")
+    return q, scale, normed
+
+
+def moe_quantize_fp8(x, q=None, scale=None):
+    """Rows of a bf16 matrix to e4m3: (q [N, H], scale fp32 [N]), q * scale = x.
+    Used for weights (once, at load) and for activations."""
+    N, H = _matrix(x, "x")
+    if q is None:
+        q = torch.empty((N, H), dtype=torch.float8_e4m3fn, device=x.device)
+    if scale is None:
+        scale = torch.empty(N, dtype=torch.float32, device=x.device)
+    _check(lib().moe_quantize_fp8(
+        _typed(x, "x", torch.bfloat16, (N, H)), N, H, _typed(q, "q", torch.float8_e4m3fn, (N, H)),
+        _typed(scale, "scale", torch.float32, (N,)), _stream()), "moe_quantize_fp8")
+    return q, scale
+
+
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
+
+
+def moe_linear(x, weight, bias=None, residual=None, activation: str = "none", x_scale=None,
+               w_scale=None, out=None, out_dtype=torch.bfloat16, workspace=None):
+    """act(x weight^T [* x_scale * w_scale] + bias) + residual, [N, O] in bf16
+    or fp32 (``out_dtype``, or ``out``'s type).  x [N, K] and weight [O, K] are
+    both bf16 (moe_linear) or both e4m3 with their scales (moe_linear_fp8).
+    ``workspace`` (uint8, optional) receives the status word of
+    moe_read_device_status."""
+    N, K = _matrix(x, "x")
+    O = _matrix(weight, "weight")[0]
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    fp8 = x.dtype == torch.float8_e4m3fn
+    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    if fp8 and (x_scale is None or w_scale is None):
+        raise ValueError("e4m3 operands need x_scale and w_scale")
+    if not fp8 and (x_scale is not None or w_scale is not None):
+        raise ValueError("x_scale and w_scale belong to e4m3 operands")
+    if out is None:
+        out = torch.empty((N, O), dtype=out_dtype, device=x.device)
+    fp32 = out.dtype == torch.float32
+    tail = (_typed_or_none(bias, "bias", torch.bfloat16, (O,)),
+            _typed_or_none(residual, "residual", torch.bfloat16, (N, O)), N, K, O, act,
+            _typed(out, "out", torch.float32 if fp32 else torch.bfloat16, (N, O)), fp32,
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel(), _stream())
+    xp, wp = _typed(x, "x", dtype, (N, K)), _typed(weight, "weight", dtype, (O, K))
+    if fp8:
+        status = lib().moe_linear_fp8(xp, _typed(x_scale, "x_scale", torch.float32, (N,)), wp,
+                                      _typed(w_scale, "w_scale", torch.float32, (O,)), *tail)
+    else:
+        status = lib().moe_linear(xp, wp, *tail)
+    _check(status, "moe_linear_fp8" if fp8 else "moe_linear")
+    return out
+
+
+def _logits(logits):
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"logits must be fp32 or bf16, got {logits.dtype}")
+    N, E = _matrix(logits, "logits")
+    return N, E, logits.dtype == torch.bfloat16, _typed(logits, "logits", logits.dtype, (N, E))
+
+
+def _mask(mask, N):
+    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
+        raise ValueError(f"mask must be bool or uint8, got {mask.dtype}")
+    return None if mask is None else _typed(mask, "mask", mask.dtype, (N,))
+
+
+def moe_balance_loss(logits, topk_ids, mask=None, losses=None, counts=None, tokens=None,
+                     workspace=None):
+    """The router's losses and load: (losses fp32 [2] = load balance and mean
+    squared log-sum-exp, counts int32 [E], tokens int32 [1]) of the logits
+    [N, E] (fp32 or bf16) and the ids [N, k] that moe_route chose; ``mask``
+    (bool [N], optional) leaves tokens out, a negative id is a dropped slot."""
+    N, E, bf16, lp = _logits(logits)
+    k = _matrix(topk_ids, "topk_ids")[1]
+    dev = logits.device
+    if losses is None:
+        losses = torch.empty(2, dtype=torch.float32, device=dev)
+    if counts is None:
+        counts = torch.empty(E, dtype=torch.int32, device=dev)
+    if tokens is None:
+        tokens = torch.empty(1, dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(lib().moe_balance_loss_workspace_bytes(N, E), 256),
+                                dtype=torch.uint8, device=dev)
+    _check(lib().moe_balance_loss(
+        lp, bf16, _typed(topk_ids, "topk_ids", torch.int32, (N, k)), _mask(mask, N), N, E, k,
+        _typed(losses, "losses", torch.float32, (2,)), _typed(counts, "counts", torch.int32, (E,)),
+        _typed(tokens, "tokens", torch.int32, (1,)), workspace.data_ptr(), workspace.numel(),
+        _stream()), "moe_balance_loss")
+    return losses, counts, tokens
+
+
+def moe_balance_loss_backward(logits, counts, tokens, k: int, grad, mask=None, dlogits=None):
+    """Gradient of grad[0] * losses[0] + grad[1] * losses[1] (grad fp32 [2] on
+    the device) with respect to the logits, in their type; counts, tokens, k
+    and mask as in the forward call."""
+    N, E, bf16, lp = _logits(logits)
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    _check(lib().moe_balance_loss_backward(
+        lp, bf16, _typed(counts, "counts", torch.int32, (E,)),
+        _typed(tokens, "tokens", torch.int32, (1,)), _mask(mask, N),
+        _typed(grad, "grad", torch.float32, (2,)), N, E, k,
+        _typed(dlogits, "dlogits", logits.dtype, (N, E)), _stream()),
+        "moe_balance_loss_backward")
+    return dlogits
 
 
 def moe_dense_mlp(x, w_gate, w_up, w_down, out=None, workspace=None):

@@ -13,6 +13,7 @@
 #include <mutex>
 #include <string>
 
+#include "block_ops.cuh"
 #include "kernels.cuh"
 #include "moe.h"
 
@@ -1258,6 +1259,229 @@ moe_status_t moe_add_rmsnorm(const moe_bf16_t *x, moe_bf16_t *residual, const mo
     MOE_CUDA(launch_add_rmsnorm(x, residual, weight, N, H, eps, gemma ? 1 : 0, normed,
                                 num_sms_of_current_device(), stream),
              "add+rmsnorm kernel launch");
+    g_launches += 1;
+    return MOE_OK;
+}
+
+// ------------------------------------------- rows to e4m3, linear, balance
+
+namespace {
+
+bool aligned_to(const void *p, uintptr_t a) {
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+moe_status_t check_rows(int64_t N, int H) {
+    if (N < 0) return fail(MOE_ERR_INVALID_ARG, "N must be >= 0 (got %lld)", (long long)N);
+    if (H < 8 || H % 8)
+        return fail(MOE_ERR_INVALID_ARG, "H must be a positive multiple of 8 (got %d)", H);
+    if (H > kMaxRowH) return fail(MOE_ERR_UNSUPPORTED, "H must be <= %d (got %d)", kMaxRowH, H);
+    return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t moe_add_rmsnorm_fp8(const moe_bf16_t *x, const moe_bf16_t *residual,
+                                 const moe_bf16_t *weight, int64_t N, int H, float eps,
+                                 int gemma, moe_bf16_t *residual_out, moe_e4m3_t *q,
+                                 float *scale, moe_bf16_t *normed, cudaStream_t stream) {
+    g_last_error.clear();
+    const moe_status_t st = check_rows(N, H);
+    if (st != MOE_OK) return st;
+    if (!(eps >= 0.f)) return fail(MOE_ERR_INVALID_ARG, "eps must be >= 0");
+    if (N == 0) return MOE_OK;
+    if (!x || !weight || !q || !scale)
+        return fail(MOE_ERR_INVALID_ARG, "x, weight, q and scale must be non-null");
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) ||
+        !aligned16(residual_out) || !aligned16(q) || !aligned16(normed) || !aligned_to(scale, 4))
+        return fail(MOE_ERR_INVALID_ARG, "arrays must be 16-byte aligned (scale 4-byte)");
+    MOE_CUDA(launch_add_rmsnorm_fp8(x, residual, weight, N, H, eps, gemma ? 1 : 0, residual_out,
+                                    q, scale, normed, num_sms_of_current_device(), stream),
+             "add+rmsnorm e4m3 kernel launch");
+    g_launches += 1;
+    return MOE_OK;
+}
+
+moe_status_t moe_quantize_fp8(const moe_bf16_t *x, int64_t N, int H, moe_e4m3_t *q,
+                              float *scale, cudaStream_t stream) {
+    g_last_error.clear();
+    const moe_status_t st = check_rows(N, H);
+    if (st != MOE_OK || N == 0) return st;
+    if (!x || !q || !scale)
+        return fail(MOE_ERR_INVALID_ARG, "x, q and scale must be non-null");
+    if (!aligned16(x) || !aligned16(q) || !aligned_to(scale, 4))
+        return fail(MOE_ERR_INVALID_ARG, "x and q must be 16-byte aligned (scale 4-byte)");
+    MOE_CUDA(launch_quantize_fp8(x, N, H, q, scale, num_sms_of_current_device(), stream),
+             "quantize e4m3 kernel launch");
+    g_launches += 1;
+    return MOE_OK;
+}
+
+namespace {
+
+moe_status_t linear_impl(LinearArgs a, void *workspace, size_t workspace_bytes,
+                         cudaStream_t stream) {
+    g_last_error.clear();
+    const int step = a.fp8 ? 16 : 8;
+    if (a.N < 0) return fail(MOE_ERR_INVALID_ARG, "N must be >= 0 (got %lld)", (long long)a.N);
+    if (a.K < step || a.K % step)
+        return fail(MOE_ERR_INVALID_ARG, "K must be a positive multiple of %d (got %d)", step,
+                    a.K);
+    if (a.O < 1) return fail(MOE_ERR_INVALID_ARG, "O must be >= 1 (got %d)", a.O);
+    if (a.act < MOE_ACT_NONE || a.act > MOE_ACT_RELU)
+        return fail(MOE_ERR_INVALID_ARG, "unknown activation %d", a.act);
+    if (a.N > INT32_MAX)
+        return fail(MOE_ERR_UNSUPPORTED, "N must be below 2^31 (got %lld)", (long long)a.N);
+    if (workspace && workspace_bytes < moe_linear_workspace_bytes())
+        return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "linear workspace needs %zu bytes, got %zu",
+                    moe_linear_workspace_bytes(), workspace_bytes);
+    if (workspace && !aligned_to(workspace, 4))
+        return fail(MOE_ERR_INVALID_ARG, "workspace must be 4-byte aligned");
+    if (a.N == 0) return MOE_OK;
+    if (!a.x || !a.w || !a.out)
+        return fail(MOE_ERR_INVALID_ARG, "x, weight and out must be non-null");
+    if (a.fp8 && (!a.x_scale || !a.w_scale))
+        return fail(MOE_ERR_INVALID_ARG, "x_scale and w_scale must be non-null");
+    if (!aligned16(a.x) || !aligned16(a.w))
+        return fail(MOE_ERR_INVALID_ARG, "x and weight must be 16-byte aligned");
+    if (!aligned_to(a.x_scale, 4) || !aligned_to(a.w_scale, 4) || !aligned_to(a.bias, 2) ||
+        !aligned_to(a.residual, 2) || !aligned_to(a.out, a.out_fp32 ? 4 : 2))
+        return fail(MOE_ERR_INVALID_ARG, "scales, bias, residual and out must be aligned to "
+                                         "their types");
+    if (a.out_fp32 && a.out == a.residual)
+        return fail(MOE_ERR_INVALID_ARG, "an fp32 out may not be the bf16 residual");
+    a.status = static_cast<int32_t *>(workspace);
+    MOE_CUDA(launch_linear(a, num_sms_of_current_device(), stream), "linear kernel launch");
+    g_launches += 1;
+    return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_linear_workspace_bytes(void) { return sizeof(int32_t); }
+
+moe_status_t moe_linear(const moe_bf16_t *x, const moe_bf16_t *weight, const moe_bf16_t *bias,
+                        const moe_bf16_t *residual, int64_t N, int K, int O, int act, void *out,
+                        int out_fp32, void *workspace, size_t workspace_bytes,
+                        cudaStream_t stream) {
+    return linear_impl({x, weight, nullptr, nullptr, bias, residual, out, N, K, O, act, 0,
+                        out_fp32 ? 1 : 0, nullptr},
+                       workspace, workspace_bytes, stream);
+}
+
+moe_status_t moe_linear_fp8(const moe_e4m3_t *x, const float *x_scale, const moe_e4m3_t *weight,
+                            const float *w_scale, const moe_bf16_t *bias,
+                            const moe_bf16_t *residual, int64_t N, int K, int O, int act,
+                            void *out, int out_fp32, void *workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+    return linear_impl({x, weight, x_scale, w_scale, bias, residual, out, N, K, O, act, 1,
+                        out_fp32 ? 1 : 0, nullptr},
+                       workspace, workspace_bytes, stream);
+}
+
+namespace {
+
+struct BalanceLayout {
+    size_t part_s, part_p, part_c, total;  // the status word comes first
+    int blocks;
+};
+
+BalanceLayout balance_layout(int64_t N, int E) {
+    BalanceLayout L;
+    L.blocks = balance_blocks(N, E);
+    L.part_s = kAlign;
+    L.part_p = round_up(L.part_s + sizeof(BalancePart) * L.blocks, kAlign);
+    L.part_c = round_up(L.part_p + sizeof(float) * L.blocks * E, kAlign);
+    L.total = round_up(L.part_c + sizeof(int32_t) * L.blocks * E, kAlign);
+    return L;
+}
+
+moe_status_t check_balance(int64_t N, int E, int k) {
+    if (N < 0) return fail(MOE_ERR_INVALID_ARG, "N must be >= 0 (got %lld)", (long long)N);
+    if (E < 1) return fail(MOE_ERR_INVALID_ARG, "E must be >= 1 (got %d)", E);
+    if (k < 1) return fail(MOE_ERR_INVALID_ARG, "k must be >= 1 (got %d)", k);
+    if (E > MOE_MAX_EXPERTS)
+        return fail(MOE_ERR_UNSUPPORTED, "E must be <= %d (got %d)", MOE_MAX_EXPERTS, E);
+    if (N >= ((int64_t(1) << 31) + k - 1) / k)
+        return fail(MOE_ERR_UNSUPPORTED, "N*k must stay below 2^31");
+    return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_balance_loss_workspace_bytes(int64_t N, int E) {
+    if (N < 0 || E < 1 || E > MOE_MAX_EXPERTS) return 0;
+    return balance_layout(N, E).total;
+}
+
+moe_status_t moe_balance_loss(const void *logits, int logits_bf16, const int32_t *topk_ids,
+                              const uint8_t *mask, int64_t N, int E, int k, float *losses,
+                              int32_t *counts, int32_t *tokens, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+    g_last_error.clear();
+    const moe_status_t st = check_balance(N, E, k);
+    if (st != MOE_OK) return st;
+    if (!losses || !counts || !tokens || !workspace || (N > 0 && (!logits || !topk_ids)))
+        return fail(MOE_ERR_INVALID_ARG,
+                    "logits, topk_ids, losses, counts, tokens and workspace must be non-null");
+    if (!aligned_to(logits, logits_bf16 ? 2 : 4) || !aligned_to(topk_ids, 4) ||
+        !aligned_to(losses, 4) || !aligned_to(counts, 4) || !aligned_to(tokens, 4))
+        return fail(MOE_ERR_INVALID_ARG, "arrays must be aligned to their types");
+    if (!aligned_to(workspace, kAlign))
+        return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    const BalanceLayout L = balance_layout(N, E);
+    if (workspace_bytes < L.total)
+        return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "balance workspace needs %zu bytes, got %zu",
+                    L.total, workspace_bytes);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    BalanceArgs a = {};
+    a.logits = logits;
+    a.bf16 = logits_bf16 ? 1 : 0;
+    a.ids = topk_ids;
+    a.mask = mask;
+    a.N = N;
+    a.E = E;
+    a.k = k;
+    a.blocks = L.blocks;
+    a.part_p = reinterpret_cast<float *>(ws + L.part_p);
+    a.part_c = reinterpret_cast<int32_t *>(ws + L.part_c);
+    a.part_s = reinterpret_cast<BalancePart *>(ws + L.part_s);
+    a.losses = losses;
+    a.counts = counts;
+    a.tokens = tokens;
+    a.status = reinterpret_cast<int32_t *>(ws);
+    MOE_CUDA(launch_balance(a, stream), "balance kernel launch");
+    g_launches += 2;
+    return MOE_OK;
+}
+
+moe_status_t moe_balance_loss_backward(const void *logits, int logits_bf16,
+                                       const int32_t *counts, const int32_t *tokens,
+                                       const uint8_t *mask, const float *grad, int64_t N, int E,
+                                       int k, void *dlogits, cudaStream_t stream) {
+    g_last_error.clear();
+    const moe_status_t st = check_balance(N, E, k);
+    if (st != MOE_OK || N == 0) return st;
+    if (!logits || !counts || !tokens || !grad || !dlogits)
+        return fail(MOE_ERR_INVALID_ARG,
+                    "logits, counts, tokens, grad and dlogits must be non-null");
+    const uintptr_t size = logits_bf16 ? 2 : 4;
+    if (!aligned_to(logits, size) || !aligned_to(dlogits, size) || !aligned_to(counts, 4) ||
+        !aligned_to(tokens, 4) || !aligned_to(grad, 4))
+        return fail(MOE_ERR_INVALID_ARG, "arrays must be aligned to their types");
+    BalanceArgs a = {};
+    a.logits = logits;
+    a.bf16 = logits_bf16 ? 1 : 0;
+    a.mask = mask;
+    a.N = N;
+    a.E = E;
+    a.k = k;
+    a.tokens = const_cast<int32_t *>(tokens);
+    a.counts_in = counts;
+    a.grad = grad;
+    a.dlogits = dlogits;
+    MOE_CUDA(launch_balance_backward(a, num_sms_of_current_device(), stream),
+             "balance backward kernel launch");
     g_launches += 1;
     return MOE_OK;
 }
