@@ -43,8 +43,6 @@ struct LinearArgs {
     int32_t *status;  // nullable
 };
 
-cudaError_t launch_linear(const LinearArgs &a, int num_sms, cudaStream_t s);
-
 // ------------------------------------------------------------ balance loss
 
 constexpr int kBalanceMaxBlocks = 304;

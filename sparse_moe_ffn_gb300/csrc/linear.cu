@@ -1,70 +1,53 @@
-// linear.cu -- out = act(x W^T [* sx sw] + bias) + residual.
-//
-// A plain tiled product on the CUDA cores: 64 x 64 outputs a block, K slices
-// of 32 widened to fp32 in shared memory, one fp32 accumulator an output.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
-
-#include "block_ops.cuh"
-#include "linear_epilogue.cuh"
-#include "ptx.cuh"
+// linear.cu -- which kernel and tile moe_linear takes for its sizes.
+#include "linear_gemm.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kT = 64, kKs = 32;
+// Estimated SM cycles of a call.  A CTA takes in about 64 bytes a cycle
+// from L2 and its tensor core 128 x 128 outputs of a K slice in 256 cycles.
+constexpr double kBytesPerCycle = 64.0;
+constexpr double kCallCycles = 3000.0;
 
-template <bool kFp8>
-__device__ __forceinline__ float element(const void *p, int64_t i) {
-    if (kFp8) {
-        const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t *>(p)[i],
-                                                     __NV_E4M3);
-        return __half2float(__half(h));
-    }
-    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]) << 16);
+double ceil_div(double a, double b) { return static_cast<double>(static_cast<int64_t>((a + b - 1) / b)); }
+
+double pair_cycles(double N, double O, double nk, int bn, int sms) {
+    const double slice = bn * 2.0 > (16384 + bn * 64) / kBytesPerCycle
+                             ? bn * 2.0 : (16384 + bn * 64) / kBytesPerCycle;
+    const double waves = ceil_div(ceil_div(N, 256) * ceil_div(O, bn), sms / 2);
+    return kCallCycles + waves * nk * slice + 12.0 * bn;
 }
 
-template <bool kFp8>
-__global__ void __launch_bounds__(256) linear_plain_kernel(const LinearArgs a) {
-    __shared__ float xs[kKs][kT + 1], ws[kKs][kT + 1];
-    griddep_launch_dependents();
-    griddep_wait();
-    const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kT;
-    const int64_t o0 = static_cast<int64_t>(blockIdx.x) * kT;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < a.K; k0 += kKs) {
-        for (int i = threadIdx.x; i < kT * kKs; i += 256) {
-            const int r = i / kKs, k = i % kKs;
-            const bool in = k0 + k < a.K;
-            xs[k][r] = in && n0 + r < a.N ? element<kFp8>(a.x, (n0 + r) * a.K + k0 + k) : 0.f;
-            ws[k][r] = in && o0 + r < a.O ? element<kFp8>(a.w, (o0 + r) * a.K + k0 + k) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll 8
-        for (int k = 0; k < kKs; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = fmaf(xs[k][ty + 16 * i], ws[k][tx + 16 * j], acc[i][j]);
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + ty + 16 * i, o = o0 + tx + 16 * j;
-            if (n < a.N && o < a.O) store_linear(a, n, o, acc[i][j]);
-        }
+double split_cycles(double N, double O, double nk, int bn, int split, int sms) {
+    const double slice = bn * 2.0 > (16384 + bn * 128) / kBytesPerCycle
+                             ? bn * 2.0 : (16384 + bn * 128) / kBytesPerCycle;
+    const double waves = ceil_div(ceil_div(N, bn) * ceil_div(O, 128) * split, sms);
+    return kCallCycles + waves * (1500.0 + ceil_div(nk, split) * slice + 30.0 * bn);
 }
 
 }  // namespace
 
-cudaError_t launch_linear(const LinearArgs &a, int num_sms, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>((a.O + kT - 1) / kT),
-                    static_cast<unsigned>((a.N + kT - 1) / kT));
-    return a.fp8 ? launch_pdl(linear_plain_kernel<true>, grid, dim3(256), 0, s, 1, a)
-                 : launch_pdl(linear_plain_kernel<false>, grid, dim3(256), 0, s, 1, a);
+LinearTiling linear_tiling(const LinearArgs &a, int num_sms) {
+    const double nk = ceil_div(a.K, a.fp8 ? 128 : 64);
+    LinearTiling best = {1, 256, 1};
+    double cost = pair_cycles(a.N, a.O, nk, 256, num_sms);
+    const auto take = [&](double c, LinearTiling t) {
+        if (c < cost) {
+            cost = c;
+            best = t;
+        }
+    };
+    take(pair_cycles(a.N, a.O, nk, 128, num_sms), {1, 128, 1});
+    for (int bn = 16; bn <= 128; bn *= 2) {
+        if ((a.N + bn - 1) / bn > 4096) continue;
+        for (int split = 1; split <= 8 && split <= nk; split *= 2)
+            take(split_cycles(a.N, a.O, nk, bn, split, num_sms), {0, bn, split});
+    }
+    return best;
 }
+
+int linear_x_box(const LinearTiling &t) { return t.pair ? 128 : t.bn; }
+int linear_w_box(const LinearTiling &t) { return t.pair ? t.bn / 2 : 128; }
 
 }  // namespace moe

@@ -1,0 +1,397 @@
+// linear_pair.cu -- moe_linear for large batches: the two CTAs of a cluster
+// run one tcgen05 MMA of 256 tokens x kBN outputs (cta_group::2), so that every
+// operand byte a CTA fetches serves 256 rows of the other side.
+//
+// Even CTA: tokens 0-127 of the tile and the first half of its weight rows;
+// odd CTA: tokens 128-255 and the second half; each CTA's TMEM receives its
+// own 128 tokens x kBN outputs.  Persistent clusters take tiles in an order
+// that keeps the tiles in flight within a few token and output tiles (see
+// tile_of), so that an operand is read from memory about once.
+//
+//   warp 0     producer (one lane): TMA copies of both operands' K slices; the
+//              even CTA's barrier counts both CTAs' bytes
+//   warp 1     TMEM; in the even CTA one lane issues the MMAs
+//   warps 2-9  epilogue: warp w owns TMEM lanes 32 (w % 4) .. + 31 (one token a
+//              lane) and half of the outputs; two accumulators alternate, so
+//              a tile's epilogue runs under the next tile's MMAs.  Four warps
+//              would take as long for an activation as the MMAs of 2048 e4m3
+//              values take.
+//
+// A lane holds 32 consecutive outputs of one token: whole 32-byte sectors in
+// one store when rows are aligned for it; otherwise (an odd number of outputs,
+// an output that starts anywhere) 16 columns at a time go through shared
+// memory and leave with neighbouring lanes on neighbouring outputs.
+// Every wait is bounded; a CTA that gives up records MOE_ERR_DEVICE_TIMEOUT.
+#include "linear_epilogue.cuh"
+#include "linear_gemm.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kEpiWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kEpiWarps;
+constexpr int kStages = 6;
+constexpr int kTokens = 256;  // of a tile
+constexpr int kStagePad = 17; // floats of a staged row of 16 columns
+
+template <int kBN>
+struct PairTile {
+    static constexpr int kBBytes = kBN / 2 * kSliceBytes;
+    static constexpr int kStageBytes = kRowsBytes128 + kBBytes;
+    static constexpr int kColsPerWarp = kBN / 2;
+};
+
+struct PairShared {
+    uint64_t full[kStages];   // even CTA: both CTAs' bytes of a stage landed
+    uint64_t empty[kStages];  // both: the MMAs are done with a stage
+    uint64_t acc_full[2];     // both: an accumulator is complete
+    uint64_t acc_empty[2];    // even CTA: both CTAs' epilogues have read one
+    uint64_t drain;           // even CTA: every MMA has completed
+    uint32_t tmem_base;
+    int abort_flag;
+    alignas(16) float scale[kEpiWarps][128];  // w_scale of a warp's columns
+    alignas(16) float bias[kEpiWarps][128];
+    float stage[kEpiWarps][32 * kStagePad];
+};
+
+// Tiles run through bands of kBand token tiles, output tile by output tile:
+// the ~76 tiles in flight cover 8 token tiles and ~10 output tiles.
+constexpr int kBand = 8;
+
+__device__ __forceinline__ void tile_of(int tile, int m_tiles, int n_tiles, int *m, int *n) {
+    const int band = tile / (kBand * n_tiles);
+    const int first = band * kBand;
+    const int rows = min(kBand, m_tiles - first);
+    const int in = tile - band * kBand * n_tiles;
+    *m = first + in % rows;
+    *n = in / rows;
+}
+
+template <int kCols>
+__device__ __forceinline__ void act_all(int act, float (&v)[kCols]) {
+    switch (act) {
+#define MOE_ACT_CASE(A)                                                    \
+    case A:                                                                \
+        _Pragma("unroll") for (int i = 0; i < kCols; ++i) v[i] = linear_act<A>(v[i]); \
+        break;
+        MOE_ACT_CASE(MOE_ACT_SILU)
+        MOE_ACT_CASE(MOE_ACT_GELU)
+        MOE_ACT_CASE(MOE_ACT_GELU_TANH)
+        MOE_ACT_CASE(MOE_ACT_RELU)
+#undef MOE_ACT_CASE
+        default: break;
+    }
+}
+
+__device__ __forceinline__ void store_8words(void *p, const uint32_t (&w)[8], bool wide) {
+    if (wide) {
+        st_global_v8(p, w);
+    } else {
+        static_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// 32 outputs [o, o + 32) of token n whose row is aligned for vectors
+__device__ __forceinline__ void store_row32(const LinearArgs &a, int64_t at, bool wide,
+                                            float (&v)[32]) {
+    if (a.residual) {
+        const uint4 *r = reinterpret_cast<const uint4 *>(a.residual + at);
+        uint4 u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = __ldcg(r + i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(&u[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = unpack_bf16x2(w[j]);
+                v[8 * i + 2 * j] += f.x;
+                v[8 * i + 2 * j + 1] += f.y;
+            }
+        }
+    }
+    if (a.out_fp32) {
+        float *p = static_cast<float *>(a.out) + at;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[i + j]);
+            store_8words(p + i, w, wide);
+        }
+    } else {
+        uint16_t *p = static_cast<uint16_t *>(a.out) + at;
+#pragma unroll
+        for (int i = 0; i < 32; i += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(v[i + 2 * j], v[i + 2 * j + 1]);
+            store_8words(p + i, w, wide);
+        }
+    }
+}
+
+// The same outputs, any alignment and any part of them inside [0, O): 16
+// columns at a time, then a half warp a row.
+__device__ __forceinline__ void store_staged(const LinearArgs &a, float *stage, int64_t n0, int o0,
+                                             int lane, const float (&v)[32]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) stage[lane * kStagePad + i] = v[16 * h + i];
+        __syncwarp();
+        const int o = o0 + 16 * h + lane % 16;
+#pragma unroll 4
+        for (int r = lane / 16; r < 32; r += 2) {
+            const int64_t n = n0 + r;
+            if (n < a.N && o < a.O) {
+                const int64_t at = n * a.O + o;
+                float x = stage[r * kStagePad + lane % 16];
+                if (a.residual)
+                    x += __uint_as_float(static_cast<uint32_t>(__ldcg(a.residual + at)) << 16);
+                if (a.out_fp32) static_cast<float *>(a.out)[at] = x;
+                else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(x);
+            }
+        }
+        __syncwarp();
+    }
+}
+
+template <bool kFp8, int kBN>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x,
+                       const __grid_constant__ CUtensorMap tm_w, const LinearArgs a) {
+    using T = PairTile<kBN>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *tiles = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    PairShared *sm = reinterpret_cast<PairShared *>(tiles + kStages * T::kStageBytes);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm->full[s], 1);
+            mbar_init(&sm->empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm->acc_full[i], 1);
+            mbar_init(&sm->acc_empty[i], 2 * kEpiWarps);
+        }
+        mbar_init(&sm->drain, 1);
+        sm->abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensor_map(&tm_x);
+        prefetch_tensor_map(&tm_w);
+    }
+    if (warp == 1) tmem_alloc_2cta(&sm->tmem_base, 2 * kBN);
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_barrier();  // both CTAs' barriers exist before any remote arrival
+    tc_fence_after_sync();
+    const uint32_t tmem = sm->tmem_base;
+    volatile int *abort_flag = &sm->abort_flag;
+    griddep_launch_dependents();
+    griddep_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0 && a.status) *a.status = MOE_OK;
+
+    const int m_tiles = static_cast<int>((a.N + kTokens - 1) / kTokens);
+    const int n_tiles = (a.O + kBN - 1) / kBN;
+    const int total = m_tiles * n_tiles;
+    const int first = blockIdx.x / 2, step = gridDim.x / 2;
+    const int per_slice = kFp8 ? kSliceBytes : kSliceBytes / 2;  // values of K
+    const int nk = (a.K + per_slice - 1) / per_slice;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int g = 0;
+            bool failed = false;
+            for (int tile = first; tile < total && !failed; tile += step) {
+                int m, n;
+                tile_of(tile, m_tiles, n_tiles, &m, &n);
+                const int row = m * kTokens + static_cast<int>(rank) * 128;
+                const int wrow = n * kBN + static_cast<int>(rank) * (kBN / 2);
+                for (int kc = 0; kc < nk; ++kc, ++g) {
+                    const int s = g % kStages;
+                    const uint32_t use = g / kStages;
+                    if (use > 0 && !mbar_wait(&sm->empty[s], (use - 1) & 1, abort_flag)) {
+                        record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+                        *abort_flag = 1;
+                        failed = true;
+                        break;
+                    }
+                    uint8_t *st = tiles + s * T::kStageBytes;
+                    const uint32_t bar = map_to_rank(smem_addr(&sm->full[s]), 0);
+                    if (leader) mbar_arrive_expect_tx(&sm->full[s], 2 * T::kStageBytes);
+                    tma_load_2d_pair(st, &tm_x, bar, kc * per_slice, row);
+                    tma_load_2d_pair(st + kRowsBytes128, &tm_w, bar, kc * per_slice, wrow);
+                }
+            }
+            // no copy may be in flight when the pair ends
+            if (leader)
+                for (int i = (g > kStages ? g - kStages : 0); i < g; ++i)
+                    mbar_wait(&sm->full[i % kStages], (i / kStages) & 1, abort_flag);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (leader && lane == 0) {
+            constexpr uint32_t idesc = linear_idesc<kFp8>(kTokens, kBN);
+            int g = 0, it = 0;
+            bool failed = false;
+            for (int tile = first; tile < total && !failed; tile += step, ++it) {
+                const int acc = it & 1;
+                const uint32_t use = it >> 1;
+                if (use > 0 && !mbar_wait(&sm->acc_empty[acc], (use - 1) & 1, abort_flag)) {
+                    failed = true;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t d = tmem + acc * kBN;
+                for (int kc = 0; kc < nk; ++kc, ++g) {
+                    const int s = g % kStages;
+                    if (!mbar_wait(&sm->full[s], (g / kStages) & 1, abort_flag)) {
+                        failed = true;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint8_t *st = tiles + s * T::kStageBytes;
+                    const uint64_t da = sw128_kmajor_desc(smem_addr(st));
+                    const uint64_t db = sw128_kmajor_desc(smem_addr(st + kRowsBytes128));
+#pragma unroll
+                    for (int kk = 0; kk < kSliceBytes / kMmaBytes; ++kk)
+                        linear_mma_pair<kFp8>(d, da + 2 * kk, db + 2 * kk, idesc, (kc | kk) != 0);
+                    commit_2cta(&sm->empty[s], 3);
+                }
+                if (!failed) commit_2cta(&sm->acc_full[acc], 3);
+            }
+            if (failed) {
+                record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+                *abort_flag = 1;
+            }
+            commit_2cta(&sm->drain, 1);
+            mbar_wait(&sm->drain, 0, abort_flag);
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp % 4, half = (warp - 2) / 4, ew = warp - 2;
+        constexpr int kCols = T::kColsPerWarp;
+        float *scale_s = sm->scale[ew], *bias_s = sm->bias[ew];
+        const uint32_t empty0 = map_to_rank(smem_addr(&sm->acc_empty[0]), 0);
+        const uint32_t empty1 = map_to_rank(smem_addr(&sm->acc_empty[1]), 0);
+        // vector stores: rows of out (and residual) that start on 16 bytes
+        const int esize = a.out_fp32 ? 4 : 2;
+        const uintptr_t out_at = reinterpret_cast<uintptr_t>(a.out);
+        const int64_t ld = static_cast<int64_t>(a.O) * esize;
+        const bool vec = ld % 16 == 0 && out_at % 16 == 0 &&
+                         (!a.residual || (a.O % 8 == 0 &&
+                                          reinterpret_cast<uintptr_t>(a.residual) % 16 == 0));
+        const bool wide = ld % 32 == 0 && out_at % 32 == 0;
+        int it = 0;
+        for (int tile = first; tile < total; tile += step, ++it) {
+            int m, nt;
+            tile_of(tile, m_tiles, n_tiles, &m, &nt);
+            const int acc = it & 1;
+            const int o0 = nt * kBN + half * kCols;
+            const int64_t n0 = static_cast<int64_t>(m) * kTokens + rank * 128 + quarter * 32;
+            const int64_t n = n0 + lane;
+            // this tile's scales and bias, before its accumulator is ready
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kCols / 32; ++i) {
+                const int o = o0 + 32 * i + lane;
+                if (kFp8) scale_s[32 * i + lane] = o < a.O ? __ldcg(a.w_scale + o) : 0.f;
+                bias_s[32 * i + lane] =
+                    a.bias && o < a.O
+                        ? __uint_as_float(static_cast<uint32_t>(__ldcg(a.bias + o)) << 16)
+                        : 0.f;
+            }
+            const float sx = kFp8 && n < a.N ? __ldcg(a.x_scale + n) : 1.f;
+            __syncwarp();
+            bool ok = true;
+            if (lane == 0) ok = mbar_wait(&sm->acc_full[acc], (it >> 1) & 1, abort_flag);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) {
+                if (lane == 0) {
+                    record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                break;
+            }
+            tc_fence_after_sync();
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                   acc * kBN + half * kCols;
+#pragma unroll 1
+            for (int c = 0; c < kCols; c += 32) {
+                if (n0 >= a.N || o0 + c >= a.O) break;  // warp-uniform
+                float v[32];
+                tmem_load32(taddr + c, v);
+                tmem_load_wait();
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 b = *reinterpret_cast<const float4 *>(bias_s + c + i);
+                    if (kFp8) {
+                        const float4 w = *reinterpret_cast<const float4 *>(scale_s + c + i);
+                        v[i] = fmaf(v[i], sx * w.x, b.x);
+                        v[i + 1] = fmaf(v[i + 1], sx * w.y, b.y);
+                        v[i + 2] = fmaf(v[i + 2], sx * w.z, b.z);
+                        v[i + 3] = fmaf(v[i + 3], sx * w.w, b.w);
+                    } else {
+                        v[i] += b.x;
+                        v[i + 1] += b.y;
+                        v[i + 2] += b.z;
+                        v[i + 3] += b.w;
+                    }
+                }
+                act_all(a.act, v);
+                if (vec && o0 + c + 32 <= a.O) {
+                    if (n < a.N) store_row32(a, n * a.O + o0 + c, wide, v);
+                } else {
+                    store_staged(a, sm->stage[ew], n0, o0 + c, lane, v);
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) arrive_remote_relaxed(acc ? empty1 : empty0);
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_barrier();  // both CTAs are done with TMEM and each other's barriers
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc_2cta(tmem, 2 * kBN);
+    }
+}
+
+template <bool kFp8, int kBN>
+cudaError_t launch_one(const CUtensorMap &tm_x, const CUtensorMap &tm_w, const LinearArgs &a,
+                       int num_sms, cudaStream_t s) {
+    const size_t smem = 1024 + static_cast<size_t>(kStages) * PairTile<kBN>::kStageBytes +
+                        sizeof(PairShared);
+    auto kern = linear_pair_kernel<kFp8, kBN>;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           static_cast<int>(smem));
+    if (err != cudaSuccess) return err;
+    const int64_t tiles = (a.N + kTokens - 1) / kTokens * ((a.O + kBN - 1) / kBN);
+    const int64_t pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kPairThreads), smem, s, 2,
+                      tm_x, tm_w, a);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_pair(const CUtensorMap &tm_x, const CUtensorMap &tm_w,
+                               const LinearArgs &a, const LinearTiling &t, int num_sms,
+                               cudaStream_t s) {
+    if (t.bn == 256)
+        return a.fp8 ? launch_one<true, 256>(tm_x, tm_w, a, num_sms, s)
+                     : launch_one<false, 256>(tm_x, tm_w, a, num_sms, s);
+    return a.fp8 ? launch_one<true, 128>(tm_x, tm_w, a, num_sms, s)
+                 : launch_one<false, 128>(tm_x, tm_w, a, num_sms, s);
+}
+
+}  // namespace moe

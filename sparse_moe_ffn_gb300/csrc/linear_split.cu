@@ -1,0 +1,226 @@
+// linear_split.cu -- moe_linear for small and middling batches: a tile of 128
+// outputs x kBN tokens whose K is shared by the CTAs of a cluster.
+//
+// With few tokens the call streams the weights once, and there are too few
+// tiles of 128 outputs to keep every SM loading; the cluster's CTAs take a
+// part of K each.  The weights are on the MMA's M side (128 rows, all real
+// but in the last tile), the tokens on its N side, which goes down to 16.
+// Each CTA writes its partial sums straight into the shared memory of the CTA
+// that owns the token (tokens are dealt out in equal runs), one cluster
+// barrier later every CTA adds the parts of its own tokens in rank order and
+// stores them: no workspace, no second kernel, the same bits every time.
+// Going through shared memory also turns the tile: neighbouring threads then
+// hold neighbouring outputs of a token.
+//
+//   warp 0  producer (one lane): TMA copies; up to kStages slices in flight
+//   warp 1  TMEM, and one lane issues the MMAs
+//   all     4 warps read the accumulator (32 TMEM lanes = outputs each), then
+//           all add and store
+// Every wait is bounded; a CTA that gives up records MOE_ERR_DEVICE_TIMEOUT
+// and still takes part in the cluster's barriers.
+#include "linear_epilogue.cuh"
+#include "linear_gemm.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kSplitThreads = 128;
+constexpr int kOut = 128;  // outputs of a tile
+
+template <int kBN>
+struct SplitTile {
+    static constexpr int kXBytes = kBN * kSliceBytes;
+    static constexpr int kStageBytes = kRowsBytes128 + kXBytes;
+    static constexpr int kStages = kBN >= 128 ? 4 : kBN >= 64 ? 6 : 8;
+    static constexpr uint32_t kCols = kBN < 32 ? 32 : kBN;
+    static constexpr int kPartFloats = kBN * kOut;
+};
+
+struct SplitShared {
+    uint64_t full[8], empty[8], acc_full;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+template <bool kFp8, int kBN>
+__global__ void __launch_bounds__(kSplitThreads, 1)
+    linear_split_kernel(const __grid_constant__ CUtensorMap tm_x,
+                        const __grid_constant__ CUtensorMap tm_w, const LinearArgs a,
+                        const int split) {
+    using T = SplitTile<kBN>;
+    constexpr int kStages = T::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *tiles = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // [split ranks][tokens of this CTA][128 outputs]
+    float *part = reinterpret_cast<float *>(tiles + kStages * T::kStageBytes);
+    SplitShared *sm = reinterpret_cast<SplitShared *>(part + T::kPartFloats);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = static_cast<int>(cluster_ctarank());
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm->full[s], 1);
+            mbar_init(&sm->empty[s], 1);
+        }
+        mbar_init(&sm->acc_full, 1);
+        sm->abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensor_map(&tm_x);
+        prefetch_tensor_map(&tm_w);
+    }
+    if (warp == 1) {
+        tmem_alloc(&sm->tmem_base, T::kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    // the cluster's CTAs have all started before any of them is written to;
+    // waited for where the partial sums leave
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    tc_fence_after_sync();
+    const uint32_t tmem = sm->tmem_base;
+    volatile int *abort_flag = &sm->abort_flag;
+    griddep_launch_dependents();
+    griddep_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && a.status) *a.status = MOE_OK;
+
+    const int o0 = blockIdx.x / split * kOut;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kBN;
+    const int per_slice = kFp8 ? kSliceBytes : kSliceBytes / 2;
+    const int nk = (a.K + per_slice - 1) / per_slice;
+    const int k_first = static_cast<int>(static_cast<int64_t>(nk) * rank / split);
+    const int k_end = static_cast<int>(static_cast<int64_t>(nk) * (rank + 1) / split);
+    const int slices = k_end - k_first;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int g = 0;
+            for (; g < slices; ++g) {
+                const int s = g % kStages;
+                const uint32_t use = g / kStages;
+                if (use > 0 && !mbar_wait(&sm->empty[s], (use - 1) & 1, abort_flag)) {
+                    record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+                    *abort_flag = 1;
+                    break;
+                }
+                uint8_t *st = tiles + s * T::kStageBytes;
+                mbar_arrive_expect_tx(&sm->full[s], T::kStageBytes);
+                tma_load_2d(st, &tm_w, &sm->full[s], (k_first + g) * per_slice, o0);
+                tma_load_2d(st + kRowsBytes128, &tm_x, &sm->full[s], (k_first + g) * per_slice,
+                            static_cast<int>(n0));
+            }
+            // no copy may be in flight when the CTA ends
+            for (int i = (g > kStages ? g - kStages : 0); i < g; ++i)
+                mbar_wait(&sm->full[i % kStages], (i / kStages) & 1, abort_flag);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = linear_idesc<kFp8>(kOut, kBN);
+            for (int g = 0; g < slices; ++g) {
+                const int s = g % kStages;
+                if (!mbar_wait(&sm->full[s], (g / kStages) & 1, abort_flag)) {
+                    record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+                    *abort_flag = 1;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint8_t *st = tiles + s * T::kStageBytes;
+                const uint64_t da = sw128_kmajor_desc(smem_addr(st));
+                const uint64_t db = sw128_kmajor_desc(smem_addr(st + kRowsBytes128));
+#pragma unroll
+                for (int kk = 0; kk < kSliceBytes / kMmaBytes; ++kk)
+                    linear_mma<kFp8>(tmem, da + 2 * kk, db + 2 * kk, idesc, (g | kk) != 0);
+                mma_commit(&sm->empty[s]);
+            }
+            mma_commit(&sm->acc_full);  // after a failure too: the MMAs issued so far
+        }
+        __syncwarp();
+    }
+
+    bool ok = true;
+    if (lane == 0) ok = mbar_wait(&sm->acc_full, 0, abort_flag);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (!ok && lane == 0) {
+        record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+        *abort_flag = 1;
+    }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const int own = kBN / split;  // tokens of each CTA
+    if (ok) {
+        tc_fence_after_sync();
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        const uint32_t mine = smem_addr(part + rank * own * kOut + warp * 32 + lane);
+        constexpr int kChunk = kBN < 32 ? 16 : 32;
+#pragma unroll 1
+        for (int c = 0; c < kBN; c += kChunk) {
+            float v[32];
+            tmem_load32(taddr + c, v);  // a tile of 16 tokens has 32 columns allocated
+            tmem_load_wait();
+            if (n0 + c >= a.N) break;
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+                const int t = c + i;
+                const int to = t / own;
+                st_cluster_f32(map_to_rank(mine + (t - to * own) * kOut * 4, to), v[i]);
+            }
+        }
+        tc_fence_before_sync();
+    }
+    cluster_barrier();
+    if (*abort_flag == 0) {
+        const int o = o0 + static_cast<int>(threadIdx.x);
+        if (o < a.O) {
+            for (int t = 0; t < own; ++t) {
+                const int64_t n = n0 + rank * own + t;
+                if (n >= a.N) break;
+                float v = 0.f;
+                for (int r = 0; r < split; ++r) v += part[(r * own + t) * kOut + threadIdx.x];
+                store_linear(a, n, o, v);
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, T::kCols);
+    }
+}
+
+template <bool kFp8, int kBN>
+cudaError_t launch_one(const CUtensorMap &tm_x, const CUtensorMap &tm_w, const LinearArgs &a,
+                       int split, cudaStream_t s) {
+    using T = SplitTile<kBN>;
+    const size_t smem = 1024 + static_cast<size_t>(T::kStages) * T::kStageBytes +
+                        sizeof(float) * T::kPartFloats + sizeof(SplitShared);
+    auto kern = linear_split_kernel<kFp8, kBN>;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           static_cast<int>(smem));
+    if (err != cudaSuccess) return err;
+    const dim3 grid(static_cast<unsigned>((a.O + kOut - 1) / kOut * split),
+                    static_cast<unsigned>((a.N + kBN - 1) / kBN));
+    return launch_pdl(kern, grid, dim3(kSplitThreads), smem, s, static_cast<unsigned>(split), tm_x,
+                      tm_w, a, split);
+}
+
+template <bool kFp8>
+cudaError_t launch_bn(const CUtensorMap &tm_x, const CUtensorMap &tm_w, const LinearArgs &a,
+                      const LinearTiling &t, cudaStream_t s) {
+    switch (t.bn) {
+        case 16: return launch_one<kFp8, 16>(tm_x, tm_w, a, t.split, s);
+        case 32: return launch_one<kFp8, 32>(tm_x, tm_w, a, t.split, s);
+        case 64: return launch_one<kFp8, 64>(tm_x, tm_w, a, t.split, s);
+        default: return launch_one<kFp8, 128>(tm_x, tm_w, a, t.split, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_linear_split(const CUtensorMap &tm_x, const CUtensorMap &tm_w,
+                                const LinearArgs &a, const LinearTiling &t, cudaStream_t s) {
+    return a.fp8 ? launch_bn<true>(tm_x, tm_w, a, t, s) : launch_bn<false>(tm_x, tm_w, a, t, s);
+}
+
+}  // namespace moe
