@@ -555,8 +555,8 @@ moe_status_t moe_linear_fp8(const moe_e4m3_t *x, const float *x_scale, const moe
  *   topk_ids [N, k] int32, as moe_route gives them; a negative id is a
  *            dropped slot and counts nowhere; an id >= E does not either and
  *            is recorded as MOE_ERR_DEVICE_CHECK
- *   mask     [N] bytes or NULL: a token with 0 takes no part (its logits and
- *            ids are not read, its gradient is 0)
+ *   mask     [N] bytes or NULL: a token with 0 takes no part (whatever its
+ *            logits and ids hold), its gradient is 0
  *   losses   [2] fp32 out    counts [E] int32 out    tokens [1] int32 out: T
  *   grad     [2] fp32 (device): the losses' incoming gradients
  *   dlogits  [N, E] out, in the logits' type; may be logits itself

@@ -1413,16 +1413,16 @@ namespace {
 
 struct BalanceLayout {
     size_t part_s, part_p, part_c, total;  // the status word comes first
-    int blocks;
+    int clusters;
 };
 
 BalanceLayout balance_layout(int64_t N, int E) {
     BalanceLayout L;
-    L.blocks = balance_blocks(N, E);
+    L.clusters = balance_clusters(N, E);
     L.part_s = kAlign;
-    L.part_p = round_up(L.part_s + sizeof(BalancePart) * L.blocks, kAlign);
-    L.part_c = round_up(L.part_p + sizeof(float) * L.blocks * E, kAlign);
-    L.total = round_up(L.part_c + sizeof(int32_t) * L.blocks * E, kAlign);
+    L.part_p = round_up(L.part_s + sizeof(BalancePart) * L.clusters, kAlign);
+    L.part_c = round_up(L.part_p + sizeof(float) * L.clusters * E, kAlign);
+    L.total = round_up(L.part_c + sizeof(int32_t) * L.clusters * E, kAlign);
     return L;
 }
 
@@ -1472,7 +1472,7 @@ moe_status_t moe_balance_loss(const void *logits, int logits_bf16, const int32_t
     a.N = N;
     a.E = E;
     a.k = k;
-    a.blocks = L.blocks;
+    a.clusters = L.clusters;
     a.part_p = reinterpret_cast<float *>(ws + L.part_p);
     a.part_c = reinterpret_cast<int32_t *>(ws + L.part_c);
     a.part_s = reinterpret_cast<BalancePart *>(ws + L.part_s);
@@ -1480,8 +1480,9 @@ moe_status_t moe_balance_loss(const void *logits, int logits_bf16, const int32_t
     a.counts = counts;
     a.tokens = tokens;
     a.status = reinterpret_cast<int32_t *>(ws);
-    MOE_CUDA(launch_balance(a, stream), "balance kernel launch");
-    g_launches += 2;
+    int launches = 0;
+    MOE_CUDA(launch_balance(a, &launches, stream), "balance kernel launch");
+    g_launches += launches;
     return MOE_OK;
 }
 

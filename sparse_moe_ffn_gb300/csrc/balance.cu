@@ -11,14 +11,15 @@
 // f is a count and has no gradient.  sum_j p_nj = 1, so taking 1/E off f
 // changes no gradient; it removes the cancellation in f_e - sum_j f_j p_nj,
 // whose two terms agree in all but the last few percent when the load is
-// nearly even.  d_e is formed in 64 bits from the counts.
+// nearly even.  d_e is formed in whole numbers from the counts.
 // A token whose logits are all -inf has p = 0 and lse = 0 and still counts in
-// T; a masked token is never read and gets gradient 0.
+// T; a masked token takes no part, whatever it holds, and gets gradient 0.
 //
 // A row is held by kLanes lanes, 8 values each (kLanes is the power of two
-// that covers E); sums over tokens run in registers, then per block in shared
-// memory, and the blocks' partial sums are joined in block order in 64 bits:
-// no atomics on floats, the same bits every time.
+// that covers E), four rows at a time; sums over tokens run in registers, then
+// per block, per cluster of eight blocks (distributed shared memory) and, when
+// there is more than one cluster, in a second kernel: each in a fixed order,
+// with no atomics on floats, so the same inputs give the same bits.
 #include <cuda_bf16.h>
 
 #include "block_ops.cuh"
@@ -146,15 +147,76 @@ __device__ __forceinline__ float softmax_row(float (&x)[kVals]) {
     return sum == 0.f ? 0.f : top + logf(sum);
 }
 
+// The rows that a warp holds at once: kUnroll per group of kLanes lanes, so
+// that many loads are in flight.  Row u of lane group `sub` is
+// base + u (32 / kLanes) + sub.
+constexpr int kUnroll = 4;
+
+template <int kLanes>
+constexpr int kRowsPerWarp = kUnroll * (32 / kLanes);
+
+// A sum that keeps what each fp32 addition rounds off (two-sum), so that the
+// order and number of terms cost nothing; the GPU has few 64-bit units.
+struct Sum {
+    float hi = 0.f, lo = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float s = __fadd_rn(hi, x);
+        const float b = __fsub_rn(s, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
+        hi = s;
+    }
+    __device__ __forceinline__ float value() const { return hi + lo; }
+};
+
+__device__ __forceinline__ uint32_t cluster_rank_of() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_wait_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The 32-bit word at `p` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t ld_rank(const void *p, int rank) {
+    uint32_t a, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float ld_rank(const float *p, int rank) {
+    return __uint_as_float(ld_rank(static_cast<const void *>(p), rank));
+}
+
+struct Totals {
+    float z;
+    int tokens, bad;
+};
+
+// The two losses and the token count, from sum_e p_e c_e and the totals.
+__device__ __forceinline__ void write_losses(const BalanceArgs &a, float pc, const Totals &t) {
+    const float inv = t.tokens > 0 ? 1.f / static_cast<float>(t.tokens) : 0.f;
+    a.losses[0] = static_cast<float>(a.E) / static_cast<float>(a.k) * (pc * inv) * inv;
+    a.losses[1] = t.z * inv;
+    *a.tokens = t.tokens;
+    *a.status = t.bad ? MOE_ERR_DEVICE_CHECK : MOE_OK;
+}
+
 template <bool kBf16, int kLanes, bool kVec>
 __global__ void __launch_bounds__(kThreads) balance_stats_kernel(const BalanceArgs a) {
     constexpr int kPerWarp = 32 / kLanes;
     constexpr int kWarps = kThreads / 32;
+    constexpr int kRows = kRowsPerWarp<kLanes>;
     __shared__ float ps[kWarps][MOE_MAX_EXPERTS];
+    __shared__ float p_block[MOE_MAX_EXPERTS];
     __shared__ int cs[MOE_MAX_EXPERTS];
-    __shared__ double zs[kWarps];
+    __shared__ float zs[kWarps], pcs[kWarps], pc_rank;
     __shared__ int ts[kWarps];
     __shared__ int bad;
+    __shared__ Totals total;
     griddep_launch_dependents();
     griddep_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -163,40 +225,58 @@ __global__ void __launch_bounds__(kThreads) balance_stats_kernel(const BalanceAr
     if (threadIdx.x == 0) bad = 0;
     __syncthreads();
 
-    // this block's tokens [first, last)
-    const int64_t per = (a.N + gridDim.x - 1) / gridDim.x;
-    const int64_t first = blockIdx.x * per;
-    const int64_t last = first + per < a.N ? first + per : a.N;
-
     float p[kVals];
 #pragma unroll
     for (int v = 0; v < kVals; ++v) p[v] = 0.f;
     float z = 0.f;
     int tokens = 0;
-    for (int64_t base = first + warp * kPerWarp; base < last; base += kWarps * kPerWarp) {
-        const int64_t n = base + sub;
-        const bool in = n < last && (!a.mask || __ldcg(a.mask + n));
-        float x[kVals];
-        if (in) {
-            load_row<kBf16, kLanes, kVec>(a.logits, n, a.E, t, x);
-        } else {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * kRows;
+    for (int64_t base = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRows; base < a.N;
+         base += step) {
+        float x[kUnroll][kVals];
+        int id[kUnroll];
+        bool in[kUnroll];
 #pragma unroll
-            for (int v = 0; v < kVals; ++v) x[v] = kNegInf;
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t n = base + u * kPerWarp + sub;
+            in[u] = n < a.N;
+            id[u] = -1;
+            if (in[u]) {
+                load_row<kBf16, kLanes, kVec>(a.logits, n, a.E, t, x[u]);
+                if (t < a.k) id[u] = __ldcg(a.ids + n * a.k + t);
+                if (a.mask) in[u] = __ldcg(a.mask + n);
+            }
         }
-        const float lse = softmax_row<kLanes>(x);
 #pragma unroll
-        for (int v = 0; v < kVals; ++v) p[v] += x[v];
-        z = fmaf(lse, lse, z);
-        tokens += in;
+        for (int u = 0; u < kUnroll; ++u) {
+            if (!in[u]) {
+#pragma unroll
+                for (int v = 0; v < kVals; ++v) x[u][v] = kNegInf;
+            } else {
+                if (id[u] >= a.E) bad = 1;
+                else if (id[u] >= 0) atomicAdd(&cs[id[u]], 1);
+                const int64_t n = base + u * kPerWarp + sub;
+                for (int j = t + kLanes; j < a.k; j += kLanes) {  // more slots than lanes
+                    const int more = __ldcg(a.ids + n * a.k + j);
+                    if (more >= a.E) bad = 1;
+                    else if (more >= 0) atomicAdd(&cs[more], 1);
+                }
+                tokens += t == 0;
+            }
+            const float lse = softmax_row<kLanes>(x[u]);
+#pragma unroll
+            for (int v = 0; v < kVals; ++v) p[v] += x[u][v];
+            if (t == 0) z = fmaf(lse, lse, z);
+        }
     }
     // rows of the warp, then the warps of the block, in order
 #pragma unroll
     for (int d = kLanes; d < 32; d <<= 1) {
 #pragma unroll
         for (int v = 0; v < kVals; ++v) p[v] += __shfl_xor_sync(0xffffffffu, p[v], d);
-        z += __shfl_xor_sync(0xffffffffu, z, d);
-        tokens += __shfl_xor_sync(0xffffffffu, tokens, d);
     }
+    z = row_sum<32>(z);
+    tokens = __reduce_add_sync(0xffffffffu, tokens);
     if (sub == 0) {
 #pragma unroll
         for (int v = 0; v < kVals; ++v) {
@@ -208,151 +288,193 @@ __global__ void __launch_bounds__(kThreads) balance_stats_kernel(const BalanceAr
         zs[warp] = z;
         ts[warp] = tokens;
     }
-    // the slots of the block's tokens, side by side
-    for (int64_t i = first * a.k + threadIdx.x; i < last * a.k; i += kThreads) {
-        if (a.mask && !__ldcg(a.mask + i / a.k)) continue;
-        const int id = __ldcg(a.ids + i);
-        if (id >= a.E) bad = 1;
-        else if (id >= 0) atomicAdd(&cs[id], 1);
-    }
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += kThreads) {
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) s += ps[w][e];
-        a.part_p[static_cast<int64_t>(blockIdx.x) * a.E + e] = s;
-        a.part_c[static_cast<int64_t>(blockIdx.x) * a.E + e] = cs[e];
+        p_block[e] = s;
     }
     if (threadIdx.x == 0) {
-        double zz = 0.0;
-        int tt = 0;
+        Totals b = {0.f, 0, bad};
         for (int w = 0; w < kWarps; ++w) {
-            zz += zs[w];
-            tt += ts[w];
+            b.z += zs[w];
+            b.tokens += ts[w];
         }
-        a.part_s[blockIdx.x] = {zz, tt, bad};
+        total = b;
     }
+    cluster_wait_all();
+
+    // the blocks of the cluster, in order: each takes a run of the experts
+    const int rank = static_cast<int>(cluster_rank_of());
+    const int share = (a.E + kBalanceCluster - 1) / kBalanceCluster;
+    const int e = rank * share + static_cast<int>(threadIdx.x);
+    const bool mine = static_cast<int>(threadIdx.x) < share && e < a.E;
+    const bool alone = gridDim.x == kBalanceCluster;
+    float pc = 0.f;
+    if (mine) {
+        Sum s;
+        int c = 0;
+#pragma unroll
+        for (int r = 0; r < kBalanceCluster; ++r) {
+            s.add(ld_rank(&p_block[e], r));
+            c += static_cast<int>(ld_rank(static_cast<const void *>(&cs[e]), r));
+        }
+        if (alone) {
+            a.counts[e] = c;
+            pc = s.value() * static_cast<float>(c);
+        } else {
+            const int64_t at = static_cast<int64_t>(blockIdx.x / kBalanceCluster) * a.E + e;
+            a.part_p[at] = s.value();
+            a.part_c[at] = c;
+        }
+    }
+    Totals sum = {0.f, 0, 0};
+    if (threadIdx.x == 0 && rank == 0) {
+        for (int r = 0; r < kBalanceCluster; ++r) {
+            sum.z += ld_rank(&total.z, r);
+            sum.tokens += static_cast<int>(ld_rank(static_cast<const void *>(&total.tokens), r));
+            sum.bad |= static_cast<int>(ld_rank(static_cast<const void *>(&total.bad), r));
+        }
+        if (!alone) a.part_s[blockIdx.x / kBalanceCluster] = {sum.z, sum.tokens, sum.bad};
+    }
+    if (alone) {  // one cluster holds every token: it ends the call
+        pc = row_sum<32>(pc);
+        if (lane == 0) pcs[warp] = pc;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            pc = 0.f;
+            for (int w = 0; w < kWarps; ++w) pc += pcs[w];
+            pc_rank = pc;
+        }
+        cluster_wait_all();
+        if (threadIdx.x == 0 && rank == 0) {
+            pc = 0.f;
+            for (int r = 0; r < kBalanceCluster; ++r) pc += ld_rank(&pc_rank, r);
+            write_losses(a, pc, sum);
+        }
+    }
+    cluster_wait_all();  // nobody leaves while its shared memory is read
 }
 
-// Joins the blocks' partial sums: kSeg threads an expert, each over every
-// kSeg-th block, then in order.
+// Joins the clusters' partial sums: kSeg threads an expert, each over every
+// kSeg-th cluster, then in order.
 constexpr int kJoinThreads = 1024;
+constexpr int kJoinPer = (kBalanceMaxClusters + 3) / 4;  // at most, with E = 256
 
 __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const BalanceArgs a) {
-    __shared__ double ps[kJoinThreads];
+    __shared__ float ps[kJoinThreads];
     __shared__ int cs[kJoinThreads];
-    __shared__ double zs[kJoinThreads / 32], ls[kJoinThreads / 32];
-    __shared__ int ts[kJoinThreads / 32], bs[kJoinThreads / 32];
+    __shared__ float ls[kJoinThreads / 32];
+    __shared__ Totals total;
     griddep_launch_dependents();
     griddep_wait();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int seg = kJoinThreads / a.E;
     const int e = threadIdx.x % a.E, s = threadIdx.x / a.E;
-    double p = 0.0;
+    Sum p;
     int c = 0;
     if (s < seg) {
-#pragma unroll 8
-        for (int b = s; b < a.blocks; b += seg) {
-            p += __ldcg(a.part_p + static_cast<int64_t>(b) * a.E + e);
-            c += __ldcg(a.part_c + static_cast<int64_t>(b) * a.E + e);
+#pragma unroll
+        for (int i = 0; i < kJoinPer; ++i) {
+            const int b = s + i * seg;
+            if (b < a.clusters) {
+                p.add(__ldcg(a.part_p + b * a.E + e));
+                c += __ldcg(a.part_c + b * a.E + e);
+            }
         }
     }
-    ps[threadIdx.x] = p;
+    ps[threadIdx.x] = p.value();
     cs[threadIdx.x] = c;
-    double z = 0.0;
-    int tokens = 0, bad = 0;
-    for (int b = threadIdx.x; b < a.blocks; b += kJoinThreads) {
-        z += __ldcg(&a.part_s[b].z);
-        tokens += __ldcg(&a.part_s[b].tokens);
-        bad |= __ldcg(&a.part_s[b].bad);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        z += __shfl_xor_sync(0xffffffffu, z, d);
-        tokens += __shfl_xor_sync(0xffffffffu, tokens, d);
-        bad |= __shfl_xor_sync(0xffffffffu, bad, d);
-    }
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (lane == 0) {
-        zs[warp] = z;
-        ts[warp] = tokens;
-        bs[warp] = bad;
+    if (warp == kJoinThreads / 32 - 1) {
+        Totals t = {0.f, 0, 0};
+        for (int b = lane; b < a.clusters; b += 32) {
+            t.z += __ldcg(&a.part_s[b].z);
+            t.tokens += __ldcg(&a.part_s[b].tokens);
+            t.bad |= __ldcg(&a.part_s[b].bad);
+        }
+        t.z = row_sum<32>(t.z);
+        t.tokens = __reduce_add_sync(0xffffffffu, t.tokens);
+        t.bad = __reduce_or_sync(0xffffffffu, t.bad);
+        if (lane == 0) total = t;
     }
     __syncthreads();
-    double loss = 0.0;
+    float pc = 0.f;
     if (threadIdx.x < a.E) {
-        p = 0.0;
+        Sum q;
         c = 0;
-        for (int i = 0; i < seg; ++i) {
-            p += ps[i * a.E + threadIdx.x];
+        const int n = seg < a.clusters ? seg : a.clusters;
+        for (int i = 0; i < n; ++i) {
+            q.add(ps[i * a.E + threadIdx.x]);
             c += cs[i * a.E + threadIdx.x];
         }
         a.counts[threadIdx.x] = c;
-        loss = p * c;
+        pc = q.value() * static_cast<float>(c);
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, d);
-    if (lane == 0) ls[warp] = loss;
+    pc = row_sum<32>(pc);
+    if (lane == 0) ls[warp] = pc;
     __syncthreads();
     if (threadIdx.x == 0) {
-        z = loss = 0.0;
-        tokens = bad = 0;
-        for (int w = 0; w < kJoinThreads / 32; ++w) {
-            z += zs[w];
-            loss += ls[w];
-            tokens += ts[w];
-            bad |= bs[w];
-        }
-        const double inv = tokens > 0 ? 1.0 / tokens : 0.0;
-        a.losses[0] = static_cast<float>(a.E * loss * inv * inv / a.k);
-        a.losses[1] = static_cast<float>(z * inv);
-        *a.tokens = tokens;
-        *a.status = bad ? MOE_ERR_DEVICE_CHECK : MOE_OK;
+        pc = 0.f;
+        for (int w = 0; w < MOE_MAX_EXPERTS / 32; ++w) pc += ls[w];
+        write_losses(a, pc, total);
     }
 }
 
 template <bool kBf16, int kLanes, bool kVec>
 __global__ void __launch_bounds__(kThreads) balance_grad_kernel(const BalanceArgs a) {
     constexpr int kPerWarp = 32 / kLanes;
+    constexpr int kRows = kRowsPerWarp<kLanes>;
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x % 32;
     const int t = lane % kLanes, sub = lane / kLanes;
     const int T = __ldcg(a.tokens);
     const float invT = T > 0 ? 1.f / static_cast<float>(T) : 0.f;
-    const float g0 = __ldcg(a.grad) * static_cast<float>(a.E) * invT;
+    // E d_e = (E c_e - k T) / (k T): the difference in whole numbers
+    const int64_t kT = static_cast<int64_t>(a.k) * T;
+    const float g0 =
+        T > 0 ? __ldcg(a.grad) * invT / static_cast<float>(kT) : 0.f;
     const float g1 = 2.f * __ldcg(a.grad + 1) * invT;
     float d[kVals];
 #pragma unroll
     for (int v = 0; v < kVals; ++v) {
         const int e = expert_of<kLanes, kVec>(t, v);
-        d[v] = 0.f;
-        if (e < a.E && T > 0)
-            d[v] = static_cast<float>(
-                static_cast<double>(__ldcg(a.counts_in + e)) / (static_cast<double>(a.k) * T) -
-                1.0 / a.E);
+        d[v] = e < a.E ? static_cast<float>(static_cast<int64_t>(__ldcg(a.counts_in + e)) * a.E -
+                                            kT)
+                       : 0.f;
     }
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * kPerWarp;
-    for (int64_t base = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / 32 *
-                        kPerWarp;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * kRows;
+    for (int64_t base = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / 32 * kRows;
          base < a.N; base += step) {
-        const int64_t n = base + sub;
-        const bool in = n < a.N && (!a.mask || __ldcg(a.mask + n));
-        float x[kVals];
-        if (in) {
-            load_row<kBf16, kLanes, kVec>(a.logits, n, a.E, t, x);
-        } else {
+        float x[kUnroll][kVals];
+        bool in[kUnroll];
 #pragma unroll
-            for (int v = 0; v < kVals; ++v) x[v] = kNegInf;
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t n = base + u * kPerWarp + sub;
+            in[u] = n < a.N;
+            if (in[u]) {
+                load_row<kBf16, kLanes, kVec>(a.logits, n, a.E, t, x[u]);
+                if (a.mask) in[u] = __ldcg(a.mask + n);
+            }
         }
-        const float lse = softmax_row<kLanes>(x);
-        float mean = 0.f;
 #pragma unroll
-        for (int v = 0; v < kVals; ++v) mean = fmaf(d[v], x[v], mean);
-        mean = row_sum<kLanes>(mean);
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t n = base + u * kPerWarp + sub;
+            if (!in[u]) {
 #pragma unroll
-        for (int v = 0; v < kVals; ++v)
-            x[v] = in ? x[v] * fmaf(g0, d[v] - mean, g1 * lse) : 0.f;
-        if (n < a.N) store_row<kBf16, kLanes, kVec>(a.dlogits, n, a.E, t, x);
+                for (int v = 0; v < kVals; ++v) x[u][v] = kNegInf;
+            }
+            const float lse = softmax_row<kLanes>(x[u]);
+            float mean = 0.f;
+#pragma unroll
+            for (int v = 0; v < kVals; ++v) mean = fmaf(d[v], x[u][v], mean);
+            mean = row_sum<kLanes>(mean);
+#pragma unroll
+            for (int v = 0; v < kVals; ++v)
+                x[u][v] = in[u] ? x[u][v] * fmaf(g0, d[v] - mean, g1 * lse) : 0.f;
+            if (n < a.N) store_row<kBf16, kLanes, kVec>(a.dlogits, n, a.E, t, x[u]);
+        }
     }
 }
 
@@ -387,31 +509,34 @@ cudaError_t launch(const BalanceArgs &a, int blocks, cudaStream_t s) {
         a.bf16 ? (vec ? kernel_of<kGrad, true, true>(lanes) : kernel_of<kGrad, true, false>(lanes))
                : (vec ? kernel_of<kGrad, false, true>(lanes)
                       : kernel_of<kGrad, false, false>(lanes));
-    return launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, 1, a);
+    return launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s,
+                      kGrad ? 1 : kBalanceCluster, a);
 }
 
-int rows_per_pass(int E) {
+int rows_per_block(int E) {
     int lanes = 1;
     while (lanes * kVals < E) lanes *= 2;
-    return kThreads / lanes;
+    return kThreads / lanes * kUnroll;
 }
 
 }  // namespace
 
-int balance_blocks(int64_t N, int E) {
-    const int64_t b = (N + rows_per_pass(E) - 1) / rows_per_pass(E);
-    return b < 1 ? 1 : static_cast<int>(b < kBalanceMaxBlocks ? b : kBalanceMaxBlocks);
+int balance_clusters(int64_t N, int E) {
+    const int64_t rows = static_cast<int64_t>(kBalanceCluster) * rows_per_block(E);
+    const int64_t c = (N + rows - 1) / rows;
+    return c < 1 ? 1 : static_cast<int>(c < kBalanceMaxClusters ? c : kBalanceMaxClusters);
 }
 
-cudaError_t launch_balance(const BalanceArgs &a, cudaStream_t s) {
-    cudaError_t e = launch<false>(a, a.blocks, s);
-    if (e != cudaSuccess) return e;
+cudaError_t launch_balance(const BalanceArgs &a, int *launches, cudaStream_t s) {
+    *launches = a.clusters > 1 ? 2 : 1;
+    cudaError_t e = launch<false>(a, a.clusters * kBalanceCluster, s);
+    if (e != cudaSuccess || a.clusters == 1) return e;
     return launch_pdl(balance_join_kernel, dim3(1), dim3(kJoinThreads), 0, s, 1, a);
 }
 
 cudaError_t launch_balance_backward(const BalanceArgs &a, int num_sms, cudaStream_t s) {
-    int64_t blocks = (a.N + rows_per_pass(a.E) - 1) / rows_per_pass(a.E);
-    if (blocks > num_sms * 8) blocks = num_sms * 8;
+    int64_t blocks = (a.N + rows_per_block(a.E) - 1) / rows_per_block(a.E);
+    if (blocks > num_sms * 4) blocks = num_sms * 4;
     return launch<true>(a, static_cast<int>(blocks), s);
 }
 

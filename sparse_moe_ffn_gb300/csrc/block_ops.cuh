@@ -45,10 +45,11 @@ struct LinearArgs {
 
 // ------------------------------------------------------------ balance loss
 
-constexpr int kBalanceMaxBlocks = 304;
+constexpr int kBalanceCluster = 8;       // blocks that join their sums on chip
+constexpr int kBalanceMaxClusters = 38;  // two blocks an SM
 
 struct BalancePart {
-    double z;     // sum of lse^2 over the block's tokens
+    float z;      // sum of lse^2 over the cluster's tokens
     int tokens;
     int bad;      // an id >= E was seen
 };
@@ -61,10 +62,10 @@ struct BalanceArgs {
     int64_t N;
     int E, k;
     // forward
-    int blocks;
-    float *part_p;           // [blocks, E]
-    int32_t *part_c;         // [blocks, E]
-    BalancePart *part_s;     // [blocks]
+    int clusters;
+    float *part_p;           // [clusters, E]
+    int32_t *part_c;         // [clusters, E]
+    BalancePart *part_s;     // [clusters]
     float *losses;           // [2]
     int32_t *counts;         // [E]
     int32_t *tokens;         // [1]; read by the backward pass
@@ -75,8 +76,8 @@ struct BalanceArgs {
     void *dlogits;
 };
 
-int balance_blocks(int64_t N, int E);
-cudaError_t launch_balance(const BalanceArgs &a, cudaStream_t s);
+int balance_clusters(int64_t N, int E);
+cudaError_t launch_balance(const BalanceArgs &a, int *launches, cudaStream_t s);
 cudaError_t launch_balance_backward(const BalanceArgs &a, int num_sms, cudaStream_t s);
 
 }  // namespace moe
