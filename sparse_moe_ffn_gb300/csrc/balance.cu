@@ -40,9 +40,14 @@ __device__ __forceinline__ int expert_of(int t, int v) {
     return kVec ? 4 * (t + kLanes * (v / 4)) + v % 4 : t + kLanes * v;
 }
 
+// Element `i` of the logits (a row's start), as the type says.
+template <bool kBf16, typename P>
+__device__ __forceinline__ P *at_element(P *base, int64_t i) {
+    return reinterpret_cast<P *>(reinterpret_cast<uintptr_t>(base) + i * (kBf16 ? 2 : 4));
+}
+
 template <bool kBf16, int kLanes, bool kVec>
-__device__ __forceinline__ void load_row(const void *logits, int64_t n, int E, int t,
-                                         float (&x)[kVals]) {
+__device__ __forceinline__ void load_row(const void *row, int E, int t, float (&x)[kVals]) {
     if (kVec) {
 #pragma unroll
         for (int c = 0; c < kVals / 4; ++c) {
@@ -51,12 +56,12 @@ __device__ __forceinline__ void load_row(const void *logits, int64_t n, int E, i
             if (e < E) {
                 if (kBf16) {
                     const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(
-                        static_cast<const uint16_t *>(logits) + n * E + e));
+                        static_cast<const uint16_t *>(row) + e));
                     const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y);
                     f = make_float4(a.x, a.y, b.x, b.y);
                 } else {
-                    f = __ldcg(reinterpret_cast<const float4 *>(
-                        static_cast<const float *>(logits) + n * E + e));
+                    f = __ldcg(reinterpret_cast<const float4 *>(static_cast<const float *>(row) +
+                                                                e));
                 }
             }
             x[4 * c] = f.x;
@@ -72,30 +77,28 @@ __device__ __forceinline__ void load_row(const void *logits, int64_t n, int E, i
             if (e < E) {
                 if (kBf16)
                     x[v] = __uint_as_float(
-                        static_cast<uint32_t>(
-                            __ldcg(static_cast<const uint16_t *>(logits) + n * E + e))
+                        static_cast<uint32_t>(__ldcg(static_cast<const uint16_t *>(row) + e))
                         << 16);
                 else
-                    x[v] = __ldcg(static_cast<const float *>(logits) + n * E + e);
+                    x[v] = __ldcg(static_cast<const float *>(row) + e);
             }
         }
     }
 }
 
 template <bool kBf16, int kLanes, bool kVec>
-__device__ __forceinline__ void store_row(void *out, int64_t n, int E, int t,
-                                          const float (&x)[kVals]) {
+__device__ __forceinline__ void store_row(void *row, int E, int t, const float (&x)[kVals]) {
     if (kVec) {
 #pragma unroll
         for (int c = 0; c < kVals / 4; ++c) {
             const int e = 4 * (t + kLanes * c);
             if (e >= E) continue;
             if (kBf16)
-                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + n * E + e) =
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(row) + e) =
                     make_uint2(pack_bf16x2(x[4 * c], x[4 * c + 1]),
                                pack_bf16x2(x[4 * c + 2], x[4 * c + 3]));
             else
-                *reinterpret_cast<float4 *>(static_cast<float *>(out) + n * E + e) =
+                *reinterpret_cast<float4 *>(static_cast<float *>(row) + e) =
                     make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
         }
     } else {
@@ -104,9 +107,9 @@ __device__ __forceinline__ void store_row(void *out, int64_t n, int E, int t,
             const int e = t + kLanes * v;
             if (e >= E) continue;
             if (kBf16)
-                static_cast<__nv_bfloat16 *>(out)[n * E + e] = __float2bfloat16_rn(x[v]);
+                static_cast<__nv_bfloat16 *>(row)[e] = __float2bfloat16_rn(x[v]);
             else
-                static_cast<float *>(out)[n * E + e] = x[v];
+                static_cast<float *>(row)[e] = x[v];
         }
     }
 }
@@ -125,26 +128,36 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// x <- softmax of the row; returns its log-sum-exp.  A NaN logit reaches both
-// (fmaxf drops it, the sum does not).
+// 2^x, 1/x and log2 x in one instruction each (off by two steps at most, and
+// below 2^-126 it is 0): softmax spends its time on these.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// x <- e^(x - top) of the row; returns the factor that makes them
+// probabilities, and the row's log-sum-exp in *lse.  The exponent is one fma:
+// what the rounding of top log2(e) leaves is a factor common to the row.  A
+// NaN logit reaches both results (fmaxf drops it, the sum does not).
 template <int kLanes>
-__device__ __forceinline__ float softmax_row(float (&x)[kVals]) {
-    float top = kNegInf;
+__device__ __forceinline__ float softmax_row(float (&x)[kVals], float *lse) {
+    constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+    float top = x[0];
 #pragma unroll
-    for (int v = 0; v < kVals; ++v) top = fmaxf(top, x[v]);
+    for (int v = 1; v < kVals; ++v) top = fmaxf(top, x[v]);
     top = row_max<kLanes>(top);
     if (top == kNegInf) top = 0.f;
+    const float off = -top * kLog2e;
     float sum = 0.f;
 #pragma unroll
     for (int v = 0; v < kVals; ++v) {
-        x[v] = __expf(x[v] - top);
+        x[v] = exp2_fast(fmaf(x[v], kLog2e, off));
         sum += x[v];
     }
     sum = row_sum<kLanes>(sum);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int v = 0; v < kVals; ++v) x[v] *= inv;
-    return sum == 0.f ? 0.f : top + logf(sum);
+    *lse = sum == 0.f ? 0.f : fmaf(kLn2, __log2f(sum), top);
+    return sum == 0.f ? 0.f : __fdividef(1.f, sum);
 }
 
 // The rows that a warp holds at once: kUnroll per group of kLanes lanes, so
@@ -233,40 +246,48 @@ __global__ void __launch_bounds__(kThreads) balance_stats_kernel(const BalanceAr
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * kRows;
     for (int64_t base = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRows; base < a.N;
          base += step) {
+        const int left = a.N - base < kRows ? static_cast<int>(a.N - base) : kRows;
+        const void *rows = at_element<kBf16>(a.logits, base * a.E);
+        const int32_t *ids = a.ids + base * a.k;
         float x[kUnroll][kVals];
         int id[kUnroll];
         bool in[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int64_t n = base + u * kPerWarp + sub;
-            in[u] = n < a.N;
-            id[u] = -1;
-            if (in[u]) {
-                load_row<kBf16, kLanes, kVec>(a.logits, n, a.E, t, x[u]);
-                if (t < a.k) id[u] = __ldcg(a.ids + n * a.k + t);
-                if (a.mask) in[u] = __ldcg(a.mask + n);
+            // past the end: the last row again, with no weight
+            const int r = min(u * kPerWarp + sub, left - 1);
+            in[u] = u * kPerWarp + sub < left;
+            load_row<kBf16, kLanes, kVec>(at_element<kBf16>(rows, r * a.E), a.E, t, x[u]);
+            id[u] = t < a.k ? __ldcg(ids + r * a.k + t) : -1;
+        }
+        if (a.mask) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                in[u] = in[u] && __ldcg(a.mask + base + u * kPerWarp + sub);
+#pragma unroll
+                for (int v = 0; v < kVals; ++v) x[u][v] = in[u] ? x[u][v] : kNegInf;
             }
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            if (!in[u]) {
-#pragma unroll
-                for (int v = 0; v < kVals; ++v) x[u][v] = kNegInf;
-            } else {
+            if (in[u]) {
                 if (id[u] >= a.E) bad = 1;
                 else if (id[u] >= 0) atomicAdd(&cs[id[u]], 1);
-                const int64_t n = base + u * kPerWarp + sub;
                 for (int j = t + kLanes; j < a.k; j += kLanes) {  // more slots than lanes
-                    const int more = __ldcg(a.ids + n * a.k + j);
+                    const int more = __ldcg(ids + (u * kPerWarp + sub) * a.k + j);
                     if (more >= a.E) bad = 1;
                     else if (more >= 0) atomicAdd(&cs[more], 1);
                 }
-                tokens += t == 0;
             }
-            const float lse = softmax_row<kLanes>(x[u]);
+            float lse;
+            const float f = softmax_row<kLanes>(x[u], &lse);
+            const float w = in[u] ? f : 0.f;
 #pragma unroll
-            for (int v = 0; v < kVals; ++v) p[v] += x[u][v];
-            if (t == 0) z = fmaf(lse, lse, z);
+            for (int v = 0; v < kVals; ++v) p[v] = fmaf(x[u][v], w, p[v]);
+            if (in[u] && t == 0) {
+                z = fmaf(lse, lse, z);
+                ++tokens;
+            }
         }
     }
     // rows of the warp, then the warps of the block, in order
@@ -431,49 +452,54 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(const BalanceArg
     const int t = lane % kLanes, sub = lane / kLanes;
     const int T = __ldcg(a.tokens);
     const float invT = T > 0 ? 1.f / static_cast<float>(T) : 0.f;
-    // E d_e = (E c_e - k T) / (k T): the difference in whole numbers
+    // g0 E d_e / T with E d_e = (E c_e - k T) / (k T): the difference in whole
+    // numbers
     const int64_t kT = static_cast<int64_t>(a.k) * T;
-    const float g0 =
-        T > 0 ? __ldcg(a.grad) * invT / static_cast<float>(kT) : 0.f;
+    const float g0 = T > 0 ? __ldcg(a.grad) * invT / static_cast<float>(kT) : 0.f;
     const float g1 = 2.f * __ldcg(a.grad + 1) * invT;
     float d[kVals];
 #pragma unroll
     for (int v = 0; v < kVals; ++v) {
         const int e = expert_of<kLanes, kVec>(t, v);
-        d[v] = e < a.E ? static_cast<float>(static_cast<int64_t>(__ldcg(a.counts_in + e)) * a.E -
-                                            kT)
+        d[v] = e < a.E ? g0 * static_cast<float>(
+                                  static_cast<int64_t>(__ldcg(a.counts_in + e)) * a.E - kT)
                        : 0.f;
     }
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * kRows;
     for (int64_t base = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / 32 * kRows;
          base < a.N; base += step) {
+        const int left = a.N - base < kRows ? static_cast<int>(a.N - base) : kRows;
+        const void *rows = at_element<kBf16>(a.logits, base * a.E);
+        void *out = at_element<kBf16>(a.dlogits, base * a.E);
         float x[kUnroll][kVals];
         bool in[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int64_t n = base + u * kPerWarp + sub;
-            in[u] = n < a.N;
-            if (in[u]) {
-                load_row<kBf16, kLanes, kVec>(a.logits, n, a.E, t, x[u]);
-                if (a.mask) in[u] = __ldcg(a.mask + n);
-            }
+            const int r = u * kPerWarp + sub;
+            in[u] = r < left;
+            if (in[u])  // rows of its own only: out may be the logits
+                load_row<kBf16, kLanes, kVec>(at_element<kBf16>(rows, r * a.E), a.E, t, x[u]);
+        }
+        if (a.mask) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                in[u] = in[u] && __ldcg(a.mask + base + u * kPerWarp + sub);
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int64_t n = base + u * kPerWarp + sub;
-            if (!in[u]) {
-#pragma unroll
-                for (int v = 0; v < kVals; ++v) x[u][v] = kNegInf;
-            }
-            const float lse = softmax_row<kLanes>(x[u]);
+            float lse;
+            const float f = softmax_row<kLanes>(x[u], &lse);
             float mean = 0.f;
 #pragma unroll
             for (int v = 0; v < kVals; ++v) mean = fmaf(d[v], x[u][v], mean);
-            mean = row_sum<kLanes>(mean);
+            mean = row_sum<kLanes>(mean) * f;
+            const float rest = fmaf(g1, lse, -mean);
 #pragma unroll
             for (int v = 0; v < kVals; ++v)
-                x[u][v] = in[u] ? x[u][v] * fmaf(g0, d[v] - mean, g1 * lse) : 0.f;
-            if (n < a.N) store_row<kBf16, kLanes, kVec>(a.dlogits, n, a.E, t, x[u]);
+                x[u][v] = in[u] ? x[u][v] * f * (d[v] + rest) : 0.f;
+            const int r = u * kPerWarp + sub;
+            if (r < left)
+                store_row<kBf16, kLanes, kVec>(at_element<kBf16>(out, r * a.E), a.E, t, x[u]);
         }
     }
 }
