@@ -35,18 +35,4 @@ __device__ __forceinline__ float linear_act(int act, float v) {
     }
 }
 
-// Output (n, o) from its accumulator.
-__device__ __forceinline__ void store_linear(const LinearArgs &a, int64_t n, int64_t o,
-                                             float v) {
-    if (a.x_scale) v = v * __ldcg(a.x_scale + n) * __ldcg(a.w_scale + o);
-    if (a.bias) v += __uint_as_float(static_cast<uint32_t>(__ldcg(a.bias + o)) << 16);
-    v = linear_act(a.act, v);
-    const int64_t i = n * a.O + o;
-    if (a.residual) v += __uint_as_float(static_cast<uint32_t>(__ldcg(a.residual + i)) << 16);
-    if (a.out_fp32)
-        static_cast<float *>(a.out)[i] = v;
-    else
-        static_cast<__nv_bfloat16 *>(a.out)[i] = __float2bfloat16_rn(v);
-}
-
 }  // namespace moe

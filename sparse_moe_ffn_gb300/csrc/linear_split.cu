@@ -14,8 +14,9 @@
 //
 //   warp 0  producer (one lane): TMA copies; up to kStages slices in flight
 //   warp 1  TMEM, and one lane issues the MMAs
-//   all     4 warps read the accumulator (32 TMEM lanes = outputs each), then
-//           all add and store
+//   all     read the accumulator (warp w the TMEM lanes = outputs 32 (w % 4) ..
+//           + 31), then add and store; bias, scales and residual are fetched
+//           before the accumulator is waited for
 // Every wait is bounded; a CTA that gives up records MOE_ERR_DEVICE_TIMEOUT
 // and still takes part in the cluster's barriers.
 #include "linear_epilogue.cuh"
@@ -25,7 +26,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kSplitThreads = 128;
+constexpr int kSplitThreads = 256;
 constexpr int kOut = 128;  // outputs of a tile
 
 template <int kBN>
@@ -43,12 +44,124 @@ struct SplitShared {
     int abort_flag;
 };
 
+// kVec outputs from o on of a residual row
+template <int kVec>
+struct ResidualOf;
+template <>
+struct ResidualOf<4> {
+    uint2 u;
+    __device__ __forceinline__ void load(const uint16_t *p) {
+        u = __ldcg(reinterpret_cast<const uint2 *>(p));
+    }
+    __device__ __forceinline__ void add(float (&v)[4]) const {
+        const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y);
+        v[0] += a.x;
+        v[1] += a.y;
+        v[2] += b.x;
+        v[3] += b.y;
+    }
+};
+template <>
+struct ResidualOf<1> {
+    uint16_t u;
+    __device__ __forceinline__ void load(const uint16_t *p) { u = __ldcg(p); }
+    __device__ __forceinline__ void add(float (&v)[1]) const {
+        v[0] += __uint_as_float(static_cast<uint32_t>(u) << 16);
+    }
+};
+
+// Adds the ranks' parts of this CTA's `mine` tokens and stores them, kVec
+// outputs a thread; a thread keeps its outputs from token to token.  The
+// epilogue's operands are fetched before `ready` waits for the parts.
+template <bool kFp8, int kVec, typename Ready>
+__device__ __forceinline__ void store_parts(const LinearArgs &a, const float *part, int o0,
+                                            int64_t first, int mine, int split, int own_log,
+                                            volatile int *abort_flag, const Ready &ready) {
+    constexpr int kLanes = kOut / kVec;               // threads a token
+    constexpr int kStep = kSplitThreads / kLanes;     // tokens in one go
+    constexpr int kBatch = 4;                         // of them fetched ahead
+    const int ch = threadIdx.x % kLanes * kVec;
+    const int o = o0 + ch;
+    const bool live = o < a.O;
+    float ws[kVec], bias[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        ws[i] = kFp8 && live ? __ldcg(a.w_scale + o + i) : 1.f;
+        bias[i] = a.bias && live
+                      ? __uint_as_float(static_cast<uint32_t>(__ldcg(a.bias + o + i)) << 16)
+                      : 0.f;
+    }
+    ResidualOf<kVec> res[kBatch];
+    float xs[kBatch];
+    const int t0 = threadIdx.x / kLanes;
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int64_t n = first + t + b * kStep;
+            if (t + b * kStep < mine && live) {
+                if (a.residual) res[b].load(a.residual + n * a.O + o);
+                if (kFp8) xs[b] = __ldcg(a.x_scale + n);
+            }
+        }
+    };
+    fetch(t0);
+    ready();
+    if (!live || *abort_flag) return;
+    for (int t = t0; t < mine; t += kBatch * kStep) {
+        if (t != t0) fetch(t);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int tt = t + b * kStep;
+            if (tt >= mine) break;
+            float v[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) v[i] = 0.f;
+            for (int r = 0; r < split; ++r) {
+                const float *p = part + (((r << own_log) + tt) * kOut + ch);
+                if (kVec == 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(p);
+                    v[0] += f.x;
+                    v[1 % kVec] += f.y;
+                    v[2 % kVec] += f.z;
+                    v[3 % kVec] += f.w;
+                } else {
+                    v[0] += *p;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                v[i] = linear_act(a.act, kFp8 ? fmaf(v[i], xs[b] * ws[i], bias[i])
+                                              : v[i] + bias[i]);
+            if (a.residual) res[b].add(v);
+            const int64_t at = (first + tt) * a.O + o;
+            if (a.out_fp32) {
+                float *out = static_cast<float *>(a.out) + at;
+                if (kVec == 4)
+                    *reinterpret_cast<float4 *>(out) =
+                        make_float4(v[0], v[1 % kVec], v[2 % kVec], v[3 % kVec]);
+                else
+                    *out = v[0];
+            } else {
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + at;
+                if (kVec == 4)
+                    *reinterpret_cast<uint2 *>(out) =
+                        make_uint2(pack_bf16x2(v[0], v[1 % kVec]),
+                                   pack_bf16x2(v[2 % kVec], v[3 % kVec]));
+                else
+                    *out = __float2bfloat16_rn(v[0]);
+            }
+        }
+    }
+}
+
 template <bool kFp8, int kBN>
 __global__ void __launch_bounds__(kSplitThreads, 1)
     linear_split_kernel(const __grid_constant__ CUtensorMap tm_x,
                         const __grid_constant__ CUtensorMap tm_w, const LinearArgs a,
-                        const int split) {
+                        const int split_log) {
     using T = SplitTile<kBN>;
+    constexpr int kBNLog = kBN == 16 ? 4 : kBN == 32 ? 5 : kBN == 64 ? 6 : 7;
+    const int split = 1 << split_log;
     constexpr int kStages = T::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = reinterpret_cast<uint8_t *>(
@@ -86,12 +199,12 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     griddep_wait();
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && a.status) *a.status = MOE_OK;
 
-    const int o0 = blockIdx.x / split * kOut;
+    const int o0 = (blockIdx.x >> split_log) * kOut;
     const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kBN;
     const int per_slice = kFp8 ? kSliceBytes : kSliceBytes / 2;
     const int nk = (a.K + per_slice - 1) / per_slice;
-    const int k_first = static_cast<int>(static_cast<int64_t>(nk) * rank / split);
-    const int k_end = static_cast<int>(static_cast<int64_t>(nk) * (rank + 1) / split);
+    const int k_first = static_cast<int>(static_cast<int64_t>(nk) * rank >> split_log);
+    const int k_end = static_cast<int>(static_cast<int64_t>(nk) * (rank + 1) >> split_log);
     const int slices = k_end - k_first;
 
     if (warp == 0) {
@@ -140,48 +253,54 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         __syncwarp();
     }
 
-    bool ok = true;
-    if (lane == 0) ok = mbar_wait(&sm->acc_full, 0, abort_flag);
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (!ok && lane == 0) {
-        record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
-        *abort_flag = 1;
-    }
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    const int own = kBN / split;  // tokens of each CTA
-    if (ok) {
-        tc_fence_after_sync();
-        const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        const uint32_t mine = smem_addr(part + rank * own * kOut + warp * 32 + lane);
-        constexpr int kChunk = kBN < 32 ? 16 : 32;
+    // tokens [n0, n0 + tokens) of the tile exist; this CTA stores [first, first
+    // + 2^own_log) of them
+    const int tokens = a.N - n0 < kBN ? static_cast<int>(a.N - n0) : kBN;
+    const int own_log = kBNLog - split_log;
+    const int mine = min(1 << own_log, tokens - (rank << own_log));  // may be <= 0
+    const int64_t first = n0 + (rank << own_log);
+    // vectors of four outputs where every row allows them
+    const bool vec = a.O % 4 == 0 &&
+                     reinterpret_cast<uintptr_t>(a.out) % (a.out_fp32 ? 16 : 8) == 0 &&
+                     reinterpret_cast<uintptr_t>(a.residual) % 8 == 0;
+    auto ready = [&] {  // the accumulator, then the parts of all ranks
+        bool ok = true;
+        if (lane == 0) ok = mbar_wait(&sm->acc_full, 0, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok && lane == 0) {
+            record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+            *abort_flag = 1;
+        }
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (ok) {
+            tc_fence_after_sync();
+            const int quarter = warp % 4;
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+            const uint32_t to = smem_addr(part) +
+                                4 * ((rank << own_log) * kOut + quarter * 32 + lane);
+            constexpr int kChunk = kBN < 32 ? 16 : 32;
 #pragma unroll 1
-        for (int c = 0; c < kBN; c += kChunk) {
-            float v[32];
-            tmem_load32(taddr + c, v);  // a tile of 16 tokens has 32 columns allocated
-            tmem_load_wait();
-            if (n0 + c >= a.N) break;
+            for (int c = warp / 4 * kChunk; c < tokens; c += kSplitThreads / 128 * kChunk) {
+                float v[32];
+                tmem_load32(taddr + c, v);  // a tile of 16 tokens has 32 columns allocated
+                tmem_load_wait();
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-                const int t = c + i;
-                const int to = t / own;
-                st_cluster_f32(map_to_rank(mine + (t - to * own) * kOut * 4, to), v[i]);
+                for (int i = 0; i < kChunk; ++i) {
+                    const int t = c + i;
+                    if (t < tokens)
+                        st_cluster_f32(map_to_rank(to + 4 * kOut * (t & ((1 << own_log) - 1)),
+                                                   t >> own_log),
+                                       v[i]);
+                }
             }
+            tc_fence_before_sync();
         }
-        tc_fence_before_sync();
-    }
-    cluster_barrier();
-    if (*abort_flag == 0) {
-        const int o = o0 + static_cast<int>(threadIdx.x);
-        if (o < a.O) {
-            for (int t = 0; t < own; ++t) {
-                const int64_t n = n0 + rank * own + t;
-                if (n >= a.N) break;
-                float v = 0.f;
-                for (int r = 0; r < split; ++r) v += part[(r * own + t) * kOut + threadIdx.x];
-                store_linear(a, n, o, v);
-            }
-        }
-    }
+        cluster_barrier();
+    };
+    if (vec)
+        store_parts<kFp8, 4>(a, part, o0, first, mine, split, own_log, abort_flag, ready);
+    else
+        store_parts<kFp8, 1>(a, part, o0, first, mine, split, own_log, abort_flag, ready);
     __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
@@ -192,6 +311,8 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 template <bool kFp8, int kBN>
 cudaError_t launch_one(const CUtensorMap &tm_x, const CUtensorMap &tm_w, const LinearArgs &a,
                        int split, cudaStream_t s) {
+    int split_log = 0;
+    while ((1 << split_log) < split) ++split_log;
     using T = SplitTile<kBN>;
     const size_t smem = 1024 + static_cast<size_t>(T::kStages) * T::kStageBytes +
                         sizeof(float) * T::kPartFloats + sizeof(SplitShared);
@@ -202,7 +323,7 @@ cudaError_t launch_one(const CUtensorMap &tm_x, const CUtensorMap &tm_w, const L
     const dim3 grid(static_cast<unsigned>((a.O + kOut - 1) / kOut * split),
                     static_cast<unsigned>((a.N + kBN - 1) / kBN));
     return launch_pdl(kern, grid, dim3(kSplitThreads), smem, s, static_cast<unsigned>(split), tm_x,
-                      tm_w, a, split);
+                      tm_w, a, split_log);
 }
 
 template <bool kFp8>
