@@ -84,6 +84,15 @@ __device__ __forceinline__ void act_all(int act, float (&v)[kCols]) {
     }
 }
 
+// 32-byte load that stays out of L1 (8 words; p 32-byte aligned)
+__device__ __forceinline__ void ld_global_v8(const void *p, uint32_t *v) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                   "=r"(v[6]), "=r"(v[7])
+                 : "l"(p)
+                 : "memory");
+}
+
 __device__ __forceinline__ void store_8words(void *p, const uint32_t (&w)[8], bool wide) {
     if (wide) {
         st_global_v8(p, w);
@@ -93,25 +102,37 @@ __device__ __forceinline__ void store_8words(void *p, const uint32_t (&w)[8], bo
     }
 }
 
-// 32 outputs [o, o + 32) of token n whose row is aligned for vectors
-__device__ __forceinline__ void store_row32(const LinearArgs &a, int64_t at, bool wide,
-                                            float (&v)[32]) {
-    if (a.residual) {
-        const uint4 *r = reinterpret_cast<const uint4 *>(a.residual + at);
-        uint4 u[4];
+// 32 bf16 values of a residual row whose start is aligned for vectors.
+struct Residual32 {
+    uint32_t w[16];
+    __device__ __forceinline__ void load(const uint16_t *p, bool wide) {
+        if (wide) {
+            ld_global_v8(p, &w[0]);
+            ld_global_v8(p + 16, &w[8]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = __ldcg(r + i);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t *w = reinterpret_cast<const uint32_t *>(&u[i]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = unpack_bf16x2(w[j]);
-                v[8 * i + 2 * j] += f.x;
-                v[8 * i + 2 * j + 1] += f.y;
+            for (int i = 0; i < 4; ++i) {
+                const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = u.x;
+                w[4 * i + 1] = u.y;
+                w[4 * i + 2] = u.z;
+                w[4 * i + 3] = u.w;
             }
         }
     }
+    __device__ __forceinline__ void add(float (&v)[32]) const {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 f = unpack_bf16x2(w[i]);
+            v[2 * i] += f.x;
+            v[2 * i + 1] += f.y;
+        }
+    }
+};
+
+// 32 outputs from element `at` on, in a row that is aligned for vectors
+__device__ __forceinline__ void store_row32(const LinearArgs &a, int64_t at, bool wide,
+                                            const float (&v)[32]) {
     if (a.out_fp32) {
         float *p = static_cast<float *>(a.out) + at;
 #pragma unroll
@@ -289,6 +310,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                          (!a.residual || (a.O % 8 == 0 &&
                                           reinterpret_cast<uintptr_t>(a.residual) % 16 == 0));
         const bool wide = ld % 32 == 0 && out_at % 32 == 0;
+        const bool wide_res =
+            a.O % 16 == 0 && reinterpret_cast<uintptr_t>(a.residual) % 32 == 0;
         int it = 0;
         for (int tile = first; tile < total; tile += step, ++it) {
             int m, nt;
@@ -309,6 +332,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         : 0.f;
             }
             const float sx = kFp8 && n < a.N ? __ldcg(a.x_scale + n) : 1.f;
+            // the residual is read 32 columns ahead of their use
+            Residual32 res;
+            auto fetch = [&](int c) {
+                if (vec && a.residual && c < kCols && n < a.N && o0 + c + 32 <= a.O)
+                    res.load(a.residual + n * a.O + o0 + c, wide_res);
+            };
+            fetch(0);
             __syncwarp();
             bool ok = true;
             if (lane == 0) ok = mbar_wait(&sm->acc_full[acc], (it >> 1) & 1, abort_flag);
@@ -347,6 +377,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 }
                 act_all(a.act, v);
                 if (vec && o0 + c + 32 <= a.O) {
+                    if (a.residual) res.add(v);
+                    fetch(c + 32);
                     if (n < a.N) store_row32(a, n * a.O + o0 + c, wide, v);
                 } else {
                     store_staged(a, sm->stage[ew], n0, o0 + c, lane, v);
