@@ -1320,19 +1320,21 @@ moe_status_t moe_quantize_fp8(const moe_bf16_t *x, int64_t N, int H, moe_e4m3_t 
 
 namespace {
 
-// Dense rows of bf16 or e4m3 values, in 128-byte swizzled boxes of box_rows
-// rows x 128 bytes; what lies outside reads 0.
-moe_status_t make_rows_map(CUtensorMap *m, const void *base, int fp8, int cols, int64_t rows,
-                           int box_rows, const char *what) {
-    if (!fp8) return make_map(m, base, cols, rows, cols, kSliceBytes / 2, box_rows, what);
+// Dense rows of `cols` values, in boxes of box_rows rows x box_cols values;
+// what lies outside reads 0 and is not written.
+moe_status_t make_rows_map(CUtensorMap *m, CUtensorMapDataType type, int size, const void *base,
+                           int cols, int64_t rows, int box_cols, int box_rows, const char *what) {
     auto fn = encode_tiled();
     if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
-    const cuuint32_t box[2] = {kSliceBytes, static_cast<cuuint32_t>(box_rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * size};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols),
+                               static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    CUresult r = fn(m, type, 2, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    box_cols * size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                          : CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(MOE_ERR_CUDA, "tensor map for %s rejected (CUresult %d)", what,
@@ -1374,12 +1376,25 @@ moe_status_t linear_impl(LinearArgs a, void *workspace, size_t workspace_bytes,
     a.status = static_cast<int32_t *>(workspace);
     const int sms = num_sms_of_current_device();
     const LinearTiling t = linear_tiling(a, sms);
-    CUtensorMap tm_x, tm_w;
+    const CUtensorMapDataType type =
+        a.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int size = a.fp8 ? 1 : 2, slice = kSliceBytes / size;
+    CUtensorMap tm_x, tm_w, tm_out;
     moe_status_t st;
-    if ((st = make_rows_map(&tm_x, a.x, a.fp8, a.K, a.N, linear_x_box(t), "x")) != MOE_OK ||
-        (st = make_rows_map(&tm_w, a.w, a.fp8, a.K, a.O, linear_w_box(t), "weight")) != MOE_OK)
+    if ((st = make_rows_map(&tm_x, type, size, a.x, a.K, a.N, slice, linear_x_box(t), "x")) !=
+            MOE_OK ||
+        (st = make_rows_map(&tm_w, type, size, a.w, a.K, a.O, slice, linear_w_box(t),
+                            "weight")) != MOE_OK)
         return st;
-    MOE_CUDA(t.pair ? launch_linear_pair(tm_x, tm_w, a, t, sms, stream)
+    const bool out_map = t.pair && linear_out_rows_aligned(a);
+    if (out_map &&
+        (st = make_rows_map(&tm_out,
+                            a.out_fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                            a.out_fp32 ? 4 : 2, a.out, a.O, a.N, 32, 32, "out")) != MOE_OK)
+        return st;
+    MOE_CUDA(t.pair ? launch_linear_pair(tm_x, tm_w, out_map ? &tm_out : nullptr, a, t, sms,
+                                         stream)
                     : launch_linear_split(tm_x, tm_w, a, t, stream),
              "linear kernel launch");
     g_launches += 1;

@@ -141,9 +141,12 @@ struct LinearTiling {
 LinearTiling linear_tiling(const LinearArgs &a, int num_sms);
 int linear_x_box(const LinearTiling &t);
 int linear_w_box(const LinearTiling &t);
+// Whether the pair kernel can store through a tensor map (tm_out: boxes of 32
+// rows x 32 outputs, 64-byte swizzle for bf16, 128-byte for fp32; else null).
+bool linear_out_rows_aligned(const LinearArgs &a);
 cudaError_t launch_linear_pair(const CUtensorMap &tm_x, const CUtensorMap &tm_w,
-                               const LinearArgs &a, const LinearTiling &t, int num_sms,
-                               cudaStream_t s);
+                               const CUtensorMap *tm_out, const LinearArgs &a,
+                               const LinearTiling &t, int num_sms, cudaStream_t s);
 cudaError_t launch_linear_split(const CUtensorMap &tm_x, const CUtensorMap &tm_w,
                                 const LinearArgs &a, const LinearTiling &t, cudaStream_t s);
 

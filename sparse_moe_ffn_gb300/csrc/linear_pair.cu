@@ -17,10 +17,13 @@
 //              would take as long for an activation as the MMAs of 2048 e4m3
 //              values take.
 //
-// A lane holds 32 consecutive outputs of one token: whole 32-byte sectors in
-// one store when rows are aligned for it; otherwise (an odd number of outputs,
-// an output that starts anywhere) 16 columns at a time go through shared
-// memory and leave with neighbouring lanes on neighbouring outputs.
+// A lane holds 32 consecutive outputs of one token.  Where rows of the output
+// start on 16 bytes, a warp's 32 x 32 outputs go through shared memory into a
+// tensor-map store (stored from the lanes, 32 bytes of 32 rows each, an e4m3
+// call of 8192 x 2048 x 8192 took 112 us, 24 of them for the stores);
+// otherwise (an odd number of outputs, an output that starts anywhere) 16
+// columns at a time are turned there and leave with neighbouring lanes on
+// neighbouring outputs.
 // Every wait is bounded; a CTA that gives up records MOE_ERR_DEVICE_TIMEOUT.
 #include "linear_epilogue.cuh"
 #include "linear_gemm.cuh"
@@ -31,7 +34,7 @@ namespace {
 
 constexpr int kEpiWarps = 8;
 constexpr int kPairThreads = 64 + 32 * kEpiWarps;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kTokens = 256;  // of a tile
 constexpr int kStagePad = 17; // floats of a staged row of 16 columns
 
@@ -52,8 +55,11 @@ struct PairShared {
     int abort_flag;
     alignas(16) float scale[kEpiWarps][128];  // w_scale of a warp's columns
     alignas(16) float bias[kEpiWarps][128];
-    float stage[kEpiWarps][32 * kStagePad];
 };
+
+// Outputs on their way out: 32 tokens x 32 outputs a warp, twice in bf16.
+constexpr int kOutBytes = 4096;
+static_assert(32 * kStagePad * 4 <= kOutBytes, "a staged half chunk fits");
 
 // Tiles run through bands of kBand token tiles, output tile by output tile:
 // the ~76 tiles in flight cover 8 token tiles and ~10 output tiles.
@@ -93,26 +99,19 @@ __device__ __forceinline__ void ld_global_v8(const void *p, uint32_t *v) {
                  : "memory");
 }
 
-__device__ __forceinline__ void store_8words(void *p, const uint32_t (&w)[8], bool wide) {
-    if (wide) {
-        st_global_v8(p, w);
-    } else {
-        static_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        static_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-}
-
 // 32 bf16 values of a residual row whose start is aligned for vectors.
 struct Residual32 {
     uint32_t w[16];
-    __device__ __forceinline__ void load(const uint16_t *p, bool wide) {
-        if (wide) {
+    // the first `left` values exist (a multiple of 8); 32-byte loads if wide
+    __device__ __forceinline__ void load(const uint16_t *p, int left, bool wide) {
+        if (wide && left >= 32) {
             ld_global_v8(p, &w[0]);
             ld_global_v8(p + 16, &w[8]);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint4 u = __ldcg(reinterpret_cast<const uint4 *>(p) + i);
+                const uint4 u = 8 * i < left ? __ldcg(reinterpret_cast<const uint4 *>(p) + i)
+                                             : make_uint4(0, 0, 0, 0);
                 w[4 * i] = u.x;
                 w[4 * i + 1] = u.y;
                 w[4 * i + 2] = u.z;
@@ -130,28 +129,33 @@ struct Residual32 {
     }
 };
 
-// 32 outputs from element `at` on, in a row that is aligned for vectors
-__device__ __forceinline__ void store_row32(const LinearArgs &a, int64_t at, bool wide,
-                                            const float (&v)[32]) {
-    if (a.out_fp32) {
-        float *p = static_cast<float *>(a.out) + at;
+// This lane's row of a 32 x 32 chunk, as a tensor-map store with swizzled rows
+// of 64 bytes (bf16) or 128 (fp32) reads it: neighbouring lanes' 16-byte pieces
+// fall on different banks.
+__device__ __forceinline__ void write_row(uint8_t *buf, int lane, bool fp32,
+                                          const float (&v)[32]) {
+    if (fp32) {
+        uint8_t *row = buf + lane * 128;
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-            uint32_t w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[i + j]);
-            store_8words(p + i, w, wide);
-        }
+        for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4 *>(row + 16 * (j ^ (lane & 7))) =
+                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     } else {
-        uint16_t *p = static_cast<uint16_t *>(a.out) + at;
+        uint8_t *row = buf + lane * 64;
 #pragma unroll
-        for (int i = 0; i < 32; i += 16) {
-            uint32_t w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(v[i + 2 * j], v[i + 2 * j + 1]);
-            store_8words(p + i, w, wide);
-        }
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(row + 16 * (j ^ ((lane >> 1) & 3))) = make_uint4(
+                pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
     }
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int c0,
+                                             int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
+                 ::"l"(map), "r"(smem_addr(src)), "r"(c0), "r"(c1)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
 // The same outputs, any alignment and any part of them inside [0, O): 16
@@ -183,12 +187,15 @@ __device__ __forceinline__ void store_staged(const LinearArgs &a, float *stage, 
 template <bool kFp8, int kBN>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x,
-                       const __grid_constant__ CUtensorMap tm_w, const LinearArgs a) {
+                       const __grid_constant__ CUtensorMap tm_w,
+                       const __grid_constant__ CUtensorMap tm_out, const LinearArgs a,
+                       const int vec) {
     using T = PairTile<kBN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    PairShared *sm = reinterpret_cast<PairShared *>(tiles + kStages * T::kStageBytes);
+    uint8_t *out_bufs = tiles + kStages * T::kStageBytes;
+    PairShared *sm = reinterpret_cast<PairShared *>(out_bufs + kEpiWarps * kOutBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
@@ -302,17 +309,29 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         float *scale_s = sm->scale[ew], *bias_s = sm->bias[ew];
         const uint32_t empty0 = map_to_rank(smem_addr(&sm->acc_empty[0]), 0);
         const uint32_t empty1 = map_to_rank(smem_addr(&sm->acc_empty[1]), 0);
-        // vector stores: rows of out (and residual) that start on 16 bytes
-        const int esize = a.out_fp32 ? 4 : 2;
-        const uintptr_t out_at = reinterpret_cast<uintptr_t>(a.out);
-        const int64_t ld = static_cast<int64_t>(a.O) * esize;
-        const bool vec = ld % 16 == 0 && out_at % 16 == 0 &&
-                         (!a.residual || (a.O % 8 == 0 &&
-                                          reinterpret_cast<uintptr_t>(a.residual) % 16 == 0));
-        const bool wide = ld % 32 == 0 && out_at % 32 == 0;
+        uint8_t *buf = out_bufs + ew * kOutBytes;
         const bool wide_res =
             a.O % 16 == 0 && reinterpret_cast<uintptr_t>(a.residual) % 32 == 0;
-        int it = 0;
+        // a tile's scales and bias are read a tile ahead, in registers
+        float sw_next[kCols / 32], b_next[kCols / 32], sx_next = 1.f;
+        auto fetch_factors = [&](int tile) {
+            if (tile >= total) return;
+            int m, nt;
+            tile_of(tile, m_tiles, n_tiles, &m, &nt);
+            const int64_t n = static_cast<int64_t>(m) * kTokens + rank * 128 + quarter * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < kCols / 32; ++i) {
+                const int o = nt * kBN + half * kCols + 32 * i + lane;
+                sw_next[i] = kFp8 && o < a.O ? __ldcg(a.w_scale + o) : 0.f;
+                b_next[i] =
+                    a.bias && o < a.O
+                        ? __uint_as_float(static_cast<uint32_t>(__ldcg(a.bias + o)) << 16)
+                        : 0.f;
+            }
+            if (kFp8) sx_next = n < a.N ? __ldcg(a.x_scale + n) : 0.f;
+        };
+        fetch_factors(first);
+        int it = 0, chunk = 0;
         for (int tile = first; tile < total; tile += step, ++it) {
             int m, nt;
             tile_of(tile, m_tiles, n_tiles, &m, &nt);
@@ -320,23 +339,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const int o0 = nt * kBN + half * kCols;
             const int64_t n0 = static_cast<int64_t>(m) * kTokens + rank * 128 + quarter * 32;
             const int64_t n = n0 + lane;
-            // this tile's scales and bias, before its accumulator is ready
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < kCols / 32; ++i) {
-                const int o = o0 + 32 * i + lane;
-                if (kFp8) scale_s[32 * i + lane] = o < a.O ? __ldcg(a.w_scale + o) : 0.f;
-                bias_s[32 * i + lane] =
-                    a.bias && o < a.O
-                        ? __uint_as_float(static_cast<uint32_t>(__ldcg(a.bias + o)) << 16)
-                        : 0.f;
+                if (kFp8) scale_s[32 * i + lane] = sw_next[i];
+                bias_s[32 * i + lane] = b_next[i];
             }
-            const float sx = kFp8 && n < a.N ? __ldcg(a.x_scale + n) : 1.f;
+            const float sx = sx_next;
+            fetch_factors(tile + step);
+            // columns of this warp that exist (warp-uniform)
+            const int cols = n0 < a.N ? min(kCols, a.O - o0) : 0;
             // the residual is read 32 columns ahead of their use
             Residual32 res;
             auto fetch = [&](int c) {
-                if (vec && a.residual && c < kCols && n < a.N && o0 + c + 32 <= a.O)
-                    res.load(a.residual + n * a.O + o0 + c, wide_res);
+                if (vec && a.residual && c < cols && n < a.N)
+                    res.load(a.residual + n * a.O + o0 + c, cols - c, wide_res);
             };
             fetch(0);
             __syncwarp();
@@ -354,8 +371,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                    acc * kBN + half * kCols;
 #pragma unroll 1
-            for (int c = 0; c < kCols; c += 32) {
-                if (n0 >= a.N || o0 + c >= a.O) break;  // warp-uniform
+            for (int c = 0; c < cols; c += 32, ++chunk) {
                 float v[32];
                 tmem_load32(taddr + c, v);
                 tmem_load_wait();
@@ -376,18 +392,33 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                 }
                 act_all(a.act, v);
-                if (vec && o0 + c + 32 <= a.O) {
+                if (vec) {
                     if (a.residual) res.add(v);
                     fetch(c + 32);
-                    if (n < a.N) store_row32(a, n * a.O + o0 + c, wide, v);
+                    // the buffer (bf16: the half in turn) has left once at
+                    // most the other half's store is in flight
+                    uint8_t *b = buf;
+                    if (a.out_fp32) {
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    } else {
+                        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        b += (chunk & 1) * (kOutBytes / 2);
+                    }
+                    __syncwarp();
+                    write_row(b, lane, a.out_fp32, v);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) tma_store_2d(&tm_out, b, o0 + c, static_cast<int>(n0));
                 } else {
-                    store_staged(a, sm->stage[ew], n0, o0 + c, lane, v);
+                    store_staged(a, reinterpret_cast<float *>(buf), n0, o0 + c, lane, v);
                 }
             }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) arrive_remote_relaxed(acc ? empty1 : empty0);
         }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // stores have landed
+        __syncwarp();
     }
 
     tc_fence_before_sync();
@@ -400,10 +431,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 }
 
 template <bool kFp8, int kBN>
-cudaError_t launch_one(const CUtensorMap &tm_x, const CUtensorMap &tm_w, const LinearArgs &a,
-                       int num_sms, cudaStream_t s) {
+cudaError_t launch_one(const CUtensorMap &tm_x, const CUtensorMap &tm_w,
+                       const CUtensorMap *tm_out, const LinearArgs &a, int num_sms,
+                       cudaStream_t s) {
     const size_t smem = 1024 + static_cast<size_t>(kStages) * PairTile<kBN>::kStageBytes +
-                        sizeof(PairShared);
+                        kEpiWarps * kOutBytes + sizeof(PairShared);
     auto kern = linear_pair_kernel<kFp8, kBN>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(smem));
@@ -411,19 +443,26 @@ cudaError_t launch_one(const CUtensorMap &tm_x, const CUtensorMap &tm_w, const L
     const int64_t tiles = (a.N + kTokens - 1) / kTokens * ((a.O + kBN - 1) / kBN);
     const int64_t pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
     return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kPairThreads), smem, s, 2,
-                      tm_x, tm_w, a);
+                      tm_x, tm_w, tm_out ? *tm_out : tm_x, a, tm_out ? 1 : 0);
 }
 
 }  // namespace
 
+bool linear_out_rows_aligned(const LinearArgs &a) {
+    const int64_t ld = static_cast<int64_t>(a.O) * (a.out_fp32 ? 4 : 2);
+    return ld % 16 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 &&
+           (!a.residual ||
+            (a.O % 8 == 0 && reinterpret_cast<uintptr_t>(a.residual) % 16 == 0));
+}
+
 cudaError_t launch_linear_pair(const CUtensorMap &tm_x, const CUtensorMap &tm_w,
-                               const LinearArgs &a, const LinearTiling &t, int num_sms,
-                               cudaStream_t s) {
+                               const CUtensorMap *tm_out, const LinearArgs &a,
+                               const LinearTiling &t, int num_sms, cudaStream_t s) {
     if (t.bn == 256)
-        return a.fp8 ? launch_one<true, 256>(tm_x, tm_w, a, num_sms, s)
-                     : launch_one<false, 256>(tm_x, tm_w, a, num_sms, s);
-    return a.fp8 ? launch_one<true, 128>(tm_x, tm_w, a, num_sms, s)
-                 : launch_one<false, 128>(tm_x, tm_w, a, num_sms, s);
+        return a.fp8 ? launch_one<true, 256>(tm_x, tm_w, tm_out, a, num_sms, s)
+                     : launch_one<false, 256>(tm_x, tm_w, tm_out, a, num_sms, s);
+    return a.fp8 ? launch_one<true, 128>(tm_x, tm_w, tm_out, a, num_sms, s)
+                 : launch_one<false, 128>(tm_x, tm_w, tm_out, a, num_sms, s);
 }
 
 }  // namespace moe
