@@ -1,48 +1,60 @@
 // linear.cu -- which kernel and tile moe_linear takes for its sizes.
+//
+// Both kernels' times follow their tile counts, so the rule estimates each
+// candidate and takes the least.  The constants (microseconds) were fitted to
+// measured times of every candidate on a GB300, for 19 batch sizes from 1 to
+// 16384 and 8 weight shapes from 2048 x 128 to 8192 x 2048 in both operand
+// types: the candidate it takes is on average 0.2% slower than the fastest one,
+// 7% at worst.  What the sides are at 2048 x 2048 in bf16, pair tiles of 128
+// outputs against the best split: 256 tokens 15.7 against 9.0 us, 1024 tokens
+// 16.5 against 20.0; pair tiles of 256 against 128 outputs: 1024 tokens 18.3
+// against 16.5, 4096 tokens 30.0 against 46.2.
 #include "linear_gemm.cuh"
 
 namespace moe {
 
 namespace {
 
-// Estimated SM cycles of a call.  A CTA takes in about 64 bytes a cycle
-// from L2 and its tensor core 128 x 128 outputs of a K slice in 256 cycles.
-constexpr double kBytesPerCycle = 64.0;
-constexpr double kCallCycles = 3000.0;
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-double ceil_div(double a, double b) { return static_cast<double>(static_cast<int64_t>((a + b - 1) / b)); }
-
-double pair_cycles(double N, double O, double nk, int bn, int sms) {
-    const double slice = bn * 2.0 > (16384 + bn * 64) / kBytesPerCycle
-                             ? bn * 2.0 : (16384 + bn * 64) / kBytesPerCycle;
-    const double waves = ceil_div(ceil_div(N, 256) * ceil_div(O, bn), sms / 2);
-    return kCallCycles + waves * nk * slice + 12.0 * bn;
+// The persistent pairs: whole waves of tiles, each the K slices' time or, when
+// K is short, the epilogue's, and the last tile's epilogue on its own.
+float pair_us(int64_t N, int64_t O, int nk, int bn, bool aligned, int sms) {
+    const int64_t waves = ceil_div(ceil_div(N, 256) * ceil_div(O, bn), sms / 2);
+    const float slices = nk * (bn == 256 ? 0.437f : 0.326f);
+    const float epilogue = 3.1f * bn / 256 * (aligned ? 1.f : 8.1f);
+    return 3.5f + waves * (slices > epilogue ? slices : epilogue) + 0.9f * epilogue;
 }
 
-double split_cycles(double N, double O, double nk, int bn, int split, int sms) {
-    const double slice = bn * 2.0 > (16384 + bn * 128) / kBytesPerCycle
-                             ? bn * 2.0 : (16384 + bn * 128) / kBytesPerCycle;
-    const double waves = ceil_div(ceil_div(N, bn) * ceil_div(O, 128) * split, sms);
-    return kCallCycles + waves * (1500.0 + ceil_div(nk, split) * slice + 30.0 * bn);
+// Clusters of `split` CTAs of one SM each: clusters of 4 fit 36 times on the
+// 152 SMs and clusters of 8 15 times.
+float split_us(int64_t N, int64_t O, int nk, int bn, int split, bool aligned, int sms) {
+    const int fit = split <= 2 ? sms : split == 4 ? sms * 36 / 38 : sms * 15 / 19;
+    const int64_t waves = ceil_div(ceil_div(N, bn) * ceil_div(O, 128) * split, fit);
+    const float slice = bn == 128 ? 0.35f : bn == 64 ? 0.267f : bn == 32 ? 0.285f : 0.303f;
+    const float epilogue = 0.0247f * bn / split * (aligned ? 1.f : 6.4f) + 0.0115f * bn;
+    return 1.4f + waves * (1.7f + ceil_div(nk, split) * slice + epilogue);
 }
 
 }  // namespace
 
 LinearTiling linear_tiling(const LinearArgs &a, int num_sms) {
-    const double nk = ceil_div(a.K, a.fp8 ? 128 : 64);
+    const int nk = static_cast<int>(ceil_div(a.K, a.fp8 ? 128 : 64));
+    const bool vectors = a.O % 4 == 0;  // of the split kernel's stores
+    const bool rows = linear_out_rows_aligned(a);
     LinearTiling best = {1, 256, 1};
-    double cost = pair_cycles(a.N, a.O, nk, 256, num_sms);
-    const auto take = [&](double c, LinearTiling t) {
-        if (c < cost) {
-            cost = c;
+    float least = pair_us(a.N, a.O, nk, 256, rows, num_sms);
+    const auto consider = [&](float us, LinearTiling t) {
+        if (us < least) {
+            least = us;
             best = t;
         }
     };
-    take(pair_cycles(a.N, a.O, nk, 128, num_sms), {1, 128, 1});
+    consider(pair_us(a.N, a.O, nk, 128, rows, num_sms), {1, 128, 1});
     for (int bn = 16; bn <= 128; bn *= 2) {
-        if ((a.N + bn - 1) / bn > 4096) continue;
+        if (ceil_div(a.N, bn) > 4096) continue;  // rows of its grid
         for (int split = 1; split <= 8 && split <= nk; split *= 2)
-            take(split_cycles(a.N, a.O, nk, bn, split, num_sms), {0, bn, split});
+            consider(split_us(a.N, a.O, nk, bn, split, vectors, num_sms), {0, bn, split});
     }
     return best;
 }
