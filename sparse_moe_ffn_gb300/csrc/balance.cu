@@ -40,6 +40,14 @@ __device__ __forceinline__ int expert_of(int t, int v) {
     return kVec ? 4 * (t + kLanes * (v / 4)) + v % 4 : t + kLanes * v;
 }
 
+// The rows that a warp holds at once: kUnroll per group of kLanes lanes, so
+// that many loads are in flight.  Row u of lane group `sub` is
+// base + u (32 / kLanes) + sub.
+constexpr int kUnroll = 4;
+
+template <int kLanes>
+constexpr int kRowsPerWarp = kUnroll * (32 / kLanes);
+
 // Element `i` of the logits (a row's start), as the type says.
 template <bool kBf16, typename P>
 __device__ __forceinline__ P *at_element(P *base, int64_t i) {
@@ -115,17 +123,29 @@ __device__ __forceinline__ void store_row(void *row, int E, int t, const float (
 }
 
 template <int kLanes>
-__device__ __forceinline__ float row_max(float v) {
-#pragma unroll
-    for (int d = kLanes / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-    return v;
-}
-
-template <int kLanes>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
     for (int d = kLanes / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
+}
+
+// The same over the rows that a warp holds at once, side by side: each step's
+// shuffles are independent of one another.
+template <int kLanes>
+__device__ __forceinline__ void rows_max(float (&v)[kUnroll]) {
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1)
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            v[u] = fmaxf(v[u], __shfl_xor_sync(0xffffffffu, v[u], d));
+}
+
+template <int kLanes>
+__device__ __forceinline__ void rows_sum(float (&v)[kUnroll]) {
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1)
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], d);
 }
 
 // 2^x, 1/x and log2 x in one instruction each (off by two steps at most, and
@@ -136,37 +156,40 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
-// x <- e^(x - top) of the row; returns the factor that makes them
-// probabilities, and the row's log-sum-exp in *lse.  The exponent is one fma:
-// what the rounding of top log2(e) leaves is a factor common to the row.  A
-// NaN logit reaches both results (fmaxf drops it, the sum does not).
+// x[u] <- e^(x - top) of row u; f[u]: the factor that makes them
+// probabilities, lse[u]: the row's log-sum-exp.  The exponent is one fma: what
+// the rounding of top log2(e) leaves is a factor common to the row.  A NaN
+// logit reaches both results (fmaxf drops it, the sum does not).
 template <int kLanes>
-__device__ __forceinline__ float softmax_row(float (&x)[kVals], float *lse) {
+__device__ __forceinline__ void softmax_rows(float (&x)[kUnroll][kVals], float (&f)[kUnroll],
+                                             float (&lse)[kUnroll]) {
     constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-    float top = x[0];
+    float top[kUnroll];
 #pragma unroll
-    for (int v = 1; v < kVals; ++v) top = fmaxf(top, x[v]);
-    top = row_max<kLanes>(top);
-    if (top == kNegInf) top = 0.f;
-    const float off = -top * kLog2e;
-    float sum = 0.f;
+    for (int u = 0; u < kUnroll; ++u) {
+        top[u] = x[u][0];
 #pragma unroll
-    for (int v = 0; v < kVals; ++v) {
-        x[v] = exp2_fast(fmaf(x[v], kLog2e, off));
-        sum += x[v];
+        for (int v = 1; v < kVals; ++v) top[u] = fmaxf(top[u], x[u][v]);
     }
-    sum = row_sum<kLanes>(sum);
-    *lse = sum == 0.f ? 0.f : fmaf(kLn2, __log2f(sum), top);
-    return sum == 0.f ? 0.f : __fdividef(1.f, sum);
+    rows_max<kLanes>(top);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        if (top[u] == kNegInf) top[u] = 0.f;
+        const float off = -top[u] * kLog2e;
+        f[u] = 0.f;
+#pragma unroll
+        for (int v = 0; v < kVals; ++v) {
+            x[u][v] = exp2_fast(fmaf(x[u][v], kLog2e, off));
+            f[u] += x[u][v];
+        }
+    }
+    rows_sum<kLanes>(f);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        lse[u] = f[u] == 0.f ? 0.f : fmaf(kLn2, __log2f(f[u]), top[u]);
+        f[u] = f[u] == 0.f ? 0.f : __fdividef(1.f, f[u]);
+    }
 }
-
-// The rows that a warp holds at once: kUnroll per group of kLanes lanes, so
-// that many loads are in flight.  Row u of lane group `sub` is
-// base + u (32 / kLanes) + sub.
-constexpr int kUnroll = 4;
-
-template <int kLanes>
-constexpr int kRowsPerWarp = kUnroll * (32 / kLanes);
 
 // A sum that keeps what each fp32 addition rounds off (two-sum), so that the
 // order and number of terms cost nothing; the GPU has few 64-bit units.
@@ -279,13 +302,16 @@ __global__ void __launch_bounds__(kThreads) balance_stats_kernel(const BalanceAr
                     else if (more >= 0) atomicAdd(&cs[more], 1);
                 }
             }
-            float lse;
-            const float f = softmax_row<kLanes>(x[u], &lse);
-            const float w = in[u] ? f : 0.f;
+        }
+        float f[kUnroll], lse[kUnroll];
+        softmax_rows<kLanes>(x, f, lse);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const float w = in[u] ? f[u] : 0.f;
 #pragma unroll
             for (int v = 0; v < kVals; ++v) p[v] = fmaf(x[u][v], w, p[v]);
             if (in[u] && t == 0) {
-                z = fmaf(lse, lse, z);
+                z = fmaf(lse[u], lse[u], z);
                 ++tokens;
             }
         }
@@ -485,18 +511,21 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(const BalanceArg
             for (int u = 0; u < kUnroll; ++u)
                 in[u] = in[u] && __ldcg(a.mask + base + u * kPerWarp + sub);
         }
+        float f[kUnroll], lse[kUnroll], mean[kUnroll];
+        softmax_rows<kLanes>(x, f, lse);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            float lse;
-            const float f = softmax_row<kLanes>(x[u], &lse);
-            float mean = 0.f;
+            mean[u] = 0.f;
 #pragma unroll
-            for (int v = 0; v < kVals; ++v) mean = fmaf(d[v], x[u][v], mean);
-            mean = row_sum<kLanes>(mean) * f;
-            const float rest = fmaf(g1, lse, -mean);
+            for (int v = 0; v < kVals; ++v) mean[u] = fmaf(d[v], x[u][v], mean[u]);
+        }
+        rows_sum<kLanes>(mean);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const float rest = fmaf(g1, lse[u], -mean[u] * f[u]);
 #pragma unroll
             for (int v = 0; v < kVals; ++v)
-                x[u][v] = in[u] ? x[u][v] * f * (d[v] + rest) : 0.f;
+                x[u][v] = in[u] ? x[u][v] * f[u] * (d[v] + rest) : 0.f;
             const int r = u * kPerWarp + sub;
             if (r < left)
                 store_row<kBf16, kLanes, kVec>(at_element<kBf16>(out, r * a.E), a.E, t, x[u]);

@@ -6,9 +6,9 @@
 // 16384 and 8 weight shapes from 2048 x 128 to 8192 x 2048 in both operand
 // types: the candidate it takes is on average 0.2% slower than the fastest one,
 // 7% at worst.  What the sides are at 2048 x 2048 in bf16, pair tiles of 128
-// outputs against the best split: 256 tokens 15.7 against 9.0 us, 1024 tokens
-// 16.5 against 20.0; pair tiles of 256 against 128 outputs: 1024 tokens 18.3
-// against 16.5, 4096 tokens 30.0 against 46.2.
+// outputs against the best split: 256 tokens 15.2 against 9.0 us, 1024 tokens
+// 16.2 against 20.1; pair tiles of 256 against 128 outputs: 1024 tokens 18.5
+// against 16.2, 4096 tokens 31.1 against 46.7.
 #include "linear_gemm.cuh"
 
 namespace moe {
