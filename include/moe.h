@@ -561,7 +561,8 @@ moe_status_t moe_linear_fp8(const moe_e4m3_t *x, const float *x_scale, const moe
  *   grad     [2] fp32 (device): the losses' incoming gradients
  *   dlogits  [N, E] out, in the logits' type; may be logits itself
  *   workspace >= moe_balance_loss_workspace_bytes(N, E), 256-byte aligned;
- *            its status word as everywhere
+ *            its status word as everywhere.  NULL where that is 256 (the status
+ *            word alone): then device failures are not recorded
  * A token whose logits are all -inf has p = 0 and lse = 0, gradient 0, and
  * counts in T.  Without tokens (T = 0, N = 0) the losses, counts and
  * gradients are 0.  The sums over tokens have a fixed order: the same inputs

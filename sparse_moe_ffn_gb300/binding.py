@@ -432,13 +432,15 @@ def moe_balance_loss(logits, topk_ids, mask=None, losses=None, counts=None, toke
         counts = torch.empty(E, dtype=torch.int32, device=dev)
     if tokens is None:
         tokens = torch.empty(1, dtype=torch.int32, device=dev)
-    if workspace is None:
-        workspace = torch.empty(_balance_workspace_bytes(N, E), dtype=torch.uint8, device=dev)
+    need = _balance_workspace_bytes(N, E)
+    if workspace is None and need > 256:  # else the status word alone
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _check(lib().moe_balance_loss(
         lp, bf16, _typed(topk_ids, "topk_ids", torch.int32, (N, k)), _mask(mask, N), N, E, k,
         _typed(losses, "losses", torch.float32, (2,)), _typed(counts, "counts", torch.int32, (E,)),
-        _typed(tokens, "tokens", torch.int32, (1,)), workspace.data_ptr(), workspace.numel(),
-        _raw_stream(logits)), "moe_balance_loss")
+        _typed(tokens, "tokens", torch.int32, (1,)),
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel(), _raw_stream(logits)), "moe_balance_loss")
     return losses, counts, tokens
 
 

@@ -1434,6 +1434,11 @@ struct BalanceLayout {
 BalanceLayout balance_layout(int64_t N, int E) {
     BalanceLayout L;
     L.clusters = balance_clusters(N, E);
+    if (L.clusters == 1) {  // its sums stay on chip
+        L.part_s = L.part_p = L.part_c = 0;
+        L.total = kAlign;
+        return L;
+    }
     L.part_s = kAlign;
     L.part_p = round_up(L.part_s + sizeof(BalancePart) * L.clusters, kAlign);
     L.part_c = round_up(L.part_p + sizeof(float) * L.clusters * E, kAlign);
@@ -1466,16 +1471,18 @@ moe_status_t moe_balance_loss(const void *logits, int logits_bf16, const int32_t
     g_last_error.clear();
     const moe_status_t st = check_balance(N, E, k);
     if (st != MOE_OK) return st;
-    if (!losses || !counts || !tokens || !workspace || (N > 0 && (!logits || !topk_ids)))
+    if (!losses || !counts || !tokens || (N > 0 && (!logits || !topk_ids)))
         return fail(MOE_ERR_INVALID_ARG,
-                    "logits, topk_ids, losses, counts, tokens and workspace must be non-null");
+                    "logits, topk_ids, losses, counts and tokens must be non-null");
     if (!aligned_to(logits, logits_bf16 ? 2 : 4) || !aligned_to(topk_ids, 4) ||
         !aligned_to(losses, 4) || !aligned_to(counts, 4) || !aligned_to(tokens, 4))
         return fail(MOE_ERR_INVALID_ARG, "arrays must be aligned to their types");
     if (!aligned_to(workspace, kAlign))
         return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     const BalanceLayout L = balance_layout(N, E);
-    if (workspace_bytes < L.total)
+    if (!workspace && L.clusters > 1)
+        return fail(MOE_ERR_INVALID_ARG, "workspace must be non-null for this many tokens");
+    if (workspace && workspace_bytes < L.total)
         return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "balance workspace needs %zu bytes, got %zu",
                     L.total, workspace_bytes);
     uint8_t *ws = static_cast<uint8_t *>(workspace);

@@ -22,6 +22,8 @@
 // with no atomics on floats, so the same inputs give the same bits.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "block_ops.cuh"
 #include "ptx.cuh"
 
@@ -54,44 +56,83 @@ __device__ __forceinline__ P *at_element(P *base, int64_t i) {
     return reinterpret_cast<P *>(reinterpret_cast<uintptr_t>(base) + i * (kBf16 ? 2 : 4));
 }
 
+// This lane's values of a row as they come from memory: loading them uses none
+// of them, so the loads of all rows, and of the next ones, go out together.
+template <bool kBf16, bool kVec>
+struct RawRow;
+template <>
+struct RawRow<false, true> {
+    float4 c[kVals / 4];
+};
+template <>
+struct RawRow<true, true> {
+    uint2 c[kVals / 4];
+};
+template <>
+struct RawRow<false, false> {
+    float c[kVals];
+};
+template <>
+struct RawRow<true, false> {
+    uint16_t c[kVals];
+};
+
 template <bool kBf16, int kLanes, bool kVec>
-__device__ __forceinline__ void load_row(const void *row, int E, int t, float (&x)[kVals]) {
-    if (kVec) {
+__device__ __forceinline__ void load_row(const void *row, int E, int t,
+                                         RawRow<kBf16, kVec> &raw) {
+    constexpr int kStep = kVec ? 4 : 1;
+    using Piece = typename std::remove_reference<decltype(raw.c[0])>::type;
+#pragma unroll
+    for (int c = 0; c < kVals / kStep; ++c) {
+        const int e = kStep * (t + kLanes * c);
+        if (e < E)
+            raw.c[c] = __ldcg(reinterpret_cast<const Piece *>(at_element<kBf16>(row, e)));
+    }
+}
+
+template <bool kBf16, int kLanes, bool kVec>
+__device__ __forceinline__ void unpack_row(const RawRow<kBf16, kVec> &raw, int E, int t,
+                                           float (&x)[kVals]) {
+    if constexpr (kVec) {
 #pragma unroll
         for (int c = 0; c < kVals / 4; ++c) {
-            const int e = 4 * (t + kLanes * c);
-            float4 f = make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
-            if (e < E) {
-                if (kBf16) {
-                    const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(
-                        static_cast<const uint16_t *>(row) + e));
-                    const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y);
-                    f = make_float4(a.x, a.y, b.x, b.y);
-                } else {
-                    f = __ldcg(reinterpret_cast<const float4 *>(static_cast<const float *>(row) +
-                                                                e));
-                }
+            float4 f;
+            if constexpr (kBf16) {
+                const float2 a = unpack_bf16x2(raw.c[c].x), b = unpack_bf16x2(raw.c[c].y);
+                f = make_float4(a.x, a.y, b.x, b.y);
+            } else {
+                f = raw.c[c];
             }
-            x[4 * c] = f.x;
-            x[4 * c + 1] = f.y;
-            x[4 * c + 2] = f.z;
-            x[4 * c + 3] = f.w;
+            const bool live = 4 * (t + kLanes * c) < E;
+            x[4 * c] = live ? f.x : kNegInf;
+            x[4 * c + 1] = live ? f.y : kNegInf;
+            x[4 * c + 2] = live ? f.z : kNegInf;
+            x[4 * c + 3] = live ? f.w : kNegInf;
         }
     } else {
 #pragma unroll
         for (int v = 0; v < kVals; ++v) {
-            const int e = t + kLanes * v;
-            x[v] = kNegInf;
-            if (e < E) {
-                if (kBf16)
-                    x[v] = __uint_as_float(
-                        static_cast<uint32_t>(__ldcg(static_cast<const uint16_t *>(row) + e))
-                        << 16);
-                else
-                    x[v] = __ldcg(static_cast<const float *>(row) + e);
-            }
+            float f;
+            if constexpr (kBf16) f = __uint_as_float(static_cast<uint32_t>(raw.c[v]) << 16);
+            else f = raw.c[v];
+            x[v] = t + kLanes * v < E ? f : kNegInf;
         }
     }
+}
+
+// The rows of a warp that start at row `base`; past the end the last row stands
+// in (it gets no weight).  `left` of them exist.
+template <bool kBf16, int kLanes, bool kVec>
+__device__ __forceinline__ void load_rows(const BalanceArgs &a, int64_t base, int t, int sub,
+                                          RawRow<kBf16, kVec> (&raw)[kUnroll]) {
+    if (base >= a.N) return;
+    const int left = a.N - base < kRowsPerWarp<kLanes>
+                         ? static_cast<int>(a.N - base) : kRowsPerWarp<kLanes>;
+    const void *rows = at_element<kBf16>(a.logits, base * a.E);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+        load_row<kBf16, kLanes, kVec>(
+            at_element<kBf16>(rows, min(u * (32 / kLanes) + sub, left - 1) * a.E), a.E, t, raw[u]);
 }
 
 template <bool kBf16, int kLanes, bool kVec>
@@ -238,11 +279,11 @@ __device__ __forceinline__ void write_losses(const BalanceArgs &a, float pc, con
     a.losses[0] = static_cast<float>(a.E) / static_cast<float>(a.k) * (pc * inv) * inv;
     a.losses[1] = t.z * inv;
     *a.tokens = t.tokens;
-    *a.status = t.bad ? MOE_ERR_DEVICE_CHECK : MOE_OK;
+    if (a.status) *a.status = t.bad ? MOE_ERR_DEVICE_CHECK : MOE_OK;
 }
 
 template <bool kBf16, int kLanes, bool kVec>
-__global__ void __launch_bounds__(kThreads) balance_stats_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) balance_stats_kernel(const BalanceArgs a) {
     constexpr int kPerWarp = 32 / kLanes;
     constexpr int kWarps = kThreads / 32;
     constexpr int kRows = kRowsPerWarp<kLanes>;
@@ -266,23 +307,33 @@ __global__ void __launch_bounds__(kThreads) balance_stats_kernel(const BalanceAr
     for (int v = 0; v < kVals; ++v) p[v] = 0.f;
     float z = 0.f;
     int tokens = 0;
+    bool over = false;  // an id >= E was seen
     const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * kRows;
-    for (int64_t base = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRows; base < a.N;
-         base += step) {
+    int64_t base = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRows;
+    RawRow<kBf16, kVec> raw[kUnroll];
+    int id_next[kUnroll];  // slot t of each row
+    auto load_next = [&](int64_t at) {
+        load_rows<kBf16, kLanes, kVec>(a, at, t, sub, raw);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t n = at + u * kPerWarp + sub;
+            id_next[u] = n < a.N && t < a.k ? __ldcg(a.ids + n * a.k + t) : -1;
+        }
+    };
+    load_next(base);
+    for (; base < a.N; base += step) {
         const int left = a.N - base < kRows ? static_cast<int>(a.N - base) : kRows;
-        const void *rows = at_element<kBf16>(a.logits, base * a.E);
         const int32_t *ids = a.ids + base * a.k;
         float x[kUnroll][kVals];
         int id[kUnroll];
         bool in[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            // past the end: the last row again, with no weight
-            const int r = min(u * kPerWarp + sub, left - 1);
             in[u] = u * kPerWarp + sub < left;
-            load_row<kBf16, kLanes, kVec>(at_element<kBf16>(rows, r * a.E), a.E, t, x[u]);
-            id[u] = t < a.k ? __ldcg(ids + r * a.k + t) : -1;
+            id[u] = id_next[u];
+            unpack_row<kBf16, kLanes, kVec>(raw[u], a.E, t, x[u]);
         }
+        load_next(base + step);
         if (a.mask) {
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
@@ -293,15 +344,16 @@ __global__ void __launch_bounds__(kThreads) balance_stats_kernel(const BalanceAr
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            if (in[u]) {
-                if (id[u] >= a.E) bad = 1;
-                else if (id[u] >= 0) atomicAdd(&cs[id[u]], 1);
-                for (int j = t + kLanes; j < a.k; j += kLanes) {  // more slots than lanes
+            over |= in[u] && id[u] >= a.E;
+            if (in[u] && id[u] >= 0 && id[u] < a.E) atomicAdd(&cs[id[u]], 1);
+        }
+        if (a.k > kLanes) {  // more slots than lanes
+            for (int u = 0; u < kUnroll; ++u)
+                for (int j = t + kLanes; in[u] && j < a.k; j += kLanes) {
                     const int more = __ldcg(ids + (u * kPerWarp + sub) * a.k + j);
-                    if (more >= a.E) bad = 1;
-                    else if (more >= 0) atomicAdd(&cs[more], 1);
+                    over |= more >= a.E;
+                    if (more >= 0 && more < a.E) atomicAdd(&cs[more], 1);
                 }
-            }
         }
         float f[kUnroll], lse[kUnroll];
         softmax_rows<kLanes>(x, f, lse);
@@ -310,12 +362,13 @@ __global__ void __launch_bounds__(kThreads) balance_stats_kernel(const BalanceAr
             const float w = in[u] ? f[u] : 0.f;
 #pragma unroll
             for (int v = 0; v < kVals; ++v) p[v] = fmaf(x[u][v], w, p[v]);
-            if (in[u] && t == 0) {
-                z = fmaf(lse[u], lse[u], z);
-                ++tokens;
-            }
+            z = in[u] ? fmaf(lse[u], lse[u], z) : z;  // each lane of the row alike
+            tokens += in[u];
         }
     }
+    if (over) bad = 1;
+    z = t == 0 ? z : 0.f;
+    tokens = t == 0 ? tokens : 0;
     // rows of the warp, then the warps of the block, in order
 #pragma unroll
     for (int d = kLanes; d < 32; d <<= 1) {
@@ -469,13 +522,16 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(const Balanc
 }
 
 template <bool kBf16, int kLanes, bool kVec>
-__global__ void __launch_bounds__(kThreads) balance_grad_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) balance_grad_kernel(const BalanceArgs a) {
     constexpr int kPerWarp = 32 / kLanes;
     constexpr int kRows = kRowsPerWarp<kLanes>;
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x % 32;
     const int t = lane % kLanes, sub = lane / kLanes;
+    int64_t base = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / 32 * kRows;
+    RawRow<kBf16, kVec> raw[kUnroll];
+    load_rows<kBf16, kLanes, kVec>(a, base, t, sub, raw);
     const int T = __ldcg(a.tokens);
     const float invT = T > 0 ? 1.f / static_cast<float>(T) : 0.f;
     // g0 E d_e / T with E d_e = (E c_e - k T) / (k T): the difference in whole
@@ -492,20 +548,19 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(const BalanceArg
                        : 0.f;
     }
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32) * kRows;
-    for (int64_t base = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / 32 * kRows;
-         base < a.N; base += step) {
+    for (; base < a.N; base += step) {
         const int left = a.N - base < kRows ? static_cast<int>(a.N - base) : kRows;
-        const void *rows = at_element<kBf16>(a.logits, base * a.E);
         void *out = at_element<kBf16>(a.dlogits, base * a.E);
         float x[kUnroll][kVals];
         bool in[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int r = u * kPerWarp + sub;
-            in[u] = r < left;
-            if (in[u])  // rows of its own only: out may be the logits
-                load_row<kBf16, kLanes, kVec>(at_element<kBf16>(rows, r * a.E), a.E, t, x[u]);
+            in[u] = u * kPerWarp + sub < left;
+            unpack_row<kBf16, kLanes, kVec>(raw[u], a.E, t, x[u]);
         }
+        // out may be the logits: rows of other warps are never read, and this
+        // warp's next rows are not the ones stored below
+        load_rows<kBf16, kLanes, kVec>(a, base + step, t, sub, raw);
         if (a.mask) {
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u)
@@ -579,7 +634,9 @@ int rows_per_block(int E) {
 int balance_clusters(int64_t N, int E) {
     const int64_t rows = static_cast<int64_t>(kBalanceCluster) * rows_per_block(E);
     const int64_t c = (N + rows - 1) / rows;
-    return c < 1 ? 1 : static_cast<int>(c < kBalanceMaxClusters ? c : kBalanceMaxClusters);
+    // two passes of one cluster take what one pass and the second kernel take
+    // (2048 x 60: 6.4 us), without its launch
+    return c <= 2 ? 1 : static_cast<int>(c < kBalanceMaxClusters ? c : kBalanceMaxClusters);
 }
 
 cudaError_t launch_balance(const BalanceArgs &a, int *launches, cudaStream_t s) {
@@ -591,7 +648,7 @@ cudaError_t launch_balance(const BalanceArgs &a, int *launches, cudaStream_t s) 
 
 cudaError_t launch_balance_backward(const BalanceArgs &a, int num_sms, cudaStream_t s) {
     int64_t blocks = (a.N + rows_per_block(a.E) - 1) / rows_per_block(a.E);
-    if (blocks > num_sms * 4) blocks = num_sms * 4;
+    if (blocks > num_sms * 2) blocks = num_sms * 2;
     return launch<true>(a, static_cast<int>(blocks), s);
 }
 

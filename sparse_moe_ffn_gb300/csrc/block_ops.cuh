@@ -46,7 +46,10 @@ struct LinearArgs {
 // ------------------------------------------------------------ balance loss
 
 constexpr int kBalanceCluster = 8;       // blocks that join their sums on chip
-constexpr int kBalanceMaxClusters = 38;  // two blocks an SM
+// As many clusters as fit at two blocks an SM: a cluster stays within one group
+// of SMs, and 38 of them (304 blocks) took a second wave (131072 x 128: 25.8 us
+// forward, 20.3 with 32).
+constexpr int kBalanceMaxClusters = 32;
 
 struct BalancePart {
     float z;      // sum of lse^2 over the cluster's tokens
