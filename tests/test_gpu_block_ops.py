@@ -109,8 +109,16 @@ def test_add_rmsnorm_fp8(N, H, form):
         assert_within(nm.t, y, (2.0 ** -8 + 2 * ROW_REL) * y.abs() + 1e-38, "normed")
 
 
+@pytest.mark.parametrize("N,H", [(7001, 256), (4001, 512), (3001, 1000), (1501, 2040), (33, 16384),
+                                 (17, 20000), (9, 40000)])
+def test_add_rmsnorm_fp8_larger(N, H):
+    """Batches and rows that take the other threads-per-row variants."""
+    test_add_rmsnorm_fp8(N, H, "full")
+
+
 @pytest.mark.parametrize("N,H", [(1, 8), (1, 2048), (5, 72), (1000, 264), (333, 4104),
-                                 (2, 65536), (40000, 64)])
+                                 (2, 65536), (40000, 64), (7001, 512), (2001, 1000),
+                                 (1501, 2040), (33, 16384), (17, 20000), (9, 40000)])
 def test_quantize_fp8(N, H):
     g = gen(H + N)
     x = (normal(g, N, H) * torch.exp(normal(g, N, 1, std=4.0))).to(BF16)
