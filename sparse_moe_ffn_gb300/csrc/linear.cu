@@ -9,6 +9,8 @@
 // outputs against the best split: 256 tokens 15.2 against 9.0 us, 1024 tokens
 // 16.2 against 20.1; pair tiles of 256 against 128 outputs: 1024 tokens 18.5
 // against 16.2, 4096 tokens 31.1 against 46.7.
+#include <cmath>
+
 #include "linear_gemm.cuh"
 
 namespace moe {
@@ -17,44 +19,51 @@ namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The persistent pairs: whole waves of tiles, each the K slices' time or, when
-// K is short, the epilogue's, and the last tile's epilogue on its own.
-float pair_us(int64_t N, int64_t O, int nk, int bn, bool aligned, int sms) {
-    const int64_t waves = ceil_div(ceil_div(N, 256) * ceil_div(O, bn), sms / 2);
-    const float slices = nk * (bn == 256 ? 0.437f : 0.326f);
-    const float epilogue = 3.1f * bn / 256 * (aligned ? 1.f : 8.1f);
-    return 3.5f + waves * (slices > epilogue ? slices : epilogue) + 0.9f * epilogue;
+// Whole waves of `tiles` on `at_once`, in float: the rule is on the path of
+// every call, and 64-bit divisions were a third of a microsecond of it.
+float waves_of(int64_t tiles, float at_once) {
+    return ceilf(static_cast<float>(tiles) / at_once - 1e-6f);
 }
 
-// Clusters of `split` CTAs of one SM each: clusters of 4 fit 36 times on the
-// 152 SMs and clusters of 8 15 times.
-float split_us(int64_t N, int64_t O, int nk, int bn, int split, bool aligned, int sms) {
-    const int fit = split <= 2 ? sms : split == 4 ? sms * 36 / 38 : sms * 15 / 19;
-    const int64_t waves = ceil_div(ceil_div(N, bn) * ceil_div(O, 128) * split, fit);
-    const float slice = bn == 128 ? 0.35f : bn == 64 ? 0.267f : bn == 32 ? 0.285f : 0.303f;
-    const float epilogue = 0.0247f * bn / split * (aligned ? 1.f : 6.4f) + 0.0115f * bn;
-    return 1.4f + waves * (1.7f + ceil_div(nk, split) * slice + epilogue);
+// The persistent pairs: whole waves of tiles, each the K slices' time or, when
+// K is short, the epilogue's, and the last tile's epilogue on its own.
+float pair_us(int64_t tiles, int nk, int bn, bool aligned, int sms) {
+    const float slices = nk * (bn == 256 ? 0.437f : 0.326f);
+    const float epilogue = 3.1f * bn / 256 * (aligned ? 1.f : 8.1f);
+    return 3.5f + waves_of(tiles, static_cast<float>(sms / 2)) *
+                      (slices > epilogue ? slices : epilogue) + 0.9f * epilogue;
 }
 
 }  // namespace
 
 LinearTiling linear_tiling(const LinearArgs &a, int num_sms) {
     const int nk = static_cast<int>(ceil_div(a.K, a.fp8 ? 128 : 64));
-    const bool vectors = a.O % 4 == 0;  // of the split kernel's stores
+    const int64_t m256 = (a.N + 255) >> 8, o128 = (a.O + 127) >> 7;
     const bool rows = linear_out_rows_aligned(a);
     LinearTiling best = {1, 256, 1};
-    float least = pair_us(a.N, a.O, nk, 256, rows, num_sms);
+    float least = pair_us(m256 * ((o128 + 1) >> 1), nk, 256, rows, num_sms);
     const auto consider = [&](float us, LinearTiling t) {
         if (us < least) {
             least = us;
             best = t;
         }
     };
-    consider(pair_us(a.N, a.O, nk, 128, rows, num_sms), {1, 128, 1});
-    for (int bn = 16; bn <= 128; bn *= 2) {
-        if (ceil_div(a.N, bn) > 4096) continue;  // rows of its grid
-        for (int split = 1; split <= 8 && split <= nk; split *= 2)
-            consider(split_us(a.N, a.O, nk, bn, split, vectors, num_sms), {0, bn, split});
+    consider(pair_us(m256 * o128, nk, 128, rows, num_sms), {1, 128, 1});
+    // Clusters of `split` CTAs of one SM each: clusters of 4 fit 36 times on
+    // the 152 SMs and clusters of 8 15 times.
+    const float fit[4] = {1.f, 1.f, 36.f / 38.f, 15.f / 19.f};
+    const float slice[4] = {0.303f, 0.285f, 0.267f, 0.35f};
+    const float store = a.O % 4 == 0 ? 0.0247f : 0.158f;  // vectors or single values
+    for (int b = 0; b < 4; ++b) {
+        const int bn = 16 << b;
+        const int64_t tiles = ((a.N + bn - 1) >> (4 + b)) * o128;
+        if (a.N > static_cast<int64_t>(bn) * 4096) continue;  // rows of its grid
+        for (int l = 0; l < 4 && (1 << l) <= nk; ++l) {
+            const float w = waves_of(tiles << l, num_sms * fit[l]);
+            const int slices = (nk + (1 << l) - 1) >> l;
+            consider(1.4f + w * (1.7f + slices * slice[b] + store * bn / (1 << l) + 0.0115f * bn),
+                     {0, bn, 1 << l});
+        }
     }
     return best;
 }

@@ -9,6 +9,8 @@
 #include <cuda.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "block_ops.cuh"
 #include "ptx.cuh"
 
@@ -129,6 +131,21 @@ __device__ __forceinline__ void commit_2cta(uint64_t *bar, uint16_t mask) {
 }
 
 // ---------------------------------------------------------------- launchers
+
+// Lets `kern` have `bytes` of dynamic shared memory, once a device (`done`: one
+// bit each; the call costs 0.2 us).
+template <typename Kernel>
+cudaError_t allow_shared(Kernel kern, size_t bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(bytes));
+    if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return err;
+}
 
 // tm_x / tm_w: boxes of rows x 128 bytes over the operands (rows: see
 // linear_tiling); see the kernels for how they split a tile.

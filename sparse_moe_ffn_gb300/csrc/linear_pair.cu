@@ -437,8 +437,8 @@ cudaError_t launch_one(const CUtensorMap &tm_x, const CUtensorMap &tm_w,
     const size_t smem = 1024 + static_cast<size_t>(kStages) * PairTile<kBN>::kStageBytes +
                         kEpiWarps * kOutBytes + sizeof(PairShared);
     auto kern = linear_pair_kernel<kFp8, kBN>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(smem));
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_shared(kern, smem, allowed);
     if (err != cudaSuccess) return err;
     const int64_t tiles = (a.N + kTokens - 1) / kTokens * ((a.O + kBN - 1) / kBN);
     const int64_t pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;

@@ -317,8 +317,8 @@ cudaError_t launch_one(const CUtensorMap &tm_x, const CUtensorMap &tm_w, const L
     const size_t smem = 1024 + static_cast<size_t>(T::kStages) * T::kStageBytes +
                         sizeof(float) * T::kPartFloats + sizeof(SplitShared);
     auto kern = linear_split_kernel<kFp8, kBN>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(smem));
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_shared(kern, smem, allowed);
     if (err != cudaSuccess) return err;
     const dim3 grid(static_cast<unsigned>((a.O + kOut - 1) / kOut * split),
                     static_cast<unsigned>((a.N + kBN - 1) / kBN));
