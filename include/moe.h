@@ -517,10 +517,12 @@ moe_status_t moe_quantize_fp8(const moe_bf16_t *x, int64_t N, int H, moe_e4m3_t 
  *   workspace >= moe_linear_workspace_bytes() bytes, or NULL (then device
  *            failures are not recorded)
  * Precision: products and sums in fp32 on the tensor cores, the epilogue in
- * fp32, one rounding of out.  Every output element's value depends on its own
- * row and N alone selects the tiling: other N may differ in the last bit of
- * the fp32 sum.  Limits: K % 8 == 0 (bf16) or K % 16 == 0 (e4m3), any O >= 1;
- * x, weight 16-byte aligned; bias, residual and out aligned to their type.
+ * fp32, one rounding of out.  An output depends on its own token and weight
+ * row alone, and the same call gives the same bits; the sizes and the outputs'
+ * alignment choose the tiling, and with it the order of the fp32 sum.
+ * Limits: K % 8 == 0 (bf16) or K % 16 == 0 (e4m3), any O >= 1, each size
+ * <= 2^31 - 512; x, weight 16-byte aligned; scales, bias, residual and out
+ * aligned to their types.
  * ---------------------------------------------------------------------- */
 typedef enum {
     MOE_ACT_NONE = 0,
@@ -566,7 +568,7 @@ moe_status_t moe_linear_fp8(const moe_e4m3_t *x, const float *x_scale, const moe
  * A token whose logits are all -inf has p = 0 and lse = 0, gradient 0, and
  * counts in T.  Without tokens (T = 0, N = 0) the losses, counts and
  * gradients are 0.  The sums over tokens have a fixed order: the same inputs
- * give the same bits.  Limits: 1 <= E <= 256, k >= 1, N * k < 2^31.
+ * give the same bits.  Limits: 1 <= k <= E <= 256, N * k < 2^31.
  * ---------------------------------------------------------------------- */
 size_t moe_balance_loss_workspace_bytes(int64_t N, int E);
 moe_status_t moe_balance_loss(const void *logits, int logits_bf16, const int32_t *topk_ids,

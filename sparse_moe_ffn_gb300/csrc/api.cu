@@ -1353,8 +1353,11 @@ moe_status_t linear_impl(LinearArgs a, void *workspace, size_t workspace_bytes,
     if (a.O < 1) return fail(MOE_ERR_INVALID_ARG, "O must be >= 1 (got %d)", a.O);
     if (a.act < MOE_ACT_NONE || a.act > MOE_ACT_RELU)
         return fail(MOE_ERR_INVALID_ARG, "unknown activation %d", a.act);
-    if (a.N > INT32_MAX)
-        return fail(MOE_ERR_UNSUPPORTED, "N must be below 2^31 (got %lld)", (long long)a.N);
+    // tile coordinates and the ends of the last tiles are 32-bit
+    constexpr int64_t kMost = (int64_t(1) << 31) - 512;
+    if (a.N > kMost || a.K > kMost || a.O > kMost)
+        return fail(MOE_ERR_UNSUPPORTED, "N, K and O must be <= 2^31 - 512 (got %lld, %d, %d)",
+                    (long long)a.N, a.K, a.O);
     if (workspace && workspace_bytes < moe_linear_workspace_bytes())
         return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "linear workspace needs %zu bytes, got %zu",
                     moe_linear_workspace_bytes(), workspace_bytes);
@@ -1449,7 +1452,8 @@ BalanceLayout balance_layout(int64_t N, int E) {
 moe_status_t check_balance(int64_t N, int E, int k) {
     if (N < 0) return fail(MOE_ERR_INVALID_ARG, "N must be >= 0 (got %lld)", (long long)N);
     if (E < 1) return fail(MOE_ERR_INVALID_ARG, "E must be >= 1 (got %d)", E);
-    if (k < 1) return fail(MOE_ERR_INVALID_ARG, "k must be >= 1 (got %d)", k);
+    if (k < 1 || k > E)
+        return fail(MOE_ERR_INVALID_ARG, "k must be in [1, E] (k=%d, E=%d)", k, E);
     if (E > MOE_MAX_EXPERTS)
         return fail(MOE_ERR_UNSUPPORTED, "E must be <= %d (got %d)", MOE_MAX_EXPERTS, E);
     if (N >= ((int64_t(1) << 31) + k - 1) / k)

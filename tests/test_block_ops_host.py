@@ -67,6 +67,8 @@ def test_linear_argument_errors(L, fp8):
     assert call(act=5) == INVALID
     assert call(act=-1) == INVALID
     assert call(N=1 << 31) == UNSUPPORTED
+    assert call(O=(1 << 31) - 16) == UNSUPPORTED
+    assert call(K=(1 << 31) - 16) == UNSUPPORTED
     assert call(wsb=0) == SMALL
     assert call(ws=P + 2) == INVALID
     for name in ("x", "w", "out") + (("sx", "sw") if fp8 else ()):
@@ -94,6 +96,7 @@ def test_balance_argument_errors(L):
     assert fwd(N=-1) == INVALID
     assert fwd(E=0) == INVALID
     assert fwd(k=0) == INVALID
+    assert fwd(k=65) == INVALID
     assert fwd(E=257) == UNSUPPORTED
     assert fwd(N=1 << 28, k=8) == UNSUPPORTED
     for name in ("lg", "ids", "lo", "c", "t", "ws"):
