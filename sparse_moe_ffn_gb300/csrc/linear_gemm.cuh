@@ -62,6 +62,24 @@ __device__ __forceinline__ void linear_mma_pair(uint32_t d, uint64_t a, uint64_t
             : "memory");
 }
 
+// One lane of the warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
+}
+
+// mbar_wait by a whole warp, the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity,
+                                          volatile int *abort_flag) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+
 // ------------------------------------------------------------------ clusters
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {

@@ -234,73 +234,91 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int nk = (a.K + per_slice - 1) / per_slice;
 
     if (warp == 0) {
-        if (lane == 0) {
-            int g = 0;
-            bool failed = false;
-            for (int tile = first; tile < total && !failed; tile += step) {
-                int m, n;
-                tile_of(tile, m_tiles, n_tiles, &m, &n);
-                const int row = m * kTokens + static_cast<int>(rank) * 128;
-                const int wrow = n * kBN + static_cast<int>(rank) * (kBN / 2);
-                for (int kc = 0; kc < nk; ++kc, ++g) {
-                    const int s = g % kStages;
-                    const uint32_t use = g / kStages;
-                    if (use > 0 && !mbar_wait(&sm->empty[s], (use - 1) & 1, abort_flag)) {
+        const bool issues = elect_one();
+        // stages filled so far; the stage and the parity of its last release
+        int64_t g = 0;
+        int s = 0;
+        uint32_t parity = 1;
+        bool failed = false;
+        for (int tile = first; tile < total && !failed; tile += step) {
+            int m, n;
+            tile_of(tile, m_tiles, n_tiles, &m, &n);
+            const int row = m * kTokens + static_cast<int>(rank) * 128;
+            const int wrow = n * kBN + static_cast<int>(rank) * (kBN / 2);
+            for (int kc = 0; kc < nk; ++kc, ++g) {
+                if (g >= kStages && !warp_wait(&sm->empty[s], parity, abort_flag)) {
+                    if (issues) {
                         record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
                         *abort_flag = 1;
-                        failed = true;
-                        break;
                     }
+                    failed = true;
+                    break;
+                }
+                if (issues) {
                     uint8_t *st = tiles + s * T::kStageBytes;
                     const uint32_t bar = map_to_rank(smem_addr(&sm->full[s]), 0);
                     if (leader) mbar_arrive_expect_tx(&sm->full[s], 2 * T::kStageBytes);
                     tma_load_2d_pair(st, &tm_x, bar, kc * per_slice, row);
                     tma_load_2d_pair(st + kRowsBytes128, &tm_w, bar, kc * per_slice, wrow);
                 }
+                if (++s == kStages) {
+                    s = 0;
+                    parity ^= 1;
+                }
             }
-            // no copy may be in flight when the pair ends
-            if (leader)
-                for (int i = (g > kStages ? g - kStages : 0); i < g; ++i)
-                    mbar_wait(&sm->full[i % kStages], (i / kStages) & 1, abort_flag);
         }
+        // no copy may be in flight when the pair ends
+        if (leader && issues)
+            for (int64_t i = (g > kStages ? g - kStages : 0); i < g; ++i)
+                mbar_wait(&sm->full[i % kStages], (i / kStages) & 1, abort_flag);
         __syncwarp();
     } else if (warp == 1) {
-        if (leader && lane == 0) {
+        if (leader) {
+            // The whole warp runs the loop and one lane of it issues, so that
+            // the compiler keeps descriptors and barriers in uniform registers.
+            const bool issues = elect_one();
             constexpr uint32_t idesc = linear_idesc<kFp8>(kTokens, kBN);
-            int g = 0, it = 0;
+            const uint64_t desc0 = sw128_kmajor_desc(smem_addr(tiles));
+            int s = 0, it = 0;
+            uint32_t phase = 0;
             bool failed = false;
             for (int tile = first; tile < total && !failed; tile += step, ++it) {
                 const int acc = it & 1;
                 const uint32_t use = it >> 1;
-                if (use > 0 && !mbar_wait(&sm->acc_empty[acc], (use - 1) & 1, abort_flag)) {
+                if (use > 0 && !warp_wait(&sm->acc_empty[acc], (use - 1) & 1, abort_flag)) {
                     failed = true;
                     break;
                 }
                 tc_fence_after_sync();
                 const uint32_t d = tmem + acc * kBN;
-                for (int kc = 0; kc < nk; ++kc, ++g) {
-                    const int s = g % kStages;
-                    if (!mbar_wait(&sm->full[s], (g / kStages) & 1, abort_flag)) {
+                for (int kc = 0; kc < nk; ++kc) {
+                    if (!warp_wait(&sm->full[s], phase, abort_flag)) {
                         failed = true;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint8_t *st = tiles + s * T::kStageBytes;
-                    const uint64_t da = sw128_kmajor_desc(smem_addr(st));
-                    const uint64_t db = sw128_kmajor_desc(smem_addr(st + kRowsBytes128));
+                    const uint64_t da = desc0 + s * (T::kStageBytes >> 4);
+                    const uint64_t db = da + (kRowsBytes128 >> 4);
+                    if (issues) {
 #pragma unroll
-                    for (int kk = 0; kk < kSliceBytes / kMmaBytes; ++kk)
-                        linear_mma_pair<kFp8>(d, da + 2 * kk, db + 2 * kk, idesc, (kc | kk) != 0);
-                    commit_2cta(&sm->empty[s], 3);
+                        for (int kk = 0; kk < kSliceBytes / kMmaBytes; ++kk)
+                            linear_mma_pair<kFp8>(d, da + 2 * kk, db + 2 * kk, idesc,
+                                                  kk == 0 ? kc != 0 : 1);
+                        commit_2cta(&sm->empty[s], 3);
+                    }
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
-                if (!failed) commit_2cta(&sm->acc_full[acc], 3);
+                if (!failed && issues) commit_2cta(&sm->acc_full[acc], 3);
             }
-            if (failed) {
+            if (failed && issues) {
                 record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
                 *abort_flag = 1;
             }
-            commit_2cta(&sm->drain, 1);
-            mbar_wait(&sm->drain, 0, abort_flag);
+            if (issues) commit_2cta(&sm->drain, 1);
+            warp_wait(&sm->drain, 0, abort_flag);
         }
         __syncwarp();
     } else {
