@@ -208,48 +208,57 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     const int slices = k_end - k_first;
 
     if (warp == 0) {
-        if (lane == 0) {
-            int g = 0;
-            for (; g < slices; ++g) {
-                const int s = g % kStages;
-                const uint32_t use = g / kStages;
-                if (use > 0 && !mbar_wait(&sm->empty[s], (use - 1) & 1, abort_flag)) {
+        const bool issues = elect_one();
+        int g = 0;
+        for (; g < slices; ++g) {
+            const int s = g % kStages;
+            const uint32_t use = g / kStages;
+            if (use > 0 && !warp_wait(&sm->empty[s], (use - 1) & 1, abort_flag)) {
+                if (issues) {
                     record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
                     *abort_flag = 1;
-                    break;
                 }
+                break;
+            }
+            if (issues) {
                 uint8_t *st = tiles + s * T::kStageBytes;
                 mbar_arrive_expect_tx(&sm->full[s], T::kStageBytes);
                 tma_load_2d(st, &tm_w, &sm->full[s], (k_first + g) * per_slice, o0);
                 tma_load_2d(st + kRowsBytes128, &tm_x, &sm->full[s], (k_first + g) * per_slice,
                             static_cast<int>(n0));
             }
-            // no copy may be in flight when the CTA ends
+        }
+        // no copy may be in flight when the CTA ends
+        if (issues)
             for (int i = (g > kStages ? g - kStages : 0); i < g; ++i)
                 mbar_wait(&sm->full[i % kStages], (i / kStages) & 1, abort_flag);
-        }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = linear_idesc<kFp8>(kOut, kBN);
-            for (int g = 0; g < slices; ++g) {
-                const int s = g % kStages;
-                if (!mbar_wait(&sm->full[s], (g / kStages) & 1, abort_flag)) {
+        // the whole warp runs the loop and one lane issues: descriptors and
+        // barriers stay in uniform registers
+        const bool issues = elect_one();
+        constexpr uint32_t idesc = linear_idesc<kFp8>(kOut, kBN);
+        const uint64_t desc0 = sw128_kmajor_desc(smem_addr(tiles));
+        for (int g = 0; g < slices; ++g) {
+            const int s = g % kStages;
+            if (!warp_wait(&sm->full[s], (g / kStages) & 1, abort_flag)) {
+                if (issues) {
                     record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
                     *abort_flag = 1;
-                    break;
                 }
-                tc_fence_after_sync();
-                const uint8_t *st = tiles + s * T::kStageBytes;
-                const uint64_t da = sw128_kmajor_desc(smem_addr(st));
-                const uint64_t db = sw128_kmajor_desc(smem_addr(st + kRowsBytes128));
+                break;
+            }
+            tc_fence_after_sync();
+            if (issues) {
+                const uint64_t da = desc0 + s * (T::kStageBytes >> 4);
+                const uint64_t db = da + (kRowsBytes128 >> 4);
 #pragma unroll
                 for (int kk = 0; kk < kSliceBytes / kMmaBytes; ++kk)
                     linear_mma<kFp8>(tmem, da + 2 * kk, db + 2 * kk, idesc, (g | kk) != 0);
                 mma_commit(&sm->empty[s]);
             }
-            mma_commit(&sm->acc_full);  // after a failure too: the MMAs issued so far
         }
+        if (issues) mma_commit(&sm->acc_full);  // after a failure too: the MMAs issued so far
         __syncwarp();
     }
 
