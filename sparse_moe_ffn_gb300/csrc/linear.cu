@@ -4,11 +4,11 @@
 // candidate and takes the least.  The constants (microseconds) were fitted to
 // measured times of every candidate on a GB300, for 19 batch sizes from 1 to
 // 16384 and 8 weight shapes from 2048 x 128 to 8192 x 2048 in both operand
-// types: the candidate it takes is on average 0.2% slower than the fastest one,
-// 7% at worst.  What the sides are at 2048 x 2048 in bf16, pair tiles of 128
-// outputs against the best split: 256 tokens 15.2 against 9.0 us, 1024 tokens
-// 16.2 against 20.1; pair tiles of 256 against 128 outputs: 1024 tokens 18.5
-// against 16.2, 4096 tokens 31.1 against 46.7.
+// types: the candidate it takes is on average 0.4% slower than the fastest one,
+// 10% at worst (on 7 other weight shapes 0.7%, 21% at worst).  What the sides are at 2048 x 2048 in bf16, pair tiles of 128
+// outputs against the best split: 256 tokens 10.3 against 8.2 us, 512 tokens
+// 11.3 against 11.1, 1024 tokens 12.9 against 18.5; pair tiles of 256 against
+// 128 outputs: 1024 tokens 17.5 against 12.9, 4096 tokens 27.7 against 32.9.
 #include <cmath>
 
 #include "linear_gemm.cuh"
@@ -28,9 +28,9 @@ float waves_of(int64_t tiles, float at_once) {
 // The persistent pairs: whole waves of tiles, each the K slices' time or, when
 // K is short, the epilogue's, and the last tile's epilogue on its own.
 float pair_us(int64_t tiles, int nk, int bn, bool aligned, int sms) {
-    const float slices = nk * (bn == 256 ? 0.437f : 0.326f);
-    const float epilogue = 3.1f * bn / 256 * (aligned ? 1.f : 8.1f);
-    return 3.5f + waves_of(tiles, static_cast<float>(sms / 2)) *
+    const float slices = nk * (bn == 256 ? 0.389f : 0.2305f);
+    const float epilogue = 2.6f * bn / 256 * (aligned ? 1.f : 9.8f);
+    return 3.9f + waves_of(tiles, static_cast<float>(sms / 2)) *
                       (slices > epilogue ? slices : epilogue) + 0.9f * epilogue;
 }
 
@@ -52,8 +52,8 @@ LinearTiling linear_tiling(const LinearArgs &a, int num_sms) {
     // Clusters of `split` CTAs of one SM each: clusters of 4 fit 36 times on
     // the 152 SMs and clusters of 8 15 times.
     const float fit[4] = {1.f, 1.f, 36.f / 38.f, 15.f / 19.f};
-    const float slice[4] = {0.303f, 0.285f, 0.267f, 0.35f};
-    const float store = a.O % 4 == 0 ? 0.0247f : 0.158f;  // vectors or single values
+    const float slice[4] = {0.216f, 0.216f, 0.283f, 0.35f};
+    const float store = a.O % 4 == 0 ? 0.0257f : 0.164f;  // vectors or single values
     for (int b = 0; b < 4; ++b) {
         const int bn = 16 << b;
         const int64_t tiles = ((a.N + bn - 1) >> (4 + b)) * o128;
@@ -61,7 +61,7 @@ LinearTiling linear_tiling(const LinearArgs &a, int num_sms) {
         for (int l = 0; l < 4 && (1 << l) <= nk; ++l) {
             const float w = waves_of(tiles << l, num_sms * fit[l]);
             const int slices = (nk + (1 << l) - 1) >> l;
-            consider(1.4f + w * (1.7f + slices * slice[b] + store * bn / (1 << l) + 0.0115f * bn),
+            consider(1.1f + w * (1.5f + slices * slice[b] + store * bn / (1 << l) + 0.0141f * bn),
                      {0, bn, 1 << l});
         }
     }
