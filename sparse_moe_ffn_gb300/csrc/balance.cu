@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kVals = 8;
 constexpr int kThreads = 256;
+constexpr int kAloneThreads = 512;  // of a block when one cluster does it all
 constexpr float kNegInf = -__builtin_huge_valf();
 
 // Value v of lane t of a row is expert 4 (t + kLanes (v / 4)) + v % 4 when
@@ -282,10 +283,10 @@ __device__ __forceinline__ void write_losses(const BalanceArgs &a, float pc, con
     if (a.status) *a.status = t.bad ? MOE_ERR_DEVICE_CHECK : MOE_OK;
 }
 
-template <bool kBf16, int kLanes, bool kVec>
-__global__ void __launch_bounds__(kThreads, 2) balance_stats_kernel(const BalanceArgs a) {
+template <bool kBf16, int kLanes, bool kVec, int kBlock>
+__global__ void __launch_bounds__(kBlock, 512 / kBlock) balance_stats_kernel(const BalanceArgs a) {
     constexpr int kPerWarp = 32 / kLanes;
-    constexpr int kWarps = kThreads / 32;
+    constexpr int kWarps = kBlock / 32;
     constexpr int kRows = kRowsPerWarp<kLanes>;
     __shared__ float ps[kWarps][MOE_MAX_EXPERTS];
     __shared__ float p_block[MOE_MAX_EXPERTS];
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 2) balance_stats_kernel(const Balanc
     griddep_wait();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int t = lane % kLanes, sub = lane / kLanes;
-    for (int e = threadIdx.x; e < MOE_MAX_EXPERTS; e += kThreads) cs[e] = 0;
+    for (int e = threadIdx.x; e < MOE_MAX_EXPERTS; e += kBlock) cs[e] = 0;
     if (threadIdx.x == 0) bad = 0;
     __syncthreads();
 
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 2) balance_stats_kernel(const Balanc
         ts[warp] = tokens;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    for (int e = threadIdx.x; e < a.E; e += kBlock) {
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) s += ps[w][e];
@@ -590,66 +591,78 @@ __global__ void __launch_bounds__(kThreads, 2) balance_grad_kernel(const Balance
 
 using BalanceKernel = void (*)(BalanceArgs);
 
-template <bool kGrad, bool kBf16, bool kVec>
+enum Pass { kStats, kStatsAlone, kGrad };
+
+template <Pass kPass, bool kBf16, bool kVec, int kLanes>
+BalanceKernel kernel_at() {
+    if constexpr (kPass == kGrad) return balance_grad_kernel<kBf16, kLanes, kVec>;
+    else if constexpr (kPass == kStats) return balance_stats_kernel<kBf16, kLanes, kVec, kThreads>;
+    else return balance_stats_kernel<kBf16, kLanes, kVec, kAloneThreads>;
+}
+
+template <Pass kPass, bool kBf16, bool kVec>
 BalanceKernel kernel_of(int lanes) {
-#define MOE_BALANCE_KERNEL(L)                                                \
-    (kGrad ? static_cast<void (*)(const BalanceArgs)>(balance_grad_kernel<kBf16, L, kVec>) \
-           : static_cast<void (*)(const BalanceArgs)>(balance_stats_kernel<kBf16, L, kVec>))
     switch (lanes) {
-        case 1: return MOE_BALANCE_KERNEL(1);
-        case 2: return MOE_BALANCE_KERNEL(2);
-        case 4: return MOE_BALANCE_KERNEL(4);
-        case 8: return MOE_BALANCE_KERNEL(8);
-        case 16: return MOE_BALANCE_KERNEL(16);
-        default: return MOE_BALANCE_KERNEL(32);
+        case 1: return kernel_at<kPass, kBf16, kVec, 1>();
+        case 2: return kernel_at<kPass, kBf16, kVec, 2>();
+        case 4: return kernel_at<kPass, kBf16, kVec, 4>();
+        case 8: return kernel_at<kPass, kBf16, kVec, 8>();
+        case 16: return kernel_at<kPass, kBf16, kVec, 16>();
+        default: return kernel_at<kPass, kBf16, kVec, 32>();
     }
-#undef MOE_BALANCE_KERNEL
+}
+
+int lanes_of(int E) {
+    int lanes = 1;
+    while (lanes * kVals < E) lanes *= 2;
+    return lanes;
 }
 
 // Rows are read four values at a time when every row starts on such a
 // boundary (E a multiple of 4, the arrays aligned), else one at a time.
-template <bool kGrad>
+template <Pass kPass>
 cudaError_t launch(const BalanceArgs &a, int blocks, cudaStream_t s) {
-    int lanes = 1;
-    while (lanes * kVals < a.E) lanes *= 2;
+    const int lanes = lanes_of(a.E);
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.logits) |
-                         (kGrad ? reinterpret_cast<uintptr_t>(a.dlogits) : 0);
+                         (kPass == kGrad ? reinterpret_cast<uintptr_t>(a.dlogits) : 0);
     const bool vec = a.E % 4 == 0 && at % (a.bf16 ? 8 : 16) == 0;
     const BalanceKernel k =
-        a.bf16 ? (vec ? kernel_of<kGrad, true, true>(lanes) : kernel_of<kGrad, true, false>(lanes))
-               : (vec ? kernel_of<kGrad, false, true>(lanes)
-                      : kernel_of<kGrad, false, false>(lanes));
-    return launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s,
-                      kGrad ? 1 : kBalanceCluster, a);
+        a.bf16 ? (vec ? kernel_of<kPass, true, true>(lanes) : kernel_of<kPass, true, false>(lanes))
+               : (vec ? kernel_of<kPass, false, true>(lanes)
+                      : kernel_of<kPass, false, false>(lanes));
+    return launch_pdl(k, dim3(static_cast<unsigned>(blocks)),
+                      dim3(kPass == kStatsAlone ? kAloneThreads : kThreads), 0, s,
+                      kPass == kGrad ? 1 : kBalanceCluster, a);
 }
 
-int rows_per_block(int E) {
-    int lanes = 1;
-    while (lanes * kVals < E) lanes *= 2;
-    return kThreads / lanes * kUnroll;
-}
+int64_t rows_per_block(int E, int threads) { return threads / lanes_of(E) * kUnroll; }
 
 }  // namespace
 
+// One cluster of twice the threads does up to three passes on its own: two take
+// less than the second kernel (1024 x 128: 5.4 against 5.8 us), the third 1 us
+// more (4099 x 60: 7.2 against 6.2), and the host saves a launch and the
+// workspace (9 us of 24 for a forward and backward call).
 int balance_clusters(int64_t N, int E) {
-    const int64_t rows = static_cast<int64_t>(kBalanceCluster) * rows_per_block(E);
+    if (N <= 3 * kBalanceCluster * rows_per_block(E, kAloneThreads)) return 1;
+    const int64_t rows = kBalanceCluster * rows_per_block(E, kThreads);
     const int64_t c = (N + rows - 1) / rows;
-    // two passes of one cluster take what one pass and the second kernel take
-    // (2048 x 60: 6.4 us), without its launch
-    return c <= 2 ? 1 : static_cast<int>(c < kBalanceMaxClusters ? c : kBalanceMaxClusters);
+    return static_cast<int>(c < kBalanceMaxClusters ? c : kBalanceMaxClusters);
 }
 
 cudaError_t launch_balance(const BalanceArgs &a, int *launches, cudaStream_t s) {
     *launches = a.clusters > 1 ? 2 : 1;
-    cudaError_t e = launch<false>(a, a.clusters * kBalanceCluster, s);
-    if (e != cudaSuccess || a.clusters == 1) return e;
+    if (a.clusters == 1) return launch<kStatsAlone>(a, kBalanceCluster, s);
+    cudaError_t e = launch<kStats>(a, a.clusters * kBalanceCluster, s);
+    if (e != cudaSuccess) return e;
     return launch_pdl(balance_join_kernel, dim3(1), dim3(kJoinThreads), 0, s, 1, a);
 }
 
 cudaError_t launch_balance_backward(const BalanceArgs &a, int num_sms, cudaStream_t s) {
-    int64_t blocks = (a.N + rows_per_block(a.E) - 1) / rows_per_block(a.E);
+    const int64_t rows = rows_per_block(a.E, kThreads);
+    int64_t blocks = (a.N + rows - 1) / rows;
     if (blocks > num_sms * 2) blocks = num_sms * 2;
-    return launch<true>(a, static_cast<int>(blocks), s);
+    return launch<kGrad>(a, static_cast<int>(blocks), s);
 }
 
 }  // namespace moe
