@@ -21,9 +21,8 @@
 // start on 16 bytes, a warp's 32 x 32 outputs go through shared memory into a
 // tensor-map store (stored from the lanes, 32 bytes of 32 rows each, an e4m3
 // call of 8192 x 2048 x 8192 took 112 us, 24 of them for the stores);
-// otherwise (an odd number of outputs, an output that starts anywhere) 16
-// columns at a time are turned there and leave with neighbouring lanes on
-// neighbouring outputs.
+// otherwise (an odd number of outputs, an output that starts anywhere) they are
+// turned there and leave with neighbouring lanes on neighbouring outputs.
 // Every wait is bounded; a CTA that gives up records MOE_ERR_DEVICE_TIMEOUT.
 #include "linear_epilogue.cuh"
 #include "linear_gemm.cuh"
@@ -36,7 +35,6 @@ constexpr int kEpiWarps = 8;
 constexpr int kPairThreads = 64 + 32 * kEpiWarps;
 constexpr int kStages = 5;
 constexpr int kTokens = 256;  // of a tile
-constexpr int kStagePad = 17; // floats of a staged row of 16 columns
 
 template <int kBN>
 struct PairTile {
@@ -59,7 +57,7 @@ struct PairShared {
 
 // Outputs on their way out: 32 tokens x 32 outputs a warp, twice in bf16.
 constexpr int kOutBytes = 4096;
-static_assert(32 * kStagePad * 4 <= kOutBytes, "a staged half chunk fits");
+static_assert(32 * 32 * 4 <= kOutBytes, "a turned chunk fits");
 
 // Tiles run through bands of kBand token tiles, output tile by output tile:
 // the ~76 tiles in flight cover 8 token tiles and ~10 output tiles.
@@ -158,30 +156,47 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void 
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// The same outputs, any alignment and any part of them inside [0, O): 16
-// columns at a time, then a half warp a row.
-__device__ __forceinline__ void store_staged(const LinearArgs &a, float *stage, int64_t n0, int o0,
-                                             int lane, const float (&v)[32]) {
+// The same outputs, any alignment and any part of them inside [0, O): turned in
+// the buffer (columns swapped by row, so that neither side's words share a
+// bank), then a lane an output, eight tokens at a time with the next eight's
+// residuals on their way.
+constexpr int kTurn = 8;
+
+__device__ __forceinline__ void load_turned(const LinearArgs &a, int64_t at, int left,
+                                            uint16_t (&u)[kTurn]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int r = 0; r < kTurn; ++r)
+        u[r] = r < left ? __ldcg(a.residual + at + static_cast<int64_t>(r) * a.O) : 0;
+}
+
+// `at`: the lane's output of the first token; `rows`: tokens that exist (0 for
+// a lane whose output does not).
+__device__ __forceinline__ void store_turned(const LinearArgs &a, float *buf, int64_t at, int rows,
+                                             int lane, const float (&v)[32],
+                                             uint16_t (&next)[kTurn]) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) stage[lane * kStagePad + i] = v[16 * h + i];
-        __syncwarp();
-        const int o = o0 + 16 * h + lane % 16;
-#pragma unroll 4
-        for (int r = lane / 16; r < 32; r += 2) {
-            const int64_t n = n0 + r;
-            if (n < a.N && o < a.O) {
-                const int64_t at = n * a.O + o;
-                float x = stage[r * kStagePad + lane % 16];
-                if (a.residual)
-                    x += __uint_as_float(static_cast<uint32_t>(__ldcg(a.residual + at)) << 16);
-                if (a.out_fp32) static_cast<float *>(a.out)[at] = x;
-                else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(x);
-            }
+    for (int i = 0; i < 32; ++i) buf[lane * 32 + (i ^ lane)] = v[i];
+    __syncwarp();
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += kTurn, at += static_cast<int64_t>(kTurn) * a.O) {
+        float x[kTurn];
+#pragma unroll
+        for (int r = 0; r < kTurn; ++r) x[r] = buf[(r0 + r) * 32 + (lane ^ (r0 + r))];
+        if (a.residual) {
+#pragma unroll
+            for (int r = 0; r < kTurn; ++r)
+                x[r] += __uint_as_float(static_cast<uint32_t>(next[r]) << 16);
+            load_turned(a, at + static_cast<int64_t>(kTurn) * a.O, rows - r0 - kTurn, next);
         }
-        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < kTurn; ++r) {
+            if (r0 + r >= rows) break;
+            const int64_t i = at + static_cast<int64_t>(r) * a.O;
+            if (a.out_fp32) static_cast<float *>(a.out)[i] = x[r];
+            else static_cast<__nv_bfloat16 *>(a.out)[i] = __float2bfloat16_rn(x[r]);
+        }
     }
+    __syncwarp();
 }
 
 template <bool kFp8, int kBN>
@@ -367,6 +382,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             fetch_factors(tile + step);
             // columns of this warp that exist (warp-uniform)
             const int cols = n0 < a.N ? min(kCols, a.O - o0) : 0;
+            const int rows = a.N - n0 < 32 ? static_cast<int>(a.N - n0) : 32;
             // the residual is read 32 columns ahead of their use
             Residual32 res;
             auto fetch = [&](int c) {
@@ -391,6 +407,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < cols; c += 32, ++chunk) {
                 float v[32];
+                // (unaligned rows) this lane's output of the chunk
+                const int64_t at = n0 * a.O + o0 + c + lane;
+                const int mine = o0 + c + lane < a.O ? rows : 0;
+                uint16_t turned[kTurn];
+                if (!vec && a.residual) load_turned(a, at, mine, turned);
                 tmem_load32(taddr + c, v);
                 tmem_load_wait();
 #pragma unroll
@@ -428,7 +449,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     __syncwarp();
                     if (lane == 0) tma_store_2d(&tm_out, b, o0 + c, static_cast<int>(n0));
                 } else {
-                    store_staged(a, reinterpret_cast<float *>(buf), n0, o0 + c, lane, v);
+                    store_turned(a, reinterpret_cast<float *>(buf), at, mine, lane, v, turned);
                 }
             }
             tc_fence_before_sync();

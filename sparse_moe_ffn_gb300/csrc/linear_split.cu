@@ -70,16 +70,36 @@ struct ResidualOf<1> {
     }
 };
 
+template <int kBatch, int kVec>
+__device__ __forceinline__ void act_batch(int act, float (&v)[kBatch][kVec]) {
+    switch (act) {
+#define MOE_ACT_CASE(A)                                             \
+    case A:                                                         \
+        _Pragma("unroll") for (int b = 0; b < kBatch; ++b)          \
+            _Pragma("unroll") for (int i = 0; i < kVec; ++i)        \
+                v[b][i] = linear_act<A>(v[b][i]);                   \
+        break;
+        MOE_ACT_CASE(MOE_ACT_SILU)
+        MOE_ACT_CASE(MOE_ACT_GELU)
+        MOE_ACT_CASE(MOE_ACT_GELU_TANH)
+        MOE_ACT_CASE(MOE_ACT_RELU)
+#undef MOE_ACT_CASE
+        default: break;
+    }
+}
+
 // Adds the ranks' parts of this CTA's `mine` tokens and stores them, kVec
 // outputs a thread; a thread keeps its outputs from token to token.  The
 // epilogue's operands are fetched before `ready` waits for the parts.
-template <bool kFp8, int kVec, typename Ready>
+template <bool kFp8, int kVec, int kBN, typename Ready>
 __device__ __forceinline__ void store_parts(const LinearArgs &a, const float *part, int o0,
                                             int64_t first, int mine, int split, int own_log,
                                             volatile int *abort_flag, const Ready &ready) {
     constexpr int kLanes = kOut / kVec;               // threads a token
     constexpr int kStep = kSplitThreads / kLanes;     // tokens in one go
-    constexpr int kBatch = 4;                         // of them fetched ahead
+    // goes side by side: what a tile can have, as far as registers pay
+    constexpr int kMost = kVec == 4 ? 4 : 8;
+    constexpr int kBatch = kBN / kStep < kMost ? kBN / kStep : kMost;
     const int ch = threadIdx.x % kLanes * kVec;
     const int o = o0 + ch;
     const bool live = o < a.O;
@@ -91,8 +111,8 @@ __device__ __forceinline__ void store_parts(const LinearArgs &a, const float *pa
                       ? __uint_as_float(static_cast<uint32_t>(__ldcg(a.bias + o + i)) << 16)
                       : 0.f;
     }
-    ResidualOf<kVec> res[kBatch];
-    float xs[kBatch];
+    ResidualOf<kVec> res[kBatch] = {};
+    float xs[kBatch] = {};
     const int t0 = threadIdx.x / kLanes;
     auto fetch = [&](int t) {
 #pragma unroll
@@ -109,46 +129,56 @@ __device__ __forceinline__ void store_parts(const LinearArgs &a, const float *pa
     if (!live || *abort_flag) return;
     for (int t = t0; t < mine; t += kBatch * kStep) {
         if (t != t0) fetch(t);
+        // the batch's tokens side by side: sums, epilogue, stores
+        float v[kBatch][kVec];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int tt = t + b * kStep;
-            if (tt >= mine) break;
-            float v[kVec];
+        for (int b = 0; b < kBatch; ++b)
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) v[i] = 0.f;
-            for (int r = 0; r < split; ++r) {
-                const float *p = part + (((r << own_log) + tt) * kOut + ch);
-                if (kVec == 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(p);
-                    v[0] += f.x;
-                    v[1 % kVec] += f.y;
-                    v[2 % kVec] += f.z;
-                    v[3 % kVec] += f.w;
+            for (int i = 0; i < kVec; ++i) v[b][i] = 0.f;
+        for (int r = 0; r < split; ++r) {
+            const float *p = part + ((r << own_log) + t) * kOut + ch;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (t + b * kStep >= mine) continue;
+                if constexpr (kVec == 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(p + b * kStep * kOut);
+                    v[b][0] += f.x;
+                    v[b][1] += f.y;
+                    v[b][2] += f.z;
+                    v[b][3] += f.w;
                 } else {
-                    v[0] += *p;
+                    v[b][0] += p[b * kStep * kOut];
                 }
             }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
 #pragma unroll
             for (int i = 0; i < kVec; ++i)
-                v[i] = linear_act(a.act, kFp8 ? fmaf(v[i], xs[b] * ws[i], bias[i])
-                                              : v[i] + bias[i]);
-            if (a.residual) res[b].add(v);
-            const int64_t at = (first + tt) * a.O + o;
+                v[b][i] = kFp8 ? fmaf(v[b][i], xs[b] * ws[i], bias[i]) : v[b][i] + bias[i];
+        }
+        act_batch(a.act, v);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (a.residual) res[b].add(v[b]);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (t + b * kStep >= mine) continue;
+            const int64_t at = (first + t + b * kStep) * a.O + o;
             if (a.out_fp32) {
                 float *out = static_cast<float *>(a.out) + at;
-                if (kVec == 4)
+                if constexpr (kVec == 4)
                     *reinterpret_cast<float4 *>(out) =
-                        make_float4(v[0], v[1 % kVec], v[2 % kVec], v[3 % kVec]);
+                        make_float4(v[b][0], v[b][1], v[b][2], v[b][3]);
                 else
-                    *out = v[0];
+                    *out = v[b][0];
             } else {
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + at;
-                if (kVec == 4)
-                    *reinterpret_cast<uint2 *>(out) =
-                        make_uint2(pack_bf16x2(v[0], v[1 % kVec]),
-                                   pack_bf16x2(v[2 % kVec], v[3 % kVec]));
+                if constexpr (kVec == 4)
+                    *reinterpret_cast<uint2 *>(out) = make_uint2(
+                        pack_bf16x2(v[b][0], v[b][1]), pack_bf16x2(v[b][2], v[b][3]));
                 else
-                    *out = __float2bfloat16_rn(v[0]);
+                    *out = __float2bfloat16_rn(v[b][0]);
             }
         }
     }
@@ -307,9 +337,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         cluster_barrier();
     };
     if (vec)
-        store_parts<kFp8, 4>(a, part, o0, first, mine, split, own_log, abort_flag, ready);
+        store_parts<kFp8, 4, kBN>(a, part, o0, first, mine, split, own_log, abort_flag, ready);
     else
-        store_parts<kFp8, 1>(a, part, o0, first, mine, split, own_log, abort_flag, ready);
+        store_parts<kFp8, 1, kBN>(a, part, o0, first, mine, split, own_log, abort_flag, ready);
     __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
