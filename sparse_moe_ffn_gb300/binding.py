@@ -312,14 +312,11 @@ def _typed(t, name, dtype, shape):
                      f"{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _typed_or_none(t, name, dtype, shape):
-    return None if t is None else _typed(t, name, dtype, shape)
-
-
 def _matrix(t, name):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
-    return t.shape
+    raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
+
+
+_BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
 
 
 def moe_add_rmsnorm_fp8(x, residual, weight, eps: float = 1e-6, gemma: bool = False, q=None,
@@ -327,36 +324,44 @@ def moe_add_rmsnorm_fp8(x, residual, weight, eps: float = 1e-6, gemma: bool = Fa
     """r = bf16(x + residual) (x without a residual), y = RMSNorm(r): returns
     (q e4m3 [N, H], scale fp32 [N], normed bf16 [N, H] or None) with q * scale
     = y.  r goes to ``residual_out``, or without one back to ``residual``."""
-    N, H = _matrix(x, "x")
-    bf16 = torch.bfloat16
+    if x.dim() != 2:
+        _matrix(x, "x")
+    shape = N, H = x.shape
     if residual_out is None:
         residual_out = residual
     if q is None:
-        q = torch.empty((N, H), dtype=torch.float8_e4m3fn, device=x.device)
+        q = torch.empty(shape, dtype=_E4M3, device=x.device)
     if scale is None:
-        scale = torch.empty(N, dtype=torch.float32, device=x.device)
+        scale = torch.empty(N, dtype=_F32, device=x.device)
     if normed is None and want_normed:
-        normed = torch.empty((N, H), dtype=bf16, device=x.device)
-    _check(lib().moe_add_rmsnorm_fp8(
-        _typed(x, "x", bf16, (N, H)), _typed_or_none(residual, "residual", bf16, (N, H)),
-        _typed(weight, "weight", bf16, (H,)), N, H, eps, bool(gemma),
-        _typed_or_none(residual_out, "residual_out", bf16, (N, H)),
-        _typed(q, "q", torch.float8_e4m3fn, (N, H)), _typed(scale, "scale", torch.float32, (N,)),
-        _typed_or_none(normed, "normed", bf16, (N, H)), _raw_stream(x)), "moe_add_rmsnorm_fp8")
+        normed = torch.empty(shape, dtype=_BF16, device=x.device)
+    status = lib().moe_add_rmsnorm_fp8(
+        _typed(x, "x", _BF16, shape),
+        None if residual is None else _typed(residual, "residual", _BF16, shape),
+        _typed(weight, "weight", _BF16, (H,)), N, H, eps, bool(gemma),
+        None if residual_out is None else _typed(residual_out, "residual_out", _BF16, shape),
+        _typed(q, "q", _E4M3, shape), _typed(scale, "scale", _F32, (N,)),
+        None if normed is None else _typed(normed, "normed", _BF16, shape), _raw_stream(x))
+    if status:
+        _check(status, "moe_add_rmsnorm_fp8")
     return q, scale, normed
 
 
 def moe_quantize_fp8(x, q=None, scale=None):
     """Rows of a bf16 matrix to e4m3: (q [N, H], scale fp32 [N]), q * scale = x.
     Used for weights (once, at load) and for activations."""
-    N, H = _matrix(x, "x")
+    if x.dim() != 2:
+        _matrix(x, "x")
+    shape = N, H = x.shape
     if q is None:
-        q = torch.empty((N, H), dtype=torch.float8_e4m3fn, device=x.device)
+        q = torch.empty(shape, dtype=_E4M3, device=x.device)
     if scale is None:
-        scale = torch.empty(N, dtype=torch.float32, device=x.device)
-    _check(lib().moe_quantize_fp8(
-        _typed(x, "x", torch.bfloat16, (N, H)), N, H, _typed(q, "q", torch.float8_e4m3fn, (N, H)),
-        _typed(scale, "scale", torch.float32, (N,)), _raw_stream(x)), "moe_quantize_fp8")
+        scale = torch.empty(N, dtype=_F32, device=x.device)
+    status = lib().moe_quantize_fp8(_typed(x, "x", _BF16, shape), N, H,
+                                    _typed(q, "q", _E4M3, shape),
+                                    _typed(scale, "scale", _F32, (N,)), _raw_stream(x))
+    if status:
+        _check(status, "moe_quantize_fp8")
     return q, scale
 
 
@@ -368,34 +373,43 @@ def moe_linear(x, weight, bias=None, residual=None, activation: str = "none", x_
     """act(x weight^T [* x_scale * w_scale] + bias) + residual, [N, O] in bf16
     or fp32 (``out_dtype``, or ``out``'s type).  x [N, K] and weight [O, K] are
     both bf16 (moe_linear) or both e4m3 with their scales (moe_linear_fp8).
-    ``workspace`` (uint8, optional) receives the status word of
+    ``workspace`` (uint8 CUDA tensor, optional) receives the status word of
     moe_read_device_status."""
-    N, K = _matrix(x, "x")
-    O = _matrix(weight, "weight")[0]
+    if x.dim() != 2:
+        _matrix(x, "x")
+    if weight.dim() != 2:
+        _matrix(weight, "weight")
+    N, K = x.shape
+    O = weight.shape[0]
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
-    fp8 = x.dtype == torch.float8_e4m3fn
-    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
-    if fp8 and (x_scale is None or w_scale is None):
-        raise ValueError("e4m3 operands need x_scale and w_scale")
-    if not fp8 and (x_scale is not None or w_scale is not None):
-        raise ValueError("x_scale and w_scale belong to e4m3 operands")
     if out is None:
         out = torch.empty((N, O), dtype=out_dtype, device=x.device)
-    fp32 = out.dtype == torch.float32
-    tail = (_typed_or_none(bias, "bias", torch.bfloat16, (O,)),
-            _typed_or_none(residual, "residual", torch.bfloat16, (N, O)), N, K, O, act,
-            _typed(out, "out", torch.float32 if fp32 else torch.bfloat16, (N, O)), fp32,
-            None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel(), _raw_stream(x))
-    xp, wp = _typed(x, "x", dtype, (N, K)), _typed(weight, "weight", dtype, (O, K))
-    if fp8:
-        status = lib().moe_linear_fp8(xp, _typed(x_scale, "x_scale", torch.float32, (N,)), wp,
-                                      _typed(w_scale, "w_scale", torch.float32, (O,)), *tail)
+    fp32 = out.dtype is _F32
+    b = None if bias is None else _typed(bias, "bias", _BF16, (O,))
+    r = None if residual is None else _typed(residual, "residual", _BF16, (N, O))
+    ws, bytes_ = None, 0
+    if workspace is not None:
+        bytes_ = workspace.numel()
+        ws = _typed(workspace, "workspace", torch.uint8, (bytes_,))
+    if x.dtype is _E4M3:
+        if x_scale is None or w_scale is None:
+            raise ValueError("e4m3 operands need x_scale and w_scale")
+        status = lib().moe_linear_fp8(
+            _typed(x, "x", _E4M3, (N, K)), _typed(x_scale, "x_scale", _F32, (N,)),
+            _typed(weight, "weight", _E4M3, (O, K)), _typed(w_scale, "w_scale", _F32, (O,)), b, r,
+            N, K, O, act, _typed(out, "out", _F32 if fp32 else _BF16, (N, O)), fp32, ws, bytes_,
+            _raw_stream(x))
     else:
-        status = lib().moe_linear(xp, wp, *tail)
-    _check(status, "moe_linear_fp8" if fp8 else "moe_linear")
+        if x_scale is not None or w_scale is not None:
+            raise ValueError("x_scale and w_scale belong to e4m3 operands")
+        status = lib().moe_linear(
+            _typed(x, "x", _BF16, (N, K)), _typed(weight, "weight", _BF16, (O, K)), b, r, N, K, O,
+            act, _typed(out, "out", _F32 if fp32 else _BF16, (N, O)), fp32, ws, bytes_,
+            _raw_stream(x))
+    if status:
+        _check(status, "moe_linear_fp8" if x.dtype is _E4M3 else "moe_linear")
     return out
 
 
@@ -405,16 +419,18 @@ def _balance_workspace_bytes(N, E):
 
 
 def _logits(logits):
-    if logits.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"logits must be fp32 or bf16, got {logits.dtype}")
-    N, E = _matrix(logits, "logits")
-    return N, E, logits.dtype == torch.bfloat16, _typed(logits, "logits", logits.dtype, (N, E))
+    dtype = logits.dtype
+    if dtype is not _F32 and dtype is not _BF16:
+        raise ValueError(f"logits must be fp32 or bf16, got {dtype}")
+    if logits.dim() != 2:
+        _matrix(logits, "logits")
+    return dtype is _BF16, _typed(logits, "logits", dtype, logits.shape)
 
 
 def _mask(mask, N):
-    if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
+    if mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
         raise ValueError(f"mask must be bool or uint8, got {mask.dtype}")
-    return None if mask is None else _typed(mask, "mask", mask.dtype, (N,))
+    return _typed(mask, "mask", mask.dtype, (N,))
 
 
 def moe_balance_loss(logits, topk_ids, mask=None, losses=None, counts=None, tokens=None,
@@ -422,25 +438,34 @@ def moe_balance_loss(logits, topk_ids, mask=None, losses=None, counts=None, toke
     """The router's losses and load: (losses fp32 [2] = load balance and mean
     squared log-sum-exp, counts int32 [E], tokens int32 [1]) of the logits
     [N, E] (fp32 or bf16) and the ids [N, k] that moe_route chose; ``mask``
-    (bool [N], optional) leaves tokens out, a negative id is a dropped slot."""
-    N, E, bf16, lp = _logits(logits)
-    k = _matrix(topk_ids, "topk_ids")[1]
-    dev = logits.device
+    (bool [N], optional) leaves tokens out, a negative id is a dropped slot.
+    ``workspace`` (uint8 CUDA tensor, optional) receives the status word of
+    moe_read_device_status."""
+    bf16, lp = _logits(logits)
+    N, E = logits.shape
+    if topk_ids.dim() != 2:
+        _matrix(topk_ids, "topk_ids")
+    k = topk_ids.shape[1]
     if losses is None:
-        losses = torch.empty(2, dtype=torch.float32, device=dev)
+        losses = torch.empty(2, dtype=_F32, device=logits.device)
     if counts is None:
-        counts = torch.empty(E, dtype=torch.int32, device=dev)
+        counts = torch.empty(E, dtype=_I32, device=logits.device)
     if tokens is None:
-        tokens = torch.empty(1, dtype=torch.int32, device=dev)
+        tokens = torch.empty(1, dtype=_I32, device=logits.device)
     need = _balance_workspace_bytes(N, E)
     if workspace is None and need > 256:  # else the status word alone
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _check(lib().moe_balance_loss(
-        lp, bf16, _typed(topk_ids, "topk_ids", torch.int32, (N, k)), _mask(mask, N), N, E, k,
-        _typed(losses, "losses", torch.float32, (2,)), _typed(counts, "counts", torch.int32, (E,)),
-        _typed(tokens, "tokens", torch.int32, (1,)),
-        None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel(), _raw_stream(logits)), "moe_balance_loss")
+        workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+    ws, bytes_ = None, 0
+    if workspace is not None:
+        bytes_ = workspace.numel()
+        ws = _typed(workspace, "workspace", torch.uint8, (bytes_,))
+    status = lib().moe_balance_loss(
+        lp, bf16, _typed(topk_ids, "topk_ids", _I32, (N, k)),
+        None if mask is None else _mask(mask, N), N, E, k, _typed(losses, "losses", _F32, (2,)),
+        _typed(counts, "counts", _I32, (E,)), _typed(tokens, "tokens", _I32, (1,)), ws, bytes_,
+        _raw_stream(logits))
+    if status:
+        _check(status, "moe_balance_loss")
     return losses, counts, tokens
 
 
@@ -448,15 +473,16 @@ def moe_balance_loss_backward(logits, counts, tokens, k: int, grad, mask=None, d
     """Gradient of grad[0] * losses[0] + grad[1] * losses[1] (grad fp32 [2] on
     the device) with respect to the logits, in their type; counts, tokens, k
     and mask as in the forward call."""
-    N, E, bf16, lp = _logits(logits)
+    bf16, lp = _logits(logits)
+    N, E = logits.shape
     if dlogits is None:
         dlogits = torch.empty_like(logits)
-    _check(lib().moe_balance_loss_backward(
-        lp, bf16, _typed(counts, "counts", torch.int32, (E,)),
-        _typed(tokens, "tokens", torch.int32, (1,)), _mask(mask, N),
-        _typed(grad, "grad", torch.float32, (2,)), N, E, k,
-        _typed(dlogits, "dlogits", logits.dtype, (N, E)), _raw_stream(logits)),
-        "moe_balance_loss_backward")
+    status = lib().moe_balance_loss_backward(
+        lp, bf16, _typed(counts, "counts", _I32, (E,)), _typed(tokens, "tokens", _I32, (1,)),
+        None if mask is None else _mask(mask, N), _typed(grad, "grad", _F32, (2,)), N, E, k,
+        _typed(dlogits, "dlogits", logits.dtype, (N, E)), _raw_stream(logits))
+    if status:
+        _check(status, "moe_balance_loss_backward")
     return dlogits
 
 

@@ -1,5 +1,4 @@
-// linear_epilogue.cuh -- what follows the accumulator of moe_linear: scales,
-// bias, activation, residual and the one rounding of the output, all in fp32.
+// linear_epilogue.cuh -- the activations of moe_linear, in fp32.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -60,13 +59,20 @@ __device__ __forceinline__ float linear_act(float v) {
     return v;
 }
 
-__device__ __forceinline__ float linear_act(int act, float v) {
+// The activation of a thread's outputs, one branch for all of them.
+template <int kN>
+__device__ __forceinline__ void act_all(int act, float (&v)[kN]) {
     switch (act) {
-        case MOE_ACT_SILU: return linear_act<MOE_ACT_SILU>(v);
-        case MOE_ACT_GELU: return linear_act<MOE_ACT_GELU>(v);
-        case MOE_ACT_GELU_TANH: return linear_act<MOE_ACT_GELU_TANH>(v);
-        case MOE_ACT_RELU: return linear_act<MOE_ACT_RELU>(v);
-        default: return v;
+#define MOE_ACT_CASE(A)                                                              \
+    case A:                                                                          \
+        _Pragma("unroll") for (int i = 0; i < kN; ++i) v[i] = linear_act<A>(v[i]);   \
+        break;
+        MOE_ACT_CASE(MOE_ACT_SILU)
+        MOE_ACT_CASE(MOE_ACT_GELU)
+        MOE_ACT_CASE(MOE_ACT_GELU_TANH)
+        MOE_ACT_CASE(MOE_ACT_RELU)
+#undef MOE_ACT_CASE
+        default: break;
     }
 }
 

@@ -84,22 +84,6 @@ __device__ __forceinline__ void tile_of(int tile, int m_tiles, int n_tiles, int 
     *n = in / rows;
 }
 
-template <int kCols>
-__device__ __forceinline__ void act_all(int act, float (&v)[kCols]) {
-    switch (act) {
-#define MOE_ACT_CASE(A)                                                    \
-    case A:                                                                \
-        _Pragma("unroll") for (int i = 0; i < kCols; ++i) v[i] = linear_act<A>(v[i]); \
-        break;
-        MOE_ACT_CASE(MOE_ACT_SILU)
-        MOE_ACT_CASE(MOE_ACT_GELU)
-        MOE_ACT_CASE(MOE_ACT_GELU_TANH)
-        MOE_ACT_CASE(MOE_ACT_RELU)
-#undef MOE_ACT_CASE
-        default: break;
-    }
-}
-
 // 32-byte load that stays out of L1 (8 words; p 32-byte aligned)
 __device__ __forceinline__ void ld_global_v8(const void *p, uint32_t *v) {
     asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"

@@ -76,24 +76,6 @@ struct ResidualOf<1> {
     }
 };
 
-template <int kBatch, int kVec>
-__device__ __forceinline__ void act_batch(int act, float (&v)[kBatch][kVec]) {
-    switch (act) {
-#define MOE_ACT_CASE(A)                                             \
-    case A:                                                         \
-        _Pragma("unroll") for (int b = 0; b < kBatch; ++b)          \
-            _Pragma("unroll") for (int i = 0; i < kVec; ++i)        \
-                v[b][i] = linear_act<A>(v[b][i]);                   \
-        break;
-        MOE_ACT_CASE(MOE_ACT_SILU)
-        MOE_ACT_CASE(MOE_ACT_GELU)
-        MOE_ACT_CASE(MOE_ACT_GELU_TANH)
-        MOE_ACT_CASE(MOE_ACT_RELU)
-#undef MOE_ACT_CASE
-        default: break;
-    }
-}
-
 // Adds the ranks' parts of this CTA's `mine` tokens and stores them, kVec
 // outputs a thread; a thread keeps its outputs from token to token.  The
 // epilogue's operands are fetched before `ready` waits for the parts.
@@ -163,7 +145,7 @@ __device__ __forceinline__ void store_parts(const LinearArgs &a, const float *pa
             for (int i = 0; i < kVec; ++i)
                 v[b][i] = kFp8 ? fmaf(v[b][i], xs[b] * ws[i], bias[i]) : v[b][i] + bias[i];
         }
-        act_batch(a.act, v);
+        act_all(a.act, reinterpret_cast<float(&)[kBatch * kVec]>(v));
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
             if (a.residual) res[b].add(v[b]);

@@ -129,12 +129,18 @@ def test_binding_refuses_wrong_tensors():
         binding.moe_quantize_fp8(x)
     with pytest.raises(ValueError, match="two dimensions"):
         binding.moe_quantize_fp8(w)
+    with pytest.raises(ValueError, match="two dimensions"):
+        binding.moe_linear(x, w)
+    with pytest.raises(ValueError, match="two dimensions"):
+        binding.moe_balance_loss(w, torch.zeros(4, 2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="workspace"):
+        binding.moe_linear(x, x, out=x, workspace=torch.zeros(64))
     with pytest.raises(ValueError, match="activation"):
         binding.moe_linear(x, x, activation="swish")
     with pytest.raises(ValueError, match="x_scale"):
-        binding.moe_linear(x.to(torch.float8_e4m3fn), x.to(torch.float8_e4m3fn))
+        binding.moe_linear(x.to(torch.float8_e4m3fn), x.to(torch.float8_e4m3fn), out=x)
     with pytest.raises(ValueError, match="e4m3"):
-        binding.moe_linear(x, x, x_scale=torch.ones(4))
+        binding.moe_linear(x, x, x_scale=torch.ones(4), out=x)
     with pytest.raises(ValueError, match="CUDA"):
         binding.moe_linear(x, x)
     with pytest.raises(ValueError, match="fp32 or bf16"):
