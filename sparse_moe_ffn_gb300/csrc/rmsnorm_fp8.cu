@@ -15,8 +15,8 @@
 // with a NaN or an infinity gets a NaN scale and not a plausible one.
 //
 // What bounds it: memory.  9 bytes an element with residual, sum and bf16 output
-// (3 without the norm): 8192 x 2048 takes 25.3 us, 5970 GB/s (a plain copy of
-// as many bytes: 6200), quantising alone 9.9 us, 5060 GB/s; one row 1.8 us.
+// (3 without the norm): 8192 x 2048 takes 24.3 us, 6220 GB/s (a plain copy of
+// as many bytes: 6200), quantising alone 9.4 us, 5340 GB/s; one row 1.8 us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -196,7 +196,11 @@ cudaError_t launch_rows(const RowArgs &a, int num_sms, cudaStream_t s) {
                                                       kThreads, 0);
         return n > 0 ? n : 1;
     }();
-    const int64_t limit = static_cast<int64_t>(num_sms) * resident;
+    // Four times what fits at once: blocks that follow one another keep the
+    // memory busier than a loop does (8192 x 2048, norm 25.7 -> 24.3 us); rows
+    // of up to 512 values are too short for that (65536 x 256 in one go 33.6 us
+    // against 26.5).
+    const int64_t limit = static_cast<int64_t>(num_sms) * resident * (a.H > 512 ? 4 : 1);
     if (blocks > limit) blocks = limit;
     return launch_pdl(rows_to_e4m3_kernel<kRow, kChunks, kNorm>,
                       dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, 1, a);
@@ -206,7 +210,7 @@ cudaError_t launch_rows(const RowArgs &a, int num_sms, cudaStream_t s) {
 // chunk a thread, that is the shortest path; beyond it (by about 200000 chunks
 // for the norm, 100000 without it) fewer threads a row, two or four chunks each,
 // keep more bytes in flight between the reductions: 8192 x 2048, norm 27.1
-// -> 25.1 us and plain 11.3 -> 9.6; 64 x 2048 the other way, 2.1 against 2.3 and
+// -> 25.1 us and plain 11.3 -> 9.6 (in a loop, as fits at once); 64 x 2048 the other way, 2.1 against 2.3 and
 // 1.5 against 1.9.  Rows over 2048 take two or four chunks a thread in any case.
 template <bool kNorm>
 cudaError_t launch_any(const RowArgs &a, int num_sms, cudaStream_t s) {
