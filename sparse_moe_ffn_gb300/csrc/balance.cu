@@ -463,8 +463,8 @@ __global__ void __launch_bounds__(kBlock, 512 / kBlock) balance_stats_kernel(con
     cluster_wait_all();  // nobody leaves while its shared memory is read
 }
 
-// Joins the clusters' partial sums: kSeg threads an expert, each over every
-// kSeg-th cluster, then in order.
+// Joins the clusters' partial sums: `seg` threads an expert, each over every
+// seg-th cluster, then in order.
 constexpr int kJoinThreads = 1024;
 constexpr int kJoinPer = (kBalanceMaxClusters + 3) / 4;  // at most, with E = 256
 
