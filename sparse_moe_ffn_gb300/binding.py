@@ -299,8 +299,7 @@ def moe_add_rmsnorm(x, residual, weight, eps: float = 1e-6, gemma: bool = False,
 # The operators below take a few microseconds each, so their wrappers keep to
 # what the checks need: plain integers for pointers, and the current stream of
 # the tensors' device without a Stream object (2.9 us of a 12 us call).
-def _raw_stream(t):
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # none without CUDA
 
 
 def _typed(t, name, dtype, shape):
@@ -341,7 +340,8 @@ def moe_add_rmsnorm_fp8(x, residual, weight, eps: float = 1e-6, gemma: bool = Fa
         _typed(weight, "weight", _BF16, (H,)), N, H, eps, bool(gemma),
         None if residual_out is None else _typed(residual_out, "residual_out", _BF16, shape),
         _typed(q, "q", _E4M3, shape), _typed(scale, "scale", _F32, (N,)),
-        None if normed is None else _typed(normed, "normed", _BF16, shape), _raw_stream(x))
+        None if normed is None else _typed(normed, "normed", _BF16, shape),
+        _stream_of(x.get_device()))
     if status:
         _check(status, "moe_add_rmsnorm_fp8")
     return q, scale, normed
@@ -359,7 +359,7 @@ def moe_quantize_fp8(x, q=None, scale=None):
         scale = torch.empty(N, dtype=_F32, device=x.device)
     status = lib().moe_quantize_fp8(_typed(x, "x", _BF16, shape), N, H,
                                     _typed(q, "q", _E4M3, shape),
-                                    _typed(scale, "scale", _F32, (N,)), _raw_stream(x))
+                                    _typed(scale, "scale", _F32, (N,)), _stream_of(x.get_device()))
     if status:
         _check(status, "moe_quantize_fp8")
     return q, scale
@@ -400,14 +400,14 @@ def moe_linear(x, weight, bias=None, residual=None, activation: str = "none", x_
             _typed(x, "x", _E4M3, (N, K)), _typed(x_scale, "x_scale", _F32, (N,)),
             _typed(weight, "weight", _E4M3, (O, K)), _typed(w_scale, "w_scale", _F32, (O,)), b, r,
             N, K, O, act, _typed(out, "out", _F32 if fp32 else _BF16, (N, O)), fp32, ws, bytes_,
-            _raw_stream(x))
+            _stream_of(x.get_device()))
     else:
         if x_scale is not None or w_scale is not None:
             raise ValueError("x_scale and w_scale belong to e4m3 operands")
         status = lib().moe_linear(
             _typed(x, "x", _BF16, (N, K)), _typed(weight, "weight", _BF16, (O, K)), b, r, N, K, O,
             act, _typed(out, "out", _F32 if fp32 else _BF16, (N, O)), fp32, ws, bytes_,
-            _raw_stream(x))
+            _stream_of(x.get_device()))
     if status:
         _check(status, "moe_linear_fp8" if x.dtype is _E4M3 else "moe_linear")
     return out
@@ -463,7 +463,7 @@ def moe_balance_loss(logits, topk_ids, mask=None, losses=None, counts=None, toke
         lp, bf16, _typed(topk_ids, "topk_ids", _I32, (N, k)),
         None if mask is None else _mask(mask, N), N, E, k, _typed(losses, "losses", _F32, (2,)),
         _typed(counts, "counts", _I32, (E,)), _typed(tokens, "tokens", _I32, (1,)), ws, bytes_,
-        _raw_stream(logits))
+        _stream_of(logits.get_device()))
     if status:
         _check(status, "moe_balance_loss")
     return losses, counts, tokens
@@ -480,7 +480,7 @@ def moe_balance_loss_backward(logits, counts, tokens, k: int, grad, mask=None, d
     status = lib().moe_balance_loss_backward(
         lp, bf16, _typed(counts, "counts", _I32, (E,)), _typed(tokens, "tokens", _I32, (1,)),
         None if mask is None else _mask(mask, N), _typed(grad, "grad", _F32, (2,)), N, E, k,
-        _typed(dlogits, "dlogits", logits.dtype, (N, E)), _raw_stream(logits))
+        _typed(dlogits, "dlogits", logits.dtype, (N, E)), _stream_of(logits.get_device()))
     if status:
         _check(status, "moe_balance_loss_backward")
     return dlogits

@@ -80,6 +80,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity,
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
 }
 
+// Waits for work already in flight, after a failure too (which mbar_wait would
+// cut short): nothing may be under way when a kernel gives its memory back.
+// Bounded like every wait.
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
+    volatile int never = 0;
+    mbar_wait(bar, parity, &never);
+}
+
 // ------------------------------------------------------------------ clusters
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {

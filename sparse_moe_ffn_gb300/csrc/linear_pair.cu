@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // no copy may be in flight when the pair ends
         if (leader && issues)
             for (int64_t i = (g > kStages ? g - kStages : 0); i < g; ++i)
-                mbar_wait(&sm->full[i % kStages], (i / kStages) & 1, abort_flag);
+                drain_wait(&sm->full[i % kStages], (i / kStages) & 1);
         __syncwarp();
     } else if (warp == 1) {
         if (leader) {
@@ -328,8 +328,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
                 *abort_flag = 1;
             }
-            if (issues) commit_2cta(&sm->drain, 1);
-            warp_wait(&sm->drain, 0, abort_flag);
+            if (issues) {
+                commit_2cta(&sm->drain, 1);
+                drain_wait(&sm->drain, 0);
+            }
         }
         __syncwarp();
     } else {

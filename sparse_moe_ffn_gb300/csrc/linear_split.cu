@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
         // no copy may be in flight when the CTA ends
         if (issues)
             for (int i = (g > kStages ? g - kStages : 0); i < g; ++i)
-                mbar_wait(&sm->full[i % kStages], (i / kStages) & 1, abort_flag);
+                drain_wait(&sm->full[i % kStages], (i / kStages) & 1);
         __syncwarp();
     } else if (warp == 1) {
         // the whole warp runs the loop and one lane issues: descriptors and
@@ -276,7 +276,10 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
                 mma_commit(&sm->empty[s]);
             }
         }
-        if (issues) mma_commit(&sm->acc_full);  // after a failure too: the MMAs issued so far
+        if (issues) {
+            mma_commit(&sm->acc_full);  // after a failure too: the MMAs issued so far
+            drain_wait(&sm->acc_full, 0);
+        }
         __syncwarp();
     }
 

@@ -501,3 +501,82 @@ def test_balance_same_bits_in_place_and_in_a_graph():
     for a, b in zip(first, held):
         assert torch.equal(a, b)
     assert torch.equal(first[3], again)
+
+
+# ------------------------------------------- other streams, far offsets
+
+
+def test_norm_and_balance_on_another_stream_and_in_a_graph():
+    g = gen(31)
+    x, res = normal(g, 300, 2048).to(BF16), normal(g, 300, 2048).to(BF16)
+    w = torch.ones(2048, dtype=BF16, device="cuda")
+    out = torch.empty_like(res)
+    logits, ids, mask = balance_case(3000, 64, 6, BF16, 2, True)
+    grad = torch.tensor([0.5, 0.1], dtype=F32, device="cuda")
+
+    def all_of_them():
+        a = binding.moe_add_rmsnorm_fp8(x, res, w, want_normed=True, residual_out=out)
+        b = binding.moe_quantize_fp8(x)
+        c = binding.moe_balance_loss(logits, ids, mask)
+        d = binding.moe_balance_loss_backward(logits, c[1], c[2], 6, grad, mask)
+        return [t.float() for t in (*a, *b, *c, d)]
+
+    first = all_of_them()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = all_of_them()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = all_of_them()
+    graph.replay()
+    for a, b, c in zip(first, other, held):
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("kind,O,residual", [("bf16", 8200, True), ("e4m3", 8001, False)])
+def test_linear_past_2_31_outputs(kind, O, residual):
+    """Outputs whose element offsets pass 32 bits, in tensor-map stores and in
+    single values; sampled rows, the last ones among them."""
+    N, K = 270000, 64
+    x, w, scales = linear_case(N, K, O, kind, 77)
+    r = normal(gen(78), N, O).to(BF16) if residual else None
+    out = binding.moe_linear(x, w, residual=r, **scales)
+    rows = torch.cat([torch.arange(0, N, 9973, device="cuda"),
+                      torch.arange(N - 70, N, device="cuda")])
+    part = {n: (t[rows] if n == "x_scale" else t) for n, t in scales.items()}
+    ref, tol = linear_ref(x[rows], w, part, None, None if r is None else r[rows], "none", BF16)
+    assert_within(out[rows], ref, tol, "far rows")
+
+
+def test_rows_past_2_31_elements():
+    N, H = 270000, 8200
+    g = gen(5)
+    x = torch.empty((N, H), dtype=BF16, device="cuda")
+    for i in range(0, N, 30000):
+        x[i:i + 30000] = normal(g, min(30000, N - i), H).to(BF16)
+    q, s = binding.moe_quantize_fp8(x)
+    rows = torch.cat([torch.arange(0, N, 9973, device="cuda"),
+                      torch.arange(N - 70, N, device="cuda")])
+    y = x[rows].double()
+    check_e4m3(q[rows], s[rows], y, scale_of(y))
+
+
+def test_balance_past_2_31_logits():
+    N, E = (1 << 23) + 1001, 256
+    logits = torch.empty((N, E), dtype=BF16, device="cuda")
+    g = gen(6)
+    for i in range(0, N, 1 << 20):
+        logits[i:i + (1 << 20)] = normal(g, min(1 << 20, N - i), E).to(BF16)
+    ids = torch.randint(0, E, (N, 1), generator=g, device="cuda", dtype=torch.int32)
+    losses, counts, tokens = binding.moe_balance_loss(logits, ids)
+    assert int(tokens) == N
+    assert torch.equal(counts.long(), torch.bincount(ids[:, 0].long(), minlength=E))
+    grad = torch.tensor([0.3, -0.02], dtype=F32, device="cuda")
+    d = binding.moe_balance_loss_backward(logits, counts, tokens, 1, grad)
+    rows = torch.cat([torch.arange(0, N, 99991, device="cuda"),
+                      torch.arange(N - 70, N, device="cuda")])
+    p, lse, _, _, _ = balance64(logits[rows], ids[rows], None, 1)
+    ref, tol = grad64(p, lse, counts.double() / N, N, grad)
+    assert_within(d[rows], ref, tol + HALF[BF16] * (ref.abs() + tol) + 1e-38, "far rows")
