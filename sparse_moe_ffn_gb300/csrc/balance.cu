@@ -30,6 +30,7 @@
 #include <type_traits>
 
 #include "block_ops.cuh"
+#include "cluster.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -251,27 +252,12 @@ struct Sum {
     __device__ __forceinline__ float value() const { return hi + lo; }
 };
 
-__device__ __forceinline__ uint32_t cluster_rank_of() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
+__device__ __forceinline__ float of_rank(const float *p, int rank) {
+    return __uint_as_float(ld_cluster_u32(p, rank));
 }
 
-__device__ __forceinline__ void cluster_wait_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// The 32-bit word at `p` in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t ld_rank(const void *p, int rank) {
-    uint32_t a, v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ float ld_rank(const float *p, int rank) {
-    return __uint_as_float(ld_rank(static_cast<const void *>(p), rank));
+__device__ __forceinline__ int of_rank(const int *p, int rank) {
+    return static_cast<int>(ld_cluster_u32(p, rank));
 }
 
 struct Totals {
@@ -409,10 +395,10 @@ __global__ void __launch_bounds__(kBlock, 512 / kBlock) balance_stats_kernel(con
         }
         total = b;
     }
-    cluster_wait_all();
+    cluster_barrier();
 
     // the blocks of the cluster, in order: each takes a run of the experts
-    const int rank = static_cast<int>(cluster_rank_of());
+    const int rank = static_cast<int>(cluster_ctarank());
     const int share = (a.E + kBalanceCluster - 1) / kBalanceCluster;
     const int e = rank * share + static_cast<int>(threadIdx.x);
     const bool mine = static_cast<int>(threadIdx.x) < share && e < a.E;
@@ -423,8 +409,8 @@ __global__ void __launch_bounds__(kBlock, 512 / kBlock) balance_stats_kernel(con
         int c = 0;
 #pragma unroll
         for (int r = 0; r < kBalanceCluster; ++r) {
-            s.add(ld_rank(&p_block[e], r));
-            c += static_cast<int>(ld_rank(static_cast<const void *>(&cs[e]), r));
+            s.add(of_rank(&p_block[e], r));
+            c += of_rank(&cs[e], r);
         }
         if (alone) {
             a.counts[e] = c;
@@ -438,9 +424,9 @@ __global__ void __launch_bounds__(kBlock, 512 / kBlock) balance_stats_kernel(con
     Totals sum = {0.f, 0, 0};
     if (threadIdx.x == 0 && rank == 0) {
         for (int r = 0; r < kBalanceCluster; ++r) {
-            sum.z += ld_rank(&total.z, r);
-            sum.tokens += static_cast<int>(ld_rank(static_cast<const void *>(&total.tokens), r));
-            sum.bad |= static_cast<int>(ld_rank(static_cast<const void *>(&total.bad), r));
+            sum.z += of_rank(&total.z, r);
+            sum.tokens += of_rank(&total.tokens, r);
+            sum.bad |= of_rank(&total.bad, r);
         }
         if (!alone) a.part_s[blockIdx.x / kBalanceCluster] = {sum.z, sum.tokens, sum.bad};
     }
@@ -453,14 +439,14 @@ __global__ void __launch_bounds__(kBlock, 512 / kBlock) balance_stats_kernel(con
             for (int w = 0; w < kWarps; ++w) pc += pcs[w];
             pc_rank = pc;
         }
-        cluster_wait_all();
+        cluster_barrier();
         if (threadIdx.x == 0 && rank == 0) {
             pc = 0.f;
-            for (int r = 0; r < kBalanceCluster; ++r) pc += ld_rank(&pc_rank, r);
+            for (int r = 0; r < kBalanceCluster; ++r) pc += of_rank(&pc_rank, r);
             write_losses(a, pc, sum);
         }
     }
-    cluster_wait_all();  // nobody leaves while its shared memory is read
+    cluster_barrier();  // nobody leaves while its shared memory is read
 }
 
 // Joins the clusters' partial sums: `seg` threads an expert, each over every

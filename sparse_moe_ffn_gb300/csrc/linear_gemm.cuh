@@ -12,6 +12,7 @@
 #include <atomic>
 
 #include "block_ops.cuh"
+#include "cluster.cuh"
 #include "ptx.cuh"
 
 namespace moe {
@@ -88,29 +89,7 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
     mbar_wait(bar, parity, &never);
 }
 
-// ------------------------------------------------------------------ clusters
-
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Address of this CTA's shared variable in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-    return r;
-}
-
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
+// ------------------------------------------------------------------ CTA pairs
 
 // Arrival that orders no memory accesses (the waiter only needs to know that
 // this warp's TMEM reads have returned).
@@ -118,8 +97,6 @@ __device__ __forceinline__ void arrive_remote_relaxed(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");
 }
-
-// ------------------------------------------------------------------ CTA pairs
 
 // Tiled load into this CTA's shared memory that completes on a barrier of the
 // pair's even CTA (`bar`: a shared::cluster address).
