@@ -14,11 +14,10 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
     return r;
 }
 
-// All threads of the cluster; whole warps (.aligned), whatever came before.
+// All threads of the cluster; the lanes of a warp need not arrive together.
 __device__ __forceinline__ void cluster_barrier() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;\n\t"
+                 "barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Address of this CTA's shared variable in CTA `rank` of the cluster.
