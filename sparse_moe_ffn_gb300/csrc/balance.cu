@@ -274,7 +274,7 @@ __device__ __forceinline__ void write_losses(const BalanceArgs &a, float pc, con
     if (a.status) *a.status = t.bad ? MOE_ERR_DEVICE_CHECK : MOE_OK;
 }
 
-template <bool kBf16, int kLanes, bool kVec, int kBlock>
+template <bool kBf16, int kLanes, bool kVec, int kBlock, int kCluster>
 __global__ void __launch_bounds__(kBlock, 512 / kBlock) balance_stats_kernel(const BalanceArgs a) {
     constexpr int kPerWarp = 32 / kLanes;
     constexpr int kWarps = kBlock / 32;
@@ -399,16 +399,16 @@ __global__ void __launch_bounds__(kBlock, 512 / kBlock) balance_stats_kernel(con
 
     // the blocks of the cluster, in order: each takes a run of the experts
     const int rank = static_cast<int>(cluster_ctarank());
-    const int share = (a.E + kBalanceCluster - 1) / kBalanceCluster;
+    const int share = (a.E + kCluster - 1) / kCluster;
     const int e = rank * share + static_cast<int>(threadIdx.x);
     const bool mine = static_cast<int>(threadIdx.x) < share && e < a.E;
-    const bool alone = gridDim.x == kBalanceCluster;
+    const bool alone = gridDim.x == kCluster;
     float pc = 0.f;
     if (mine) {
         Sum s;
         int c = 0;
 #pragma unroll
-        for (int r = 0; r < kBalanceCluster; ++r) {
+        for (int r = 0; r < kCluster; ++r) {
             s.add(of_rank(&p_block[e], r));
             c += of_rank(&cs[e], r);
         }
@@ -416,19 +416,19 @@ __global__ void __launch_bounds__(kBlock, 512 / kBlock) balance_stats_kernel(con
             a.counts[e] = c;
             pc = s.value() * static_cast<float>(c);
         } else {
-            const int64_t at = static_cast<int64_t>(blockIdx.x / kBalanceCluster) * a.E + e;
+            const int64_t at = static_cast<int64_t>(blockIdx.x / kCluster) * a.E + e;
             a.part_p[at] = s.value();
             a.part_c[at] = c;
         }
     }
     Totals sum = {0.f, 0, 0};
     if (threadIdx.x == 0 && rank == 0) {
-        for (int r = 0; r < kBalanceCluster; ++r) {
+        for (int r = 0; r < kCluster; ++r) {
             sum.z += of_rank(&total.z, r);
             sum.tokens += of_rank(&total.tokens, r);
             sum.bad |= of_rank(&total.bad, r);
         }
-        if (!alone) a.part_s[blockIdx.x / kBalanceCluster] = {sum.z, sum.tokens, sum.bad};
+        if (!alone) a.part_s[blockIdx.x / kCluster] = {sum.z, sum.tokens, sum.bad};
     }
     if (alone) {  // one cluster holds every token: it ends the call
         pc = row_sum<32>(pc);
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kBlock, 512 / kBlock) balance_stats_kernel(con
         cluster_barrier();
         if (threadIdx.x == 0 && rank == 0) {
             pc = 0.f;
-            for (int r = 0; r < kBalanceCluster; ++r) pc += of_rank(&pc_rank, r);
+            for (int r = 0; r < kCluster; ++r) pc += of_rank(&pc_rank, r);
             write_losses(a, pc, sum);
         }
     }
@@ -582,13 +582,17 @@ __global__ void __launch_bounds__(kThreads, 2) balance_grad_kernel(const Balance
 
 using BalanceKernel = void (*)(BalanceArgs);
 
-enum Pass { kStats, kStatsAlone, kGrad };
+enum Pass { kStats, kAlone8, kAlone16, kGrad };
 
 template <Pass kPass, bool kBf16, bool kVec, int kLanes>
 BalanceKernel kernel_at() {
-    if constexpr (kPass == kGrad) return balance_grad_kernel<kBf16, kLanes, kVec>;
-    else if constexpr (kPass == kStats) return balance_stats_kernel<kBf16, kLanes, kVec, kThreads>;
-    else return balance_stats_kernel<kBf16, kLanes, kVec, kAloneThreads>;
+    if constexpr (kPass == kGrad)
+        return balance_grad_kernel<kBf16, kLanes, kVec>;
+    else if constexpr (kPass == kStats)
+        return balance_stats_kernel<kBf16, kLanes, kVec, kThreads, kBalanceCluster>;
+    else
+        return balance_stats_kernel<kBf16, kLanes, kVec, kAloneThreads,
+                                    kPass == kAlone8 ? 8 : 16>;
 }
 
 template <Pass kPass, bool kBf16, bool kVec>
@@ -621,21 +625,31 @@ cudaError_t launch(const BalanceArgs &a, int blocks, cudaStream_t s) {
         a.bf16 ? (vec ? kernel_of<kPass, true, true>(lanes) : kernel_of<kPass, true, false>(lanes))
                : (vec ? kernel_of<kPass, false, true>(lanes)
                       : kernel_of<kPass, false, false>(lanes));
+    if (kPass == kAlone16) {  // clusters of more than 8 have to be asked for
+        cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k),
+                                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    constexpr bool kAlone = kPass == kAlone8 || kPass == kAlone16;
+    constexpr unsigned kCluster = kPass == kGrad      ? 1
+                                  : kPass == kAlone16 ? 16
+                                  : kPass == kAlone8  ? 8
+                                                      : kBalanceCluster;
     return launch_pdl(k, dim3(static_cast<unsigned>(blocks)),
-                      dim3(kPass == kStatsAlone ? kAloneThreads : kThreads), 0, s,
-                      kPass == kGrad ? 1 : kBalanceCluster, a);
+                      dim3(kAlone ? kAloneThreads : kThreads), 0, s, kCluster, a);
 }
 
 int64_t rows_per_block(int E, int threads) { return threads / lanes_of(E) * kUnroll; }
 
 }  // namespace
 
-// One cluster of twice the threads does up to three passes on its own: two take
-// less than the second kernel (1024 x 128: 5.4 against 5.8 us), the third 1 us
-// more (4099 x 60: 7.2 against 6.2), and the host saves a launch and the
-// workspace (9 us of 24 for a forward and backward call).
+// One cluster does small batches on its own, of 8 blocks for one pass and of 16
+// for up to three: two passes take less than the second kernel (2048 x 128: 5.8
+// against 6.2 us, 3000 x 60: 5.5 against 6.0), a third at most 1.5 us more (6144
+// x 128: 8.7 against 7.2), and the host saves a launch and the workspace (9 us
+// of 24 for a forward and backward call).
 int balance_clusters(int64_t N, int E) {
-    if (N <= 3 * kBalanceCluster * rows_per_block(E, kAloneThreads)) return 1;
+    if (N <= 3 * 16 * rows_per_block(E, kAloneThreads)) return 1;
     const int64_t rows = kBalanceCluster * rows_per_block(E, kThreads);
     const int64_t c = (N + rows - 1) / rows;
     return static_cast<int>(c < kBalanceMaxClusters ? c : kBalanceMaxClusters);
@@ -643,7 +657,9 @@ int balance_clusters(int64_t N, int E) {
 
 cudaError_t launch_balance(const BalanceArgs &a, int *launches, cudaStream_t s) {
     *launches = a.clusters > 1 ? 2 : 1;
-    if (a.clusters == 1) return launch<kStatsAlone>(a, kBalanceCluster, s);
+    if (a.clusters == 1)
+        return a.N <= 8 * rows_per_block(a.E, kAloneThreads) ? launch<kAlone8>(a, 8, s)
+                                                             : launch<kAlone16>(a, 16, s);
     cudaError_t e = launch<kStats>(a, a.clusters * kBalanceCluster, s);
     if (e != cudaSuccess) return e;
     return launch_pdl(balance_join_kernel, dim3(1), dim3(kJoinThreads), 0, s, 1, a);

@@ -415,7 +415,10 @@ def test_balance_sizes(N, E, k, masked, dtype):
     check_balance(*balance_case(N, E, k, dtype, N * 1000 + E, masked), k)
 
 
-@pytest.mark.parametrize("N,E,k", [(40000, 128, 8), (100003, 60, 4), (300000, 6, 2)])
+# one cluster of 16 blocks (up to three passes), then several of 8
+@pytest.mark.parametrize("N,E,k", [(2500, 256, 8), (5000, 128, 8), (12000, 60, 4), (3075, 255, 3),
+                                   (6200, 128, 8), (40000, 128, 8), (100003, 60, 4),
+                                   (300000, 6, 2)])
 @pytest.mark.parametrize("masked", [False, True])
 def test_balance_many_tokens(N, E, k, masked):
     check_balance(*balance_case(N, E, k, F32, N, masked), k)
