@@ -17,7 +17,7 @@
 //
 // A row is held by kLanes lanes, 8 values each (kLanes is the power of two
 // that covers E), four rows at a time; sums over tokens run in registers, then
-// per block, per cluster of eight blocks (distributed shared memory) and, when
+// per block, per cluster of blocks (distributed shared memory) and, when
 // there is more than one cluster, in a second kernel: each in a fixed order,
 // with no atomics on floats, so the same inputs give the same bits.
 //
