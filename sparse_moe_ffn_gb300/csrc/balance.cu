@@ -204,10 +204,26 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
+// a, b <- (a - top) m, (b - top) m: two values an instruction.
+__device__ __forceinline__ void sub_mul_pair(float &a, float &b, float top, float m) {
+    asm("{\n\t.reg .b64 x, t;\n\t"
+        "mov.b64 x, {%0, %1};\n\t"
+        "mov.b64 t, {%2, %2};\n\t"
+        "add.rn.f32x2 x, x, t;\n\t"
+        "mov.b64 t, {%3, %3};\n\t"
+        "mul.rn.f32x2 x, x, t;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(-top), "f"(m));
+}
+
 // x[u] <- e^(x - top) of row u; f[u]: the factor that makes them
-// probabilities, lse[u]: the row's log-sum-exp.  The exponent is one fma: what
-// the rounding of top log2(e) leaves is a factor common to the row.  A NaN
-// logit reaches both results (fmaxf drops it, the sum does not).
+// probabilities, lse[u]: the row's log-sum-exp.  The largest logit is taken off
+// before the product with log2(e): in one fma, with top log2(e) rounded beside
+// it, rows of values beyond 1e9 (experts disabled with a large finite value)
+// over- or underflow.  Two values an instruction make it no slower than that
+// fma (131072 x 128 forward 20.0 us either way, 20.3 one value at a time).  A
+// NaN logit reaches both results (fmaxf drops it, the sum does not).
 template <int kLanes>
 __device__ __forceinline__ void softmax_rows(float (&x)[kUnroll][kVals], float (&f)[kUnroll],
                                              float (&lse)[kUnroll]) {
@@ -223,12 +239,14 @@ __device__ __forceinline__ void softmax_rows(float (&x)[kUnroll][kVals], float (
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         if (top[u] == kNegInf) top[u] = 0.f;
-        const float off = -top[u] * kLog2e;
         f[u] = 0.f;
 #pragma unroll
-        for (int v = 0; v < kVals; ++v) {
-            x[u][v] = exp2_fast(fmaf(x[u][v], kLog2e, off));
+        for (int v = 0; v < kVals; v += 2) {
+            sub_mul_pair(x[u][v], x[u][v + 1], top[u], kLog2e);
+            x[u][v] = exp2_fast(x[u][v]);
+            x[u][v + 1] = exp2_fast(x[u][v + 1]);
             f[u] += x[u][v];
+            f[u] += x[u][v + 1];
         }
     }
     rows_sum<kLanes>(f);
