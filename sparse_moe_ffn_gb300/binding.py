@@ -299,15 +299,28 @@ def moe_add_rmsnorm(x, residual, weight, eps: float = 1e-6, gemma: bool = False,
 # The operators below take a few microseconds each, so their wrappers keep to
 # what the checks need: plain integers for pointers, and the current stream of
 # the tensors' device without a Stream object (2.9 us of a 12 us call).
-_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # none without CUDA
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # none without CUDA
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _typed(t, name, dtype, shape):
-    """The data pointer of a contiguous CUDA tensor of this type and shape."""
-    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+def _stream_of(device):
+    """The current stream of a device, which has to be the current one: the
+    library launches there, and takes its number of SMs from there."""
+    if device != _current_device():
+        raise ValueError(f"the tensors are on cuda:{device}, which is not the current device "
+                         f"(cuda:{_current_device()}): call within torch.cuda.device({device})")
+    return _raw_stream(device)
+
+
+def _typed(t, name, dtype, shape, device=-1):
+    """The data pointer of a contiguous tensor of this type and shape on the
+    CUDA device of this index (negative: the first operand is on none)."""
+    if (t.dtype is dtype and t.get_device() == device >= 0 and t.shape == shape
+            and t.is_contiguous()):
         return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape "
-                     f"{tuple(shape)}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+    raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}"
+                     f"{f' on cuda:{device} like the first operand' if device >= 0 else ''}, got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}"
                      f"{'' if t.is_contiguous() else ', not contiguous'}")
 
 
@@ -326,6 +339,7 @@ def moe_add_rmsnorm_fp8(x, residual, weight, eps: float = 1e-6, gemma: bool = Fa
     if x.dim() != 2:
         _matrix(x, "x")
     shape = N, H = x.shape
+    dev = x.get_device()
     if residual_out is None:
         residual_out = residual
     if q is None:
@@ -335,13 +349,13 @@ def moe_add_rmsnorm_fp8(x, residual, weight, eps: float = 1e-6, gemma: bool = Fa
     if normed is None and want_normed:
         normed = torch.empty(shape, dtype=_BF16, device=x.device)
     status = lib().moe_add_rmsnorm_fp8(
-        _typed(x, "x", _BF16, shape),
-        None if residual is None else _typed(residual, "residual", _BF16, shape),
-        _typed(weight, "weight", _BF16, (H,)), N, H, eps, bool(gemma),
-        None if residual_out is None else _typed(residual_out, "residual_out", _BF16, shape),
-        _typed(q, "q", _E4M3, shape), _typed(scale, "scale", _F32, (N,)),
-        None if normed is None else _typed(normed, "normed", _BF16, shape),
-        _stream_of(x.get_device()))
+        _typed(x, "x", _BF16, shape, dev),
+        None if residual is None else _typed(residual, "residual", _BF16, shape, dev),
+        _typed(weight, "weight", _BF16, (H,), dev), N, H, eps, bool(gemma),
+        None if residual_out is None else _typed(residual_out, "residual_out", _BF16, shape, dev),
+        _typed(q, "q", _E4M3, shape, dev), _typed(scale, "scale", _F32, (N,), dev),
+        None if normed is None else _typed(normed, "normed", _BF16, shape, dev),
+        _stream_of(dev))
     if status:
         _check(status, "moe_add_rmsnorm_fp8")
     return q, scale, normed
@@ -353,13 +367,14 @@ def moe_quantize_fp8(x, q=None, scale=None):
     if x.dim() != 2:
         _matrix(x, "x")
     shape = N, H = x.shape
+    dev = x.get_device()
     if q is None:
         q = torch.empty(shape, dtype=_E4M3, device=x.device)
     if scale is None:
         scale = torch.empty(N, dtype=_F32, device=x.device)
-    status = lib().moe_quantize_fp8(_typed(x, "x", _BF16, shape), N, H,
-                                    _typed(q, "q", _E4M3, shape),
-                                    _typed(scale, "scale", _F32, (N,)), _stream_of(x.get_device()))
+    status = lib().moe_quantize_fp8(_typed(x, "x", _BF16, shape, dev), N, H,
+                                    _typed(q, "q", _E4M3, shape, dev),
+                                    _typed(scale, "scale", _F32, (N,), dev), _stream_of(dev))
     if status:
         _check(status, "moe_quantize_fp8")
     return q, scale
@@ -381,33 +396,35 @@ def moe_linear(x, weight, bias=None, residual=None, activation: str = "none", x_
         _matrix(weight, "weight")
     N, K = x.shape
     O = weight.shape[0]
+    dev = x.get_device()
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
     if out is None:
         out = torch.empty((N, O), dtype=out_dtype, device=x.device)
     fp32 = out.dtype is _F32
-    b = None if bias is None else _typed(bias, "bias", _BF16, (O,))
-    r = None if residual is None else _typed(residual, "residual", _BF16, (N, O))
+    b = None if bias is None else _typed(bias, "bias", _BF16, (O,), dev)
+    r = None if residual is None else _typed(residual, "residual", _BF16, (N, O), dev)
     ws, bytes_ = None, 0
     if workspace is not None:
         bytes_ = workspace.numel()
-        ws = _typed(workspace, "workspace", torch.uint8, (bytes_,))
+        ws = _typed(workspace, "workspace", torch.uint8, (bytes_,), dev)
     if x.dtype is _E4M3:
         if x_scale is None or w_scale is None:
             raise ValueError("e4m3 operands need x_scale and w_scale")
         status = lib().moe_linear_fp8(
-            _typed(x, "x", _E4M3, (N, K)), _typed(x_scale, "x_scale", _F32, (N,)),
-            _typed(weight, "weight", _E4M3, (O, K)), _typed(w_scale, "w_scale", _F32, (O,)), b, r,
-            N, K, O, act, _typed(out, "out", _F32 if fp32 else _BF16, (N, O)), fp32, ws, bytes_,
-            _stream_of(x.get_device()))
+            _typed(x, "x", _E4M3, (N, K), dev), _typed(x_scale, "x_scale", _F32, (N,), dev),
+            _typed(weight, "weight", _E4M3, (O, K), dev),
+            _typed(w_scale, "w_scale", _F32, (O,), dev), b, r, N, K, O, act,
+            _typed(out, "out", _F32 if fp32 else _BF16, (N, O), dev), fp32, ws, bytes_,
+            _stream_of(dev))
     else:
         if x_scale is not None or w_scale is not None:
             raise ValueError("x_scale and w_scale belong to e4m3 operands")
         status = lib().moe_linear(
-            _typed(x, "x", _BF16, (N, K)), _typed(weight, "weight", _BF16, (O, K)), b, r, N, K, O,
-            act, _typed(out, "out", _F32 if fp32 else _BF16, (N, O)), fp32, ws, bytes_,
-            _stream_of(x.get_device()))
+            _typed(x, "x", _BF16, (N, K), dev), _typed(weight, "weight", _BF16, (O, K), dev), b, r,
+            N, K, O, act, _typed(out, "out", _F32 if fp32 else _BF16, (N, O), dev), fp32, ws,
+            bytes_, _stream_of(dev))
     if status:
         _check(status, "moe_linear_fp8" if x.dtype is _E4M3 else "moe_linear")
     return out
@@ -418,19 +435,19 @@ def _balance_workspace_bytes(N, E):
     return max(lib().moe_balance_loss_workspace_bytes(N, E), 256)
 
 
-def _logits(logits):
+def _logits(logits, dev):
     dtype = logits.dtype
     if dtype is not _F32 and dtype is not _BF16:
         raise ValueError(f"logits must be fp32 or bf16, got {dtype}")
     if logits.dim() != 2:
         _matrix(logits, "logits")
-    return dtype is _BF16, _typed(logits, "logits", dtype, logits.shape)
+    return dtype is _BF16, _typed(logits, "logits", dtype, logits.shape, dev)
 
 
-def _mask(mask, N):
+def _mask(mask, N, dev=-1):
     if mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
         raise ValueError(f"mask must be bool or uint8, got {mask.dtype}")
-    return _typed(mask, "mask", mask.dtype, (N,))
+    return _typed(mask, "mask", mask.dtype, (N,), dev)
 
 
 def moe_balance_loss(logits, topk_ids, mask=None, losses=None, counts=None, tokens=None,
@@ -441,7 +458,8 @@ def moe_balance_loss(logits, topk_ids, mask=None, losses=None, counts=None, toke
     (bool [N], optional) leaves tokens out, a negative id is a dropped slot.
     ``workspace`` (uint8 CUDA tensor, optional) receives the status word of
     moe_read_device_status."""
-    bf16, lp = _logits(logits)
+    dev = logits.get_device()
+    bf16, lp = _logits(logits, dev)
     N, E = logits.shape
     if topk_ids.dim() != 2:
         _matrix(topk_ids, "topk_ids")
@@ -458,12 +476,12 @@ def moe_balance_loss(logits, topk_ids, mask=None, losses=None, counts=None, toke
     ws, bytes_ = None, 0
     if workspace is not None:
         bytes_ = workspace.numel()
-        ws = _typed(workspace, "workspace", torch.uint8, (bytes_,))
+        ws = _typed(workspace, "workspace", torch.uint8, (bytes_,), dev)
     status = lib().moe_balance_loss(
-        lp, bf16, _typed(topk_ids, "topk_ids", _I32, (N, k)),
-        None if mask is None else _mask(mask, N), N, E, k, _typed(losses, "losses", _F32, (2,)),
-        _typed(counts, "counts", _I32, (E,)), _typed(tokens, "tokens", _I32, (1,)), ws, bytes_,
-        _stream_of(logits.get_device()))
+        lp, bf16, _typed(topk_ids, "topk_ids", _I32, (N, k), dev),
+        None if mask is None else _mask(mask, N, dev), N, E, k,
+        _typed(losses, "losses", _F32, (2,), dev), _typed(counts, "counts", _I32, (E,), dev),
+        _typed(tokens, "tokens", _I32, (1,), dev), ws, bytes_, _stream_of(dev))
     if status:
         _check(status, "moe_balance_loss")
     return losses, counts, tokens
@@ -473,14 +491,16 @@ def moe_balance_loss_backward(logits, counts, tokens, k: int, grad, mask=None, d
     """Gradient of grad[0] * losses[0] + grad[1] * losses[1] (grad fp32 [2] on
     the device) with respect to the logits, in their type; counts, tokens, k
     and mask as in the forward call."""
-    bf16, lp = _logits(logits)
+    dev = logits.get_device()
+    bf16, lp = _logits(logits, dev)
     N, E = logits.shape
     if dlogits is None:
         dlogits = torch.empty_like(logits)
     status = lib().moe_balance_loss_backward(
-        lp, bf16, _typed(counts, "counts", _I32, (E,)), _typed(tokens, "tokens", _I32, (1,)),
-        None if mask is None else _mask(mask, N), _typed(grad, "grad", _F32, (2,)), N, E, k,
-        _typed(dlogits, "dlogits", logits.dtype, (N, E)), _stream_of(logits.get_device()))
+        lp, bf16, _typed(counts, "counts", _I32, (E,), dev),
+        _typed(tokens, "tokens", _I32, (1,), dev), None if mask is None else _mask(mask, N, dev),
+        _typed(grad, "grad", _F32, (2,), dev), N, E, k,
+        _typed(dlogits, "dlogits", logits.dtype, (N, E), dev), _stream_of(dev))
     if status:
         _check(status, "moe_balance_loss_backward")
     return dlogits
