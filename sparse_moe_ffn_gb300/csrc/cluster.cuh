@@ -14,10 +14,19 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
     return r;
 }
 
-// All threads of the cluster; the lanes of a warp need not arrive together.
+// The barrier of all threads of the cluster, in two steps or one; the lanes of
+// a warp need not come together to either.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 __device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release;\n\t"
-                 "barrier.cluster.wait.acquire;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 // Address of this CTA's shared variable in CTA `rank` of the cluster.

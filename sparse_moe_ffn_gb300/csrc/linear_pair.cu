@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const int mine = o0 + c + lane < a.O ? rows : 0;
                 uint16_t turned[kTurn];
                 if (!vec && a.residual) load_turned(a, at, mine, turned);
+                __syncwarp();  // TMEM wants whole warps
                 tmem_load32(taddr + c, v);
                 tmem_load_wait();
 #pragma unroll
@@ -463,6 +464,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     cluster_barrier();  // both CTAs are done with TMEM and each other's barriers
     if (warp == 1) {
         tc_fence_after_sync();
+        __syncwarp();
         tmem_dealloc_2cta(tmem, 2 * kBN);
     }
 }

@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     __syncthreads();
     // the cluster's CTAs have all started before any of them is written to;
     // waited for where the partial sums leave
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    cluster_arrive();
     tc_fence_after_sync();
     const uint32_t tmem = sm->tmem_base;
     volatile int *abort_flag = &sm->abort_flag;
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
             record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
             *abort_flag = 1;
         }
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        cluster_wait();
         if (ok) {
             tc_fence_after_sync();
             const int quarter = warp % 4;
@@ -312,7 +312,9 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
 #pragma unroll 1
             for (int c = warp / 4 * kChunk; c < tokens; c += kSplitThreads / 128 * kChunk) {
                 float v[32];
-                tmem_load32(taddr + c, v);  // a tile of 16 tokens has 32 columns allocated
+                // a tile of 16 tokens has 32 columns allocated; TMEM wants whole warps
+                __syncwarp();
+                tmem_load32(taddr + c, v);
                 tmem_load_wait();
 #pragma unroll
                 for (int i = 0; i < kChunk; ++i) {
@@ -334,6 +336,7 @@ __global__ void __launch_bounds__(kSplitThreads, 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
+        __syncwarp();
         tmem_dealloc(tmem, T::kCols);
     }
 }
