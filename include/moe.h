@@ -657,6 +657,11 @@ moe_status_t moe_read_device_status(const void *workspace, cudaStream_t stream);
 moe_status_t moe_selftest_wait_timeout(void *workspace, size_t workspace_bytes,
                                        uint64_t limit_ns, cudaStream_t stream);
 
+/* Self-check (not part of the layer): while `only` is non-zero, moe_balance_loss
+ * keeps to clusters of 8 blocks, as it does by itself on a device without room
+ * for 16 (a partition of a GPU). */
+void moe_selftest_portable_clusters(int only);
+
 /* -------------------------------------------------------------------------
  * Instrumentation
  * ---------------------------------------------------------------------- */

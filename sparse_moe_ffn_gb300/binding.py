@@ -83,6 +83,7 @@ def lib():
         "moe_kernel_launch_count": ([], ctypes.c_uint64),
         "moe_set_stage_events": ([P, i32], i32),
         "moe_selftest_wait_timeout": ([P, sz, ctypes.c_uint64, P], i32),
+        "moe_selftest_portable_clusters": ([i32], None),
         "moe_align_noalloc": ([P, i64, i32, i32, i32, P, P, P, P, P, P, P], i32),
         "moe_dense_mlp_workspace_bytes": ([i64, i32, i32], sz),
         "moe_add_rmsnorm": ([P, P, P, i64, i32, ctypes.c_float, i32, P, P], i32),

@@ -1674,6 +1674,8 @@ moe_status_t moe_dense_mlp_prepared(const moe_bf16_t *x, const moe_bf16_t *w_gat
                           workspace_bytes, stream);
 }
 
+void moe_selftest_portable_clusters(int only) { balance_portable_clusters(only != 0); }
+
 moe_status_t moe_selftest_wait_timeout(void *workspace, size_t workspace_bytes,
                                        uint64_t limit_ns, cudaStream_t stream) {
     g_last_error.clear();

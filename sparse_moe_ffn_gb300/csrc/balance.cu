@@ -27,6 +27,7 @@
 // 21.5); 64 x 128 forward 4.7 us, latency.
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "block_ops.cuh"
@@ -671,6 +672,36 @@ int lanes_of(int E) {
     return lanes;
 }
 
+std::atomic<bool> g_portable_only{false};
+
+// Whether the device has room for a cluster of 16 blocks of this kernel, which
+// no device promises (one that is partitioned may not have it); asked once a
+// device, as the kernels that come here take the same threads and registers.
+bool room_for_16(const void *kernel) {
+    static std::atomic<uint64_t> asked{0}, room{0};
+    if (g_portable_only.load(std::memory_order_relaxed)) return false;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (asked.load(std::memory_order_acquire) & bit)
+        return room.load(std::memory_order_relaxed) & bit;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 16;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(kAloneThreads);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const bool fits = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0;
+    if (!fits) cudaGetLastError();  // an answer, not an error of a later call
+    if (fits) room.fetch_or(bit, std::memory_order_relaxed);
+    asked.fetch_or(bit, std::memory_order_release);
+    return fits;
+}
+
 // Rows are read four values at a time when every row starts on such a
 // boundary (E a multiple of 4, the arrays aligned), else one at a time.
 template <Pass kPass>
@@ -683,10 +714,12 @@ cudaError_t launch(const BalanceArgs &a, int blocks, cudaStream_t s) {
         a.bf16 ? (vec ? kernel_of<kPass, true, true>(lanes) : kernel_of<kPass, true, false>(lanes))
                : (vec ? kernel_of<kPass, false, true>(lanes)
                       : kernel_of<kPass, false, false>(lanes));
-    if (kPass == kAlone16) {  // clusters of more than 8 have to be asked for
-        cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k),
-                                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if constexpr (kPass == kAlone16) {  // clusters of more than 8 have to be asked for
+        const void *f = reinterpret_cast<const void *>(k);
+        cudaError_t e =
+            cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
+        if (!room_for_16(f)) return launch<kAlone8>(a, 8, s);  // in more passes
     }
     constexpr bool kAlone = kPass == kAlone8 || kPass == kAlone16;
     constexpr unsigned kCluster = kPass == kGrad      ? 1
@@ -712,6 +745,8 @@ int balance_clusters(int64_t N, int E) {
     const int64_t c = (N + rows - 1) / rows;
     return static_cast<int>(c < kBalanceMaxClusters ? c : kBalanceMaxClusters);
 }
+
+void balance_portable_clusters(bool only) { g_portable_only = only; }
 
 cudaError_t launch_balance(const BalanceArgs &a, int *launches, cudaStream_t s) {
     *launches = a.clusters > 1 ? 2 : 1;

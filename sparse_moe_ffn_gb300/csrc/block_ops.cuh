@@ -80,6 +80,8 @@ struct BalanceArgs {
 };
 
 int balance_clusters(int64_t N, int E);
+// Whether clusters stay at the 8 blocks that every device has room for.
+void balance_portable_clusters(bool only);
 cudaError_t launch_balance(const BalanceArgs &a, int *launches, cudaStream_t s);
 cudaError_t launch_balance_backward(const BalanceArgs &a, int num_sms, cudaStream_t s);
 
