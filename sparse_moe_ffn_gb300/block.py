@@ -67,7 +67,10 @@ def router_step(normed, router, k: int, balance_weight: float = 0.01, z_weight: 
     losses, counts, tokens = binding.moe_balance_loss(logits, ids, mask)
     grad = torch.tensor([balance_weight, z_weight], dtype=torch.float32, device=normed.device)
     dlogits = binding.moe_balance_loss_backward(logits, counts, tokens, k, grad, mask)
-    return losses, counts, dlogits.t() @ normed.float()
+    hidden = normed.float()
+    if mask is not None:  # whatever a token left out holds: 0 * NaN is NaN
+        hidden = hidden.masked_fill(mask.logical_not()[:, None], 0)
+    return losses, counts, dlogits.t() @ hidden
 
 
 def main(N: int = 2048, H: int = 512, E: int = 32, k: int = 4, I: int = 256, steps: int = 60):
