@@ -517,9 +517,11 @@ moe_status_t moe_quantize_fp8(const moe_bf16_t *x, int64_t N, int H, moe_e4m3_t 
  *   workspace >= moe_linear_workspace_bytes() bytes, or NULL (then device
  *            failures are not recorded)
  * Precision: products and sums in fp32 on the tensor cores, the epilogue in
- * fp32, one rounding of out.  An output depends on its own token and weight
- * row alone, and the same call gives the same bits; the sizes and the outputs'
- * alignment choose the tiling, and with it the order of the fp32 sum.
+ * fp32 with SiLU and both GELUs within 2^-20 |v| (their exponentials, quotients
+ * and erf are approximations), one rounding of out.  An output depends on its
+ * own token and weight row alone, and the same call gives the same bits; the
+ * sizes and the outputs' alignment choose the tiling, and with it the order of
+ * the fp32 sum.
  * Limits: K % 8 == 0 (bf16) or K % 16 == 0 (e4m3), any O >= 1, each size
  * <= 2^31 - 512; x, weight 16-byte aligned; scales, bias, residual and out
  * aligned to their types.
@@ -567,8 +569,10 @@ moe_status_t moe_linear_fp8(const moe_e4m3_t *x, const float *x_scale, const moe
  *            word alone): then device failures are not recorded
  * A token whose logits are all -inf has p = 0 and lse = 0, gradient 0, and
  * counts in T.  Without tokens (T = 0, N = 0) the losses, counts and
- * gradients are 0.  The sums over tokens have a fixed order: the same inputs
- * give the same bits.  Limits: 1 <= k <= E <= 256, N * k < 2^31.
+ * gradients are 0.  Precision: softmax, sums and losses in fp32 (losses[1] is
+ * infinite where the sum of lse^2 passes 3.4e38).  The sums over tokens have a
+ * fixed order: the same inputs give the same bits on the same device.  Limits:
+ * 1 <= k <= E <= 256, N * k < 2^31.
  * ---------------------------------------------------------------------- */
 size_t moe_balance_loss_workspace_bytes(int64_t N, int E);
 moe_status_t moe_balance_loss(const void *logits, int logits_bf16, const int32_t *topk_ids,

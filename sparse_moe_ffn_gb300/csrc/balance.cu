@@ -19,12 +19,15 @@
 // that covers E), four rows at a time; sums over tokens run in registers, then
 // per block, per cluster of blocks (distributed shared memory) and, when
 // there is more than one cluster, in a second kernel: each in a fixed order,
-// with no atomics on floats, so the same inputs give the same bits.
+// with no atomics on floats, so the same inputs give the same bits.  All sums
+// are fp32; the joins of P and the long sums of a lane (kFoldPasses) keep what
+// each addition rounds off.
 //
-// What bounds it: 131072 x 128 in fp32, forward 20.0 us (71 MB, 3570 GB/s: eight
-// dependent steps of shuffles and exponentials a row; rows are read one pass
-// ahead), gradient 25.5 us (134 MB, 5270 GB/s; a plain copy of the same bytes
-// 21.5); 64 x 128 forward 4.7 us, latency.
+// What bounds it: 131072 x 128 in fp32, forward 20.0 us (71 MB, 3570 GB/s), of
+// which 8 us are the two kernels' starts and joins: eight times the rows take
+// 109 us, 5600 GB/s for those added (rows are read one pass ahead); gradient 25.5
+// us (134 MB, 5270 GB/s; a plain copy of the same bytes 21.5); 64 x 128 forward
+// 4.6 us, latency.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -197,8 +200,9 @@ __device__ __forceinline__ void rows_sum(float (&v)[kUnroll]) {
         for (int u = 0; u < kUnroll; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], d);
 }
 
-// 2^x, 1/x and log2 x in one instruction each (off by two steps at most, and
-// below 2^-126 it is 0): softmax spends its time on these.
+// 2^x in one instruction (off by two steps at most, and below 2^-126 it is 0);
+// softmax spends its time on this, and takes 1/x and log2 x in the same way (off
+// by two steps; log2 near 1 by 2^-22).
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -735,10 +739,12 @@ int64_t rows_per_block(int E, int threads) { return threads / lanes_of(E) * kUnr
 }  // namespace
 
 // One cluster does small batches on its own, of 8 blocks for one pass and of 16
-// for up to three: two passes take less than the second kernel (2048 x 128: 5.8
-// against 6.2 us, 3000 x 60: 5.5 against 6.0), a third at most 1.5 us more (6144
-// x 128: 8.7 against 7.2), and the host saves a launch and the workspace (9 us
-// of 24 for a forward and backward call).
+// for up to three.  One pass of 16 takes less than several clusters and the
+// second kernel (2048 x 128: 5.7 against 5.9 us, 3000 x 60 in bf16 5.5 against
+// 5.7).  Two take up to 0.8 us more (4000 x 128: 7.1 against 6.3; 4099 x 60 6.0
+// against 6.2), three 1.7 (6144 x 128: 8.6 against 6.9; 98304 x 8, the most
+// tokens: 11.3 against 7.6), but a call from Python saves a launch and the
+// workspace (9 us of 24 forward and backward).  A captured graph saves neither.
 int balance_clusters(int64_t N, int E) {
     if (N <= 3 * 16 * rows_per_block(E, kAloneThreads)) return 1;
     const int64_t rows = kBalanceCluster * rows_per_block(E, kThreads);

@@ -1,4 +1,5 @@
-// linear_epilogue.cuh -- the activations of moe_linear, in fp32.
+// linear_epilogue.cuh -- the activations of moe_linear, in fp32: each within
+// 2^-20 |v| of its formula.
 #pragma once
 
 #include <cuda_bf16.h>

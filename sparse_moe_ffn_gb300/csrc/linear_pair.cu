@@ -31,8 +31,10 @@
 // bf16 onto a residual: 174 us, 1580 TFLOP/s (256 tiles are 3.4 waves of 76
 // pairs and take 4); 8192 x 2048 x 8192 in e4m3 with bias and SiLU: 92 us, 3000
 // TFLOP/s, of which the epilogue's shared-memory and store traffic costs the
-// MMAs about 15 us.  Bare products in bf16 run at 0.93 to 0.97 of the library's
-// rate.  Tried and not kept: 16 epilogue warps (6% fewer cycles in e4m3, the
+// MMAs about 15 us.  Bare products in bf16 run at 0.92 to 0.97 of the library's
+// rate, 0.85 at 2048 x 2048 x 2048.  Rows of the output that start on no 16
+// bytes leave two bytes a lane and are far from any bound: 4096 x 512 x 4001 in
+// e4m3 onto a residual 65 us, 10 for its bytes.  Tried and not kept: 16 epilogue warps (6% fewer cycles in e4m3, the
 // same time), four or six stages, 128 outputs a tile where 256 fill the SMs.
 // Every wait is bounded; a CTA that gives up records MOE_ERR_DEVICE_TIMEOUT.
 #include "linear_epilogue.cuh"

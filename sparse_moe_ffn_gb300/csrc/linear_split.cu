@@ -19,8 +19,10 @@
 //           before the accumulator is waited for
 //
 // What bounds it, measured on a GB300: latency (launch, first TMA copy, cluster
-// barrier: about 3.5 us) and then the weights' bytes.  One token through 8192 x
-// 2048 in e4m3 (16.8 MB): 5.0 us, 3365 GB/s; 64 x 2048 x 128 in bf16 to fp32: 3.8
+// barrier: about 3.5 us) and then the weights' bytes, one CTA an SM (a tile's
+// stages fill its shared memory).  One token of 2048 values to 8192 outputs in
+// e4m3 (16.8 MB): 5.0 us, 3365 GB/s, 128 CTAs on 152 SMs; one of 8192 to 2048 in
+// bf16 (33.6 MB): 9.5 us, 3500 GB/s; 64 x 2048 x 128 in bf16 to fp32: 3.8
 // us; 333 x 1000 x 1111 in bf16 with gelu onto a residual, stores of
 // single values: 7.5 us (1112 outputs, in vectors: 6.5).
 // Every wait is bounded; a CTA that gives up records MOE_ERR_DEVICE_TIMEOUT

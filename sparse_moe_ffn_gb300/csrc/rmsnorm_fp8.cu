@@ -10,9 +10,10 @@
 // One pass over the row: with inv = 1 / sqrt(mean(r^2) + eps) the largest |y|
 // is inv * amax|r w|, so the sum of squares and amax|r w| go through one
 // reduction, and q = e4m3(r w * (inv / scale)) needs nothing else.  The row
-// stays in registers as packed bf16 (r is bf16, so nothing is lost), the gain
-// is read once a thread.  The reduction's maximum passes NaN on, so that a row
-// with a NaN or an infinity gets a NaN scale and not a plausible one.
+// stays in registers as packed bf16 (r is bf16, so nothing is lost; with the
+// norm, rows over 16384 values spill 76 bytes a thread and over 32768 464), the
+// gain is read once a thread.  The reduction's maximum passes NaN on, so that a
+// row with a NaN or an infinity gets a NaN scale and not a plausible one.
 //
 // What bounds it: memory.  9 bytes an element with residual, sum and bf16 output
 // (3 without the norm): 8192 x 2048 takes 24.3 us, 6220 GB/s (a plain copy of
@@ -210,8 +211,9 @@ cudaError_t launch_rows(const RowArgs &a, int num_sms, cudaStream_t s) {
 // chunk a thread, that is the shortest path; beyond it (by about 200000 chunks
 // for the norm, 100000 without it) fewer threads a row, two or four chunks each,
 // keep more bytes in flight between the reductions: 8192 x 2048, norm 27.1
-// -> 25.1 us and plain 11.3 -> 9.6 (in a loop, as fits at once); 64 x 2048 the other way, 2.1 against 2.3 and
-// 1.5 against 1.9.  Rows over 2048 take two or four chunks a thread in any case.
+// -> 25.1 us and plain 11.3 -> 9.6 (in a loop, as fits at once); 64 x 2048 the
+// other way, 2.1 against 2.3 and 1.5 against 1.9.  Rows over 2048 take two or
+// four chunks a thread in any case, over 32768 eight.
 template <bool kNorm>
 cudaError_t launch_any(const RowArgs &a, int num_sms, cudaStream_t s) {
     const int groups = a.H / 8;
