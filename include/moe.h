@@ -608,6 +608,53 @@ moe_status_t moe_dense_mlp_prepared(const moe_bf16_t *x, const moe_bf16_t *w_gat
                                     void *workspace, size_t workspace_bytes,
                                     cudaStream_t stream);
 
+/* -------------------------------------------------------------------------
+ * moe_gated_ffn, moe_gated_ffn_backward -- a dense layer's gated feed-forward
+ * block with any of the activations, and its backward pass:
+ *   gate = x Wg^T, up = x Wu^T, h = act(gate) * up
+ *   out  = h Wd^T + residual
+ * and, for the gradient dout of out,
+ *   dh  = dout Wd, dgate = dh * up * act'(gate), dup = dh * act(gate)
+ *   dx  = dgate Wg + dup Wu
+ *   dWg = dgate^T x, dWu = dup^T x, dWd = dout^T h
+ * (the residual's gradient is dout itself; act'(0) of ReLU is 0).
+ *
+ *   x, out   [N, H] bf16     w_gate, w_up [I, H] bf16     w_down [H, I] bf16
+ *   residual [N, H] bf16 or NULL
+ *   act      a moe_activation_t
+ *   gate, up [N, I] bf16: both NULL, or both written by the forward call and
+ *            given to the backward call
+ *   dout, dx [N, H] bf16; dx may be NULL (not wanted)
+ *   dw_gate, dw_up [I, H], dw_down [H, I] bf16 out: all or none NULL
+ *   workspace >= the *_workspace_bytes of the sizes (on the device of the
+ *            call), 256-byte aligned; its status word as everywhere.  Neither
+ *            call needs what an earlier one left in it.
+ * out may be residual itself; no other output may overlap an input or another
+ * output.  With N = 0 the weights' gradients are 0.
+ * Precision: products and sums in fp32 on the tensor cores; gate, up, dgate, dup
+ * and h are rounded to bf16 once each (they are operands of the next product,
+ * or kept), each output once.  h comes from the unrounded gate and up in the
+ * forward call, from the kept ones in the backward call.  The activations and
+ * their slopes are within 2^-20 of |v| and of 1.  The sums have a fixed order:
+ * the same call gives the same bits on the same device; the sizes choose the
+ * tiling, and with it that order.
+ * Limits: H % 8 == 0, I % 8 == 0, every array 16-byte aligned, sizes below
+ * 2^30 (and 2^30 tiles of 128 x 128 in any of the matrices).
+ * ---------------------------------------------------------------------- */
+size_t moe_gated_ffn_workspace_bytes(int64_t N, int H, int I);
+moe_status_t moe_gated_ffn(const moe_bf16_t *x, const moe_bf16_t *w_gate, const moe_bf16_t *w_up,
+                           const moe_bf16_t *w_down, const moe_bf16_t *residual, int64_t N, int H,
+                           int I, int act, moe_bf16_t *gate, moe_bf16_t *up, moe_bf16_t *out,
+                           void *workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t moe_gated_ffn_backward_workspace_bytes(int64_t N, int H, int I);
+moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
+                                    const moe_bf16_t *w_gate, const moe_bf16_t *w_up,
+                                    const moe_bf16_t *w_down, const moe_bf16_t *gate,
+                                    const moe_bf16_t *up, int64_t N, int H, int I, int act,
+                                    moe_bf16_t *dx, moe_bf16_t *dw_gate, moe_bf16_t *dw_up,
+                                    moe_bf16_t *dw_down, void *workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+
 /* Byte offsets of moe_forward's workspace sub-buffers (for inspecting the
  * intermediate results; every offset is 256-byte aligned).
  *

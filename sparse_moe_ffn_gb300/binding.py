@@ -95,6 +95,10 @@ def lib():
         "moe_balance_loss_workspace_bytes": ([i64, i32], sz),
         "moe_balance_loss": ([P, i32, P, P, i64, i32, i32, P, P, P, P, sz, P], i32),
         "moe_balance_loss_backward": ([P, i32, P, P, P, P, i64, i32, i32, P, P], i32),
+        "moe_gated_ffn_workspace_bytes": ([i64, i32, i32], sz),
+        "moe_gated_ffn": ([P] * 5 + [i64, i32, i32, i32, P, P, P, P, sz, P], i32),
+        "moe_gated_ffn_backward_workspace_bytes": ([i64, i32, i32], sz),
+        "moe_gated_ffn_backward": ([P] * 7 + [i64, i32, i32, i32] + [P] * 5 + [sz, P], i32),
         "moe_dense_mlp": ([P, P, P, P, i64, i32, i32, P, P, sz, P], i32),
         "moe_dense_mlp_prepared": ([P, P, P, P, i64, i32, i32, P, P, sz, P], i32),
     }
@@ -505,6 +509,108 @@ def moe_balance_loss_backward(logits, counts, tokens, k: int, grad, mask=None, d
     if status:
         _check(status, "moe_balance_loss_backward")
     return dlogits
+
+
+def _activation(name):
+    act = ACTIVATIONS.get(name)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {name!r}")
+    return act
+
+
+def moe_gated_ffn_workspace_bytes(N, H, I) -> int:
+    return int(lib().moe_gated_ffn_workspace_bytes(N, H, I))
+
+
+def moe_gated_ffn_backward_workspace_bytes(N, H, I) -> int:
+    return int(lib().moe_gated_ffn_backward_workspace_bytes(N, H, I))
+
+
+def _scratch(workspace, need, device, dev):
+    """(pointer, bytes) of the workspace, one of `need` bytes if there is none."""
+    if workspace is None:
+        workspace = torch.empty(max(need(), 256), dtype=torch.uint8, device=device)
+    bytes_ = workspace.numel()
+    return workspace, _typed(workspace, "workspace", torch.uint8, (bytes_,), dev), bytes_
+
+
+def moe_gated_ffn(x, w_gate, w_up, w_down, activation: str = "silu", residual=None, gate=None,
+                  up=None, out=None, keep: bool = False, workspace=None):
+    """(act(x Wg^T) * (x Wu^T)) Wd^T + residual: returns (out [N, H], gate, up).
+    gate and up [N, I] are what moe_gated_ffn_backward needs; they are stored
+    with ``keep`` or where tensors for them are given, else None.  x [N, H],
+    w_gate and w_up [I, H], w_down [H, I], all bf16."""
+    if x.dim() != 2:
+        _matrix(x, "x")
+    if w_gate.dim() != 2:
+        _matrix(w_gate, "w_gate")
+    shape = N, H = x.shape
+    I = w_gate.shape[0]
+    dev = x.get_device()
+    act = _activation(activation)
+    if keep or gate is not None or up is not None:
+        if gate is None:
+            gate = torch.empty((N, I), dtype=_BF16, device=x.device)
+        if up is None:
+            up = torch.empty((N, I), dtype=_BF16, device=x.device)
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=x.device)
+    xp = _typed(x, "x", _BF16, shape, dev)
+    weights = (_typed(w_gate, "w_gate", _BF16, (I, H), dev),
+               _typed(w_up, "w_up", _BF16, (I, H), dev),
+               _typed(w_down, "w_down", _BF16, (H, I), dev))
+    rp = None if residual is None else _typed(residual, "residual", _BF16, shape, dev)
+    gp = None if gate is None else _typed(gate, "gate", _BF16, (N, I), dev)
+    upp = None if up is None else _typed(up, "up", _BF16, (N, I), dev)
+    op = _typed(out, "out", _BF16, shape, dev)
+    stream = _stream_of(dev)
+    workspace, ws, bytes_ = _scratch(
+        workspace, lambda: lib().moe_gated_ffn_workspace_bytes(N, H, I), x.device, dev)
+    status = lib().moe_gated_ffn(xp, *weights, rp, N, H, I, act, gp, upp, op, ws, bytes_, stream)
+    if status:
+        _check(status, "moe_gated_ffn")
+    return out, gate, up
+
+
+def moe_gated_ffn_backward(dout, x, w_gate, w_up, w_down, gate, up, activation: str = "silu",
+                           dx=None, dw_gate=None, dw_up=None, dw_down=None,
+                           want_dx: bool = True, want_dw: bool = True, workspace=None):
+    """The gradients (dx, dw_gate, dw_up, dw_down) for the gradient dout of
+    moe_gated_ffn's out, with the gate and up that it kept; those not wanted are
+    None (the residual's gradient is dout itself)."""
+    if x.dim() != 2:
+        _matrix(x, "x")
+    if w_gate.dim() != 2:
+        _matrix(w_gate, "w_gate")
+    shape = N, H = x.shape
+    I = w_gate.shape[0]
+    dev = x.get_device()
+    act = _activation(activation)
+    if dx is None and want_dx:
+        dx = torch.empty(shape, dtype=_BF16, device=x.device)
+    if want_dw:
+        if dw_gate is None:
+            dw_gate = torch.empty((I, H), dtype=_BF16, device=x.device)
+        if dw_up is None:
+            dw_up = torch.empty((I, H), dtype=_BF16, device=x.device)
+        if dw_down is None:
+            dw_down = torch.empty((H, I), dtype=_BF16, device=x.device)
+    inputs = (_typed(dout, "dout", _BF16, shape, dev), _typed(x, "x", _BF16, shape, dev),
+              _typed(w_gate, "w_gate", _BF16, (I, H), dev),
+              _typed(w_up, "w_up", _BF16, (I, H), dev),
+              _typed(w_down, "w_down", _BF16, (H, I), dev),
+              _typed(gate, "gate", _BF16, (N, I), dev), _typed(up, "up", _BF16, (N, I), dev))
+    outputs = (None if dx is None else _typed(dx, "dx", _BF16, shape, dev),
+               None if dw_gate is None else _typed(dw_gate, "dw_gate", _BF16, (I, H), dev),
+               None if dw_up is None else _typed(dw_up, "dw_up", _BF16, (I, H), dev),
+               None if dw_down is None else _typed(dw_down, "dw_down", _BF16, (H, I), dev))
+    stream = _stream_of(dev)
+    workspace, ws, bytes_ = _scratch(
+        workspace, lambda: lib().moe_gated_ffn_backward_workspace_bytes(N, H, I), x.device, dev)
+    status = lib().moe_gated_ffn_backward(*inputs, N, H, I, act, *outputs, ws, bytes_, stream)
+    if status:
+        _check(status, "moe_gated_ffn_backward")
+    return dx, dw_gate, dw_up, dw_down
 
 
 def moe_dense_mlp(x, w_gate, w_up, w_down, out=None, workspace=None):

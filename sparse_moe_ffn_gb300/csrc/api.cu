@@ -14,6 +14,7 @@
 #include <string>
 
 #include "block_ops.cuh"
+#include "gated_ffn.cuh"
 #include "kernels.cuh"
 #include "linear_gemm.cuh"
 #include "moe.h"
@@ -1540,6 +1541,235 @@ moe_status_t moe_balance_loss_backward(const void *logits, int logits_bf16,
     MOE_CUDA(launch_balance_backward(a, num_sms_of_current_device(), stream),
              "balance backward kernel launch");
     g_launches += 1;
+    return MOE_OK;
+}
+
+// ------------------------------------------- gated feed-forward block
+
+namespace {
+
+constexpr int64_t kFfnMost = (int64_t(1) << 30) - 512;
+
+moe_status_t check_ffn(int64_t N, int H, int I, int act) {
+    if (N < 0) return fail(MOE_ERR_INVALID_ARG, "N must be >= 0 (got %lld)", (long long)N);
+    if (H < 8 || H % 8 || I < 8 || I % 8)
+        return fail(MOE_ERR_INVALID_ARG, "H and I must be positive multiples of 8 (H=%d, I=%d)",
+                    H, I);
+    if (act < MOE_ACT_NONE || act > MOE_ACT_RELU)
+        return fail(MOE_ERR_INVALID_ARG, "unknown activation %d", act);
+    // tile coordinates and tile counts are 32-bit
+    const int64_t m = (N + 127) / 128, h = (H + 127) / 128, i = (I + 127) / 128;
+    constexpr int64_t kTiles = int64_t(1) << 30;
+    if (N > kFfnMost || H > kFfnMost || I > kFfnMost || m * i > kTiles || m * h > kTiles ||
+        3 * h * i > kTiles)
+        return fail(MOE_ERR_UNSUPPORTED, "N, H and I are too large (%lld, %d, %d)", (long long)N,
+                    H, I);
+    return MOE_OK;
+}
+
+moe_status_t check_workspace(const void *workspace, size_t bytes, size_t need, const char *what) {
+    if (!workspace) return fail(MOE_ERR_INVALID_ARG, "workspace must be non-null");
+    if (!aligned_to(workspace, kAlign))
+        return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (bytes < need)
+        return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "%s workspace needs %zu bytes, got %zu", what,
+                    need, bytes);
+    return MOE_OK;
+}
+
+struct FfnLayout {
+    size_t h, dgate, dup, part, total;  // the status word comes first
+};
+
+FfnLayout ffn_layout(int64_t N, int H, int I, bool backward, int sms) {
+    FfnLayout L = {};
+    const size_t rows = round_up(2 * static_cast<size_t>(N) * I, kAlign);
+    L.h = kAlign;
+    L.dgate = L.h + rows;
+    L.dup = L.dgate + (backward ? rows : 0);
+    L.part = L.dup + (backward ? rows : 0);
+    size_t part = 0;
+    if (backward) {
+        const size_t dx = ffn_part_bytes(ffn_plan(kFfnDx, N, H, I, sms));
+        const size_t dw = ffn_part_bytes(ffn_plan(kFfnDw, N, H, I, sms));
+        part = dx > dw ? dx : dw;
+    } else {
+        part = ffn_part_bytes(ffn_plan(kFfnDown, N, H, I, sms));
+    }
+    L.total = L.part + part;
+    return L;
+}
+
+// The map of an operand: `base` [rows, cols], K-major (K along the rows) in
+// boxes of 64 values of K x 128 rows, MN-major in boxes of 64 x 64.
+moe_status_t ffn_operand(CUtensorMap *m, const void *base, int64_t rows, int cols, bool mn,
+                         const char *what) {
+    return make_rows_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, 64,
+                         mn ? 64 : 128, what);
+}
+
+moe_status_t ffn_out(CUtensorMap *m, const void *base, int64_t rows, int cols, const char *what) {
+    return make_rows_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, 32, 32, what);
+}
+
+moe_status_t run_ffn(FfnOp op, const FfnMaps &maps, FfnArgs a, int sms, cudaStream_t stream,
+                     const char *what) {
+    a.plan = ffn_plan(op, a.N, a.H, a.I, sms);
+    int launches = 0;
+    MOE_CUDA(launch_ffn(op, maps, a, &launches, stream), what);
+    g_launches += launches;
+    return MOE_OK;
+}
+
+#define MOE_TRY(call)                                \
+    do {                                             \
+        const moe_status_t st_ = (call);             \
+        if (st_ != MOE_OK) return st_;               \
+    } while (0)
+
+}  // namespace
+
+size_t moe_gated_ffn_workspace_bytes(int64_t N, int H, int I) {
+    if (check_ffn(N, H, I, MOE_ACT_NONE) != MOE_OK) return 0;
+    return ffn_layout(N, H, I, false, num_sms_of_current_device()).total;
+}
+
+size_t moe_gated_ffn_backward_workspace_bytes(int64_t N, int H, int I) {
+    if (check_ffn(N, H, I, MOE_ACT_NONE) != MOE_OK) return 0;
+    return ffn_layout(N, H, I, true, num_sms_of_current_device()).total;
+}
+
+moe_status_t moe_gated_ffn(const moe_bf16_t *x, const moe_bf16_t *w_gate, const moe_bf16_t *w_up,
+                           const moe_bf16_t *w_down, const moe_bf16_t *residual, int64_t N, int H,
+                           int I, int act, moe_bf16_t *gate, moe_bf16_t *up, moe_bf16_t *out,
+                           void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    g_last_error.clear();
+    MOE_TRY(check_ffn(N, H, I, act));
+    if ((gate == nullptr) != (up == nullptr))
+        return fail(MOE_ERR_INVALID_ARG, "gate and up are kept both or neither");
+    if (N == 0) return MOE_OK;
+    if (!x || !w_gate || !w_up || !w_down || !out)
+        return fail(MOE_ERR_INVALID_ARG, "x, w_gate, w_up, w_down and out must be non-null");
+    if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(w_down) ||
+        !aligned16(residual) || !aligned16(gate) || !aligned16(up) || !aligned16(out))
+        return fail(MOE_ERR_INVALID_ARG, "matrices must be 16-byte aligned");
+    const int sms = num_sms_of_current_device();
+    const FfnLayout L = ffn_layout(N, H, I, false, sms);
+    MOE_TRY(check_workspace(workspace, workspace_bytes, L.total, "gated feed-forward"));
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h);
+    FfnArgs a = {};
+    a.N = N;
+    a.H = H;
+    a.I = I;
+    a.act = act;
+    a.keep = gate ? 1 : 0;
+    a.part = reinterpret_cast<float *>(ws + L.part);
+    a.status = reinterpret_cast<int32_t *>(ws);
+    a.reset_status = 1;
+    FfnMaps m = {};
+    MOE_TRY(ffn_operand(&m.a[0], x, N, H, false, "x"));
+    MOE_TRY(ffn_operand(&m.b[0], w_gate, I, H, false, "w_gate"));
+    MOE_TRY(ffn_operand(&m.b[1], w_up, I, H, false, "w_up"));
+    MOE_TRY(ffn_out(&m.out[0], h, N, I, "h"));
+    if (gate) {
+        MOE_TRY(ffn_out(&m.out[1], gate, N, I, "gate"));
+        MOE_TRY(ffn_out(&m.out[2], up, N, I, "up"));
+    }
+    FfnMaps d = {};
+    MOE_TRY(ffn_operand(&d.a[0], h, N, I, false, "h"));
+    MOE_TRY(ffn_operand(&d.b[0], w_down, H, I, false, "w_down"));
+    MOE_TRY(ffn_out(&d.out[0], out, N, H, "out"));
+    MOE_TRY(run_ffn(kFfnGateUp, m, a, sms, stream, "gate and up kernel launch"));
+    a.reset_status = 0;
+    a.residual = residual;
+    a.out[0] = out;
+    return run_ffn(kFfnDown, d, a, sms, stream, "down kernel launch");
+}
+
+moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
+                                    const moe_bf16_t *w_gate, const moe_bf16_t *w_up,
+                                    const moe_bf16_t *w_down, const moe_bf16_t *gate,
+                                    const moe_bf16_t *up, int64_t N, int H, int I, int act,
+                                    moe_bf16_t *dx, moe_bf16_t *dw_gate, moe_bf16_t *dw_up,
+                                    moe_bf16_t *dw_down, void *workspace, size_t workspace_bytes,
+                                    cudaStream_t stream) {
+    g_last_error.clear();
+    MOE_TRY(check_ffn(N, H, I, act));
+    const int weights = (dw_gate ? 1 : 0) + (dw_up ? 1 : 0) + (dw_down ? 1 : 0);
+    if (weights != 0 && weights != 3)
+        return fail(MOE_ERR_INVALID_ARG, "dw_gate, dw_up and dw_down are wanted all or none");
+    if (!aligned16(dx) || !aligned16(dw_gate) || !aligned16(dw_up) || !aligned16(dw_down))
+        return fail(MOE_ERR_INVALID_ARG, "matrices must be 16-byte aligned");
+    if (N == 0) {  // sums over no tokens
+        if (weights) {
+            const size_t bytes = 2 * static_cast<size_t>(H) * I;
+            MOE_CUDA(cudaMemsetAsync(dw_gate, 0, bytes, stream), "dw_gate reset");
+            MOE_CUDA(cudaMemsetAsync(dw_up, 0, bytes, stream), "dw_up reset");
+            MOE_CUDA(cudaMemsetAsync(dw_down, 0, bytes, stream), "dw_down reset");
+        }
+        return MOE_OK;
+    }
+    if (!dout || !x || !w_gate || !w_up || !w_down || !gate || !up)
+        return fail(MOE_ERR_INVALID_ARG,
+                    "dout, x, w_gate, w_up, w_down, gate and up must be non-null");
+    if (!aligned16(dout) || !aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) ||
+        !aligned16(w_down) || !aligned16(gate) || !aligned16(up))
+        return fail(MOE_ERR_INVALID_ARG, "matrices must be 16-byte aligned");
+    const int sms = num_sms_of_current_device();
+    const FfnLayout L = ffn_layout(N, H, I, true, sms);
+    MOE_TRY(check_workspace(workspace, workspace_bytes, L.total, "gated feed-forward backward"));
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h);
+    uint16_t *dgate = reinterpret_cast<uint16_t *>(ws + L.dgate);
+    uint16_t *dup = reinterpret_cast<uint16_t *>(ws + L.dup);
+    FfnArgs a = {};
+    a.N = N;
+    a.H = H;
+    a.I = I;
+    a.act = act;
+    a.gate = gate;
+    a.up = up;
+    a.part = reinterpret_cast<float *>(ws + L.part);
+    a.status = reinterpret_cast<int32_t *>(ws);
+    a.reset_status = 1;
+    FfnMaps m = {};
+    MOE_TRY(ffn_operand(&m.a[0], dout, N, H, false, "dout"));
+    MOE_TRY(ffn_operand(&m.b[0], w_down, H, I, true, "w_down"));
+    MOE_TRY(ffn_out(&m.out[0], h, N, I, "h"));
+    MOE_TRY(ffn_out(&m.out[1], dgate, N, I, "dgate"));
+    MOE_TRY(ffn_out(&m.out[2], dup, N, I, "dup"));
+    FfnMaps w = {}, d = {};
+    if (weights) {
+        MOE_TRY(ffn_operand(&w.a[0], dgate, N, I, true, "dgate"));
+        MOE_TRY(ffn_operand(&w.a[1], dup, N, I, true, "dup"));
+        MOE_TRY(ffn_operand(&w.a[2], dout, N, H, true, "dout"));
+        MOE_TRY(ffn_operand(&w.b[0], x, N, H, true, "x"));
+        w.b[1] = w.b[0];
+        MOE_TRY(ffn_operand(&w.b[2], h, N, I, true, "h"));
+        MOE_TRY(ffn_out(&w.out[0], dw_gate, I, H, "dw_gate"));
+        MOE_TRY(ffn_out(&w.out[1], dw_up, I, H, "dw_up"));
+        MOE_TRY(ffn_out(&w.out[2], dw_down, H, I, "dw_down"));
+    }
+    if (dx) {
+        MOE_TRY(ffn_operand(&d.a[0], dgate, N, I, false, "dgate"));
+        MOE_TRY(ffn_operand(&d.a[1], dup, N, I, false, "dup"));
+        MOE_TRY(ffn_operand(&d.b[0], w_gate, I, H, true, "w_gate"));
+        MOE_TRY(ffn_operand(&d.b[1], w_up, I, H, true, "w_up"));
+        MOE_TRY(ffn_out(&d.out[0], dx, N, H, "dx"));
+    }
+    MOE_TRY(run_ffn(kFfnDh, m, a, sms, stream, "dh kernel launch"));
+    a.reset_status = 0;
+    if (weights) {
+        a.out[0] = dw_gate;
+        a.out[1] = dw_up;
+        a.out[2] = dw_down;
+        MOE_TRY(run_ffn(kFfnDw, w, a, sms, stream, "weight gradients kernel launch"));
+    }
+    if (dx) {
+        a.out[0] = dx;
+        MOE_TRY(run_ffn(kFfnDx, d, a, sms, stream, "dx kernel launch"));
+    }
     return MOE_OK;
 }
 

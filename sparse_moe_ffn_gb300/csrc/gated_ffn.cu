@@ -1,0 +1,697 @@
+// gated_ffn.cu -- the products of the gated feed-forward block and of its
+// backward pass (gated_ffn.cuh has the formulas), on CTA pairs: one tcgen05 MMA
+// of 256 rows x 256 columns (cta_group::2) reads each operand byte for 256 rows
+// of the other side, and the elementwise part runs on the accumulators.
+//
+// Operands come as they lie in memory.  A product's K runs along the rows of
+// either operand (K-major: [rows, K]) or across them (MN-major: [K, rows], as
+// the weights in dh and dx and both operands of the weights' gradients); TMA
+// brings either with 128-byte swizzled rows, and the MMA's descriptors say which
+// it is, so nothing is transposed in memory.
+//
+//   gate/up   the even CTA of a pair loads 128 rows of Wg, the odd one the same
+//             rows of Wu: a pair's accumulator is 128 columns of gate next to
+//             the 128 of up that belong to them
+//   dx        dgate Wg + dup Wu is one product whose K is the two in a row
+//   dW        the three weights' tiles are one list
+//
+//   warp 0     producer: TMA copies; the even CTA's barrier counts both CTAs'
+//              bytes
+//   warp 1     TMEM; in the even CTA, the MMAs
+//   warps 2-9  epilogue: warp w owns TMEM lanes 32 (w % 4) .. + 31 (one row a
+//              lane) and half of the columns; two accumulators alternate, so a
+//              tile's epilogue runs under the next tile's MMAs
+//
+// Rounding: gate, up, dgate, dup and h are operands of bf16 products and are
+// rounded to bf16 once each; h in the forward pass and dgate, dup in the
+// backward pass are made from fp32 accumulators.
+//
+// Tiles run in whole waves; the slices of a partial last wave are dealt out
+// evenly where K is long (FfnPlan), and ffn_join_kernel adds the partial sums
+// in a fixed order.  Every wait is bounded; a CTA that gives up records
+// MOE_ERR_DEVICE_TIMEOUT.
+#include "gated_ffn.cuh"
+#include "linear_epilogue.cuh"
+#include "linear_gemm.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kEpiWarps = 8;
+constexpr int kFfnThreads = 64 + 32 * kEpiWarps;
+constexpr int kStages = 5;
+constexpr int kBN = 256;               // columns of a tile
+constexpr int kSliceK = 64;            // values of K in a slice
+constexpr int kOperandBytes = 128 * kSliceBytes;  // a CTA's share of a slice, either side
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kMnChunk = 64 * kSliceBytes;  // MN-major: 64 rows, 64 values of K
+constexpr int kOutBytes = 2048;        // 32 x 32 bf16 on their way out
+constexpr int kOutBuffers = 3;         // a warp's
+constexpr int kMinSlices = 8;          // of a part of a tile
+
+struct FfnShared {
+    uint64_t full[kStages];   // even CTA: both CTAs' bytes of a stage landed
+    uint64_t empty[kStages];  // both: the MMAs are done with a stage
+    uint64_t acc_full[2];     // both: an accumulator is complete
+    uint64_t acc_empty[2];    // even CTA: both CTAs' epilogues have read one
+    uint64_t drain;           // even CTA: every MMA has completed
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+template <FfnOp kOp>
+struct FfnTraits {
+    static constexpr bool kAMn = kOp == kFfnDw;
+    static constexpr bool kBMn = kOp == kFfnDh || kOp == kFfnDx || kOp == kFfnDw;
+    static constexpr int kColsPerTile = kOp == kFfnGateUp ? kBN / 2 : kBN;  // of the output
+};
+
+// Shared memory descriptor of an MN-major operand: rows of 64 values along MN
+// (128 bytes, swizzled), eight values of K in 1024 bytes, 64 further rows one
+// chunk on.  A step of 16 values of K is two groups of eight.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(kMnChunk >> 4) << 16;  // leading: next 64 along MN
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;      // stride: next 8 along K
+    d |= static_cast<uint64_t>(1) << 46;              // descriptor version (sm_100 family)
+    d |= static_cast<uint64_t>(2) << 61;              // 128-byte swizzle
+    return d;
+}
+constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
+constexpr int kStepKMajor = kMmaBytes >> 4;           // 16 values of K, in 16 bytes
+constexpr int kStepMnMajor = 16 * kSliceBytes >> 4;
+
+// One piece of work of a pair: slices [k0, k1) of a tile; slot >= 0: its sums
+// go to that partial tile.
+struct FfnItem {
+    int tile, k0, k1, slot;
+};
+
+// The pieces of pair `pair`, in order.
+struct FfnWalk {
+    const FfnPlan &p;
+    int pair, tile, turn;
+    int64_t from, to;  // of the shared slices
+    __device__ __forceinline__ FfnWalk(const FfnPlan &plan, int pair_)
+        : p(plan), pair(pair_), tile(pair_), turn(0), from(0), to(0) {
+        if (p.parts > pair) {
+            const int64_t s = static_cast<int64_t>(p.tiles - p.whole) * p.nk;
+            from = s * pair / p.parts;
+            to = s * (pair + 1) / p.parts;
+        }
+    }
+    __device__ __forceinline__ bool next(FfnItem &it) {
+        if (tile < p.whole) {
+            it = {tile, 0, p.nk, -1};
+            tile += p.pairs;
+            return true;
+        }
+        if (from >= to) return false;
+        const int t = static_cast<int>(from / p.nk);
+        const int64_t first = static_cast<int64_t>(t) * p.nk;
+        const int64_t end = min(to, first + p.nk);
+        it = {p.whole + t, static_cast<int>(from - first), static_cast<int>(end - first),
+              2 * pair + turn};
+        from = end;
+        ++turn;
+        return true;
+    }
+};
+
+// Tiles run through bands of kBand row tiles, column tile by column tile: the
+// tiles in flight share few rows of either operand.
+constexpr int kBand = 8;
+
+struct FfnTile {
+    int prod, m, n;
+};
+
+template <FfnOp kOp>
+__device__ __forceinline__ void ffn_dims(const FfnArgs &a, int prod, int64_t *rows, int *cols) {
+    if (kOp == kFfnDw) {
+        *rows = prod == 2 ? a.H : a.I;
+        *cols = prod == 2 ? a.I : a.H;
+    } else {
+        *rows = a.N;
+        *cols = kOp == kFfnGateUp || kOp == kFfnDh ? a.I : a.H;
+    }
+}
+
+template <FfnOp kOp>
+__device__ __forceinline__ FfnTile ffn_tile(const FfnArgs &a, int tile) {
+    FfnTile t = {0, 0, 0};
+    if (kOp == kFfnDw) {
+        const int each = a.plan.tiles / 3;
+        t.prod = tile / each;
+        tile -= t.prod * each;
+    }
+    int64_t rows;
+    int cols;
+    ffn_dims<kOp>(a, t.prod, &rows, &cols);
+    const int m_tiles = static_cast<int>((rows + kFfnTile - 1) / kFfnTile);
+    const int n_tiles = (cols + FfnTraits<kOp>::kColsPerTile - 1) / FfnTraits<kOp>::kColsPerTile;
+    const int band = tile / (kBand * n_tiles);
+    const int first = band * kBand;
+    const int high = min(kBand, m_tiles - first);
+    const int in = tile - band * kBand * n_tiles;
+    t.m = first + in % high;
+    t.n = in / high;
+    return t;
+}
+
+__device__ __forceinline__ void tma_store_box(const CUtensorMap *map, const void *src, int c0,
+                                              int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
+                 ::"l"(map), "r"(smem_addr(src)), "r"(c0), "r"(c1)
+                 : "memory");
+}
+
+// This lane's row of a 32 x 32 chunk of bf16, as a tensor-map store with
+// swizzled rows of 64 bytes reads it.
+__device__ __forceinline__ void write_bf16_row(uint8_t *buf, int lane, const float (&v)[32]) {
+    uint8_t *row = buf + lane * 64;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4 *>(row + 16 * (j ^ ((lane >> 1) & 3))) =
+            make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                       pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
+                       pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+}
+
+// 32 values of a bf16 row (16-byte aligned), the first `left` of which exist (a
+// multiple of 8).
+struct Row32 {
+    uint32_t w[16];
+    __device__ __forceinline__ void load(const uint16_t *p, int left) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 u = 8 * i < left ? __ldcg(reinterpret_cast<const uint4 *>(p) + i)
+                                         : make_uint4(0, 0, 0, 0);
+            w[4 * i] = u.x;
+            w[4 * i + 1] = u.y;
+            w[4 * i + 2] = u.z;
+            w[4 * i + 3] = u.w;
+        }
+    }
+    __device__ __forceinline__ void add_to(float (&v)[32]) const {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 f = unpack_bf16x2(w[i]);
+            v[2 * i] += f.x;
+            v[2 * i + 1] += f.y;
+        }
+    }
+};
+
+// a = act(v) and d = act'(v).  The logistic function s is exactly 0 where 2^t
+// passes the range, so that its product with a large v vanishes.
+template <int ACT>
+__device__ __forceinline__ void act_slope(float v, float *a, float *d) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    if (ACT == MOE_ACT_SILU) {
+        const float s = rcp_fast(1.f + ex2_fast(v * -kLog2e));
+        *a = v * s;
+        *d = fmaf(*a, 1.f - s, s);
+    } else if (ACT == MOE_ACT_GELU) {
+        // q: the normal distribution's upper tail beyond |v| (see gelu)
+        const float x = fabsf(v) * 0.70710678118654752f;
+        const float t = rcp_fast(fmaf(0.3275911f, x, 1.f));
+        float poly = fmaf(t, 1.061405429f, -1.453152027f);
+        poly = fmaf(t, poly, 1.421413741f);
+        poly = fmaf(t, poly, -0.284496736f);
+        poly = fmaf(t, poly, 0.254829592f);
+        const float e = ex2_fast(v * v * -0.72134752044448170f);  // e^(-v^2/2)
+        const float q = 0.5f * t * poly * e;
+        const float c = fminf(fmaxf(v, -64.f), 64.f);
+        *a = fmaxf(v, 0.f) - fabsf(c) * q;
+        *d = fmaf(c * 0.39894228040143268f, e, v < 0.f ? q : 1.f - q);
+    } else if (ACT == MOE_ACT_GELU_TANH) {
+        constexpr float k = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+        const float vv = v * v;
+        const float s = rcp_fast(1.f + ex2_fast(-k * kLog2e * v * fmaf(0.044715f, vv, 1.f)));
+        *a = v * s;
+        const float r = *a * (1.f - s);  // 0 where z' may be infinite
+        *d = r == 0.f ? s : fmaf(r, k * fmaf(0.134145f, vv, 1.f), s);
+    } else if (ACT == MOE_ACT_RELU) {
+        *a = v < 0.f ? 0.f : v;  // a NaN stays one
+        *d = v > 0.f ? 1.f : 0.f;
+    } else {
+        *a = v;
+        *d = 1.f;
+    }
+}
+
+// dh -> dgate, with dup and h from the saved gate and up.
+template <int ACT>
+__device__ __forceinline__ void gate_grads(float (&dh)[32], const Row32 &gate, const Row32 &up,
+                                           float (&dup)[32], float (&h)[32]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float2 g = unpack_bf16x2(gate.w[i]), u = unpack_bf16x2(up.w[i]);
+        float a, d;
+        act_slope<ACT>(g.x, &a, &d);
+        dup[2 * i] = dh[2 * i] * a;
+        h[2 * i] = a * u.x;
+        dh[2 * i] *= u.x * d;
+        act_slope<ACT>(g.y, &a, &d);
+        dup[2 * i + 1] = dh[2 * i + 1] * a;
+        h[2 * i + 1] = a * u.y;
+        dh[2 * i + 1] *= u.y * d;
+    }
+}
+
+template <FfnOp kOp>
+__global__ void __launch_bounds__(kFfnThreads, 1)
+    ffn_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnArgs a) {
+    using T = FfnTraits<kOp>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *tiles = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *out_bufs = tiles + kStages * kStageBytes;
+    FfnShared *sm = reinterpret_cast<FfnShared *>(out_bufs + kEpiWarps * kOutBuffers * kOutBytes);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const bool leader = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm->full[s], 1);
+            mbar_init(&sm->empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm->acc_full[i], 1);
+            mbar_init(&sm->acc_empty[i], 2 * kEpiWarps);
+        }
+        mbar_init(&sm->drain, 1);
+        sm->abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensor_map(&maps.a[0]);
+        prefetch_tensor_map(&maps.b[0]);
+    }
+    if (warp == 1) tmem_alloc_2cta(&sm->tmem_base, 2 * kBN);
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_barrier();  // both CTAs' barriers exist before any remote arrival
+    tc_fence_after_sync();
+    const uint32_t tmem = sm->tmem_base;
+    volatile int *abort_flag = &sm->abort_flag;
+    griddep_launch_dependents();
+    griddep_wait();
+    if (a.reset_status && blockIdx.x == 0 && threadIdx.x == 0 && a.status) *a.status = MOE_OK;
+
+    const int pair = blockIdx.x / 2;
+    FfnWalk walk(a.plan, pair);
+    FfnItem it;
+
+    if (warp == 0) {
+        const bool issues = elect_one();
+        // stages filled so far; the stage and the parity of its last release
+        int64_t g = 0;
+        int s = 0;
+        uint32_t parity = 1;
+        bool failed = false;
+        while (!failed && walk.next(it)) {
+            const FfnTile t = ffn_tile<kOp>(a, it.tile);
+            const int row = t.m * kFfnTile + rank * 128;
+            const int col = kOp == kFfnGateUp ? t.n * T::kColsPerTile : t.n * kBN + rank * 128;
+            const int half = a.plan.nk / 2;  // dx: slices of the first product
+            for (int kc = it.k0; kc < it.k1; ++kc, ++g) {
+                if (g >= kStages && !warp_wait(&sm->empty[s], parity, abort_flag)) {
+                    if (issues) {
+                        record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+                        *abort_flag = 1;
+                    }
+                    failed = true;
+                    break;
+                }
+                if (issues) {
+                    uint8_t *st = tiles + s * kStageBytes;
+                    uint8_t *sb = st + kOperandBytes;
+                    const uint32_t bar = map_to_rank(smem_addr(&sm->full[s]), 0);
+                    if (leader) mbar_arrive_expect_tx(&sm->full[s], 2 * kStageBytes);
+                    const int second = kOp == kFfnDx && kc >= half ? 1 : 0;
+                    const int k = (kc - second * half) * kSliceK;
+                    const CUtensorMap *ma = &maps.a[kOp == kFfnDw ? t.prod : second];
+                    const CUtensorMap *mb = &maps.b[kOp == kFfnGateUp ? rank
+                                                    : kOp == kFfnDw   ? t.prod
+                                                                      : second];
+                    if (T::kAMn) {
+                        tma_load_2d_pair(st, ma, bar, row, k);
+                        tma_load_2d_pair(st + kMnChunk, ma, bar, row + 64, k);
+                    } else {
+                        tma_load_2d_pair(st, ma, bar, k, row);
+                    }
+                    if (T::kBMn) {
+                        tma_load_2d_pair(sb, mb, bar, col, k);
+                        tma_load_2d_pair(sb + kMnChunk, mb, bar, col + 64, k);
+                    } else {
+                        tma_load_2d_pair(sb, mb, bar, k, col);
+                    }
+                }
+                if (++s == kStages) {
+                    s = 0;
+                    parity ^= 1;
+                }
+            }
+        }
+        // no copy may be in flight when the pair ends
+        if (leader && issues)
+            for (int64_t i = (g > kStages ? g - kStages : 0); i < g; ++i)
+                drain_wait(&sm->full[i % kStages], (i / kStages) & 1);
+        __syncwarp();
+    } else if (warp == 1) {
+        if (leader) {
+            // The whole warp runs the loop and one lane of it issues, so that
+            // the compiler keeps descriptors and barriers in uniform registers.
+            const bool issues = elect_one();
+            constexpr uint32_t idesc = idesc_bf16_f32(kFfnTile, kBN) |
+                                       (T::kAMn ? kIdescAMn : 0) | (T::kBMn ? kIdescBMn : 0);
+            constexpr int kStepA = T::kAMn ? kStepMnMajor : kStepKMajor;
+            constexpr int kStepB = T::kBMn ? kStepMnMajor : kStepKMajor;
+            const uint32_t base = smem_addr(tiles);
+            const uint64_t desc_a = T::kAMn ? sw128_mnmajor_desc(base) : sw128_kmajor_desc(base);
+            const uint64_t desc_b = T::kBMn ? sw128_mnmajor_desc(base + kOperandBytes)
+                                            : sw128_kmajor_desc(base + kOperandBytes);
+            int s = 0, n = 0;
+            uint32_t phase = 0;
+            bool failed = false;
+            for (; !failed && walk.next(it); ++n) {
+                const int acc = n & 1;
+                const uint32_t use = n >> 1;
+                if (use > 0 && !warp_wait(&sm->acc_empty[acc], (use - 1) & 1, abort_flag)) {
+                    failed = true;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t d = tmem + acc * kBN;
+                for (int kc = it.k0; kc < it.k1; ++kc) {
+                    if (!warp_wait(&sm->full[s], phase, abort_flag)) {
+                        failed = true;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    if (issues) {
+                        const uint64_t da = desc_a + s * (kStageBytes >> 4);
+                        const uint64_t db = desc_b + s * (kStageBytes >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < kSliceK / 16; ++kk)
+                            linear_mma_pair<false>(d, da + kStepA * kk, db + kStepB * kk, idesc,
+                                                   kk == 0 ? kc != it.k0 : 1);
+                        commit_2cta(&sm->empty[s], 3);
+                    }
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!failed && issues) commit_2cta(&sm->acc_full[acc], 3);
+            }
+            if (failed && issues) {
+                record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+                *abort_flag = 1;
+            }
+            if (issues) {
+                commit_2cta(&sm->drain, 1);
+                drain_wait(&sm->drain, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp % 4, half = (warp - 2) / 4, ew = warp - 2;
+        constexpr int kCols = T::kColsPerTile / 2;  // a warp's
+        const uint32_t empty0 = map_to_rank(smem_addr(&sm->acc_empty[0]), 0);
+        const uint32_t empty1 = map_to_rank(smem_addr(&sm->acc_empty[1]), 0);
+        uint8_t *buf = out_bufs + ew * kOutBuffers * kOutBytes;
+        int n = 0, chunk = 0;
+        for (; walk.next(it); ++n) {
+            const FfnTile t = ffn_tile<kOp>(a, it.tile);
+            int64_t rows;
+            int all_cols;
+            ffn_dims<kOp>(a, t.prod, &rows, &all_cols);
+            const int acc = n & 1;
+            const int c0 = t.n * T::kColsPerTile + half * kCols;
+            const int64_t r0 = static_cast<int64_t>(t.m) * kFfnTile + rank * 128 + quarter * 32;
+            const int64_t r = r0 + lane;
+            // columns of this warp that exist (warp-uniform)
+            const int cols = r0 < rows ? min(kCols, all_cols - c0) : 0;
+            // operands of the elementwise part, read 32 columns ahead
+            Row32 e0, e1;
+            auto fetch = [&](int c) {
+                if (c >= cols || r >= rows) return;
+                const int64_t at = r * all_cols + c0 + c;
+                if (kOp == kFfnDh) {
+                    e0.load(a.gate + at, cols - c);
+                    e1.load(a.up + at, cols - c);
+                }
+                if (kOp == kFfnDown && a.residual && it.slot < 0)
+                    e0.load(a.residual + at, cols - c);
+            };
+            fetch(0);
+            __syncwarp();
+            bool ok = true;
+            if (lane == 0) ok = mbar_wait(&sm->acc_full[acc], (n >> 1) & 1, abort_flag);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) {
+                if (lane == 0) {
+                    record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                break;
+            }
+            tc_fence_after_sync();
+            const uint32_t taddr =
+                tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kBN + half * kCols;
+            if (it.slot >= 0) {  // (kFfnDown, kFfnDx, kFfnDw)
+                float *part = a.part + it.slot * kFfnPartFloats +
+                              ((rank * 4 + quarter) * 8 + half * 4) * 1024 + lane;
+#pragma unroll 1
+                for (int c = 0; c < cols; c += 32, part += 1024) {
+                    float v[32];
+                    __syncwarp();
+                    tmem_load32(taddr + c, v);
+                    tmem_load_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) __stcg(part + 32 * i, v[i]);
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < cols; c += 32, ++chunk) {
+                    float v[32], w[32], x[32];
+                    int outs = 1;
+                    __syncwarp();  // TMEM wants whole warps
+                    tmem_load32(taddr + c, v);
+                    if (kOp == kFfnGateUp) {
+                        __syncwarp();
+                        tmem_load32(taddr + c + kBN / 2, w);
+                    }
+                    tmem_load_wait();
+                    if (kOp == kFfnGateUp) {
+                        // x = h = act(gate) * up
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = v[i];
+                        act_all(a.act, x);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] *= w[i];
+                        outs = a.keep ? 3 : 1;
+                    }
+                    if (kOp == kFfnDh) {
+                        switch (a.act) {
+                            case MOE_ACT_SILU: gate_grads<MOE_ACT_SILU>(v, e0, e1, w, x); break;
+                            case MOE_ACT_GELU: gate_grads<MOE_ACT_GELU>(v, e0, e1, w, x); break;
+                            case MOE_ACT_GELU_TANH:
+                                gate_grads<MOE_ACT_GELU_TANH>(v, e0, e1, w, x);
+                                break;
+                            case MOE_ACT_RELU: gate_grads<MOE_ACT_RELU>(v, e0, e1, w, x); break;
+                            default: gate_grads<MOE_ACT_NONE>(v, e0, e1, w, x); break;
+                        }
+                        outs = 3;
+                    }
+                    if (kOp == kFfnDown && a.residual) e0.add_to(v);
+                    fetch(c + 32);
+                    // one output: the buffers take turns; three: all have left
+                    uint8_t *b = buf;
+                    if (outs == 1) {
+                        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        b += (chunk & 1) * kOutBytes;
+                    } else {
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    }
+                    __syncwarp();
+                    if (kOp == kFfnGateUp || kOp == kFfnDh) write_bf16_row(b, lane, x);
+                    else write_bf16_row(b, lane, v);
+                    if ((kOp == kFfnGateUp || kOp == kFfnDh) && outs == 3) {
+                        write_bf16_row(b + kOutBytes, lane, v);
+                        write_bf16_row(b + 2 * kOutBytes, lane, w);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_box(&maps.out[t.prod], b, c0 + c, static_cast<int>(r0));
+                        if (outs == 3) {
+                            tma_store_box(&maps.out[1], b + kOutBytes, c0 + c,
+                                          static_cast<int>(r0));
+                            tma_store_box(&maps.out[2], b + 2 * kOutBytes, c0 + c,
+                                          static_cast<int>(r0));
+                        }
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) arrive_remote_relaxed(acc ? empty1 : empty0);
+        }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // stores have landed
+        __syncwarp();
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_barrier();  // both CTAs are done with TMEM and each other's barriers
+    if (warp == 1) {
+        tc_fence_after_sync();
+        __syncwarp();
+        tmem_dealloc_2cta(tmem, 2 * kBN);
+    }
+}
+
+// The shared tiles: a warp adds the parts of 32 x 32 values, in the order of
+// their slices, and stores them.
+constexpr int kJoinThreads = 256;
+
+template <FfnOp kOp>
+__global__ void __launch_bounds__(kJoinThreads)
+    ffn_join_kernel(const __grid_constant__ FfnArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x % 32;
+    const int at = blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32;  // chunk of the tiles
+    const int local = at / 64, chunk = at % 64;  // 8 groups of 32 rows x 8 of 32 columns
+    const FfnPlan &p = a.plan;
+    const FfnTile t = ffn_tile<kOp>(a, p.whole + local);
+    int64_t rows;
+    int all_cols;
+    ffn_dims<kOp>(a, t.prod, &rows, &all_cols);
+    const int64_t r = static_cast<int64_t>(t.m) * kFfnTile + chunk / 8 * 32 + lane;
+    const int c0 = t.n * kBN + chunk % 8 * 32;
+    if (c0 >= all_cols || r - lane >= rows) return;
+    const int left = all_cols - c0;
+    Row32 res;
+    if (kOp == kFfnDown && a.residual && r < rows) res.load(a.residual + r * all_cols + c0, left);
+    const int64_t slices = static_cast<int64_t>(p.tiles - p.whole) * p.nk;
+    const int64_t from = static_cast<int64_t>(local) * p.nk, to = from + p.nk;
+    // the first part that ends behind `from`
+    int q = static_cast<int>(from * p.parts / slices);
+    while (slices * (q + 1) / p.parts <= from) ++q;
+    while (q > 0 && slices * q / p.parts > from) --q;
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+    for (; q < p.parts; ++q) {
+        const int64_t begin = slices * q / p.parts;
+        if (begin >= to) break;
+        const int slot = 2 * q + (begin < from ? 1 : 0);  // its second tile, or its first
+        const float *part = a.part + slot * kFfnPartFloats + chunk * 1024 + lane;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += __ldcg(part + 32 * i);
+    }
+    if (r >= rows) return;
+    if (kOp == kFfnDown && a.residual) res.add_to(v);
+    uint16_t *out = a.out[t.prod] + r * all_cols + c0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (8 * i < left)
+            *reinterpret_cast<uint4 *>(out + 8 * i) =
+                make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]),
+                           pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                           pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
+                           pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+}
+
+template <FfnOp kOp>
+cudaError_t launch_op(const FfnMaps &maps, const FfnArgs &a, int *launches, cudaStream_t s) {
+    const size_t smem = 1024 + static_cast<size_t>(kStages) * kStageBytes +
+                        kEpiWarps * kOutBuffers * kOutBytes + sizeof(FfnShared);
+    auto kern = ffn_kernel<kOp>;
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_shared(kern, smem, allowed);
+    if (err != cudaSuccess) return err;
+    err = launch_pdl(kern, dim3(static_cast<unsigned>(2 * a.plan.pairs)), dim3(kFfnThreads), smem,
+                     s, 2, maps, a);
+    if (err != cudaSuccess) return err;
+    *launches += 1;
+    if (a.plan.parts == 0) return cudaSuccess;
+    *launches += 1;
+    const int blocks = (a.plan.tiles - a.plan.whole) * (64 / (kJoinThreads / 32));
+    return launch_pdl(ffn_join_kernel<kOp>, dim3(static_cast<unsigned>(blocks)),
+                      dim3(kJoinThreads), 0, s, 1, a);
+}
+
+int64_t up_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+FfnPlan ffn_plan(FfnOp op, int64_t N, int H, int I, int num_sms) {
+    const int P = num_sms / 2 < kFfnMaxPairs ? num_sms / 2 : kFfnMaxPairs;
+    FfnPlan p;
+    int64_t tiles;
+    const int64_t m = up_div(N, kFfnTile);
+    switch (op) {
+        case kFfnGateUp:
+            tiles = m * up_div(I, kBN / 2);
+            p.nk = static_cast<int>(up_div(H, kSliceK));
+            break;
+        case kFfnDh:
+            tiles = m * up_div(I, kBN);
+            p.nk = static_cast<int>(up_div(H, kSliceK));
+            break;
+        case kFfnDown:
+            tiles = m * up_div(H, kBN);
+            p.nk = static_cast<int>(up_div(I, kSliceK));
+            break;
+        case kFfnDx:
+            tiles = m * up_div(H, kBN);
+            p.nk = static_cast<int>(2 * up_div(I, kSliceK));
+            break;
+        default:
+            tiles = 3 * up_div(I, kBN) * up_div(H, kBN);
+            p.nk = static_cast<int>(up_div(N, kSliceK));
+    }
+    p.tiles = static_cast<int>(tiles);
+    p.whole = p.tiles;
+    p.parts = 0;
+    p.pairs = p.tiles < P ? p.tiles : P;
+    if (op == kFfnGateUp || op == kFfnDh) return p;  // their epilogues need whole sums
+    const int rest = p.tiles % P;
+    const int64_t slices = static_cast<int64_t>(rest) * p.nk;
+    const int64_t most = slices / kMinSlices;
+    const int parts = most < P ? static_cast<int>(most) : P;
+    // the tiles' slices one after the other, or shared and joined
+    if (parts > rest && (p.nk - static_cast<double>(slices) / parts) * 0.3 > 5.0) {
+        p.whole = p.tiles - rest;
+        p.parts = parts;
+        p.pairs = p.whole > 0 || parts > P ? P : parts;
+    }
+    return p;
+}
+
+size_t ffn_part_bytes(const FfnPlan &p) {
+    return sizeof(float) * kFfnPartFloats * 2 * static_cast<size_t>(p.parts);
+}
+
+int ffn_block_n(FfnOp op) { return op == kFfnGateUp ? kBN / 2 : kBN; }
+
+cudaError_t launch_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, int *launches,
+                       cudaStream_t s) {
+    switch (op) {
+        case kFfnGateUp: return launch_op<kFfnGateUp>(maps, a, launches, s);
+        case kFfnDown: return launch_op<kFfnDown>(maps, a, launches, s);
+        case kFfnDh: return launch_op<kFfnDh>(maps, a, launches, s);
+        case kFfnDx: return launch_op<kFfnDx>(maps, a, launches, s);
+        default: return launch_op<kFfnDw>(maps, a, launches, s);
+    }
+}
+
+}  // namespace moe

@@ -1,0 +1,70 @@
+// gated_ffn.cuh -- the products of the gated feed-forward block and of its
+// backward pass:
+//
+//   gate = x Wg^T, up = x Wu^T, h = act(gate) * up     kFfnGateUp
+//   out = h Wd^T (+ residual)                          kFfnDown
+//   dh = dout Wd, dgate = dh * up * act'(gate),
+//   dup = dh * act(gate), h again                      kFfnDh
+//   dx = dgate Wg + dup Wu                             kFfnDx
+//   dWg = dgate^T x, dWu = dup^T x, dWd = dout^T h     kFfnDw
+//
+// with x, out, dout, dx [N, H], Wg, Wu [I, H], Wd [H, I], the rest [N, I], all
+// bf16.
+#pragma once
+
+#include <cuda.h>
+#include <stdint.h>
+
+#include "kernels.cuh"
+#include "moe.h"
+
+namespace moe {
+
+enum FfnOp { kFfnGateUp = 0, kFfnDown = 1, kFfnDh = 2, kFfnDx = 3, kFfnDw = 4 };
+
+// Pairs of CTAs that run at once at most; a launch's partial sums have room for
+// two tiles a pair.
+constexpr int kFfnMaxPairs = 76;
+constexpr int kFfnTile = 256;  // rows of a tile
+constexpr size_t kFfnPartFloats = static_cast<size_t>(kFfnTile) * 256;
+
+// How a launch's tiles go to the pairs: whole waves of tiles, then, where the
+// last wave is partial and K long, its tiles' K slices in `parts` equal runs,
+// whose partial sums a second kernel adds.
+struct FfnPlan {
+    int tiles;   // output tiles
+    int whole;   // tiles that one pair computes from end to end
+    int parts;   // > 0: pairs that share the other tiles' slices
+    int nk;      // K slices of a tile
+    int pairs;   // launched
+};
+
+struct FfnArgs {
+    int64_t N;
+    int H, I;
+    int act;
+    int keep;                   // gate and up are stored
+    const uint16_t *gate, *up;  // kFfnDh
+    const uint16_t *residual;   // kFfnDown, nullable
+    uint16_t *out[3];           // the outputs (for the partial sums' join)
+    float *part;                // [2 pairs][kFfnPartFloats]
+    int32_t *status;
+    int reset_status;
+    FfnPlan plan;
+};
+
+// The operands' and outputs' tensor maps: a: the M side's, b: the N side's,
+// out: boxes of 32 x 32 values.  A K-major operand ([rows, K]) comes in boxes of
+// 64 values of K x its rows a CTA, an MN-major one ([K, rows]) in boxes of 64
+// rows x 64 values of K.
+struct FfnMaps {
+    CUtensorMap a[3], b[3], out[3];
+};
+
+FfnPlan ffn_plan(FfnOp op, int64_t N, int H, int I, int num_sms);
+size_t ffn_part_bytes(const FfnPlan &p);
+int ffn_block_n(FfnOp op);
+cudaError_t launch_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, int *launches,
+                       cudaStream_t s);
+
+}  // namespace moe
