@@ -655,6 +655,79 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
                                     moe_bf16_t *dw_down, void *workspace, size_t workspace_bytes,
                                     cudaStream_t stream);
 
+/* -------------------------------------------------------------------------
+ * moe_layernorm, moe_layernorm_backward -- residual add + layer norm, and its
+ * backward pass:
+ *   r    = x + residual in the arrays' type      (x without a residual)
+ *   mean = sum_h r / H, rstd = 1 / sqrt(sum_h (r - mean)^2 / H + eps)
+ *   out  = n * weight + bias,  n = (r - mean) * rstd
+ * and, for the gradient dout of out, with t = dout * weight,
+ *   dx      = rstd (t - mean_h(t) - n mean_h(t n)) + dresidual
+ *   dweight = sum over rows of dout n,  dbias = sum over rows of dout
+ *
+ *   x, residual (or NULL), residual_out (or NULL: not stored), out [N, H];
+ *   weight, bias (or NULL) [H]: bf16 when bf16 != 0, else fp32, all of them
+ *   mean, rstd [N] fp32 out, each may be NULL in the forward call
+ * Backward call: x is what was normalised (r), dresidual [N, H] or NULL the
+ * gradient that reaches r by the residual stream, dx [N, H] out (x's and the
+ * residual's gradient alike), dweight, dbias [H] fp32 out; each of the three
+ * may be NULL (not wanted).
+ *   workspace >= moe_layernorm_backward_workspace_bytes(N, H) (on the device of
+ *            the call), 256-byte aligned; NULL if neither dweight nor dbias is
+ *            wanted.  It holds no status word: nothing here waits.
+ * residual_out and out may each be x or residual (not the same one), dx may be
+ * dout, x or dresidual; nothing else may overlap.  With N = 0 dweight and dbias
+ * are 0.
+ * Precision: the sums in fp32 (the variance from the squared deviations),
+ * one rounding of each output; the gradients' sums over rows in fp32 a block of
+ * rows, then in 64 bits, in a fixed order.  A row with a NaN or an infinity
+ * gives NaN.  Limits: 1 <= H <= 65536; arrays aligned to their types (16-byte
+ * accesses are taken where H and all arrays allow them).
+ * ---------------------------------------------------------------------- */
+moe_status_t moe_layernorm(const void *x, const void *residual, const void *weight,
+                           const void *bias, int bf16, int64_t N, int H, float eps,
+                           void *residual_out, void *out, float *mean, float *rstd,
+                           cudaStream_t stream);
+size_t moe_layernorm_backward_workspace_bytes(int64_t N, int H);
+moe_status_t moe_layernorm_backward(const void *dout, const void *x, const void *weight,
+                                    const float *mean, const float *rstd, const void *dresidual,
+                                    int bf16, int64_t N, int H, void *dx, float *dweight,
+                                    float *dbias, void *workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+
+/* -------------------------------------------------------------------------
+ * moe_grad_norm, moe_clip_grads -- the norm of a set of gradient tensors, and
+ * the set scaled so that its norm is max_norm at most:
+ *   norm   = sqrt(sum over all tensors and values of g^2)
+ *   factor = 1 where norm <= max_norm, else max_norm / norm
+ *   out[i] = grads[i] * factor
+ *
+ *   grads, out  n device pointers each (host arrays, read before the call
+ *               returns); out[i] may be grads[i] itself, and overlaps nothing
+ *               else
+ *   sizes       n int64: values of each tensor (0: none, its pointers are not
+ *               looked at)
+ *   bf16        n bytes: 1: grads[i] is bf16, 0: fp32;  out_bf16: the same of out
+ *   norm        [1] fp32 on the device: written by moe_grad_norm, read by
+ *               moe_clip_grads
+ *   workspace >= moe_grad_norm_workspace_bytes(n), 256-byte aligned.  It holds
+ *               no status word: nothing here waits.
+ * A norm that is NaN makes every output NaN, an infinite one 0 (and what was
+ * infinite NaN): nothing here leaves a step out, that is the caller's decision.
+ * Precision: the squares are summed in fp32 over at most 32 values, in 64 bits
+ * beyond that, and in 64 bits from the start where fp32 would overflow or lose
+ * them (the norm is infinite only where it passes 3.4e38 itself); the sums have
+ * a fixed order.  The factor in fp32, one rounding of each output.  No tensors, or empty ones, have norm 0.  Arrays aligned to their
+ * types; any sizes.
+ * ---------------------------------------------------------------------- */
+size_t moe_grad_norm_workspace_bytes(int64_t n);
+moe_status_t moe_grad_norm(const void *const *grads, const int64_t *sizes, const uint8_t *bf16,
+                           int64_t n, float *norm, void *workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+moe_status_t moe_clip_grads(const void *const *grads, const int64_t *sizes, const uint8_t *bf16,
+                            int64_t n, const float *norm, float max_norm, void *const *out,
+                            const uint8_t *out_bf16, cudaStream_t stream);
+
 /* Byte offsets of moe_forward's workspace sub-buffers (for inspecting the
  * intermediate results; every offset is 256-byte aligned).
  *

@@ -10,6 +10,7 @@ likewise for the host, experts and dense-MLP calls).
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import os
@@ -99,6 +100,12 @@ def lib():
         "moe_gated_ffn": ([P] * 5 + [i64, i32, i32, i32, P, P, P, P, sz, P], i32),
         "moe_gated_ffn_backward_workspace_bytes": ([i64, i32, i32], sz),
         "moe_gated_ffn_backward": ([P] * 7 + [i64, i32, i32, i32] + [P] * 5 + [sz, P], i32),
+        "moe_layernorm": ([P, P, P, P, i32, i64, i32, ctypes.c_float, P, P, P, P, P], i32),
+        "moe_layernorm_backward_workspace_bytes": ([i64, i32], sz),
+        "moe_layernorm_backward": ([P] * 6 + [i32, i64, i32] + [P] * 4 + [sz, P], i32),
+        "moe_grad_norm_workspace_bytes": ([i64], sz),
+        "moe_grad_norm": ([P, P, P, i64, P, P, sz, P], i32),
+        "moe_clip_grads": ([P, P, P, i64, P, ctypes.c_float, P, P, P], i32),
         "moe_dense_mlp": ([P, P, P, P, i64, i32, i32, P, P, sz, P], i32),
         "moe_dense_mlp_prepared": ([P, P, P, P, i64, i32, i32, P, P, sz, P], i32),
     }
@@ -611,6 +618,200 @@ def moe_gated_ffn_backward(dout, x, w_gate, w_up, w_down, gate, up, activation: 
     if status:
         _check(status, "moe_gated_ffn_backward")
     return dx, dw_gate, dw_up, dw_down
+
+
+def _bf16_or_fp32(t, name):
+    if t.dtype is not _BF16 and t.dtype is not _F32:
+        raise ValueError(f"{name} must be bf16 or fp32, got {t.dtype}")
+    if t.dim() != 2:
+        _matrix(t, name)
+    return t.dtype
+
+
+def moe_layernorm(x, weight, bias=None, residual=None, eps: float = 1e-5, out=None,
+                  residual_out=None, mean=None, rstd=None):
+    """r = x + residual in their type (x without a residual), out = (r - mean(r))
+    / std(r) * weight + bias: returns (out [N, H], mean fp32 [N], rstd fp32 [N]).
+    r goes to ``residual_out``, or without one back to ``residual``.  bf16 or
+    fp32, the same for every array but the statistics."""
+    dtype = _bf16_or_fp32(x, "x")
+    shape = N, H = x.shape
+    dev = x.get_device()
+    if residual_out is None:
+        residual_out = residual
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    if mean is None:
+        mean = torch.empty(N, dtype=_F32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(N, dtype=_F32, device=x.device)
+    status = lib().moe_layernorm(
+        _typed(x, "x", dtype, shape, dev),
+        None if residual is None else _typed(residual, "residual", dtype, shape, dev),
+        _typed(weight, "weight", dtype, (H,), dev),
+        None if bias is None else _typed(bias, "bias", dtype, (H,), dev), dtype is _BF16, N, H,
+        eps,
+        None if residual_out is None else _typed(residual_out, "residual_out", dtype, shape, dev),
+        _typed(out, "out", dtype, shape, dev), _typed(mean, "mean", _F32, (N,), dev),
+        _typed(rstd, "rstd", _F32, (N,), dev), _stream_of(dev))
+    if status:
+        _check(status, "moe_layernorm")
+    return out, mean, rstd
+
+
+@functools.lru_cache(maxsize=256)
+def _layernorm_backward_workspace_bytes(N, H, device):
+    return int(lib().moe_layernorm_backward_workspace_bytes(N, H))
+
+
+def moe_layernorm_backward_workspace_bytes(N, H) -> int:
+    return int(lib().moe_layernorm_backward_workspace_bytes(N, H))
+
+
+def moe_layernorm_backward(dout, x, weight, mean, rstd, dresidual=None, dx=None, dweight=None,
+                           dbias=None, want_dbias: bool = True, workspace=None):
+    """(dx [N, H], dweight fp32 [H], dbias fp32 [H] or None) for the gradient
+    dout of moe_layernorm's out; x is what was normalised (the residual_out
+    where there was a residual), dresidual the gradient that reaches it by the
+    residual stream and is added to dx."""
+    dtype = _bf16_or_fp32(x, "x")
+    shape = N, H = x.shape
+    dev = x.get_device()
+    if dx is None:
+        dx = torch.empty(shape, dtype=dtype, device=x.device)
+    if dweight is None:
+        dweight = torch.empty(H, dtype=_F32, device=x.device)
+    if dbias is None and want_dbias:
+        dbias = torch.empty(H, dtype=_F32, device=x.device)
+    inputs = (_typed(dout, "dout", dtype, shape, dev), _typed(x, "x", dtype, shape, dev),
+              _typed(weight, "weight", dtype, (H,), dev), _typed(mean, "mean", _F32, (N,), dev),
+              _typed(rstd, "rstd", _F32, (N,), dev),
+              None if dresidual is None else _typed(dresidual, "dresidual", dtype, shape, dev))
+    outputs = (_typed(dx, "dx", dtype, shape, dev), _typed(dweight, "dweight", _F32, (H,), dev),
+               None if dbias is None else _typed(dbias, "dbias", _F32, (H,), dev))
+    stream = _stream_of(dev)
+    workspace, ws, bytes_ = _scratch(
+        workspace, lambda: _layernorm_backward_workspace_bytes(N, H, dev), x.device, dev)
+    status = lib().moe_layernorm_backward(*inputs, dtype is _BF16, N, H, *outputs, ws, bytes_,
+                                          stream)
+    if status:
+        _check(status, "moe_layernorm_backward")
+    return dx, dweight, dbias
+
+
+class GradSet:
+    """Gradient tensors as moe_grad_norm and moe_clip_grads take them, for a
+    program that keeps its gradients where they are: checked once, here, instead
+    of on every call.  ``grads``: contiguous bf16 and fp32 CUDA tensors of one
+    device; ``out``: where the clipped ones go, as many tensors of the same
+    numbers of values (either type), or None: in place.  The set keeps the
+    tensors; they keep their storage as long as it is used."""
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if len(self.out) != len(self.grads):
+            raise ValueError(f"out must have as many tensors as grads ({len(self.grads)}), got "
+                             f"{len(self.out)}")
+        self.device = self.grads[0].device if self.grads else None
+        self.index = self.grads[0].get_device() if self.grads else -1
+        self._sizes = array.array("q", [t.numel() for t in self.grads])
+        self._src, self._src_bf16 = self._pointers(self.grads, "grads")
+        self._dst, self._dst_bf16 = self._src, self._src_bf16
+        if self.out is not self.grads:
+            for i, (g, o) in enumerate(zip(self.grads, self.out)):
+                if g.numel() != o.numel():
+                    raise ValueError(f"out[{i}] must have {g.numel()} values like grads[{i}], "
+                                     f"got {o.numel()}")
+            self._dst, self._dst_bf16 = self._pointers(self.out, "out")
+        self._check_overlaps()
+        n = len(self.grads)
+        self._norm_args = (self._src.buffer_info()[0], self._sizes.buffer_info()[0],
+                           self._src_bf16, n)
+        self._out_args = (self._dst.buffer_info()[0], self._dst_bf16)
+
+    def _pointers(self, tensors, name):
+        for i, t in enumerate(tensors):
+            if ((t.dtype is not _BF16 and t.dtype is not _F32) or not t.is_contiguous()
+                    or not t.get_device() == self.index >= 0):
+                raise ValueError(
+                    f"{name}[{i}] must be a contiguous bf16 or fp32 CUDA tensor"
+                    f"{f' on cuda:{self.index} like the first' if self.index >= 0 else ''}, got "
+                    f"{t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+        return (array.array("Q", [t.data_ptr() for t in tensors]),
+                bytes([t.dtype is _BF16 for t in tensors]))
+
+    def _check_overlaps(self):
+        """No output may lie in another tensor (its own gradient apart)."""
+        spans = []
+        for i, n in enumerate(self._sizes):
+            if n == 0:
+                continue
+            dst, src = self._dst[i], self._src[i]
+            spans.append((dst, dst + n * (2 if self._dst_bf16[i] else 4), True, i))
+            if src != dst or self._src_bf16[i] != self._dst_bf16[i]:
+                spans.append((src, src + n * (2 if self._src_bf16[i] else 4), False, i))
+        spans.sort()
+        far_out = far = (0, 0, False, -1)  # the spans that reach farthest so far
+        for s in spans:
+            if s[0] < far_out[1] or (s[2] and s[0] < far[1]):
+                other = far_out if s[0] < far_out[1] else far
+                raise ValueError(f"tensors {other[3]} and {s[3]} overlap: a clipped gradient may "
+                                 "lie in its own gradient only")
+            if s[1] > far[1]:
+                far = s
+            if s[2] and s[1] > far_out[1]:
+                far_out = s
+
+
+def _grad_set(grads, out=None):
+    if isinstance(grads, GradSet):
+        if out is not None:
+            raise ValueError("a GradSet has its out tensors already")
+        return grads
+    return GradSet(grads, out)
+
+
+def moe_grad_norm_workspace_bytes(n) -> int:
+    return int(lib().moe_grad_norm_workspace_bytes(n))
+
+
+@functools.lru_cache(maxsize=256)
+def _grad_norm_workspace_bytes(n, device):
+    return int(lib().moe_grad_norm_workspace_bytes(n))
+
+
+def moe_grad_norm(grads, norm=None, workspace=None):
+    """sqrt of the sum of squares of all values of the tensors (a GradSet, or a
+    sequence of bf16 and fp32 CUDA tensors): norm fp32 [1], on the device."""
+    g = _grad_set(grads)
+    if not g.grads:
+        raise ValueError("grads must have at least one tensor")
+    if norm is None:
+        norm = torch.empty(1, dtype=_F32, device=g.device)
+    n = len(g.grads)
+    np_ = _typed(norm, "norm", _F32, (1,), g.index)
+    stream = _stream_of(g.index)
+    workspace, ws, bytes_ = _scratch(
+        workspace, lambda: _grad_norm_workspace_bytes(n, g.index), g.device, g.index)
+    status = lib().moe_grad_norm(*g._norm_args, np_, ws, bytes_, stream)
+    if status:
+        _check(status, "moe_grad_norm")
+    return norm
+
+
+def moe_clip_grads(grads, norm, max_norm: float, out=None):
+    """The tensors scaled by max_norm / norm where norm (moe_grad_norm's, on the
+    device) is above max_norm, in place or to ``out`` (bf16 or fp32, whatever the
+    gradients are); returns the list of scaled tensors."""
+    g = _grad_set(grads, out)
+    if not g.grads:
+        return []
+    status = lib().moe_clip_grads(*g._norm_args, _typed(norm, "norm", _F32, (1,), g.index),
+                                  max_norm, *g._out_args, _stream_of(g.index))
+    if status:
+        _check(status, "moe_clip_grads")
+    return g.out
 
 
 def moe_dense_mlp(x, w_gate, w_up, w_down, out=None, workspace=None):

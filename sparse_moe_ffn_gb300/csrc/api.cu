@@ -15,7 +15,9 @@
 
 #include "block_ops.cuh"
 #include "gated_ffn.cuh"
+#include "grad_clip.cuh"
 #include "kernels.cuh"
+#include "layernorm.cuh"
 #include "linear_gemm.cuh"
 #include "moe.h"
 
@@ -1770,6 +1772,159 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
         a.out[0] = dx;
         MOE_TRY(run_ffn(kFfnDx, d, a, sms, stream, "dx kernel launch"));
     }
+    return MOE_OK;
+}
+
+// ------------------------------------------- layer norm
+
+namespace {
+
+moe_status_t check_layernorm(int64_t N, int H) {
+    if (N < 0) return fail(MOE_ERR_INVALID_ARG, "N must be >= 0 (got %lld)", (long long)N);
+    if (H < 1) return fail(MOE_ERR_INVALID_ARG, "H must be >= 1 (got %d)", H);
+    if (H > kMaxNormH) return fail(MOE_ERR_UNSUPPORTED, "H must be <= %d (got %d)", kMaxNormH, H);
+    return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t moe_layernorm(const void *x, const void *residual, const void *weight,
+                           const void *bias, int bf16, int64_t N, int H, float eps,
+                           void *residual_out, void *out, float *mean, float *rstd,
+                           cudaStream_t stream) {
+    g_last_error.clear();
+    const moe_status_t st = check_layernorm(N, H);
+    if (st != MOE_OK) return st;
+    if (!(eps >= 0.f)) return fail(MOE_ERR_INVALID_ARG, "eps must be >= 0");
+    if (N == 0) return MOE_OK;
+    if (!x || !weight || !out)
+        return fail(MOE_ERR_INVALID_ARG, "x, weight and out must be non-null");
+    const uintptr_t size = bf16 ? 2 : 4;
+    if (!aligned_to(x, size) || !aligned_to(residual, size) || !aligned_to(weight, size) ||
+        !aligned_to(bias, size) || !aligned_to(residual_out, size) || !aligned_to(out, size) ||
+        !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+        return fail(MOE_ERR_INVALID_ARG, "arrays must be aligned to their types");
+    MOE_CUDA(launch_layernorm({x, residual, weight, bias, N, H, eps, residual_out, out, mean, rstd},
+                              bf16 ? 1 : 0, num_sms_of_current_device(), stream),
+             "layer norm kernel launch");
+    g_launches += 1;
+    return MOE_OK;
+}
+
+size_t moe_layernorm_backward_workspace_bytes(int64_t N, int H) {
+    if (check_layernorm(N, H) != MOE_OK) return 0;
+    const size_t blocks = layernorm_grad_blocks(N, H, num_sms_of_current_device());
+    return round_up(blocks * 2 * H * sizeof(float), kAlign);
+}
+
+moe_status_t moe_layernorm_backward(const void *dout, const void *x, const void *weight,
+                                    const float *mean, const float *rstd, const void *dresidual,
+                                    int bf16, int64_t N, int H, void *dx, float *dweight,
+                                    float *dbias, void *workspace, size_t workspace_bytes,
+                                    cudaStream_t stream) {
+    g_last_error.clear();
+    const moe_status_t st = check_layernorm(N, H);
+    if (st != MOE_OK) return st;
+    const uintptr_t size = bf16 ? 2 : 4;
+    if (!aligned_to(dout, size) || !aligned_to(x, size) || !aligned_to(weight, size) ||
+        !aligned_to(dresidual, size) || !aligned_to(dx, size) || !aligned_to(mean, 4) ||
+        !aligned_to(rstd, 4) || !aligned_to(dweight, 4) || !aligned_to(dbias, 4))
+        return fail(MOE_ERR_INVALID_ARG, "arrays must be aligned to their types");
+    if (N == 0) {  // sums over no tokens
+        if (dweight) MOE_CUDA(cudaMemsetAsync(dweight, 0, 4 * size_t(H), stream), "dweight reset");
+        if (dbias) MOE_CUDA(cudaMemsetAsync(dbias, 0, 4 * size_t(H), stream), "dbias reset");
+        return MOE_OK;
+    }
+    if (!dout || !x || !weight || !mean || !rstd)
+        return fail(MOE_ERR_INVALID_ARG, "dout, x, weight, mean and rstd must be non-null");
+    if (!dx && !dweight && !dbias) return MOE_OK;
+    const int sms = num_sms_of_current_device();
+    if (dweight || dbias) {
+        const size_t need = round_up(
+            static_cast<size_t>(layernorm_grad_blocks(N, H, sms)) * 2 * H * sizeof(float), kAlign);
+        MOE_TRY(check_workspace(workspace, workspace_bytes, need, "layer norm backward"));
+    }
+    int launches = 0;
+    MOE_CUDA(launch_layernorm_grad({dout, x, weight, dresidual, mean, rstd, N, H, dx, dweight,
+                                    dbias, static_cast<float *>(workspace)},
+                                   bf16 ? 1 : 0, sms, &launches, stream),
+             "layer norm backward kernel launch");
+    g_launches += launches;
+    return MOE_OK;
+}
+
+// ------------------------------------------- gradient norm and clipping
+
+namespace {
+
+constexpr int64_t kMostGrads = int64_t(1) << 20;
+
+moe_status_t check_grads(const GradSet &g, bool out) {
+    if (g.n < 0) return fail(MOE_ERR_INVALID_ARG, "n must be >= 0 (got %lld)", (long long)g.n);
+    if (g.n > kMostGrads)
+        return fail(MOE_ERR_UNSUPPORTED, "n must be <= %lld (got %lld)", (long long)kMostGrads,
+                    (long long)g.n);
+    if (g.n > 0 && (!g.grads || !g.sizes || !g.bf16 || (out && (!g.out || !g.out_bf16))))
+        return fail(MOE_ERR_INVALID_ARG, "the host arrays must be non-null");
+    int64_t total = 0;
+    for (int64_t i = 0; i < g.n; ++i) {
+        if (g.sizes[i] < 0 || g.sizes[i] > (int64_t(1) << 40))
+            return fail(MOE_ERR_INVALID_ARG, "sizes[%lld] must be in [0, 2^40] (got %lld)",
+                        (long long)i, (long long)g.sizes[i]);
+        total += g.sizes[i];
+        // chunks of a launch are counted in 32 bits
+        if (total > (int64_t(1) << 42))
+            return fail(MOE_ERR_UNSUPPORTED, "more than 2^42 values in all");
+        if (g.sizes[i] == 0) continue;
+        if (!g.grads[i] || (out && !g.out[i]))
+            return fail(MOE_ERR_INVALID_ARG, "tensor %lld is null", (long long)i);
+        if (!aligned_to(g.grads[i], g.bf16[i] ? 2 : 4) ||
+            (out && !aligned_to(g.out[i], g.out_bf16[i] ? 2 : 4)))
+            return fail(MOE_ERR_INVALID_ARG, "tensor %lld must be aligned to its type",
+                        (long long)i);
+    }
+    return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_grad_norm_workspace_bytes(int64_t n) {
+    if (n < 0 || n > kMostGrads) return 0;
+    return round_up(sizeof(double) * grad_norm_parts(n > 0 ? n : 1, num_sms_of_current_device()),
+                    kAlign);
+}
+
+moe_status_t moe_grad_norm(const void *const *grads, const int64_t *sizes, const uint8_t *bf16,
+                           int64_t n, float *norm, void *workspace, size_t workspace_bytes,
+                           cudaStream_t stream) {
+    g_last_error.clear();
+    const GradSet g = {grads, sizes, bf16, n, nullptr, nullptr};
+    MOE_TRY(check_grads(g, false));
+    if (!norm || !aligned_to(norm, 4))
+        return fail(MOE_ERR_INVALID_ARG, "norm must be non-null and 4-byte aligned");
+    MOE_TRY(check_workspace(workspace, workspace_bytes, moe_grad_norm_workspace_bytes(n),
+                            "gradient norm"));
+    int launches = 0;
+    MOE_CUDA(launch_grad_norm(g, static_cast<double *>(workspace), norm,
+                              num_sms_of_current_device(), &launches, stream),
+             "gradient norm kernel launch");
+    g_launches += launches;
+    return MOE_OK;
+}
+
+moe_status_t moe_clip_grads(const void *const *grads, const int64_t *sizes, const uint8_t *bf16,
+                            int64_t n, const float *norm, float max_norm, void *const *out,
+                            const uint8_t *out_bf16, cudaStream_t stream) {
+    g_last_error.clear();
+    const GradSet g = {grads, sizes, bf16, n, out, out_bf16};
+    MOE_TRY(check_grads(g, true));
+    if (!norm || !aligned_to(norm, 4))
+        return fail(MOE_ERR_INVALID_ARG, "norm must be non-null and 4-byte aligned");
+    if (!(max_norm >= 0.f)) return fail(MOE_ERR_INVALID_ARG, "max_norm must be >= 0");
+    int launches = 0;
+    MOE_CUDA(launch_clip_grads(g, norm, max_norm, num_sms_of_current_device(), &launches, stream),
+             "clipping kernel launch");
+    g_launches += launches;
     return MOE_OK;
 }
 

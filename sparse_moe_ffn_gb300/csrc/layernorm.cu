@@ -1,0 +1,569 @@
+// layernorm.cu -- residual add + layer norm over rows of bf16 or fp32, and its
+// backward pass:
+//
+//   r    = x + residual, rounded to its type     (x itself without a residual)
+//   mean = sum(r) / H,  rstd = 1 / sqrt(sum((r - mean)^2) / H + eps)
+//   out  = (r - mean) rstd w + b
+//
+//   n = (r - mean) rstd,  t = dout w
+//   dx = rstd (t - mean(t) - n mean(t n)) + dresidual
+//   dw = sum over rows of dout n,  db = sum over rows of dout
+//
+// The row stays in registers, so the variance is the sum of the squared
+// deviations themselves, whatever the mean is.  In the backward pass a thread
+// keeps its columns' two sums over the block's rows in registers as well; the
+// blocks' sums are added in 64 bits, in a fixed order, by a second kernel.
+//
+// Rows whose length or arrays allow 16-byte accesses take them, others go value
+// by value.
+#include <cuda_bf16.h>
+
+#include <initializer_list>
+
+#include "kernels.cuh"
+#include "layernorm.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+// kVec neighbouring values of a row, as they lie in memory.
+template <typename T, int kVec>
+struct Piece;
+template <>
+struct Piece<__nv_bfloat16, 8> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        u = __ldcg(reinterpret_cast<const uint4 *>(p));
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+        *reinterpret_cast<uint4 *>(p) = u;
+    }
+    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y), c = unpack_bf16x2(u.z),
+                     d = unpack_bf16x2(u.w);
+        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+        v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
+    }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+        u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7]));
+    }
+};
+template <>
+struct Piece<float, 4> {
+    float4 f;
+    __device__ __forceinline__ void load(const float *p) {
+        f = __ldcg(reinterpret_cast<const float4 *>(p));
+    }
+    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float4 *>(p) = f; }
+    __device__ __forceinline__ void zero() { f = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    }
+    __device__ __forceinline__ void set(const float (&v)[4]) {
+        f = make_float4(v[0], v[1], v[2], v[3]);
+    }
+};
+template <>
+struct Piece<__nv_bfloat16, 1> {
+    uint16_t u;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        u = __ldcg(reinterpret_cast<const uint16_t *>(p));
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+        *reinterpret_cast<uint16_t *>(p) = u;
+    }
+    __device__ __forceinline__ void zero() { u = 0; }
+    __device__ __forceinline__ void get(float (&v)[1]) const {
+        v[0] = __uint_as_float(static_cast<uint32_t>(u) << 16);
+    }
+    __device__ __forceinline__ void set(const float (&v)[1]) {
+        u = static_cast<uint16_t>(pack_bf16x2(v[0], 0.f));
+    }
+};
+template <>
+struct Piece<float, 1> {
+    float f;
+    __device__ __forceinline__ void load(const float *p) { f = __ldcg(p); }
+    __device__ __forceinline__ void store(float *p) const { *p = f; }
+    __device__ __forceinline__ void zero() { f = 0.f; }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = f; }
+    __device__ __forceinline__ void set(const float (&v)[1]) { f = v[0]; }
+};
+
+// Sums of kSums values over the kRow threads of a row (all of the block's
+// threads take part, each row of its own).
+template <int kRow, int kRows, int kSums>
+struct RowSums {
+    float part[2][kRows][kRow / 32][kSums];
+};
+
+template <int kRow, int kRows, int kSums>
+__device__ __forceinline__ void row_sums(RowSums<kRow, kRows, kSums> &sm, int turn, int t, int sub,
+                                         float (&v)[kSums]) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+    if (kRow == 32) return;
+    // two buffers in turn: a warp can be one sum ahead, never two
+    if (t % 32 == 0)
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) sm.part[turn][sub][t / 32][i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) v[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRow / 32; ++w)
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) v[i] += sm.part[turn][sub][w][i];
+}
+
+template <int kRow>
+__host__ __device__ constexpr int row_threads() {
+    return kRow < 256 ? 256 : kRow;
+}
+
+// kRow threads a row, kChunks pieces a thread (piece c of thread t holds values
+// [kVec (t + c kRow), + kVec)).
+template <typename T, int kVec, int kRow, int kChunks>
+__global__ void __launch_bounds__(row_threads<kRow>())
+    layernorm_kernel(const LayerNormArgs a) {
+    constexpr int kRows = row_threads<kRow>() / kRow;
+    __shared__ RowSums<kRow, kRows, 1> sums;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int t = threadIdx.x % kRow, sub = threadIdx.x / kRow;
+    const int pieces = a.H / kVec;
+    const float inv_h = 1.f / static_cast<float>(a.H);
+    const T *x = static_cast<const T *>(a.x), *residual = static_cast<const T *>(a.residual);
+    const T *weight = static_cast<const T *>(a.weight), *bias = static_cast<const T *>(a.bias);
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kRows; base < a.N;
+         base += static_cast<int64_t>(gridDim.x) * kRows) {
+        const int64_t n = base + sub;
+        const bool row = n < a.N;
+        const int64_t at = n * a.H;
+        Piece<T, kVec> r[kChunks];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            r[c].zero();
+            if (row && t + c * kRow < pieces) r[c].load(x + at + kVec * (t + c * kRow));
+        }
+        if (residual) {
+            Piece<T, kVec> b[kChunks];
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                b[c].zero();
+                if (row && t + c * kRow < pieces) b[c].load(residual + at + kVec * (t + c * kRow));
+            }
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                float u[kVec], v[kVec];
+                r[c].get(u);
+                b[c].get(v);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) u[i] += v[i];
+                r[c].set(u);
+                if (a.residual_out && row && t + c * kRow < pieces)
+                    r[c].store(static_cast<T *>(a.residual_out) + at + kVec * (t + c * kRow));
+            }
+        } else if (a.residual_out) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+                if (row && t + c * kRow < pieces)
+                    r[c].store(static_cast<T *>(a.residual_out) + at + kVec * (t + c * kRow));
+        }
+        float s[1] = {0.f};
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            float v[kVec];
+            r[c].get(v);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) s[0] += v[i];
+        }
+        row_sums(sums, 0, t, sub, s);
+        const float mean = s[0] * inv_h;
+        s[0] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            if (t + c * kRow >= pieces) break;
+            float v[kVec];
+            r[c].get(v);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) s[0] = fmaf(v[i] - mean, v[i] - mean, s[0]);
+        }
+        row_sums(sums, 1, t, sub, s);
+        if (!row) continue;
+        const float rstd = 1.f / sqrtf(fmaf(s[0], inv_h, a.eps));
+        if (t == 0) {
+            if (a.mean) a.mean[n] = mean;
+            if (a.rstd) a.rstd[n] = rstd;
+        }
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            if (t + c * kRow >= pieces) break;
+            const int h = kVec * (t + c * kRow);
+            Piece<T, kVec> w, b;
+            w.load(weight + h);
+            float v[kVec], g[kVec], z[kVec];
+            r[c].get(v);
+            w.get(g);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) z[i] = 0.f;
+            if (bias) {
+                b.load(bias + h);
+                b.get(z);
+            }
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) v[i] = fmaf((v[i] - mean) * rstd, g[i], z[i]);
+            r[c].set(v);
+            r[c].store(static_cast<T *>(a.out) + at + h);
+        }
+    }
+}
+
+// kSumColumns: the block keeps its columns' sums (dweight, dbias) and stores
+// them as part blockIdx.x.
+template <typename T, int kVec, int kRow, int kChunks, bool kSumColumns>
+__global__ void __launch_bounds__(row_threads<kRow>())
+    layernorm_grad_kernel(const LayerNormGradArgs a) {
+    constexpr int kThreads = row_threads<kRow>();
+    constexpr int kRows = kThreads / kRow;
+    constexpr int kCols = kVec * kChunks;  // a thread's
+    __shared__ RowSums<kRow, kRows, 2> sums;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int t = threadIdx.x % kRow, sub = threadIdx.x / kRow;
+    const int pieces = a.H / kVec;
+    const float inv_h = 1.f / static_cast<float>(a.H);
+    const T *dout = static_cast<const T *>(a.dout), *x = static_cast<const T *>(a.x);
+    const T *dres = static_cast<const T *>(a.dresidual);
+    Piece<T, kVec> w[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        w[c].zero();
+        if (t + c * kRow < pieces)
+            w[c].load(static_cast<const T *>(a.weight) + kVec * (t + c * kRow));
+    }
+    float dw[kSumColumns ? kCols : 1] = {}, db[kSumColumns ? kCols : 1] = {};
+    int turn = 0;
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kRows; base < a.N;
+         base += static_cast<int64_t>(gridDim.x) * kRows, turn ^= 1) {
+        const int64_t n = base + sub;
+        const bool row = n < a.N;
+        const int64_t at = n * a.H;
+        Piece<T, kVec> r[kChunks], d[kChunks], e[kChunks];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            r[c].zero();
+            d[c].zero();
+            if (row && t + c * kRow < pieces) {
+                r[c].load(x + at + kVec * (t + c * kRow));
+                d[c].load(dout + at + kVec * (t + c * kRow));
+            }
+        }
+        if (dres) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                e[c].zero();
+                if (row && t + c * kRow < pieces) e[c].load(dres + at + kVec * (t + c * kRow));
+            }
+        }
+        const float mean = row ? __ldcg(a.mean + n) : 0.f, rstd = row ? __ldcg(a.rstd + n) : 0.f;
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            if (!row || t + c * kRow >= pieces) break;
+            float v[kVec], g[kVec], y[kVec];
+            r[c].get(v);
+            d[c].get(y);
+            w[c].get(g);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const float m = (v[i] - mean) * rstd;
+                if (kSumColumns) {
+                    dw[c * kVec + i] = fmaf(y[i], m, dw[c * kVec + i]);
+                    db[c * kVec + i] += y[i];
+                }
+                const float u = y[i] * g[i];
+                s[0] += u;
+                s[1] = fmaf(u, m, s[1]);
+            }
+        }
+        if (!a.dx) continue;
+        row_sums(sums, turn, t, sub, s);
+        if (!row) continue;
+        const float m1 = s[0] * inv_h, m2 = s[1] * inv_h;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            if (t + c * kRow >= pieces) break;
+            float v[kVec], g[kVec], y[kVec], z[kVec];
+            r[c].get(v);
+            d[c].get(y);
+            w[c].get(g);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) z[i] = 0.f;
+            if (dres) e[c].get(z);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const float m = (v[i] - mean) * rstd;
+                v[i] = fmaf(rstd, fmaf(-m, m2, fmaf(y[i], g[i], -m1)), z[i]);
+            }
+            r[c].set(v);
+            r[c].store(static_cast<T *>(a.dx) + at + kVec * (t + c * kRow));
+        }
+    }
+    if (!kSumColumns) return;
+    // the rows of the block side by side, then the block's part
+    float *out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
+    if constexpr (kRows > 1) {
+        __shared__ float side[kRows / 2][kRow * kCols];
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            float *v = which ? db : dw;
+            for (int half = kRows / 2; half > 0; half /= 2) {
+                __syncthreads();
+                if (sub >= half && sub < 2 * half)
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i) side[sub - half][i * kRow + t] = v[i];
+                __syncthreads();
+                if (sub < half)
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i) v[i] += side[sub][i * kRow + t];
+            }
+        }
+        if (sub > 0) return;
+    }
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        if (t + c * kRow >= pieces) break;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int h = kVec * (t + c * kRow) + i;
+            __stcg(out + h, dw[c * kVec + i]);
+            __stcg(out + a.H + h, db[c * kVec + i]);
+        }
+    }
+}
+
+// Rows too long for their sums in registers: a thread a column, a block a run
+// of rows (part blockIdx.y).
+constexpr int kColumnThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kColumnThreads)
+    layernorm_columns_kernel(const LayerNormGradArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int h = blockIdx.x * kColumnThreads + threadIdx.x;
+    if (h >= a.H) return;
+    const int64_t first = a.N * blockIdx.y / gridDim.y, end = a.N * (blockIdx.y + 1) / gridDim.y;
+    float dw = 0.f, db = 0.f;
+#pragma unroll 8
+    for (int64_t n = first; n < end; ++n) {
+        Piece<T, 1> r, d;
+        r.load(static_cast<const T *>(a.x) + n * a.H + h);
+        d.load(static_cast<const T *>(a.dout) + n * a.H + h);
+        float v[1], y[1];
+        r.get(v);
+        d.get(y);
+        dw = fmaf(y[0], (v[0] - __ldcg(a.mean + n)) * __ldcg(a.rstd + n), dw);
+        db += y[0];
+    }
+    float *out = a.part + static_cast<int64_t>(blockIdx.y) * 2 * a.H;
+    __stcg(out + h, dw);
+    __stcg(out + a.H + h, db);
+}
+
+// The parts' sum, in order and in 64 bits: 32 columns a block, 8 warps taking
+// the parts in turn.
+constexpr int kFinishThreads = 256;
+
+__global__ void __launch_bounds__(kFinishThreads)
+    layernorm_finish_kernel(const float *part, int blocks, int H, float *dweight, float *dbias) {
+    constexpr int kWarps = kFinishThreads / 32;
+    __shared__ double sums[kWarps][32];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;  // of the 2 H sums
+    double s = 0.0;
+    if (i < 2 * static_cast<int64_t>(H)) {
+        int b = warp;
+        for (; b + 3 * kWarps < blocks; b += 4 * kWarps) {
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = __ldcg(part + static_cast<int64_t>(b + j * kWarps) * 2 * H + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s += v[j];
+        }
+        for (; b < blocks; b += kWarps) s += __ldcg(part + static_cast<int64_t>(b) * 2 * H + i);
+    }
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp != 0 || i >= 2 * static_cast<int64_t>(H)) return;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) s += sums[w][lane];
+    float *out = i < H ? dweight : dbias;
+    if (out) out[i < H ? i : i - H] = static_cast<float>(s);
+}
+
+// ---------------------------------------------------------------- launchers
+
+// Blocks of a kernel that fit at once.
+template <typename Kernel>
+int resident(Kernel kern, int threads, int num_sms) {
+    int n = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0);
+    return (n > 0 ? n : 1) * num_sms;
+}
+
+template <typename T, int kVec, int kRow, int kChunks>
+cudaError_t launch_rows(const LayerNormArgs &a, int num_sms, cudaStream_t s) {
+    constexpr int kRows = row_threads<kRow>() / kRow;
+    auto kern = layernorm_kernel<T, kVec, kRow, kChunks>;
+    static const int fit = resident(kern, row_threads<kRow>(), 1);
+    int64_t blocks = (a.N + kRows - 1) / kRows;
+    const int64_t limit = static_cast<int64_t>(fit) * num_sms * 4;
+    if (blocks > limit) blocks = limit;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(row_threads<kRow>()), 0, s, 1,
+                      a);
+}
+
+template <typename T, int kVec>
+cudaError_t launch_forward(const LayerNormArgs &a, int num_sms, cudaStream_t s) {
+    const int pieces = a.H / kVec;
+    if (pieces <= 32) return launch_rows<T, kVec, 32, 1>(a, num_sms, s);
+    if (pieces <= 64) return launch_rows<T, kVec, 32, 2>(a, num_sms, s);
+    if (pieces <= 128) return launch_rows<T, kVec, 64, 2>(a, num_sms, s);
+    if (pieces <= 256) return launch_rows<T, kVec, 128, 2>(a, num_sms, s);
+    if (pieces <= 512) return launch_rows<T, kVec, 256, 2>(a, num_sms, s);
+    if (pieces <= 1024) return launch_rows<T, kVec, 256, 4>(a, num_sms, s);
+    if (pieces <= 2048) return launch_rows<T, kVec, 512, 4>(a, num_sms, s);
+    if (pieces <= 4096) return launch_rows<T, kVec, 1024, 4>(a, num_sms, s);
+    if (pieces <= 8192) return launch_rows<T, kVec, 1024, 8>(a, num_sms, s);
+    if constexpr (kVec <= 4) {
+        if (pieces <= 16384) return launch_rows<T, kVec, 1024, 16>(a, num_sms, s);
+    }
+    if constexpr (kVec == 1) return launch_rows<T, kVec, 1024, 64>(a, num_sms, s);
+    return cudaErrorInvalidValue;
+}
+
+template <typename T, int kVec, int kRow, int kChunks, bool kSum>
+cudaError_t launch_grad_rows(const LayerNormGradArgs &a, int64_t blocks, cudaStream_t s) {
+    constexpr int kRows = row_threads<kRow>() / kRow;
+    const int64_t most = (a.N + kRows - 1) / kRows;
+    if (blocks > most) blocks = most;
+    return launch_pdl(layernorm_grad_kernel<T, kVec, kRow, kChunks, kSum>,
+                      dim3(static_cast<unsigned>(blocks)), dim3(row_threads<kRow>()), 0, s, 1, a);
+}
+
+// 16 columns a thread (8 in rows of fewer than 512)
+template <typename T, int kVec>
+cudaError_t launch_backward(const LayerNormGradArgs &a, int64_t blocks, cudaStream_t s) {
+    const int pieces = a.H / kVec;
+    constexpr int kC = 16 / kVec;
+    if (pieces <= 16 * kC) return launch_grad_rows<T, kVec, 32, kC / 2, true>(a, blocks, s);
+    if (pieces <= 32 * kC) return launch_grad_rows<T, kVec, 32, kC, true>(a, blocks, s);
+    if (pieces <= 64 * kC) return launch_grad_rows<T, kVec, 64, kC, true>(a, blocks, s);
+    if (pieces <= 128 * kC) return launch_grad_rows<T, kVec, 128, kC, true>(a, blocks, s);
+    if (pieces <= 256 * kC) return launch_grad_rows<T, kVec, 256, kC, true>(a, blocks, s);
+    return launch_grad_rows<T, kVec, 512, kC, true>(a, blocks, s);
+}
+
+template <typename T, int kVec>
+cudaError_t launch_backward_wide(const LayerNormGradArgs &a, int64_t blocks, cudaStream_t s) {
+    const int pieces = a.H / kVec;
+    if (pieces <= 2048) return launch_grad_rows<T, kVec, 512, 4, false>(a, blocks, s);
+    if (pieces <= 4096) return launch_grad_rows<T, kVec, 1024, 4, false>(a, blocks, s);
+    if (pieces <= 8192) return launch_grad_rows<T, kVec, 1024, 8, false>(a, blocks, s);
+    if constexpr (kVec <= 4) {
+        if (pieces <= 16384) return launch_grad_rows<T, kVec, 1024, 16, false>(a, blocks, s);
+    }
+    if constexpr (kVec == 1) return launch_grad_rows<T, kVec, 1024, 64, false>(a, blocks, s);
+    return cudaErrorInvalidValue;
+}
+
+constexpr int kSumColumnsH = 8192;  // longest row whose sums stay in registers
+
+bool vectors(int H, int bf16, std::initializer_list<const void *> arrays) {
+    if (H % (bf16 ? 8 : 4)) return false;
+    for (const void *p : arrays)
+        if (reinterpret_cast<uintptr_t>(p) % 16) return false;
+    return true;
+}
+
+int rows_a_block(int H) {
+    // what launch_backward takes: 256 threads, 16 columns a thread (8 up to 256)
+    const int threads = H <= 512 ? 32 : H <= 1024 ? 64 : H <= 2048 ? 128 : 256;
+    return 256 / threads;
+}
+
+}  // namespace
+
+int layernorm_grad_blocks(int64_t N, int H, int num_sms) {
+    if (H <= kSumColumnsH) {
+        const int64_t rows = rows_a_block(H), blocks = (N + rows - 1) / rows;
+        const int64_t most = 2 * static_cast<int64_t>(num_sms);
+        return static_cast<int>(blocks < most ? blocks : most);
+    }
+    const int64_t columns = (H + kColumnThreads - 1) / kColumnThreads;
+    int64_t runs = 4 * static_cast<int64_t>(num_sms) / columns;
+    if (runs > (N + 15) / 16) runs = (N + 15) / 16;
+    return static_cast<int>(runs > 1 ? runs : 1);
+}
+
+cudaError_t launch_layernorm(const LayerNormArgs &a, int bf16, int num_sms, cudaStream_t s) {
+    const bool vec = vectors(a.H, bf16, {a.x, a.residual, a.weight, a.bias, a.residual_out, a.out});
+    if (bf16)
+        return vec ? launch_forward<__nv_bfloat16, 8>(a, num_sms, s)
+                   : launch_forward<__nv_bfloat16, 1>(a, num_sms, s);
+    return vec ? launch_forward<float, 4>(a, num_sms, s) : launch_forward<float, 1>(a, num_sms, s);
+}
+
+cudaError_t launch_layernorm_grad(const LayerNormGradArgs &a, int bf16, int num_sms, int *launches,
+                                  cudaStream_t s) {
+    const bool vec = vectors(a.H, bf16, {a.dout, a.x, a.weight, a.dresidual, a.dx});
+    const int blocks = layernorm_grad_blocks(a.N, a.H, num_sms);
+    const bool sums = a.dweight || a.dbias;
+    cudaError_t err = cudaSuccess;
+    if (a.H <= kSumColumnsH) {
+        if (bf16)
+            err = vec ? launch_backward<__nv_bfloat16, 8>(a, blocks, s)
+                      : launch_backward<__nv_bfloat16, 1>(a, blocks, s);
+        else
+            err = vec ? launch_backward<float, 4>(a, blocks, s)
+                      : launch_backward<float, 1>(a, blocks, s);
+        *launches += 1;
+    } else {
+        if (sums) {  // first: dx may be one of the inputs
+            const dim3 grid(static_cast<unsigned>((a.H + kColumnThreads - 1) / kColumnThreads),
+                            static_cast<unsigned>(blocks));
+            err = bf16 ? launch_pdl(layernorm_columns_kernel<__nv_bfloat16>, grid,
+                                    dim3(kColumnThreads), 0, s, 1, a)
+                       : launch_pdl(layernorm_columns_kernel<float>, grid, dim3(kColumnThreads), 0,
+                                    s, 1, a);
+            *launches += 1;
+        }
+        if (err == cudaSuccess && a.dx) {
+            const int64_t most = 4 * static_cast<int64_t>(num_sms);
+            if (bf16)
+                err = vec ? launch_backward_wide<__nv_bfloat16, 8>(a, most, s)
+                          : launch_backward_wide<__nv_bfloat16, 1>(a, most, s);
+            else
+                err = vec ? launch_backward_wide<float, 4>(a, most, s)
+                          : launch_backward_wide<float, 1>(a, most, s);
+            *launches += 1;
+        }
+    }
+    if (err != cudaSuccess || !sums) return err;
+    *launches += 1;
+    return launch_pdl(layernorm_finish_kernel, dim3((2 * a.H + 31) / 32), dim3(kFinishThreads), 0,
+                      s, 1, static_cast<const float *>(a.part), blocks, a.H, a.dweight, a.dbias);
+}
+
+}  // namespace moe
