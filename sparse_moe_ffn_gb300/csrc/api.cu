@@ -1669,6 +1669,17 @@ moe_status_t moe_gated_ffn(const moe_bf16_t *x, const moe_bf16_t *w_gate, const 
     a.part = reinterpret_cast<float *>(ws + L.part);
     a.status = reinterpret_cast<int32_t *>(ws);
     a.reset_status = 1;
+    if (ffn_rows_fit(N, H) && ffn_rows_fit(N, I)) {
+        a.out[0] = h;
+        MOE_CUDA(launch_ffn_rows(kFfnGateUp, a, x, w_gate, w_up, gate, up, stream),
+                 "gate and up kernel launch");
+        a.residual = residual;
+        a.out[0] = out;
+        MOE_CUDA(launch_ffn_rows(kFfnDown, a, h, w_down, nullptr, nullptr, nullptr, stream),
+                 "down kernel launch");
+        g_launches += 2;
+        return MOE_OK;
+    }
     FfnMaps m = {};
     MOE_TRY(ffn_operand(&m.a[0], x, N, H, false, "x"));
     MOE_TRY(ffn_operand(&m.b[0], w_gate, I, H, false, "w_gate"));
@@ -1730,14 +1741,14 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
     a.H = H;
     a.I = I;
     a.act = act;
-    a.gate = gate;
-    a.up = up;
     a.part = reinterpret_cast<float *>(ws + L.part);
     a.status = reinterpret_cast<int32_t *>(ws);
     a.reset_status = 1;
     FfnMaps m = {};
     MOE_TRY(ffn_operand(&m.a[0], dout, N, H, false, "dout"));
     MOE_TRY(ffn_operand(&m.b[0], w_down, H, I, true, "w_down"));
+    MOE_TRY(ffn_out(&m.a[1], gate, N, I, "gate"));
+    MOE_TRY(ffn_out(&m.a[2], up, N, I, "up"));
     MOE_TRY(ffn_out(&m.out[0], h, N, I, "h"));
     MOE_TRY(ffn_out(&m.out[1], dgate, N, I, "dgate"));
     MOE_TRY(ffn_out(&m.out[2], dup, N, I, "dup"));

@@ -40,22 +40,22 @@ namespace {
 
 constexpr int kEpiWarps = 8;
 constexpr int kFfnThreads = 64 + 32 * kEpiWarps;
-constexpr int kStages = 5;
 constexpr int kBN = 256;               // columns of a tile
 constexpr int kSliceK = 64;            // values of K in a slice
 constexpr int kOperandBytes = 128 * kSliceBytes;  // a CTA's share of a slice, either side
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMnChunk = 64 * kSliceBytes;  // MN-major: 64 rows, 64 values of K
 constexpr int kOutBytes = 2048;        // 32 x 32 bf16 on their way out
-constexpr int kOutBuffers = 3;         // a warp's
+constexpr int kMostStages = 5;
 constexpr int kMinSlices = 8;          // of a part of a tile
 
 struct FfnShared {
-    uint64_t full[kStages];   // even CTA: both CTAs' bytes of a stage landed
-    uint64_t empty[kStages];  // both: the MMAs are done with a stage
+    uint64_t full[kMostStages];   // even CTA: both CTAs' bytes of a stage landed
+    uint64_t empty[kMostStages];  // both: the MMAs are done with a stage
     uint64_t acc_full[2];     // both: an accumulator is complete
     uint64_t acc_empty[2];    // even CTA: both CTAs' epilogues have read one
     uint64_t drain;           // even CTA: every MMA has completed
+    uint64_t saved[kEpiWarps][2];  // (dh) a warp's gate and up landed
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -65,6 +65,12 @@ struct FfnTraits {
     static constexpr bool kAMn = kOp == kFfnDw;
     static constexpr bool kBMn = kOp == kFfnDh || kOp == kFfnDx || kOp == kFfnDw;
     static constexpr int kColsPerTile = kOp == kFfnGateUp ? kBN / 2 : kBN;  // of the output
+    // three values a column leave the epilogue, or one; the buffers of a warp,
+    // two sets in turn, and the stages that then fit
+    static constexpr int kSet = kOp == kFfnGateUp || kOp == kFfnDh ? 3 : 1;
+    static constexpr int kStages = kSet == 3 ? 4 : kMostStages;
+    static constexpr size_t kShared = 1024 + static_cast<size_t>(kStages) * kStageBytes +
+                                      kEpiWarps * 2 * kSet * kOutBytes + sizeof(FfnShared);
 };
 
 // Shared memory descriptor of an MN-major operand: rows of 64 values along MN
@@ -195,6 +201,18 @@ struct Row32 {
             w[4 * i + 3] = u.w;
         }
     }
+    // this lane's row of a 32 x 32 chunk that a tensor map's load brought
+    __device__ __forceinline__ void read(const uint8_t *buf, int lane) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(buf + lane * 64 +
+                                                             16 * (i ^ ((lane >> 1) & 3)));
+            w[4 * i] = u.x;
+            w[4 * i + 1] = u.y;
+            w[4 * i + 2] = u.z;
+            w[4 * i + 3] = u.w;
+        }
+    }
     __device__ __forceinline__ void add_to(float (&v)[32]) const {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -266,11 +284,12 @@ template <FfnOp kOp>
 __global__ void __launch_bounds__(kFfnThreads, 1)
     ffn_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnArgs a) {
     using T = FfnTraits<kOp>;
+    constexpr int kStages = T::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t *out_bufs = tiles + kStages * kStageBytes;
-    FfnShared *sm = reinterpret_cast<FfnShared *>(out_bufs + kEpiWarps * kOutBuffers * kOutBytes);
+    FfnShared *sm = reinterpret_cast<FfnShared *>(out_bufs + kEpiWarps * 2 * T::kSet * kOutBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = static_cast<int>(cluster_ctarank());
     const bool leader = rank == 0;
@@ -285,6 +304,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             mbar_init(&sm->acc_empty[i], 2 * kEpiWarps);
         }
         mbar_init(&sm->drain, 1);
+        if (kOp == kFfnDh)
+            for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(&sm->saved[0][0] + i, 1);
         sm->abort_flag = 0;
         fence_barrier_init();
         prefetch_tensor_map(&maps.a[0]);
@@ -297,8 +318,9 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = sm->tmem_base;
     volatile int *abort_flag = &sm->abort_flag;
-    griddep_launch_dependents();
+    // in this order: what follows may read weights before its own wait
     griddep_wait();
+    griddep_launch_dependents();
     if (a.reset_status && blockIdx.x == 0 && threadIdx.x == 0 && a.status) *a.status = MOE_OK;
 
     const int pair = blockIdx.x / 2;
@@ -423,7 +445,36 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         constexpr int kCols = T::kColsPerTile / 2;  // a warp's
         const uint32_t empty0 = map_to_rank(smem_addr(&sm->acc_empty[0]), 0);
         const uint32_t empty1 = map_to_rank(smem_addr(&sm->acc_empty[1]), 0);
-        uint8_t *buf = out_bufs + ew * kOutBuffers * kOutBytes;
+        uint8_t *buf = out_bufs + ew * 2 * T::kSet * kOutBytes;
+        // (dh) gate and up of a chunk come into the buffers that dgate and dup
+        // leave from, one chunk ahead of their use; `ahead` runs through the
+        // chunks for them
+        FfnWalk ahead(a.plan, pair);
+        int ahead_c = 0, ahead_cols = 0, ahead_c0 = 0, ahead_r0 = 0, fetched = 0;
+        auto fetch_saved = [&] {
+            while (ahead_c >= ahead_cols) {
+                FfnItem n;
+                if (!ahead.next(n)) return;
+                const FfnTile t = ffn_tile<kOp>(a, n.tile);
+                ahead_r0 = t.m * kFfnTile + rank * 128 + quarter * 32;
+                ahead_c0 = t.n * T::kColsPerTile + half * kCols;
+                ahead_cols = ahead_r0 < a.N ? min(kCols, a.I - ahead_c0) : 0;
+                ahead_c = 0;
+            }
+            if (lane == 0) {
+                uint8_t *b = buf + (fetched & 1) * T::kSet * kOutBytes;
+                uint64_t *bar = &sm->saved[ew][fetched & 1];
+                mbar_arrive_expect_tx(bar, 2 * kOutBytes);
+                tma_load_2d(b + kOutBytes, &maps.a[1], bar, ahead_c0 + ahead_c, ahead_r0);
+                tma_load_2d(b + 2 * kOutBytes, &maps.a[2], bar, ahead_c0 + ahead_c, ahead_r0);
+            }
+            ahead_c += 32;
+            ++fetched;
+        };
+        if (kOp == kFfnDh) {
+            fetch_saved();
+            fetch_saved();
+        }
         int n = 0, chunk = 0;
         for (; walk.next(it); ++n) {
             const FfnTile t = ffn_tile<kOp>(a, it.tile);
@@ -436,17 +487,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             const int64_t r = r0 + lane;
             // columns of this warp that exist (warp-uniform)
             const int cols = r0 < rows ? min(kCols, all_cols - c0) : 0;
-            // operands of the elementwise part, read 32 columns ahead
-            Row32 e0, e1;
+            // the residual, read 32 columns ahead
+            Row32 res;
             auto fetch = [&](int c) {
-                if (c >= cols || r >= rows) return;
-                const int64_t at = r * all_cols + c0 + c;
-                if (kOp == kFfnDh) {
-                    e0.load(a.gate + at, cols - c);
-                    e1.load(a.up + at, cols - c);
-                }
-                if (kOp == kFfnDown && a.residual && it.slot < 0)
-                    e0.load(a.residual + at, cols - c);
+                if (kOp == kFfnDown && a.residual && it.slot < 0 && c < cols && r < rows)
+                    res.load(a.residual + r * all_cols + c0 + c, cols - c);
             };
             fetch(0);
             __syncwarp();
@@ -465,7 +510,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kBN + half * kCols;
             if (it.slot >= 0) {  // (kFfnDown, kFfnDx, kFfnDw)
                 float *part = a.part + it.slot * kFfnPartFloats +
-                              ((rank * 4 + quarter) * 8 + half * 4) * 1024 + lane;
+                              ((rank * 4 + quarter) * 8 + half * 4) * 1024 + 4 * lane;
 #pragma unroll 1
                 for (int c = 0; c < cols; c += 32, part += 1024) {
                     float v[32];
@@ -473,13 +518,15 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                     tmem_load32(taddr + c, v);
                     tmem_load_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) __stcg(part + 32 * i, v[i]);
+                    for (int i = 0; i < 8; ++i)
+                        __stcg(reinterpret_cast<float4 *>(part + 128 * i),
+                               make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
                 }
             } else {
 #pragma unroll 1
                 for (int c = 0; c < cols; c += 32, ++chunk) {
                     float v[32], w[32], x[32];
-                    int outs = 1;
+                    uint8_t *b = buf + (chunk & 1) * T::kSet * kOutBytes;
                     __syncwarp();  // TMEM wants whole warps
                     tmem_load32(taddr + c, v);
                     if (kOp == kFfnGateUp) {
@@ -494,55 +541,66 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                         act_all(a.act, x);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] *= w[i];
-                        outs = a.keep ? 3 : 1;
                     }
                     if (kOp == kFfnDh) {
-                        switch (a.act) {
-                            case MOE_ACT_SILU: gate_grads<MOE_ACT_SILU>(v, e0, e1, w, x); break;
-                            case MOE_ACT_GELU: gate_grads<MOE_ACT_GELU>(v, e0, e1, w, x); break;
-                            case MOE_ACT_GELU_TANH:
-                                gate_grads<MOE_ACT_GELU_TANH>(v, e0, e1, w, x);
-                                break;
-                            case MOE_ACT_RELU: gate_grads<MOE_ACT_RELU>(v, e0, e1, w, x); break;
-                            default: gate_grads<MOE_ACT_NONE>(v, e0, e1, w, x); break;
+                        if (!warp_wait(&sm->saved[ew][chunk & 1], (chunk >> 1) & 1, abort_flag)) {
+                            if (lane == 0) {
+                                record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+                                *abort_flag = 1;
+                            }
+                            ok = false;
+                            break;
                         }
-                        outs = 3;
+                        Row32 gate, up;
+                        gate.read(b + kOutBytes, lane);
+                        up.read(b + 2 * kOutBytes, lane);
+                        switch (a.act) {
+                            case MOE_ACT_SILU: gate_grads<MOE_ACT_SILU>(v, gate, up, w, x); break;
+                            case MOE_ACT_GELU: gate_grads<MOE_ACT_GELU>(v, gate, up, w, x); break;
+                            case MOE_ACT_GELU_TANH:
+                                gate_grads<MOE_ACT_GELU_TANH>(v, gate, up, w, x);
+                                break;
+                            case MOE_ACT_RELU: gate_grads<MOE_ACT_RELU>(v, gate, up, w, x); break;
+                            default: gate_grads<MOE_ACT_NONE>(v, gate, up, w, x); break;
+                        }
                     }
-                    if (kOp == kFfnDown && a.residual) e0.add_to(v);
+                    if (kOp == kFfnDown && a.residual) res.add_to(v);
                     fetch(c + 32);
-                    // one output: the buffers take turns; three: all have left
-                    uint8_t *b = buf;
-                    if (outs == 1) {
+                    // the set's last outputs have left (dh: before its gate and
+                    // up were fetched)
+                    if (kOp != kFfnDh) {
                         asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                        b += (chunk & 1) * kOutBytes;
-                    } else {
-                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    if (kOp == kFfnGateUp || kOp == kFfnDh) write_bf16_row(b, lane, x);
-                    else write_bf16_row(b, lane, v);
-                    if ((kOp == kFfnGateUp || kOp == kFfnDh) && outs == 3) {
+                    write_bf16_row(b, lane, T::kSet == 3 ? x : v);
+                    if (kOp == kFfnDh || (kOp == kFfnGateUp && a.keep)) {
                         write_bf16_row(b + kOutBytes, lane, v);
                         write_bf16_row(b + 2 * kOutBytes, lane, w);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_box(&maps.out[t.prod], b, c0 + c, static_cast<int>(r0));
-                        if (outs == 3) {
-                            tma_store_box(&maps.out[1], b + kOutBytes, c0 + c,
-                                          static_cast<int>(r0));
-                            tma_store_box(&maps.out[2], b + 2 * kOutBytes, c0 + c,
-                                          static_cast<int>(r0));
+                        const int row = static_cast<int>(r0);
+                        tma_store_box(&maps.out[t.prod], b, c0 + c, row);
+                        if (kOp == kFfnDh || (kOp == kFfnGateUp && a.keep)) {
+                            tma_store_box(&maps.out[1], b + kOutBytes, c0 + c, row);
+                            tma_store_box(&maps.out[2], b + 2 * kOutBytes, c0 + c, row);
                         }
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        if (kOp == kFfnDh)
+                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     }
+                    if (kOp == kFfnDh) fetch_saved();
                 }
+                if (!ok) break;
             }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) arrive_remote_relaxed(acc ? empty1 : empty0);
         }
+        // no copy may be in flight when the pair ends (after a failure too)
+        if (kOp == kFfnDh && lane == 0)
+            for (int i = chunk; i < fetched; ++i) drain_wait(&sm->saved[ew][i & 1], (i >> 1) & 1);
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // stores have landed
         __syncwarp();
     }
@@ -557,8 +615,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     }
 }
 
-// The shared tiles: a warp adds the parts of 32 x 32 values, in the order of
-// their slices, and stores them.
+// The shared tiles: a warp adds the parts of 32 rows x 8 columns, in the order
+// of their slices, and stores them.
 constexpr int kJoinThreads = 256;
 
 template <FfnOp kOp>
@@ -567,53 +625,66 @@ __global__ void __launch_bounds__(kJoinThreads)
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x % 32;
-    const int at = blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32;  // chunk of the tiles
-    const int local = at / 64, chunk = at % 64;  // 8 groups of 32 rows x 8 of 32 columns
+    const int at = blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32;
+    // 8 groups of 32 rows x 32 of 8 columns a tile
+    const int local = at / 256, chunk = at % 256 / 4, piece = at % 4;
     const FfnPlan &p = a.plan;
     const FfnTile t = ffn_tile<kOp>(a, p.whole + local);
     int64_t rows;
     int all_cols;
     ffn_dims<kOp>(a, t.prod, &rows, &all_cols);
     const int64_t r = static_cast<int64_t>(t.m) * kFfnTile + chunk / 8 * 32 + lane;
-    const int c0 = t.n * kBN + chunk % 8 * 32;
-    if (c0 >= all_cols || r - lane >= rows) return;
-    const int left = all_cols - c0;
-    Row32 res;
-    if (kOp == kFfnDown && a.residual && r < rows) res.load(a.residual + r * all_cols + c0, left);
+    const int c0 = t.n * kBN + chunk % 8 * 32 + piece * 8;
+    if (c0 >= all_cols || r >= rows) return;
+    const int64_t to = r * all_cols + c0;
+    uint4 res = make_uint4(0, 0, 0, 0);
+    if (kOp == kFfnDown && a.residual)
+        res = __ldcg(reinterpret_cast<const uint4 *>(a.residual + to));
     const int64_t slices = static_cast<int64_t>(p.tiles - p.whole) * p.nk;
-    const int64_t from = static_cast<int64_t>(local) * p.nk, to = from + p.nk;
-    // the first part that ends behind `from`
+    const int64_t from = static_cast<int64_t>(local) * p.nk, end = from + p.nk;
+    // the parts [q, last) reach into the tile
     int q = static_cast<int>(from * p.parts / slices);
     while (slices * (q + 1) / p.parts <= from) ++q;
     while (q > 0 && slices * q / p.parts > from) --q;
-    float v[32];
+    int last = q + 1;
+    while (last < p.parts && slices * last / p.parts < end) ++last;
+    const float *part = a.part + chunk * 1024 + piece * 256 + 4 * lane;
+    float v[8] = {};
+    // the first part's second tile, else a part's first
+    int slot = 2 * q + (slices * q / p.parts < from ? 1 : 0);
+    for (; q < last; q += 4) {
+        float4 f[4][2];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0.f;
-    for (; q < p.parts; ++q) {
-        const int64_t begin = slices * q / p.parts;
-        if (begin >= to) break;
-        const int slot = 2 * q + (begin < from ? 1 : 0);  // its second tile, or its first
-        const float *part = a.part + slot * kFfnPartFloats + chunk * 1024 + lane;
+        for (int j = 0; j < 4; ++j) {
+            if (q + j < last) {
+                const float *s = part + (j == 0 ? slot : 2 * (q + j)) * kFfnPartFloats;
+                f[j][0] = __ldcg(reinterpret_cast<const float4 *>(s));
+                f[j][1] = __ldcg(reinterpret_cast<const float4 *>(s + 128));
+            }
+        }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += __ldcg(part + 32 * i);
+        for (int j = 0; j < 4; ++j) {
+            if (q + j < last) {
+                v[0] += f[j][0].x, v[1] += f[j][0].y, v[2] += f[j][0].z, v[3] += f[j][0].w;
+                v[4] += f[j][1].x, v[5] += f[j][1].y, v[6] += f[j][1].z, v[7] += f[j][1].w;
+            }
+        }
+        slot = 2 * (q + 4);
     }
-    if (r >= rows) return;
-    if (kOp == kFfnDown && a.residual) res.add_to(v);
-    uint16_t *out = a.out[t.prod] + r * all_cols + c0;
+    const uint32_t *rp = reinterpret_cast<const uint32_t *>(&res);
+    uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (8 * i < left)
-            *reinterpret_cast<uint4 *>(out + 8 * i) =
-                make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]),
-                           pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                           pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
-                           pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack_bf16x2(rp[i]);
+        o[i] = kOp == kFfnDown ? pack_bf16x2(v[2 * i] + f.x, v[2 * i + 1] + f.y)
+                               : pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+    *reinterpret_cast<uint4 *>(a.out[t.prod] + to) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <FfnOp kOp>
 cudaError_t launch_op(const FfnMaps &maps, const FfnArgs &a, int *launches, cudaStream_t s) {
-    const size_t smem = 1024 + static_cast<size_t>(kStages) * kStageBytes +
-                        kEpiWarps * kOutBuffers * kOutBytes + sizeof(FfnShared);
+    const size_t smem = FfnTraits<kOp>::kShared;
     auto kern = ffn_kernel<kOp>;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t err = allow_shared(kern, smem, allowed);
@@ -623,10 +694,13 @@ cudaError_t launch_op(const FfnMaps &maps, const FfnArgs &a, int *launches, cuda
     if (err != cudaSuccess) return err;
     *launches += 1;
     if (a.plan.parts == 0) return cudaSuccess;
-    *launches += 1;
-    const int blocks = (a.plan.tiles - a.plan.whole) * (64 / (kJoinThreads / 32));
-    return launch_pdl(ffn_join_kernel<kOp>, dim3(static_cast<unsigned>(blocks)),
-                      dim3(kJoinThreads), 0, s, 1, a);
+    if constexpr (FfnTraits<kOp>::kSet == 1) {
+        *launches += 1;
+        const int blocks = (a.plan.tiles - a.plan.whole) * (256 / (kJoinThreads / 32));
+        return launch_pdl(ffn_join_kernel<kOp>, dim3(static_cast<unsigned>(blocks)),
+                          dim3(kJoinThreads), 0, s, 1, a);
+    }
+    return cudaSuccess;
 }
 
 int64_t up_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

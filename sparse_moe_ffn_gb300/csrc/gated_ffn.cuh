@@ -44,7 +44,6 @@ struct FfnArgs {
     int H, I;
     int act;
     int keep;                   // gate and up are stored
-    const uint16_t *gate, *up;  // kFfnDh
     const uint16_t *residual;   // kFfnDown, nullable
     uint16_t *out[3];           // the outputs (for the partial sums' join)
     float *part;                // [2 pairs][kFfnPartFloats]
@@ -54,7 +53,8 @@ struct FfnArgs {
 };
 
 // The operands' and outputs' tensor maps: a: the M side's, b: the N side's,
-// out: boxes of 32 x 32 values.  A K-major operand ([rows, K]) comes in boxes of
+// out: boxes of 32 x 32 values (kFfnDh: a[1] and a[2] are gate and up in such
+// boxes).  A K-major operand ([rows, K]) comes in boxes of
 // 64 values of K x its rows a CTA, an MN-major one ([K, rows]) in boxes of 64
 // rows x 64 values of K.
 struct FfnMaps {
@@ -66,5 +66,13 @@ size_t ffn_part_bytes(const FfnPlan &p);
 int ffn_block_n(FfnOp op);
 cudaError_t launch_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, int *launches,
                        cudaStream_t s);
+
+
+// Up to four tokens (ffn_rows.cu): kFfnGateUp (w0, w1: gate, up; their outputs
+// may be null) and kFfnDown (w0), outputs in a.out[0].
+constexpr int kFfnRowsTokens = 4;
+bool ffn_rows_fit(int64_t N, int K);
+cudaError_t launch_ffn_rows(FfnOp op, const FfnArgs &a, const uint16_t *x, const uint16_t *w0,
+                            const uint16_t *w1, uint16_t *gate, uint16_t *up, cudaStream_t s);
 
 }  // namespace moe
