@@ -1610,10 +1610,6 @@ moe_status_t ffn_operand(CUtensorMap *m, const void *base, int64_t rows, int col
                          mn ? 64 : 128, what);
 }
 
-moe_status_t ffn_out(CUtensorMap *m, const void *base, int64_t rows, int cols, const char *what) {
-    return make_rows_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, 32, 32, what);
-}
-
 moe_status_t run_ffn(FfnOp op, const FfnMaps &maps, FfnArgs a, int sms, cudaStream_t stream,
                      const char *what) {
     a.plan = ffn_plan(op, a.N, a.H, a.I, sms);
@@ -1684,19 +1680,17 @@ moe_status_t moe_gated_ffn(const moe_bf16_t *x, const moe_bf16_t *w_gate, const 
     MOE_TRY(ffn_operand(&m.a[0], x, N, H, false, "x"));
     MOE_TRY(ffn_operand(&m.b[0], w_gate, I, H, false, "w_gate"));
     MOE_TRY(ffn_operand(&m.b[1], w_up, I, H, false, "w_up"));
-    MOE_TRY(ffn_out(&m.out[0], h, N, I, "h"));
-    if (gate) {
-        MOE_TRY(ffn_out(&m.out[1], gate, N, I, "gate"));
-        MOE_TRY(ffn_out(&m.out[2], up, N, I, "up"));
-    }
     FfnMaps d = {};
     MOE_TRY(ffn_operand(&d.a[0], h, N, I, false, "h"));
     MOE_TRY(ffn_operand(&d.b[0], w_down, H, I, false, "w_down"));
-    MOE_TRY(ffn_out(&d.out[0], out, N, H, "out"));
+    a.out[0] = h;
+    a.out[1] = gate;
+    a.out[2] = up;
     MOE_TRY(run_ffn(kFfnGateUp, m, a, sms, stream, "gate and up kernel launch"));
     a.reset_status = 0;
     a.residual = residual;
     a.out[0] = out;
+    a.out[1] = a.out[2] = nullptr;
     return run_ffn(kFfnDown, d, a, sms, stream, "down kernel launch");
 }
 
@@ -1741,17 +1735,14 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
     a.H = H;
     a.I = I;
     a.act = act;
+    a.gate = gate;
+    a.up = up;
     a.part = reinterpret_cast<float *>(ws + L.part);
     a.status = reinterpret_cast<int32_t *>(ws);
     a.reset_status = 1;
     FfnMaps m = {};
     MOE_TRY(ffn_operand(&m.a[0], dout, N, H, false, "dout"));
     MOE_TRY(ffn_operand(&m.b[0], w_down, H, I, true, "w_down"));
-    MOE_TRY(ffn_out(&m.a[1], gate, N, I, "gate"));
-    MOE_TRY(ffn_out(&m.a[2], up, N, I, "up"));
-    MOE_TRY(ffn_out(&m.out[0], h, N, I, "h"));
-    MOE_TRY(ffn_out(&m.out[1], dgate, N, I, "dgate"));
-    MOE_TRY(ffn_out(&m.out[2], dup, N, I, "dup"));
     FfnMaps w = {}, d = {};
     if (weights) {
         MOE_TRY(ffn_operand(&w.a[0], dgate, N, I, true, "dgate"));
@@ -1760,17 +1751,16 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
         MOE_TRY(ffn_operand(&w.b[0], x, N, H, true, "x"));
         w.b[1] = w.b[0];
         MOE_TRY(ffn_operand(&w.b[2], h, N, I, true, "h"));
-        MOE_TRY(ffn_out(&w.out[0], dw_gate, I, H, "dw_gate"));
-        MOE_TRY(ffn_out(&w.out[1], dw_up, I, H, "dw_up"));
-        MOE_TRY(ffn_out(&w.out[2], dw_down, H, I, "dw_down"));
     }
     if (dx) {
         MOE_TRY(ffn_operand(&d.a[0], dgate, N, I, false, "dgate"));
         MOE_TRY(ffn_operand(&d.a[1], dup, N, I, false, "dup"));
         MOE_TRY(ffn_operand(&d.b[0], w_gate, I, H, true, "w_gate"));
         MOE_TRY(ffn_operand(&d.b[1], w_up, I, H, true, "w_up"));
-        MOE_TRY(ffn_out(&d.out[0], dx, N, H, "dx"));
     }
+    a.out[0] = h;
+    a.out[1] = dgate;
+    a.out[2] = dup;
     MOE_TRY(run_ffn(kFfnDh, m, a, sms, stream, "dh kernel launch"));
     a.reset_status = 0;
     if (weights) {
@@ -1781,6 +1771,7 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
     }
     if (dx) {
         a.out[0] = dx;
+        a.out[1] = a.out[2] = nullptr;
         MOE_TRY(run_ffn(kFfnDx, d, a, sms, stream, "dx kernel launch"));
     }
     return MOE_OK;

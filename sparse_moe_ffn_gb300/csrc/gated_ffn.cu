@@ -40,22 +40,20 @@ namespace {
 
 constexpr int kEpiWarps = 8;
 constexpr int kFfnThreads = 64 + 32 * kEpiWarps;
+constexpr int kStages = 6;
 constexpr int kBN = 256;               // columns of a tile
 constexpr int kSliceK = 64;            // values of K in a slice
 constexpr int kOperandBytes = 128 * kSliceBytes;  // a CTA's share of a slice, either side
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMnChunk = 64 * kSliceBytes;  // MN-major: 64 rows, 64 values of K
-constexpr int kOutBytes = 2048;        // 32 x 32 bf16 on their way out
-constexpr int kMostStages = 5;
 constexpr int kMinSlices = 8;          // of a part of a tile
 
 struct FfnShared {
-    uint64_t full[kMostStages];   // even CTA: both CTAs' bytes of a stage landed
-    uint64_t empty[kMostStages];  // both: the MMAs are done with a stage
+    uint64_t full[kStages];   // even CTA: both CTAs' bytes of a stage landed
+    uint64_t empty[kStages];  // both: the MMAs are done with a stage
     uint64_t acc_full[2];     // both: an accumulator is complete
     uint64_t acc_empty[2];    // even CTA: both CTAs' epilogues have read one
     uint64_t drain;           // even CTA: every MMA has completed
-    uint64_t saved[kEpiWarps][2];  // (dh) a warp's gate and up landed
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -65,12 +63,8 @@ struct FfnTraits {
     static constexpr bool kAMn = kOp == kFfnDw;
     static constexpr bool kBMn = kOp == kFfnDh || kOp == kFfnDx || kOp == kFfnDw;
     static constexpr int kColsPerTile = kOp == kFfnGateUp ? kBN / 2 : kBN;  // of the output
-    // three values a column leave the epilogue, or one; the buffers of a warp,
-    // two sets in turn, and the stages that then fit
-    static constexpr int kSet = kOp == kFfnGateUp || kOp == kFfnDh ? 3 : 1;
-    static constexpr int kStages = kSet == 3 ? 4 : kMostStages;
-    static constexpr size_t kShared = 1024 + static_cast<size_t>(kStages) * kStageBytes +
-                                      kEpiWarps * 2 * kSet * kOutBytes + sizeof(FfnShared);
+    static constexpr size_t kShared =
+        1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(FfnShared);
 };
 
 // Shared memory descriptor of an MN-major operand: rows of 64 values along MN
@@ -167,46 +161,29 @@ __device__ __forceinline__ FfnTile ffn_tile(const FfnArgs &a, int tile) {
     return t;
 }
 
-__device__ __forceinline__ void tma_store_box(const CUtensorMap *map, const void *src, int c0,
-                                              int c1) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
-                 ::"l"(map), "r"(smem_addr(src)), "r"(c0), "r"(c1)
+// 32-byte load that stays out of L1 (8 words; p 32-byte aligned)
+__device__ __forceinline__ void ld_global_v8(const void *p, uint32_t *v) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                   "=r"(v[6]), "=r"(v[7])
+                 : "l"(p)
                  : "memory");
 }
 
-// This lane's row of a 32 x 32 chunk of bf16, as a tensor-map store with
-// swizzled rows of 64 bytes reads it.
-__device__ __forceinline__ void write_bf16_row(uint8_t *buf, int lane, const float (&v)[32]) {
-    uint8_t *row = buf + lane * 64;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4 *>(row + 16 * (j ^ ((lane >> 1) & 3))) =
-            make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                       pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
-                       pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
-}
-
-// 32 values of a bf16 row (16-byte aligned), the first `left` of which exist (a
-// multiple of 8).
+// 32 values of a bf16 row (16-byte aligned; 32-byte loads if wide), the first
+// `left` of which exist (a multiple of 8).
 struct Row32 {
     uint32_t w[16];
-    __device__ __forceinline__ void load(const uint16_t *p, int left) {
+    __device__ __forceinline__ void load(const uint16_t *p, int left, bool wide) {
+        if (wide && left >= 32) {
+            ld_global_v8(p, &w[0]);
+            ld_global_v8(p + 16, &w[8]);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint4 u = 8 * i < left ? __ldcg(reinterpret_cast<const uint4 *>(p) + i)
                                          : make_uint4(0, 0, 0, 0);
-            w[4 * i] = u.x;
-            w[4 * i + 1] = u.y;
-            w[4 * i + 2] = u.z;
-            w[4 * i + 3] = u.w;
-        }
-    }
-    // this lane's row of a 32 x 32 chunk that a tensor map's load brought
-    __device__ __forceinline__ void read(const uint8_t *buf, int lane) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(buf + lane * 64 +
-                                                             16 * (i ^ ((lane >> 1) & 3)));
             w[4 * i] = u.x;
             w[4 * i + 1] = u.y;
             w[4 * i + 2] = u.z;
@@ -222,6 +199,42 @@ struct Row32 {
         }
     }
 };
+
+// 32 values to a bf16 row, as Row32 reads them.  Each lane stores its own row's
+// whole 32-byte sectors.  Tensor-map stores of 32 x 32 values would take the
+// TMA unit's time from the operands, which keep it busy (a row of a box, of up
+// to 128 bytes, costs it about two cycles): with them dh of 8192 x 2048 x 8192
+// took 236 us and gate/up 270 instead of @DH and @GU.
+__device__ __forceinline__ void store_row(uint16_t *p, const float (&v)[32], int left, bool wide) {
+    if (wide && left >= 32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = pack_bf16x2(v[16 * h + 2 * i], v[16 * h + 2 * i + 1]);
+            st_global_v8(p + 16 * h, u);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (8 * i < left)
+            *reinterpret_cast<uint4 *>(p + 8 * i) =
+                make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]),
+                           pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                           pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
+                           pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+}
+
+// Whether the rows that the epilogue reads and writes start on 32 bytes.
+__device__ __forceinline__ bool all_wide(const FfnArgs &a, int cols) {
+    return cols % 16 == 0 &&
+           (reinterpret_cast<uintptr_t>(a.gate) | reinterpret_cast<uintptr_t>(a.up) |
+            reinterpret_cast<uintptr_t>(a.residual) | reinterpret_cast<uintptr_t>(a.out[0]) |
+            reinterpret_cast<uintptr_t>(a.out[1]) | reinterpret_cast<uintptr_t>(a.out[2])) %
+                   32 ==
+               0;
+}
 
 // a = act(v) and d = act'(v).  The logistic function s is exactly 0 where 2^t
 // passes the range, so that its product with a large v vanishes.
@@ -284,12 +297,10 @@ template <FfnOp kOp>
 __global__ void __launch_bounds__(kFfnThreads, 1)
     ffn_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnArgs a) {
     using T = FfnTraits<kOp>;
-    constexpr int kStages = T::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t *out_bufs = tiles + kStages * kStageBytes;
-    FfnShared *sm = reinterpret_cast<FfnShared *>(out_bufs + kEpiWarps * 2 * T::kSet * kOutBytes);
+    FfnShared *sm = reinterpret_cast<FfnShared *>(tiles + kStages * kStageBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = static_cast<int>(cluster_ctarank());
     const bool leader = rank == 0;
@@ -304,8 +315,6 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             mbar_init(&sm->acc_empty[i], 2 * kEpiWarps);
         }
         mbar_init(&sm->drain, 1);
-        if (kOp == kFfnDh)
-            for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(&sm->saved[0][0] + i, 1);
         sm->abort_flag = 0;
         fence_barrier_init();
         prefetch_tensor_map(&maps.a[0]);
@@ -441,41 +450,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         }
         __syncwarp();
     } else {
-        const int quarter = warp % 4, half = (warp - 2) / 4, ew = warp - 2;
+        const int quarter = warp % 4, half = (warp - 2) / 4;
         constexpr int kCols = T::kColsPerTile / 2;  // a warp's
         const uint32_t empty0 = map_to_rank(smem_addr(&sm->acc_empty[0]), 0);
         const uint32_t empty1 = map_to_rank(smem_addr(&sm->acc_empty[1]), 0);
-        uint8_t *buf = out_bufs + ew * 2 * T::kSet * kOutBytes;
-        // (dh) gate and up of a chunk come into the buffers that dgate and dup
-        // leave from, one chunk ahead of their use; `ahead` runs through the
-        // chunks for them
-        FfnWalk ahead(a.plan, pair);
-        int ahead_c = 0, ahead_cols = 0, ahead_c0 = 0, ahead_r0 = 0, fetched = 0;
-        auto fetch_saved = [&] {
-            while (ahead_c >= ahead_cols) {
-                FfnItem n;
-                if (!ahead.next(n)) return;
-                const FfnTile t = ffn_tile<kOp>(a, n.tile);
-                ahead_r0 = t.m * kFfnTile + rank * 128 + quarter * 32;
-                ahead_c0 = t.n * T::kColsPerTile + half * kCols;
-                ahead_cols = ahead_r0 < a.N ? min(kCols, a.I - ahead_c0) : 0;
-                ahead_c = 0;
-            }
-            if (lane == 0) {
-                uint8_t *b = buf + (fetched & 1) * T::kSet * kOutBytes;
-                uint64_t *bar = &sm->saved[ew][fetched & 1];
-                mbar_arrive_expect_tx(bar, 2 * kOutBytes);
-                tma_load_2d(b + kOutBytes, &maps.a[1], bar, ahead_c0 + ahead_c, ahead_r0);
-                tma_load_2d(b + 2 * kOutBytes, &maps.a[2], bar, ahead_c0 + ahead_c, ahead_r0);
-            }
-            ahead_c += 32;
-            ++fetched;
-        };
-        if (kOp == kFfnDh) {
-            fetch_saved();
-            fetch_saved();
-        }
-        int n = 0, chunk = 0;
+        int n = 0;
         for (; walk.next(it); ++n) {
             const FfnTile t = ffn_tile<kOp>(a, it.tile);
             int64_t rows;
@@ -487,11 +466,18 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             const int64_t r = r0 + lane;
             // columns of this warp that exist (warp-uniform)
             const int cols = r0 < rows ? min(kCols, all_cols - c0) : 0;
-            // the residual, read 32 columns ahead
-            Row32 res;
+            const bool wide = all_wide(a, all_cols);
+            // operands of the elementwise part, read 32 columns ahead
+            Row32 e0 = {}, e1 = {};
             auto fetch = [&](int c) {
-                if (kOp == kFfnDown && a.residual && it.slot < 0 && c < cols && r < rows)
-                    res.load(a.residual + r * all_cols + c0 + c, cols - c);
+                if (c >= cols || r >= rows) return;
+                const int64_t at = r * all_cols + c0 + c;
+                if (kOp == kFfnDh) {
+                    e0.load(a.gate + at, cols - c, wide);
+                    e1.load(a.up + at, cols - c, wide);
+                }
+                if (kOp == kFfnDown && a.residual && it.slot < 0)
+                    e0.load(a.residual + at, cols - c, wide);
             };
             fetch(0);
             __syncwarp();
@@ -524,9 +510,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 }
             } else {
 #pragma unroll 1
-                for (int c = 0; c < cols; c += 32, ++chunk) {
+                for (int c = 0; c < cols; c += 32) {
                     float v[32], w[32], x[32];
-                    uint8_t *b = buf + (chunk & 1) * T::kSet * kOutBytes;
                     __syncwarp();  // TMEM wants whole warps
                     tmem_load32(taddr + c, v);
                     if (kOp == kFfnGateUp) {
@@ -543,66 +528,33 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                         for (int i = 0; i < 32; ++i) x[i] *= w[i];
                     }
                     if (kOp == kFfnDh) {
-                        if (!warp_wait(&sm->saved[ew][chunk & 1], (chunk >> 1) & 1, abort_flag)) {
-                            if (lane == 0) {
-                                record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
-                                *abort_flag = 1;
-                            }
-                            ok = false;
-                            break;
-                        }
-                        Row32 gate, up;
-                        gate.read(b + kOutBytes, lane);
-                        up.read(b + 2 * kOutBytes, lane);
                         switch (a.act) {
-                            case MOE_ACT_SILU: gate_grads<MOE_ACT_SILU>(v, gate, up, w, x); break;
-                            case MOE_ACT_GELU: gate_grads<MOE_ACT_GELU>(v, gate, up, w, x); break;
+                            case MOE_ACT_SILU: gate_grads<MOE_ACT_SILU>(v, e0, e1, w, x); break;
+                            case MOE_ACT_GELU: gate_grads<MOE_ACT_GELU>(v, e0, e1, w, x); break;
                             case MOE_ACT_GELU_TANH:
-                                gate_grads<MOE_ACT_GELU_TANH>(v, gate, up, w, x);
+                                gate_grads<MOE_ACT_GELU_TANH>(v, e0, e1, w, x);
                                 break;
-                            case MOE_ACT_RELU: gate_grads<MOE_ACT_RELU>(v, gate, up, w, x); break;
-                            default: gate_grads<MOE_ACT_NONE>(v, gate, up, w, x); break;
+                            case MOE_ACT_RELU: gate_grads<MOE_ACT_RELU>(v, e0, e1, w, x); break;
+                            default: gate_grads<MOE_ACT_NONE>(v, e0, e1, w, x); break;
                         }
                     }
-                    if (kOp == kFfnDown && a.residual) res.add_to(v);
+                    if (kOp == kFfnDown && a.residual) e0.add_to(v);
                     fetch(c + 32);
-                    // the set's last outputs have left (dh: before its gate and
-                    // up were fetched)
-                    if (kOp != kFfnDh) {
-                        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                        __syncwarp();
-                    }
-                    write_bf16_row(b, lane, T::kSet == 3 ? x : v);
-                    if (kOp == kFfnDh || (kOp == kFfnGateUp && a.keep)) {
-                        write_bf16_row(b + kOutBytes, lane, v);
-                        write_bf16_row(b + 2 * kOutBytes, lane, w);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) {
-                        const int row = static_cast<int>(r0);
-                        tma_store_box(&maps.out[t.prod], b, c0 + c, row);
+                    if (r < rows) {
+                        const int64_t at = r * all_cols + c0 + c;
+                        constexpr bool kThree = kOp == kFfnGateUp || kOp == kFfnDh;
+                        store_row(a.out[t.prod] + at, kThree ? x : v, cols - c, wide);
                         if (kOp == kFfnDh || (kOp == kFfnGateUp && a.keep)) {
-                            tma_store_box(&maps.out[1], b + kOutBytes, c0 + c, row);
-                            tma_store_box(&maps.out[2], b + 2 * kOutBytes, c0 + c, row);
+                            store_row(a.out[1] + at, v, cols - c, wide);
+                            store_row(a.out[2] + at, w, cols - c, wide);
                         }
-                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                        if (kOp == kFfnDh)
-                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     }
-                    if (kOp == kFfnDh) fetch_saved();
                 }
-                if (!ok) break;
             }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) arrive_remote_relaxed(acc ? empty1 : empty0);
         }
-        // no copy may be in flight when the pair ends (after a failure too)
-        if (kOp == kFfnDh && lane == 0)
-            for (int i = chunk; i < fetched; ++i) drain_wait(&sm->saved[ew][i & 1], (i >> 1) & 1);
-        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // stores have landed
-        __syncwarp();
     }
 
     tc_fence_before_sync();
@@ -694,7 +646,7 @@ cudaError_t launch_op(const FfnMaps &maps, const FfnArgs &a, int *launches, cuda
     if (err != cudaSuccess) return err;
     *launches += 1;
     if (a.plan.parts == 0) return cudaSuccess;
-    if constexpr (FfnTraits<kOp>::kSet == 1) {
+    if constexpr (kOp != kFfnGateUp && kOp != kFfnDh) {
         *launches += 1;
         const int blocks = (a.plan.tiles - a.plan.whole) * (256 / (kJoinThreads / 32));
         return launch_pdl(ffn_join_kernel<kOp>, dim3(static_cast<unsigned>(blocks)),
@@ -754,8 +706,6 @@ FfnPlan ffn_plan(FfnOp op, int64_t N, int H, int I, int num_sms) {
 size_t ffn_part_bytes(const FfnPlan &p) {
     return sizeof(float) * kFfnPartFloats * 2 * static_cast<size_t>(p.parts);
 }
-
-int ffn_block_n(FfnOp op) { return op == kFfnGateUp ? kBN / 2 : kBN; }
 
 cudaError_t launch_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, int *launches,
                        cudaStream_t s) {

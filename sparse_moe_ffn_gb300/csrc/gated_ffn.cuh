@@ -44,26 +44,24 @@ struct FfnArgs {
     int H, I;
     int act;
     int keep;                   // gate and up are stored
+    const uint16_t *gate, *up;  // kFfnDh
     const uint16_t *residual;   // kFfnDown, nullable
-    uint16_t *out[3];           // the outputs (for the partial sums' join)
+    uint16_t *out[3];           // h, gate, up; h, dgate, dup; dWg, dWu, dWd; or one
     float *part;                // [2 pairs][kFfnPartFloats]
     int32_t *status;
     int reset_status;
     FfnPlan plan;
 };
 
-// The operands' and outputs' tensor maps: a: the M side's, b: the N side's,
-// out: boxes of 32 x 32 values (kFfnDh: a[1] and a[2] are gate and up in such
-// boxes).  A K-major operand ([rows, K]) comes in boxes of
-// 64 values of K x its rows a CTA, an MN-major one ([K, rows]) in boxes of 64
-// rows x 64 values of K.
+// The operands' tensor maps: a: the M side's, b: the N side's.  A K-major
+// operand ([rows, K]) comes in boxes of 64 values of K x 128 rows, an MN-major
+// one ([K, rows]) in boxes of 64 rows x 64 values of K.
 struct FfnMaps {
-    CUtensorMap a[3], b[3], out[3];
+    CUtensorMap a[3], b[3];
 };
 
 FfnPlan ffn_plan(FfnOp op, int64_t N, int H, int I, int num_sms);
 size_t ffn_part_bytes(const FfnPlan &p);
-int ffn_block_n(FfnOp op);
 cudaError_t launch_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, int *launches,
                        cudaStream_t s);
 
