@@ -40,7 +40,7 @@ namespace {
 
 constexpr int kEpiWarps = 8;
 constexpr int kFfnThreads = 64 + 32 * kEpiWarps;
-constexpr int kStages = 6;
+constexpr int kMostStages = 6;
 constexpr int kBN = 256;               // columns of a tile
 constexpr int kSliceK = 64;            // values of K in a slice
 constexpr int kOperandBytes = 128 * kSliceBytes;  // a CTA's share of a slice, either side
@@ -49,8 +49,8 @@ constexpr int kMnChunk = 64 * kSliceBytes;  // MN-major: 64 rows, 64 values of K
 constexpr int kMinSlices = 8;          // of a part of a tile
 
 struct FfnShared {
-    uint64_t full[kStages];   // even CTA: both CTAs' bytes of a stage landed
-    uint64_t empty[kStages];  // both: the MMAs are done with a stage
+    uint64_t full[kMostStages];   // even CTA: both CTAs' bytes of a stage landed
+    uint64_t empty[kMostStages];  // both: the MMAs are done with a stage
     uint64_t acc_full[2];     // both: an accumulator is complete
     uint64_t acc_empty[2];    // even CTA: both CTAs' epilogues have read one
     uint64_t drain;           // even CTA: every MMA has completed
@@ -63,6 +63,7 @@ struct FfnTraits {
     static constexpr bool kAMn = kOp == kFfnDw;
     static constexpr bool kBMn = kOp == kFfnDh || kOp == kFfnDx || kOp == kFfnDw;
     static constexpr int kColsPerTile = kOp == kFfnGateUp ? kBN / 2 : kBN;  // of the output
+    static constexpr int kStages = kOp == kFfnDh ? 5 : kMostStages;  // dh: 211 us, 216 with six
     static constexpr size_t kShared =
         1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(FfnShared);
 };
@@ -122,7 +123,7 @@ struct FfnWalk {
 
 // Tiles run through bands of kBand row tiles, column tile by column tile: the
 // tiles in flight share few rows of either operand.
-constexpr int kBand = 8;
+constexpr int kBand = 16;
 
 struct FfnTile {
     int prod, m, n;
@@ -297,6 +298,7 @@ template <FfnOp kOp>
 __global__ void __launch_bounds__(kFfnThreads, 1)
     ffn_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnArgs a) {
     using T = FfnTraits<kOp>;
+    constexpr int kStages = T::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
