@@ -23,7 +23,7 @@ LIB = os.path.join(BUILD, "libsparse_moe_ffn.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "router.cu", "align.cu", "grouped_gemm.cu", "pair_gemm.cu", "sparse_gemm.cu", "combine.cu", "selftest.cu",
            "align_noalloc.cu", "rmsnorm.cu", "convert.cu", "ep.cu", "rmsnorm_fp8.cu", "linear.cu",
-           "linear_pair.cu", "linear_split.cu", "balance.cu", "gated_ffn.cu", "ffn_rows.cu",
+           "linear_pair.cu", "linear_split.cu", "balance.cu", "gated_ffn.cu", "ffn_rows.cu", "ffn_split.cu",
            "layernorm.cu", "grad_clip.cu"]
 
 

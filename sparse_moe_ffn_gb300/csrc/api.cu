@@ -1603,11 +1603,10 @@ FfnLayout ffn_layout(int64_t N, int H, int I, bool backward, int sms) {
 }
 
 // The map of an operand: `base` [rows, cols], K-major (K along the rows) in
-// boxes of 64 values of K x 128 rows, MN-major in boxes of 64 x 64.
-moe_status_t ffn_operand(CUtensorMap *m, const void *base, int64_t rows, int cols, bool mn,
+// boxes of 64 values of K x `box` rows; MN-major in boxes of 64 x 64.
+moe_status_t ffn_operand(CUtensorMap *m, const void *base, int64_t rows, int cols, int box,
                          const char *what) {
-    return make_rows_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, 64,
-                         mn ? 64 : 128, what);
+    return make_rows_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, 64, box, what);
 }
 
 moe_status_t run_ffn(FfnOp op, const FfnMaps &maps, FfnArgs a, int sms, cudaStream_t stream,
@@ -1667,31 +1666,41 @@ moe_status_t moe_gated_ffn(const moe_bf16_t *x, const moe_bf16_t *w_gate, const 
     a.reset_status = 1;
     if (ffn_rows_fit(N, H) && ffn_rows_fit(N, I)) {
         a.out[0] = h;
-        MOE_CUDA(launch_ffn_rows(kFfnGateUp, a, x, w_gate, w_up, gate, up, stream),
+        MOE_CUDA(launch_ffn_rows(kFfnGateUp, a, x, w_gate, w_up, gate, up, sms, stream),
                  "gate and up kernel launch");
         a.residual = residual;
         a.out[0] = out;
-        MOE_CUDA(launch_ffn_rows(kFfnDown, a, h, w_down, nullptr, nullptr, nullptr, stream),
+        MOE_CUDA(launch_ffn_rows(kFfnDown, a, h, w_down, nullptr, nullptr, nullptr, sms,
+                                 stream),
                  "down kernel launch");
         g_launches += 2;
         return MOE_OK;
     }
-    FfnMaps m = {};
-    MOE_TRY(ffn_operand(&m.a[0], x, N, H, false, "x"));
-    MOE_TRY(ffn_operand(&m.b[0], w_gate, I, H, false, "w_gate"));
-    MOE_TRY(ffn_operand(&m.b[1], w_up, I, H, false, "w_up"));
-    FfnMaps d = {};
-    MOE_TRY(ffn_operand(&d.a[0], h, N, I, false, "h"));
-    MOE_TRY(ffn_operand(&d.b[0], w_down, H, I, false, "w_down"));
+    // each step's maps first, so that nothing is enqueued if one is refused
+    const FfnSplit su = ffn_split(kFfnGateUp, N, H, I, sms), sd = ffn_split(kFfnDown, N, H, I, sms);
+    FfnMaps m = {}, d = {};
+    MOE_TRY(ffn_operand(&m.a[0], x, N, H, su.bn ? su.bn : 128, "x"));
+    MOE_TRY(ffn_operand(&m.b[0], w_gate, I, H, su.bn ? 64 : 128, "w_gate"));
+    MOE_TRY(ffn_operand(&m.b[1], w_up, I, H, su.bn ? 64 : 128, "w_up"));
+    MOE_TRY(ffn_operand(&d.a[0], h, N, I, sd.bn ? sd.bn : 128, "h"));
+    MOE_TRY(ffn_operand(&d.b[0], w_down, H, I, 128, "w_down"));
     a.out[0] = h;
     a.out[1] = gate;
     a.out[2] = up;
-    MOE_TRY(run_ffn(kFfnGateUp, m, a, sms, stream, "gate and up kernel launch"));
+    if (su.bn) {
+        MOE_CUDA(launch_ffn_split(kFfnGateUp, m, a, su, stream), "gate and up kernel launch");
+        g_launches += 1;
+    } else {
+        MOE_TRY(run_ffn(kFfnGateUp, m, a, sms, stream, "gate and up kernel launch"));
+    }
     a.reset_status = 0;
     a.residual = residual;
     a.out[0] = out;
     a.out[1] = a.out[2] = nullptr;
-    return run_ffn(kFfnDown, d, a, sms, stream, "down kernel launch");
+    if (!sd.bn) return run_ffn(kFfnDown, d, a, sms, stream, "down kernel launch");
+    MOE_CUDA(launch_ffn_split(kFfnDown, d, a, sd, stream), "down kernel launch");
+    g_launches += 1;
+    return MOE_OK;
 }
 
 moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
@@ -1741,22 +1750,22 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
     a.status = reinterpret_cast<int32_t *>(ws);
     a.reset_status = 1;
     FfnMaps m = {};
-    MOE_TRY(ffn_operand(&m.a[0], dout, N, H, false, "dout"));
-    MOE_TRY(ffn_operand(&m.b[0], w_down, H, I, true, "w_down"));
+    MOE_TRY(ffn_operand(&m.a[0], dout, N, H, 128, "dout"));
+    MOE_TRY(ffn_operand(&m.b[0], w_down, H, I, 64, "w_down"));
     FfnMaps w = {}, d = {};
     if (weights) {
-        MOE_TRY(ffn_operand(&w.a[0], dgate, N, I, true, "dgate"));
-        MOE_TRY(ffn_operand(&w.a[1], dup, N, I, true, "dup"));
-        MOE_TRY(ffn_operand(&w.a[2], dout, N, H, true, "dout"));
-        MOE_TRY(ffn_operand(&w.b[0], x, N, H, true, "x"));
+        MOE_TRY(ffn_operand(&w.a[0], dgate, N, I, 64, "dgate"));
+        MOE_TRY(ffn_operand(&w.a[1], dup, N, I, 64, "dup"));
+        MOE_TRY(ffn_operand(&w.a[2], dout, N, H, 64, "dout"));
+        MOE_TRY(ffn_operand(&w.b[0], x, N, H, 64, "x"));
         w.b[1] = w.b[0];
-        MOE_TRY(ffn_operand(&w.b[2], h, N, I, true, "h"));
+        MOE_TRY(ffn_operand(&w.b[2], h, N, I, 64, "h"));
     }
     if (dx) {
-        MOE_TRY(ffn_operand(&d.a[0], dgate, N, I, false, "dgate"));
-        MOE_TRY(ffn_operand(&d.a[1], dup, N, I, false, "dup"));
-        MOE_TRY(ffn_operand(&d.b[0], w_gate, I, H, true, "w_gate"));
-        MOE_TRY(ffn_operand(&d.b[1], w_up, I, H, true, "w_up"));
+        MOE_TRY(ffn_operand(&d.a[0], dgate, N, I, 128, "dgate"));
+        MOE_TRY(ffn_operand(&d.a[1], dup, N, I, 128, "dup"));
+        MOE_TRY(ffn_operand(&d.b[0], w_gate, I, H, 64, "w_gate"));
+        MOE_TRY(ffn_operand(&d.b[1], w_up, I, H, 64, "w_up"));
     }
     a.out[0] = h;
     a.out[1] = dgate;

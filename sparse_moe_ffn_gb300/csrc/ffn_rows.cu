@@ -2,10 +2,14 @@
 // steps (gate/up with their product, then down) stream their weights once,
 // from memory straight into registers.
 //
-// A warp takes two weight rows (an output's gate and up row, or two rows of the
-// down projection) and 2048 values of K: 16 loads of 16 bytes a lane, all in
-// flight at once.  Rows with more values are shared by the block's warps, whose
-// sums are added in a fixed order.  The tokens lie in shared memory.
+// A warp takes a step of K at a time: 1024 values of an output's gate and up
+// row, or 2048 of a row of the down projection, 8 loads of 16 bytes a lane.  Two
+// steps are in flight; a step's registers are asked for again as soon as it is
+// used, across outputs too, and the blocks stay (two an SM), so that the memory
+// always has more than a step of every warp.  (One step of twice the size a
+// block, blocks that come and go: one token of 2048 x 8192 took 21.6 us, so
+// @T.)  The warps of a block share long rows where there are few; their sums are
+// added in a fixed order.  The tokens lie in shared memory.
 //
 // The down step's first weights are asked for before the kernel waits for the
 // gate/up step (programmatic dependent launch): its blocks start where the
@@ -23,8 +27,7 @@ namespace {
 
 constexpr int kRowsThreads = 256;
 constexpr int kRowsWarps = kRowsThreads / 32;
-constexpr int kLoads = 8;                    // of 16 bytes: a lane's part of a row segment
-constexpr int kSegment = kLoads * 32 * 8;    // values
+constexpr int kLoads = 8;  // of 16 bytes: a lane's part of a step
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t *p) {
     uint4 v;
@@ -48,112 +51,150 @@ struct FfnRowsArgs {
 
 template <bool kGated, int kTokens>
 __global__ void __launch_bounds__(kRowsThreads, 2) ffn_rows_kernel(const FfnRowsArgs a) {
-    extern __shared__ uint4 xs[];  // [kTokens][K / 8]
-    __shared__ float sums[kRowsWarps][2 * kTokens];
+    constexpr int kRows = kGated ? 2 : 1;             // weight rows of an output
+    constexpr int kRowLoads = kLoads / kRows;
+    constexpr int kStep = kRowLoads * 32 * 8;         // values of K
+    extern __shared__ uint4 xs[];                     // [kTokens][K / 8]
+    __shared__ float sums[2][kRowsWarps][kRows * kTokens];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int per_block = kRowsWarps / a.per_row;  // pairs of rows
-    const int mine = warp % a.per_row;             // this warp's place in the row
-    const int64_t o = static_cast<int64_t>(blockIdx.x) * per_block + warp / a.per_row;
-    const int64_t r0 = kGated ? o : 2 * o, r1 = kGated ? o : 2 * o + 1;
-    const bool has0 = r0 < a.O, has1 = r1 < a.O;
-    const uint16_t *w0 = a.w0 + (has0 ? r0 : 0) * a.K;
-    const uint16_t *w1 = (kGated ? a.w1 : a.w0) + (has1 ? r1 : 0) * a.K;
-    uint4 b0[kLoads], b1[kLoads];
-    auto load = [&](int64_t seg) {
+    const int per_block = kRowsWarps / a.per_row;     // outputs of a group
+    const int mine = warp % a.per_row;                // this warp's place in the row
+    const int steps = (a.K + kStep - 1) / kStep;
+    const int groups = (a.O + per_block - 1) / per_block;
+    const int words = a.K / 8;
+
+    // the next step to ask for
+    int load_group = blockIdx.x, load_step = mine;
+    uint4 w[2][kRows][kRowLoads];
+    auto load = [&](uint4(&b)[kRows][kRowLoads]) {
+        const int64_t o = static_cast<int64_t>(load_group) * per_block + warp / a.per_row;
+        const bool has = load_group < groups && o < a.O;
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const int64_t k = seg * kSegment + (j * 32 + lane) * 8;
-            b0[j] = has0 && k < a.K ? ld_stream(w0 + k) : make_uint4(0, 0, 0, 0);
-            b1[j] = has1 && k < a.K ? ld_stream(w1 + k) : make_uint4(0, 0, 0, 0);
+        for (int r = 0; r < kRows; ++r) {
+            const uint16_t *row = (r == 0 ? a.w0 : a.w1) + (has ? o : 0) * a.K;
+#pragma unroll
+            for (int j = 0; j < kRowLoads; ++j) {
+                const int at = load_step * (kStep / 8) + j * 32 + lane;
+                b[r][j] = has && at < words ? ld_stream(row + 8 * static_cast<int64_t>(at))
+                                            : make_uint4(0, 0, 0, 0);
+            }
+        }
+        load_step += a.per_row;
+        if (load_step >= steps) {
+            load_step = mine;
+            load_group += gridDim.x;
         }
     };
-    if (kGated) griddep_wait();
+    // the tokens first where they are there already: behind the weights they
+    // would arrive last
+    const int all = a.N * words;
+    int i = threadIdx.x;
+    uint4 token = make_uint4(0, 0, 0, 0);
+    if (kGated) {
+        griddep_wait();
+        if (i < all) token = ld_stream(a.x + 8 * i);
+    }
     griddep_launch_dependents();
-    load(mine);
-    if (!kGated) griddep_wait();
+    load(w[0]);
+    load(w[1]);
+    if (!kGated) {
+        griddep_wait();
+        if (i < all) token = ld_stream(a.x + 8 * i);
+    }
     if (kGated && blockIdx.x == 0 && threadIdx.x == 0) *a.status = MOE_OK;
-    const int groups = a.K / 8;
-    for (int i = threadIdx.x; i < a.N * groups; i += kRowsThreads)
+    if (i < all) xs[i] = token;
+    for (i += kRowsThreads; i < all; i += kRowsThreads)
         xs[i] = __ldcg(reinterpret_cast<const uint4 *>(a.x) + i);
     __syncthreads();
-    float v[2][kTokens];
+
+    float v[kRows][kTokens];
 #pragma unroll
-    for (int t = 0; t < kTokens; ++t) v[0][t] = v[1][t] = 0.f;
-    for (int64_t seg = mine; seg * kSegment < a.K;) {
+    for (int r = 0; r < kRows; ++r)
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const int64_t k = seg * kSegment + (j * 32 + lane) * 8;
-            if (k >= a.K) break;
-            const uint32_t *p0 = reinterpret_cast<const uint32_t *>(&b0[j]);
-            const uint32_t *p1 = reinterpret_cast<const uint32_t *>(&b1[j]);
+        for (int t = 0; t < kTokens; ++t) v[r][t] = 0.f;
+    int group = blockIdx.x, step = mine, turn = 0;
+    // uses a step's weights; ends the output with its last one
+    auto use = [&](const uint4(&b)[kRows][kRowLoads]) {
+#pragma unroll
+        for (int j = 0; j < kRowLoads; ++j) {
+            const int at = step * (kStep / 8) + j * 32 + lane;
+            if (at >= words) break;
 #pragma unroll
             for (int t = 0; t < kTokens; ++t) {
                 if (t >= a.N) break;
-                const uint4 u = xs[t * groups + k / 8];
+                const uint4 u = xs[t * words + at];
                 const uint32_t *px = reinterpret_cast<const uint32_t *>(&u);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 f = unpack_bf16x2(px[i]), g = unpack_bf16x2(p0[i]),
-                                 h = unpack_bf16x2(p1[i]);
-                    v[0][t] = fmaf(f.x, g.x, v[0][t]);
-                    v[0][t] = fmaf(f.y, g.y, v[0][t]);
-                    v[1][t] = fmaf(f.x, h.x, v[1][t]);
-                    v[1][t] = fmaf(f.y, h.y, v[1][t]);
+                    const float2 f = unpack_bf16x2(px[i]);
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) {
+                        const float2 g =
+                            unpack_bf16x2(reinterpret_cast<const uint32_t *>(&b[r][j])[i]);
+                        v[r][t] = fmaf(f.x, g.x, v[r][t]);
+                        v[r][t] = fmaf(f.y, g.y, v[r][t]);
+                    }
                 }
             }
         }
-        seg += a.per_row;
-        if (seg * kSegment < a.K) load(seg);
-    }
+        step += a.per_row;
+        if (step < steps) return;
+        float s[kRows];  // lane t: the sums of token t
 #pragma unroll
-    for (int t = 0; t < kTokens; ++t)
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-            v[0][t] += __shfl_xor_sync(0xffffffffu, v[0][t], d);
-            v[1][t] += __shfl_xor_sync(0xffffffffu, v[1][t], d);
-        }
-    if (a.per_row > 1) {
-        if (lane == 0)
+        for (int r = 0; r < kRows; ++r) {
+            s[r] = 0.f;
 #pragma unroll
             for (int t = 0; t < kTokens; ++t) {
-                sums[warp][2 * t] = v[0][t];
-                sums[warp][2 * t + 1] = v[1][t];
-            }
-        __syncthreads();
-        if (mine != 0) return;
+                float f = v[r][t];
 #pragma unroll
-        for (int t = 0; t < kTokens; ++t) {
-            v[0][t] = v[1][t] = 0.f;
-            for (int w = warp; w < warp + a.per_row; ++w) {
-                v[0][t] += sums[w][2 * t];
-                v[1][t] += sums[w][2 * t + 1];
+                for (int d = 16; d > 0; d >>= 1) f += __shfl_xor_sync(0xffffffffu, f, d);
+                if (lane == t) s[r] = f;
+                v[r][t] = 0.f;
             }
         }
-    }
-    // lane t finishes token t
-    float s0 = 0.f, s1 = 0.f;
+        if (a.per_row > 1) {
+            // two buffers in turn: a warp can be one output ahead, never two
+            if (lane < kTokens)
 #pragma unroll
-    for (int t = 0; t < kTokens; ++t)
-        if (lane == t) s0 = v[0][t], s1 = v[1][t];
-    if (lane >= a.N || !has0) return;
-    const int64_t at = static_cast<int64_t>(lane) * a.O + r0;
-    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) + at;
-    if (kGated) {
-        float h[1] = {s0};
-        act_all(a.act, h);
-        *out = __float2bfloat16_rn(h[0] * s1);
-        if (a.gate) {
-            reinterpret_cast<__nv_bfloat16 *>(a.gate)[at] = __float2bfloat16_rn(s0);
-            reinterpret_cast<__nv_bfloat16 *>(a.up)[at] = __float2bfloat16_rn(s1);
+                for (int r = 0; r < kRows; ++r) sums[turn][warp][r * kTokens + lane] = s[r];
+            __syncthreads();
+            if (mine == 0 && lane < kTokens)
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    s[r] = 0.f;
+                    for (int q = warp; q < warp + a.per_row; ++q)
+                        s[r] += sums[turn][q][r * kTokens + lane];
+                }
+            turn ^= 1;
         }
-    } else {
-        // O is a multiple of 8: both rows exist
-        if (a.residual) {
-            const float2 r = unpack_bf16x2(__ldcg(reinterpret_cast<const uint32_t *>(a.residual + at)));
-            s0 += r.x;
-            s1 += r.y;
+        const int64_t o = static_cast<int64_t>(group) * per_block + warp / a.per_row;
+        if (mine == 0 && lane < a.N && o < a.O) {
+            const int64_t at = lane * static_cast<int64_t>(a.O) + o;
+            float y;
+            if constexpr (kGated) {
+                float h[1] = {s[0]};
+                act_all(a.act, h);
+                y = h[0] * s[1];
+                if (a.gate) {
+                    reinterpret_cast<__nv_bfloat16 *>(a.gate)[at] = __float2bfloat16_rn(s[0]);
+                    reinterpret_cast<__nv_bfloat16 *>(a.up)[at] = __float2bfloat16_rn(s[1]);
+                }
+            } else {
+                y = s[0];
+                if (a.residual)
+                    y += __uint_as_float(static_cast<uint32_t>(__ldcg(a.residual + at)) << 16);
+            }
+            reinterpret_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(y);
         }
-        *reinterpret_cast<uint32_t *>(out) = pack_bf16x2(s0, s1);
+        step = mine;
+        group += gridDim.x;
+    };
+    while (group < groups) {
+        use(w[0]);
+        load(w[0]);
+        if (group >= groups) break;
+        use(w[1]);
+        load(w[1]);
     }
 }
 
@@ -161,25 +202,30 @@ __global__ void __launch_bounds__(kRowsThreads, 2) ffn_rows_kernel(const FfnRows
 constexpr int kRowsShared = 64 * 1024;
 
 template <bool kGated, int kTokens>
-cudaError_t launch_rows(FfnRowsArgs a, cudaStream_t s) {
+cudaError_t launch_rows(FfnRowsArgs a, int num_sms, cudaStream_t s) {
     auto kern = ffn_rows_kernel<kGated, kTokens>;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t err = allow_shared(kern, kRowsShared, allowed);
     if (err != cudaSuccess) return err;
-    const int segments = (a.K + kSegment - 1) / kSegment;
+    // warps that share a row: enough rows for all warps of two blocks an SM
+    const int steps = (a.K + (kGated ? 1023 : 2047)) / (kGated ? 1024 : 2048);
+    const int64_t warps = 2 * static_cast<int64_t>(num_sms) * kRowsWarps;
     a.per_row = 1;
-    while (a.per_row < kRowsWarps && a.per_row < segments) a.per_row *= 2;
+    while (a.per_row < kRowsWarps && 2 * a.per_row <= steps &&
+           2 * static_cast<int64_t>(a.O) * a.per_row <= warps)
+        a.per_row *= 2;
     const int per_block = kRowsWarps / a.per_row;
-    const int64_t pairs = kGated ? a.O : (a.O + 1) / 2;
-    return launch_pdl(kern, dim3(static_cast<unsigned>((pairs + per_block - 1) / per_block)),
-                      dim3(kRowsThreads), static_cast<size_t>(a.N) * a.K * 2, s, 1, a);
+    const int64_t groups = (static_cast<int64_t>(a.O) + per_block - 1) / per_block;
+    const int64_t blocks = groups < 2 * num_sms ? groups : 2 * num_sms;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kRowsThreads),
+                      static_cast<size_t>(a.N) * a.K * 2, s, 1, a);
 }
 
 template <bool kGated>
-cudaError_t launch_tokens(const FfnRowsArgs &a, cudaStream_t s) {
-    if (a.N == 1) return launch_rows<kGated, 1>(a, s);
-    if (a.N == 2) return launch_rows<kGated, 2>(a, s);
-    return launch_rows<kGated, 4>(a, s);
+cudaError_t launch_tokens(const FfnRowsArgs &a, int num_sms, cudaStream_t s) {
+    if (a.N == 1) return launch_rows<kGated, 1>(a, num_sms, s);
+    if (a.N == 2) return launch_rows<kGated, 2>(a, num_sms, s);
+    return launch_rows<kGated, 4>(a, num_sms, s);
 }
 
 }  // namespace
@@ -189,12 +235,13 @@ bool ffn_rows_fit(int64_t N, int K) {
 }
 
 cudaError_t launch_ffn_rows(FfnOp op, const FfnArgs &a, const uint16_t *x, const uint16_t *w0,
-                            const uint16_t *w1, uint16_t *gate, uint16_t *up, cudaStream_t s) {
+                            const uint16_t *w1, uint16_t *gate, uint16_t *up, int num_sms,
+                            cudaStream_t s) {
     const bool gated = op == kFfnGateUp;
     const FfnRowsArgs r = {x,     w0, w1,         static_cast<int>(a.N), gated ? a.H : a.I,
                            gated ? a.I : a.H,     a.act,
                            a.residual, gate, up, a.out[0], 1, a.status};
-    return gated ? launch_tokens<true>(r, s) : launch_tokens<false>(r, s);
+    return gated ? launch_tokens<true>(r, num_sms, s) : launch_tokens<false>(r, num_sms, s);
 }
 
 }  // namespace moe

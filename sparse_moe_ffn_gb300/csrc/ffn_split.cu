@@ -1,0 +1,313 @@
+// ffn_split.cu -- the gated feed-forward block for a decode batch: the weights
+// on the MMA's M side (128 rows, in the gate/up step 64 of Wg and the 64 of Wu
+// that belong to them), up to 128 tokens on its N side, and K shared by the CTAs
+// of a cluster.
+//
+// Each CTA writes its partial sums straight into the shared memory of the CTA
+// that owns the token (tokens are dealt out in equal runs); one cluster barrier
+// later every CTA adds the parts of its own tokens in rank order, and has gate
+// and up of the same output next to each other.
+//
+//   warp 0  producer: TMA copies
+//   warp 1  TMEM and the MMAs
+//   all     read the accumulator, then add, finish and store
+//
+// A CTA takes half an SM's shared memory, so that the down step's CTAs start
+// while the gate/up step's still run: their first weights are asked for before
+// they wait for that step (programmatic dependent launch).  The weights may be
+// read that early because the gate/up kernel lets its dependents start only
+// after its own wait: whatever wrote them has ended then.
+// Every wait is bounded; a CTA that gives up records MOE_ERR_DEVICE_TIMEOUT and
+// still takes part in the cluster's barriers.
+#include "gated_ffn.cuh"
+#include "linear_epilogue.cuh"
+#include "linear_gemm.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kSplitThreads = 256;
+constexpr int kM = 128;            // weight rows of a tile
+constexpr int kSliceValues = 64;   // of K
+constexpr int kMaxStages = 5;
+
+template <int kBN>
+struct Tile {
+    static constexpr int kXBytes = kBN * kSliceBytes;
+    static constexpr int kStageBytes = kRowsBytes128 + kXBytes;
+    static constexpr int kStages = kBN == 16 ? 5 : kBN == 64 ? 3 : 4;
+    static constexpr int kBlocks = kBN == 128 ? 1 : 2;  // an SM
+    static constexpr uint32_t kCols = kBN < 32 ? 32 : kBN;
+    static constexpr int kPartFloats = kBN * kM;
+};
+
+struct SplitShared {
+    uint64_t full[kMaxStages], empty[kMaxStages], acc_full;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+__device__ __forceinline__ void store4(uint16_t *p, const float (&v)[4]) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+
+template <bool kGated, int kBN>
+__global__ void __launch_bounds__(kSplitThreads, Tile<kBN>::kBlocks)
+    ffn_split_kernel(const __grid_constant__ CUtensorMap tm_x,
+                     const __grid_constant__ CUtensorMap tm_w0,
+                     const __grid_constant__ CUtensorMap tm_w1, const FfnArgs a,
+                     const int split_log) {
+    using T = Tile<kBN>;
+    constexpr int kBNLog = kBN == 16 ? 4 : kBN == 32 ? 5 : kBN == 64 ? 6 : 7;
+    constexpr int kStages = T::kStages;
+    constexpr int kOuts = kGated ? kM / 2 : kM;  // outputs of a tile
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *tiles = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // [split ranks][tokens of this CTA][128 weight rows]
+    float *part = reinterpret_cast<float *>(tiles + kStages * T::kStageBytes);
+    SplitShared *sm = reinterpret_cast<SplitShared *>(part + T::kPartFloats);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int K = kGated ? a.H : a.I, O = kGated ? a.I : a.H;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm->full[s], 1);
+            mbar_init(&sm->empty[s], 1);
+        }
+        mbar_init(&sm->acc_full, 1);
+        sm->abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensor_map(&tm_x);
+        prefetch_tensor_map(&tm_w0);
+    }
+    if (warp == 1) {
+        tmem_alloc(&sm->tmem_base, T::kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    // the cluster's CTAs have all started before any of them is written to;
+    // waited for where the partial sums leave
+    cluster_arrive();
+    tc_fence_after_sync();
+    const uint32_t tmem = sm->tmem_base;
+    volatile int *abort_flag = &sm->abort_flag;
+
+    const int o0 = (blockIdx.x >> split_log) * kOuts;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kBN;
+    const int nk = (K + kSliceValues - 1) / kSliceValues;
+    const int k_first = static_cast<int>(static_cast<int64_t>(nk) * rank >> split_log);
+    const int k_end = static_cast<int>(static_cast<int64_t>(nk) * (rank + 1) >> split_log);
+    const int slices = k_end - k_first;
+
+    auto load_weights = [&](int g) {
+        uint8_t *st = tiles + g % kStages * T::kStageBytes;
+        uint64_t *bar = &sm->full[g % kStages];
+        const int k = (k_first + g) * kSliceValues;
+        mbar_arrive_expect_tx(bar, T::kStageBytes);
+        tma_load_2d(st, &tm_w0, bar, k, o0);
+        if (kGated) tma_load_2d(st + kRowsBytes128 / 2, &tm_w1, bar, k, o0);
+    };
+    const int early = kGated ? 0 : min(slices, kStages);
+    if (kGated) griddep_wait();
+    if (!kGated && warp == 0 && elect_one())
+        for (int g = 0; g < early; ++g) load_weights(g);
+    griddep_launch_dependents();
+    if (!kGated) griddep_wait();
+    if (a.reset_status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+        *a.status = MOE_OK;
+
+    if (warp == 0) {
+        const bool issues = elect_one();
+        int g = 0;
+        for (; g < slices; ++g) {
+            const int s = g % kStages;
+            const uint32_t use = g / kStages;
+            if (use > 0 && !warp_wait(&sm->empty[s], (use - 1) & 1, abort_flag)) {
+                if (issues) {
+                    record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                break;
+            }
+            if (issues) {
+                if (g >= early) load_weights(g);
+                tma_load_2d(tiles + s * T::kStageBytes + kRowsBytes128, &tm_x, &sm->full[s],
+                            (k_first + g) * kSliceValues, static_cast<int>(n0));
+            }
+        }
+        // no copy may be in flight when the CTA ends
+        if (issues)
+            for (int i = (g > kStages ? g - kStages : 0); i < g; ++i)
+                drain_wait(&sm->full[i % kStages], (i / kStages) & 1);
+        __syncwarp();
+    } else if (warp == 1) {
+        // the whole warp runs the loop and one lane issues: descriptors and
+        // barriers stay in uniform registers
+        const bool issues = elect_one();
+        constexpr uint32_t idesc = idesc_bf16_f32(kM, kBN);
+        const uint64_t desc0 = sw128_kmajor_desc(smem_addr(tiles));
+        for (int g = 0; g < slices; ++g) {
+            const int s = g % kStages;
+            if (!warp_wait(&sm->full[s], (g / kStages) & 1, abort_flag)) {
+                if (issues) {
+                    record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                break;
+            }
+            tc_fence_after_sync();
+            if (issues) {
+                const uint64_t da = desc0 + s * (T::kStageBytes >> 4);
+                const uint64_t db = da + (kRowsBytes128 >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kSliceBytes / kMmaBytes; ++kk)
+                    mma_f16kind(tmem, da + 2 * kk, db + 2 * kk, idesc, (g | kk) != 0);
+                mma_commit(&sm->empty[s]);
+            }
+        }
+        if (issues) {
+            mma_commit(&sm->acc_full);  // after a failure too: the MMAs issued so far
+            drain_wait(&sm->acc_full, 0);
+        }
+        __syncwarp();
+    }
+
+    // tokens [n0, n0 + tokens) of the tile exist; this CTA stores [first, first
+    // + 2^own_log) of them
+    const int tokens = a.N - n0 < kBN ? static_cast<int>(a.N - n0) : kBN;
+    const int own_log = kBNLog - split_log;
+    const int mine = min(1 << own_log, tokens - (rank << own_log));  // may be <= 0
+    const int64_t first = n0 + (rank << own_log);
+    // the accumulator, then the parts of all ranks
+    bool ok = true;
+    if (lane == 0) ok = mbar_wait(&sm->acc_full, 0, abort_flag);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (!ok && lane == 0) {
+        record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+        *abort_flag = 1;
+    }
+    cluster_wait();
+    if (ok) {
+        tc_fence_after_sync();
+        const int quarter = warp % 4;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t to = smem_addr(part) + 4 * ((rank << own_log) * kM + quarter * 32 + lane);
+        constexpr int kChunk = kBN < 32 ? 16 : 32;
+#pragma unroll 1
+        for (int c = warp / 4 * kChunk; c < tokens; c += kSplitThreads / 128 * kChunk) {
+            float v[32];
+            // a tile of 16 tokens has 32 columns allocated; TMEM wants whole warps
+            __syncwarp();
+            tmem_load32(taddr + c, v);
+            tmem_load_wait();
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+                const int t = c + i;
+                if (t < tokens)
+                    st_cluster_f32(map_to_rank(to + 4 * kM * (t & ((1 << own_log) - 1)),
+                                               t >> own_log),
+                                   v[i]);
+            }
+        }
+        tc_fence_before_sync();
+    }
+    cluster_barrier();
+
+    // four outputs a thread; a thread keeps its outputs from token to token
+    constexpr int kLanes = kOuts / 4;                // threads a token
+    constexpr int kStep = kSplitThreads / kLanes;    // tokens in one go
+    const int ch = threadIdx.x % kLanes * 4;
+    const int o = o0 + ch;
+    const int split = 1 << split_log;
+    if (o < O && !*abort_flag) {
+        for (int t = threadIdx.x / kLanes; t < mine; t += kStep) {
+            const int64_t at = (first + t) * O + o;
+            uint2 res = make_uint2(0, 0);
+            if (!kGated && a.residual)
+                res = __ldcg(reinterpret_cast<const uint2 *>(a.residual + at));
+            float v[4] = {}, w[4] = {};
+            for (int r = 0; r < split; ++r) {
+                const float *p = part + ((r << own_log) + t) * kM + ch;
+                const float4 f = *reinterpret_cast<const float4 *>(p);
+                v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+                if (kGated) {
+                    const float4 u = *reinterpret_cast<const float4 *>(p + kM / 2);
+                    w[0] += u.x, w[1] += u.y, w[2] += u.z, w[3] += u.w;
+                }
+            }
+            if (kGated) {
+                if (a.keep) {
+                    store4(a.out[1] + at, v);
+                    store4(a.out[2] + at, w);
+                }
+                act_all(a.act, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] *= w[i];
+            } else {
+                const float2 x = unpack_bf16x2(res.x), y = unpack_bf16x2(res.y);
+                v[0] += x.x, v[1] += x.y, v[2] += y.x, v[3] += y.y;
+            }
+            store4(a.out[0] + at, v);
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        __syncwarp();
+        tmem_dealloc(tmem, T::kCols);
+    }
+}
+
+template <bool kGated, int kBN>
+cudaError_t launch_one(const FfnMaps &m, const FfnArgs &a, int split, cudaStream_t s) {
+    int split_log = 0;
+    while ((1 << split_log) < split) ++split_log;
+    using T = Tile<kBN>;
+    const size_t smem = 1024 + static_cast<size_t>(T::kStages) * T::kStageBytes +
+                        sizeof(float) * T::kPartFloats + sizeof(SplitShared);
+    auto kern = ffn_split_kernel<kGated, kBN>;
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t err = allow_shared(kern, smem, allowed);
+    if (err != cudaSuccess) return err;
+    const int outs = kGated ? kM / 2 : kM, O = kGated ? a.I : a.H;
+    const dim3 grid(static_cast<unsigned>((O + outs - 1) / outs * split),
+                    static_cast<unsigned>((a.N + kBN - 1) / kBN));
+    return launch_pdl(kern, grid, dim3(kSplitThreads), smem, s, static_cast<unsigned>(split),
+                      m.a[0], m.b[0], m.b[kGated ? 1 : 0], a, split_log);
+}
+
+template <bool kGated>
+cudaError_t launch_tokens(const FfnMaps &m, const FfnArgs &a, const FfnSplit &t, cudaStream_t s) {
+    switch (t.bn) {
+        case 16: return launch_one<kGated, 16>(m, a, t.split, s);
+        case 32: return launch_one<kGated, 32>(m, a, t.split, s);
+        case 64: return launch_one<kGated, 64>(m, a, t.split, s);
+        default: return launch_one<kGated, 128>(m, a, t.split, s);
+    }
+}
+
+}  // namespace
+
+FfnSplit ffn_split(FfnOp op, int64_t N, int H, int I, int num_sms) {
+    FfnSplit t = {0, 1};
+    if (N > 128) return t;
+    t.bn = N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 : 128;
+    const int O = op == kFfnGateUp ? I : H, K = op == kFfnGateUp ? H : I;
+    const int outs = op == kFfnGateUp ? kM / 2 : kM;
+    const int64_t tiles = (O + outs - 1) / outs;
+    const int nk = (K + kSliceValues - 1) / kSliceValues;
+    const int fit = num_sms * (t.bn == 128 ? 1 : 2);
+    while (t.split < 8 && 2 * t.split <= nk && 2 * t.split * tiles <= fit) t.split *= 2;
+    return t;
+}
+
+cudaError_t launch_ffn_split(FfnOp op, const FfnMaps &m, const FfnArgs &a, const FfnSplit &t,
+                             cudaStream_t s) {
+    return op == kFfnGateUp ? launch_tokens<true>(m, a, t, s) : launch_tokens<false>(m, a, t, s);
+}
+
+}  // namespace moe

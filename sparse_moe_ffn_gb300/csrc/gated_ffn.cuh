@@ -66,11 +66,23 @@ cudaError_t launch_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, int *lau
                        cudaStream_t s);
 
 
+// A decode batch (ffn_split.cu): kFfnGateUp and kFfnDown with the weights' rows
+// in boxes of 64 (gate, up) or 128, x's in boxes of `bn`; bn 0: not for this
+// batch.
+struct FfnSplit {
+    int bn;     // tokens of a tile
+    int split;  // CTAs of a cluster that share a tile's K
+};
+FfnSplit ffn_split(FfnOp op, int64_t N, int H, int I, int num_sms);
+cudaError_t launch_ffn_split(FfnOp op, const FfnMaps &maps, const FfnArgs &a, const FfnSplit &t,
+                             cudaStream_t s);
+
 // Up to four tokens (ffn_rows.cu): kFfnGateUp (w0, w1: gate, up; their outputs
 // may be null) and kFfnDown (w0), outputs in a.out[0].
 constexpr int kFfnRowsTokens = 4;
 bool ffn_rows_fit(int64_t N, int K);
 cudaError_t launch_ffn_rows(FfnOp op, const FfnArgs &a, const uint16_t *x, const uint16_t *w0,
-                            const uint16_t *w1, uint16_t *gate, uint16_t *up, cudaStream_t s);
+                            const uint16_t *w1, uint16_t *gate, uint16_t *up, int num_sms,
+                            cudaStream_t s);
 
 }  // namespace moe
