@@ -1,4 +1,4 @@
-// ffn_rows.cu -- the gated feed-forward block for up to four tokens: both
+// ffn_rows.cu -- the gated feed-forward block for one or two tokens: both
 // steps (gate/up with their product, then down) stream their weights once,
 // from memory straight into registers.
 //
@@ -223,9 +223,8 @@ cudaError_t launch_rows(FfnRowsArgs a, int num_sms, cudaStream_t s) {
 
 template <bool kGated>
 cudaError_t launch_tokens(const FfnRowsArgs &a, int num_sms, cudaStream_t s) {
-    if (a.N == 1) return launch_rows<kGated, 1>(a, num_sms, s);
-    if (a.N == 2) return launch_rows<kGated, 2>(a, num_sms, s);
-    return launch_rows<kGated, 4>(a, num_sms, s);
+    return a.N == 1 ? launch_rows<kGated, 1>(a, num_sms, s)
+                    : launch_rows<kGated, 2>(a, num_sms, s);
 }
 
 }  // namespace

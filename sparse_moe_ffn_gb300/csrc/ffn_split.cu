@@ -32,20 +32,27 @@ constexpr int kM = 128;            // weight rows of a tile
 constexpr int kSliceValues = 64;   // of K
 constexpr int kMaxStages = 5;
 
-template <int kBN>
-struct Tile {
-    static constexpr int kXBytes = kBN * kSliceBytes;
-    static constexpr int kStageBytes = kRowsBytes128 + kXBytes;
-    static constexpr int kStages = kBN == 16 ? 5 : kBN == 64 ? 3 : 4;
-    static constexpr int kBlocks = kBN == 128 ? 1 : 2;  // an SM
-    static constexpr uint32_t kCols = kBN < 32 ? 32 : kBN;
-    static constexpr int kPartFloats = kBN * kM;
-};
-
 struct SplitShared {
     uint64_t full[kMaxStages], empty[kMaxStages], acc_full;
     uint32_t tmem_base;
     int abort_flag;
+};
+
+template <int kBN>
+struct Tile {
+    static constexpr int kXBytes = kBN * kSliceBytes;
+    static constexpr int kStageBytes = kRowsBytes128 + kXBytes;
+    // The parts lie behind the stages; those of 128 tokens are too large for
+    // that and take the stages' place, which costs a barrier between the two (64
+    // tokens of 2048 x 8192: 27.1 us instead of 25.9; 128 tokens: 33.9, and 39.2
+    // with the parts behind the stages and one CTA an SM).
+    static constexpr bool kInPlace = kBN == 128;
+    static constexpr int kStages = kBN == 16 ? 5 : kBN == 32 ? 4 : 3;
+    static constexpr uint32_t kCols = kBN < 32 ? 32 : kBN;
+    static constexpr int kPartBytes = 4 * kBN * kM;
+    static_assert(!kInPlace || kPartBytes <= kStages * kStageBytes, "the parts fit");
+    static constexpr size_t kShared = 1024 + static_cast<size_t>(kStages) * kStageBytes +
+                                      (kInPlace ? 0 : kPartBytes) + sizeof(SplitShared);
 };
 
 __device__ __forceinline__ void store4(uint16_t *p, const float (&v)[4]) {
@@ -53,7 +60,7 @@ __device__ __forceinline__ void store4(uint16_t *p, const float (&v)[4]) {
 }
 
 template <bool kGated, int kBN>
-__global__ void __launch_bounds__(kSplitThreads, Tile<kBN>::kBlocks)
+__global__ void __launch_bounds__(kSplitThreads, 2)
     ffn_split_kernel(const __grid_constant__ CUtensorMap tm_x,
                      const __grid_constant__ CUtensorMap tm_w0,
                      const __grid_constant__ CUtensorMap tm_w1, const FfnArgs a,
@@ -65,9 +72,10 @@ __global__ void __launch_bounds__(kSplitThreads, Tile<kBN>::kBlocks)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *behind = tiles + kStages * T::kStageBytes;
     // [split ranks][tokens of this CTA][128 weight rows]
-    float *part = reinterpret_cast<float *>(tiles + kStages * T::kStageBytes);
-    SplitShared *sm = reinterpret_cast<SplitShared *>(part + T::kPartFloats);
+    float *part = reinterpret_cast<float *>(T::kInPlace ? tiles : behind);
+    SplitShared *sm = reinterpret_cast<SplitShared *>(behind + (T::kInPlace ? 0 : T::kPartBytes));
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = static_cast<int>(cluster_ctarank());
     const int K = kGated ? a.H : a.I, O = kGated ? a.I : a.H;
@@ -91,7 +99,7 @@ __global__ void __launch_bounds__(kSplitThreads, Tile<kBN>::kBlocks)
     __syncthreads();
     // the cluster's CTAs have all started before any of them is written to;
     // waited for where the partial sums leave
-    cluster_arrive();
+    if (!T::kInPlace) cluster_arrive();
     tc_fence_after_sync();
     const uint32_t tmem = sm->tmem_base;
     volatile int *abort_flag = &sm->abort_flag;
@@ -190,6 +198,7 @@ __global__ void __launch_bounds__(kSplitThreads, Tile<kBN>::kBlocks)
         record_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
         *abort_flag = 1;
     }
+    if (T::kInPlace) cluster_arrive();  // this CTA's MMAs have read its stages
     cluster_wait();
     if (ok) {
         tc_fence_after_sync();
@@ -267,8 +276,7 @@ cudaError_t launch_one(const FfnMaps &m, const FfnArgs &a, int split, cudaStream
     int split_log = 0;
     while ((1 << split_log) < split) ++split_log;
     using T = Tile<kBN>;
-    const size_t smem = 1024 + static_cast<size_t>(T::kStages) * T::kStageBytes +
-                        sizeof(float) * T::kPartFloats + sizeof(SplitShared);
+    const size_t smem = T::kShared;
     auto kern = ffn_split_kernel<kGated, kBN>;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t err = allow_shared(kern, smem, allowed);
@@ -292,15 +300,24 @@ cudaError_t launch_tokens(const FfnMaps &m, const FfnArgs &a, const FfnSplit &t,
 
 }  // namespace
 
+// The tokens' tile is the smallest that holds them all, or a smaller one where
+// the weights have so few rows that clusters of 8 still fit at once: the rows
+// are then read again, from L2, and twice as many CTAs do so (128 tokens of 2048
+// x 8192: 34.2 us with 128 tokens a tile in the down step, 28.8 with 64).
+// Beyond 128 tokens the pair kernel takes over (4096 x 12288, 256 tokens in two
+// tiles of 128: 98 us against 82; 2048 x 8192 38.8 against 40).
 FfnSplit ffn_split(FfnOp op, int64_t N, int H, int I, int num_sms) {
     FfnSplit t = {0, 1};
     if (N > 128) return t;
-    t.bn = N <= 16 ? 16 : N <= 32 ? 32 : N <= 64 ? 64 : 128;
+    const int n = static_cast<int>(N);
     const int O = op == kFfnGateUp ? I : H, K = op == kFfnGateUp ? H : I;
     const int outs = op == kFfnGateUp ? kM / 2 : kM;
-    const int64_t tiles = (O + outs - 1) / outs;
+    const int64_t rows = (O + outs - 1) / outs;
     const int nk = (K + kSliceValues - 1) / kSliceValues;
-    const int fit = num_sms * (t.bn == 128 ? 1 : 2);
+    const int64_t fit = 2 * static_cast<int64_t>(num_sms);
+    t.bn = n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : 128;
+    while (t.bn > 16 && 8 * rows * ((n + t.bn / 2 - 1) / (t.bn / 2)) <= fit) t.bn /= 2;
+    const int64_t tiles = rows * ((n + t.bn - 1) / t.bn);
     while (t.split < 8 && 2 * t.split <= nk && 2 * t.split * tiles <= fit) t.split *= 2;
     return t;
 }

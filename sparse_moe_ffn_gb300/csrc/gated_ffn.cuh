@@ -77,9 +77,9 @@ FfnSplit ffn_split(FfnOp op, int64_t N, int H, int I, int num_sms);
 cudaError_t launch_ffn_split(FfnOp op, const FfnMaps &maps, const FfnArgs &a, const FfnSplit &t,
                              cudaStream_t s);
 
-// Up to four tokens (ffn_rows.cu): kFfnGateUp (w0, w1: gate, up; their outputs
+// One or two tokens (ffn_rows.cu): kFfnGateUp (w0, w1: gate, up; their outputs
 // may be null) and kFfnDown (w0), outputs in a.out[0].
-constexpr int kFfnRowsTokens = 4;
+constexpr int kFfnRowsTokens = 2;
 bool ffn_rows_fit(int64_t N, int K);
 cudaError_t launch_ffn_rows(FfnOp op, const FfnArgs &a, const uint16_t *x, const uint16_t *w0,
                             const uint16_t *w1, uint16_t *gate, uint16_t *up, int num_sms,

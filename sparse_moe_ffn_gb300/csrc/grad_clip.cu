@@ -14,6 +14,7 @@
 // squared again in 64 bits.
 #include <cuda_bf16.h>
 
+#include "cluster.cuh"
 #include "grad_clip.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -69,15 +70,27 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float *v) {
     v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
 }
 
-// Eight values from value i of a tensor on (16-byte aligned).
+// Eight fp32 values by one access of 32 bytes, which are whole sectors: two of
+// 16 a lane would ask for each sector twice.
+__device__ __forceinline__ void ld_f32x8(const float *p, float *v) {
+    asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]),
+                   "=f"(v[6]), "=f"(v[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void st_f32x8(float *p, const float *v) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
+                 "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
+// Eight values from value i of a tensor on (32-byte aligned in fp32, else 16).
 __device__ __forceinline__ void load8(const void *src, bool bf16, int64_t i, float *v) {
     if (bf16) {
         unpack8(__ldcg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + i)), v);
     } else {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(src) + i);
-        const float4 a = __ldcg(p), b = __ldcg(p + 1);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        ld_f32x8(static_cast<const float *>(src) + i, v);
     }
 }
 
@@ -94,9 +107,7 @@ __device__ __forceinline__ void store8(void *dst, bool bf16, int64_t i, const fl
             make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                        pack_bf16x2(v[6], v[7]));
     } else {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(dst) + i);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        st_f32x8(static_cast<float *>(dst) + i, v);
     }
 }
 
@@ -106,15 +117,20 @@ __device__ __forceinline__ void store1(void *dst, bool bf16, int64_t i, float v)
 }
 
 // The chunks of block blockIdx.x, one by one: visit(tensor, first value, values).
-template <int kMax, typename Visit>
+// kBack: from the last one back.
+template <bool kBack, int kMax, typename Visit>
 __device__ __forceinline__ void for_chunks(const GradTable<kMax> &t, const Visit &visit) {
     const int64_t chunks = t.first[t.n];
     const int from = static_cast<int>(chunks * blockIdx.x / gridDim.x);
     const int to = static_cast<int>(chunks * (blockIdx.x + 1) / gridDim.x);
     if (from >= to) return;
-    int k = tensor_of(t, from);
-    for (int c = from; c < to; ++c) {
-        while (c >= t.first[k + 1]) ++k;
+    int k = tensor_of(t, kBack ? to - 1 : from);
+    for (int i = 0; i < to - from; ++i) {
+        const int c = kBack ? to - 1 - i : from + i;
+        if (kBack)
+            while (c < t.first[k]) --k;
+        else
+            while (c >= t.first[k + 1]) ++k;
         const int64_t begin = static_cast<int64_t>(c - t.first[k]) * kChunk;
         const int64_t left = t.size[k] - begin;
         visit(k, begin, left < kChunk ? static_cast<int>(left) : kChunk);
@@ -141,7 +157,7 @@ __global__ void __launch_bounds__(kThreads)
     griddep_launch_dependents();
     griddep_wait();
     double sum = 0.0;
-    for_chunks(t, [&](int k, int64_t begin, int n) {
+    for_chunks<false>(t, [&](int k, int64_t begin, int n) {
         const bool bf16 = t.flags[k] & kSrcBf16;
         const void *src = t.src[k];
         int i = 0;
@@ -172,6 +188,71 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
+// A small set in one launch: a cluster of eight blocks whose warps take pieces of
+// 1024 values each (a piece's loads are all in flight at once), and whose sums
+// are joined through shared memory, block by block in order.
+constexpr int kSmallBlocks = 8;
+constexpr int kSmallThreads = 1024;
+constexpr int kPiece = 1024;
+
+__global__ void __launch_bounds__(kSmallThreads)
+    grad_norm_small_kernel(const __grid_constant__ GradTable<64> t, float *norm) {
+    __shared__ double sums[kSmallThreads / 32];
+    __shared__ double block;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = static_cast<int>(cluster_ctarank());
+    double sum = 0.0;
+    // neighbouring pieces go to different blocks
+    for (int c = warp * kSmallBlocks + rank; c < t.first[t.n]; c += kSmallBlocks * kSmallThreads / 32) {
+        const int k = tensor_of(t, c);
+        const int64_t begin = static_cast<int64_t>(c - t.first[k]) * kPiece;
+        const int64_t left = t.size[k] - begin;
+        const int n = left < kPiece ? static_cast<int>(left) : kPiece;
+        const bool bf16 = t.flags[k] & kSrcBf16;
+        const void *src = t.src[k];
+        const bool vec = t.flags[k] & kVector;
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = 8 * (j * 32 + lane);
+            if (vec && i + 8 <= n) {
+                load8(src, bf16, begin + i, v + 8 * j);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[8 * j + e] = i + e < n ? load1(src, bf16, begin + i + e) : 0.f;
+            }
+        }
+        sum += sum_squares(v);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        sum = sums[lane];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0) block = sum;
+    }
+    cluster_barrier();
+    if (rank == 0 && warp == 0) {
+        sum = 0.0;
+        if (lane < kSmallBlocks) {
+            const uint32_t lo = ld_cluster_u32(&block, lane);
+            const uint32_t hi = ld_cluster_u32(reinterpret_cast<const uint32_t *>(&block) + 1, lane);
+            sum = __hiloint2double(static_cast<int>(hi), static_cast<int>(lo));
+        }
+#pragma unroll
+        for (int d = kSmallBlocks / 2; d > 0; d >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0) *norm = static_cast<float>(sqrt(sum));
+    }
+    cluster_barrier();  // the blocks' sums have been read
+}
+
 __global__ void __launch_bounds__(kThreads)
     grad_norm_finish_kernel(const double *parts, int64_t n, float *norm) {
     griddep_launch_dependents();
@@ -190,7 +271,8 @@ __global__ void __launch_bounds__(kThreads)
     griddep_wait();
     const float size = __ldcg(norm);
     const float factor = size <= max_norm ? 1.f : max_norm / size;
-    for_chunks(t, [&](int k, int64_t begin, int n) {
+    // backwards: what the norm's kernel read last may still be in L2
+    for_chunks<true>(t, [&](int k, int64_t begin, int n) {
         const bool bf16 = t.flags[k] & kSrcBf16, out_bf16 = t.flags[k] & kDstBf16;
         const void *src = t.src[k];
         void *dst = t.dst[k];
@@ -226,7 +308,7 @@ __global__ void __launch_bounds__(kThreads)
 
 // Tensors [at, at + kMax) of the set.
 template <int kMax>
-GradTable<kMax> table_of(const GradSet &g, int64_t at) {
+GradTable<kMax> table_of(const GradSet &g, int64_t at, int chunk = kChunk) {
     GradTable<kMax> t;
     t.n = static_cast<int>(g.n - at < kMax ? g.n - at : kMax);
     t.first[0] = 0;
@@ -237,12 +319,15 @@ GradTable<kMax> table_of(const GradSet &g, int64_t at) {
         t.src[i] = src;
         t.dst[i] = dst;
         t.size[i] = size;
-        t.first[i + 1] = t.first[i] + static_cast<int>((size + kChunk - 1) / kChunk);
+        t.first[i + 1] = t.first[i] + static_cast<int>((size + chunk - 1) / chunk);
         t.flags[i] = (g.bf16[at + i] ? kSrcBf16 : 0) |
                      (g.out && g.out_bf16[at + i] ? kDstBf16 : 0) |
-                     ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) % 16
-                          ? 0
-                          : kVector);
+                     (reinterpret_cast<uintptr_t>(src) % (g.bf16[at + i] ? 16 : 32) == 0 &&
+                              (!g.out || reinterpret_cast<uintptr_t>(dst) %
+                                                 (g.out_bf16[at + i] ? 16 : 32) ==
+                                             0)
+                          ? kVector
+                          : 0);
     }
     return t;
 }
@@ -272,6 +357,8 @@ cudaError_t clip_launch(const GradSet &g, int64_t at, const float *norm, float m
 }
 
 constexpr int kSmallTable = 64;  // a table of 1.9 KB; the large one has 15 KB
+// Four pieces a warp of the cluster: one more launch costs what a dozen more do.
+constexpr int kSmallPieces = 4 * kSmallBlocks * kSmallThreads / 32;
 
 }  // namespace
 
@@ -281,6 +368,14 @@ int64_t grad_norm_parts(int64_t n, int num_sms) {
 
 cudaError_t launch_grad_norm(const GradSet &g, double *parts, float *norm, int num_sms,
                              int *launches, cudaStream_t s) {
+    if (g.n <= kSmallTable) {
+        const GradTable<kSmallTable> t = table_of<kSmallTable>(g, 0, kPiece);
+        if (t.first[t.n] <= kSmallPieces) {
+            *launches += 1;
+            return launch_pdl(grad_norm_small_kernel, dim3(kSmallBlocks), dim3(kSmallThreads), 0, s,
+                              kSmallBlocks, t, norm);
+        }
+    }
     int64_t used = 0;
     for (int64_t at = 0; at == 0 || at < g.n; at += kGradTable) {
         float *direct = g.n <= kGradTable ? norm : nullptr;  // a single block's sum is the whole

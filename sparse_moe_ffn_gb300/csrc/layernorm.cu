@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(row_threads<kRow>())
 // kSumColumns: the block keeps its columns' sums (dweight, dbias) and stores
 // them as part blockIdx.x.
 template <typename T, int kVec, int kRow, int kChunks, bool kSumColumns>
-__global__ void __launch_bounds__(row_threads<kRow>())
+__global__ void __launch_bounds__(row_threads<kRow>(), kSumColumns ? 512 / row_threads<kRow>() : 1)
     layernorm_grad_kernel(const LayerNormGradArgs a) {
     constexpr int kThreads = row_threads<kRow>();
     constexpr int kRows = kThreads / kRow;
@@ -249,30 +249,41 @@ __global__ void __launch_bounds__(row_threads<kRow>())
             w[c].load(static_cast<const T *>(a.weight) + kVec * (t + c * kRow));
     }
     float dw[kSumColumns ? kCols : 1] = {}, db[kSumColumns ? kCols : 1] = {};
+    // a row's operands: the next one's are asked for before this one's sums,
+    // where registers are left for them
+    constexpr bool kAhead = kSumColumns && (kCols <= 8 || (kVec == 8 && kRow > 32));
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+    Piece<T, kVec> r[kChunks], d[kChunks], e[kChunks];
+    float mean = 0.f, rstd = 0.f;
+    auto load = [&](int64_t n, Piece<T, kVec>(&pr)[kChunks], Piece<T, kVec>(&pd)[kChunks],
+                    Piece<T, kVec>(&pe)[kChunks], float &m, float &q) {
+        const bool row = n < a.N;
+        const int64_t at = n * a.H;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            pr[c].zero();
+            pd[c].zero();
+            pe[c].zero();
+            if (row && t + c * kRow < pieces) {
+                pr[c].load(x + at + kVec * (t + c * kRow));
+                pd[c].load(dout + at + kVec * (t + c * kRow));
+                if (dres) pe[c].load(dres + at + kVec * (t + c * kRow));
+            }
+        }
+        m = row ? __ldcg(a.mean + n) : 0.f;
+        q = row ? __ldcg(a.rstd + n) : 0.f;
+    };
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows;
+    if (kAhead) load(first + sub, r, d, e, mean, rstd);
     int turn = 0;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kRows; base < a.N;
-         base += static_cast<int64_t>(gridDim.x) * kRows, turn ^= 1) {
+    for (int64_t base = first; base < a.N; base += stride, turn ^= 1) {
         const int64_t n = base + sub;
         const bool row = n < a.N;
         const int64_t at = n * a.H;
-        Piece<T, kVec> r[kChunks], d[kChunks], e[kChunks];
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            r[c].zero();
-            d[c].zero();
-            if (row && t + c * kRow < pieces) {
-                r[c].load(x + at + kVec * (t + c * kRow));
-                d[c].load(dout + at + kVec * (t + c * kRow));
-            }
-        }
-        if (dres) {
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                e[c].zero();
-                if (row && t + c * kRow < pieces) e[c].load(dres + at + kVec * (t + c * kRow));
-            }
-        }
-        const float mean = row ? __ldcg(a.mean + n) : 0.f, rstd = row ? __ldcg(a.rstd + n) : 0.f;
+        if (!kAhead) load(n, r, d, e, mean, rstd);
+        Piece<T, kVec> nr[kAhead ? kChunks : 1], nd[kAhead ? kChunks : 1], ne[kAhead ? kChunks : 1];
+        float nmean = 0.f, nrstd = 0.f;
+        if constexpr (kAhead) load(n + stride, nr, nd, ne, nmean, nrstd);
         float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
@@ -293,27 +304,35 @@ __global__ void __launch_bounds__(row_threads<kRow>())
                 s[1] = fmaf(u, m, s[1]);
             }
         }
-        if (!a.dx) continue;
-        row_sums(sums, turn, t, sub, s);
-        if (!row) continue;
-        const float m1 = s[0] * inv_h, m2 = s[1] * inv_h;
+        if (a.dx) {
+            row_sums(sums, turn, t, sub, s);
+            const float m1 = s[0] * inv_h, m2 = s[1] * inv_h;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            if (t + c * kRow >= pieces) break;
-            float v[kVec], g[kVec], y[kVec], z[kVec];
-            r[c].get(v);
-            d[c].get(y);
-            w[c].get(g);
+            for (int c = 0; c < kChunks; ++c) {
+                if (!row || t + c * kRow >= pieces) break;
+                float v[kVec], g[kVec], y[kVec], z[kVec];
+                r[c].get(v);
+                d[c].get(y);
+                w[c].get(g);
+                e[c].get(z);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) z[i] = 0.f;
-            if (dres) e[c].get(z);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                const float m = (v[i] - mean) * rstd;
-                v[i] = fmaf(rstd, fmaf(-m, m2, fmaf(y[i], g[i], -m1)), z[i]);
+                for (int i = 0; i < kVec; ++i) {
+                    const float m = (v[i] - mean) * rstd;
+                    v[i] = fmaf(rstd, fmaf(-m, m2, fmaf(y[i], g[i], -m1)), z[i]);
+                }
+                r[c].set(v);
+                r[c].store(static_cast<T *>(a.dx) + at + kVec * (t + c * kRow));
             }
-            r[c].set(v);
-            r[c].store(static_cast<T *>(a.dx) + at + kVec * (t + c * kRow));
+        }
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                r[c] = nr[c];
+                d[c] = nd[c];
+                e[c] = ne[c];
+            }
+            mean = nmean;
+            rstd = nrstd;
         }
     }
     if (!kSumColumns) return;
@@ -378,9 +397,12 @@ __global__ void __launch_bounds__(kColumnThreads)
     __stcg(out + a.H + h, db);
 }
 
-// The parts' sum, in order and in 64 bits: 32 columns a block, 8 warps taking
-// the parts in turn.
-constexpr int kFinishThreads = 256;
+// The parts' sum, in order: 32 columns a block, its warps taking the parts in
+// turn, eight at a time.  Eight are added in fp32, those sums and the warps' in
+// 64 bits, of which an SM adds (and widens to) few: with every part widened 304
+// parts of 2 x 1111 columns took 9.5 us, so @F.
+constexpr int kFinishThreads = 1024;
+constexpr int kFinishAhead = 8;
 
 __global__ void __launch_bounds__(kFinishThreads)
     layernorm_finish_kernel(const float *part, int blocks, int H, float *dweight, float *dbias) {
@@ -390,24 +412,26 @@ __global__ void __launch_bounds__(kFinishThreads)
     griddep_wait();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;  // of the 2 H sums
+    const bool live = i < 2 * static_cast<int64_t>(H);
     double s = 0.0;
-    if (i < 2 * static_cast<int64_t>(H)) {
-        int b = warp;
-        for (; b + 3 * kWarps < blocks; b += 4 * kWarps) {
-            float v[4];
+    for (int b = warp; live && b < blocks; b += kFinishAhead * kWarps) {
+        float v[kFinishAhead];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = __ldcg(part + static_cast<int64_t>(b + j * kWarps) * 2 * H + i);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s += v[j];
-        }
-        for (; b < blocks; b += kWarps) s += __ldcg(part + static_cast<int64_t>(b) * 2 * H + i);
+        for (int j = 0; j < kFinishAhead; ++j)
+            v[j] = b + j * kWarps < blocks
+                       ? __ldcg(part + static_cast<int64_t>(b + j * kWarps) * 2 * H + i)
+                       : 0.f;
+        s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
     }
     sums[warp][lane] = s;
     __syncthreads();
-    if (warp != 0 || i >= 2 * static_cast<int64_t>(H)) return;
+    if (warp != 0 || !live) return;
+    double f[4] = {};
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) s += sums[w][lane];
+    for (int w = 0; w < kWarps; w += 4)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] += sums[w + j][lane];
+    s = (f[0] + f[1]) + (f[2] + f[3]);
     float *out = i < H ? dweight : dbias;
     if (out) out[i < H ? i : i - H] = static_cast<float>(s);
 }
@@ -453,38 +477,48 @@ cudaError_t launch_forward(const LayerNormArgs &a, int num_sms, cudaStream_t s) 
     return cudaErrorInvalidValue;
 }
 
+// As many blocks as fit at once: two of 256 threads an SM with the sums in
+// registers, else four times that, one after the other.
 template <typename T, int kVec, int kRow, int kChunks, bool kSum>
-cudaError_t launch_grad_rows(const LayerNormGradArgs &a, int64_t blocks, cudaStream_t s) {
-    constexpr int kRows = row_threads<kRow>() / kRow;
+cudaError_t launch_grad_rows(const LayerNormGradArgs &a, int num_sms, int *blocks,
+                             cudaStream_t s) {
+    constexpr int kThreads = row_threads<kRow>(), kRows = kThreads / kRow;
     const int64_t most = (a.N + kRows - 1) / kRows;
-    if (blocks > most) blocks = most;
+    const int64_t fit = static_cast<int64_t>(num_sms) * (kSum ? 512 / kThreads : 4);
+    *blocks = static_cast<int>(most < fit ? most : fit);
     return launch_pdl(layernorm_grad_kernel<T, kVec, kRow, kChunks, kSum>,
-                      dim3(static_cast<unsigned>(blocks)), dim3(row_threads<kRow>()), 0, s, 1, a);
+                      dim3(static_cast<unsigned>(*blocks)), dim3(kThreads), 0, s, 1, a);
 }
 
-// 16 columns a thread (8 in rows of fewer than 512)
+// 16 columns a thread in vectors of eight bf16 values (8 in rows of up to 256),
+// else 8 (16 in rows over 4096): more leave no registers for the row ahead.
 template <typename T, int kVec>
-cudaError_t launch_backward(const LayerNormGradArgs &a, int64_t blocks, cudaStream_t s) {
-    const int pieces = a.H / kVec;
-    constexpr int kC = 16 / kVec;
-    if (pieces <= 16 * kC) return launch_grad_rows<T, kVec, 32, kC / 2, true>(a, blocks, s);
-    if (pieces <= 32 * kC) return launch_grad_rows<T, kVec, 32, kC, true>(a, blocks, s);
-    if (pieces <= 64 * kC) return launch_grad_rows<T, kVec, 64, kC, true>(a, blocks, s);
-    if (pieces <= 128 * kC) return launch_grad_rows<T, kVec, 128, kC, true>(a, blocks, s);
-    if (pieces <= 256 * kC) return launch_grad_rows<T, kVec, 256, kC, true>(a, blocks, s);
-    return launch_grad_rows<T, kVec, 512, kC, true>(a, blocks, s);
+cudaError_t launch_backward(const LayerNormGradArgs &a, int num_sms, int *blocks, cudaStream_t s) {
+    constexpr int kC = kVec == 8 ? 2 : 8 / kVec;  // pieces a thread
+    const int threads = (a.H / kVec + kC - 1) / kC;
+    if (kVec == 8 && a.H <= 256)
+        return launch_grad_rows<T, kVec, 32, 8 / kVec, true>(a, num_sms, blocks, s);
+    if (threads <= 32) return launch_grad_rows<T, kVec, 32, kC, true>(a, num_sms, blocks, s);
+    if (threads <= 64) return launch_grad_rows<T, kVec, 64, kC, true>(a, num_sms, blocks, s);
+    if (threads <= 128) return launch_grad_rows<T, kVec, 128, kC, true>(a, num_sms, blocks, s);
+    if (threads <= 256) return launch_grad_rows<T, kVec, 256, kC, true>(a, num_sms, blocks, s);
+    if (threads <= 512) return launch_grad_rows<T, kVec, 512, kC, true>(a, num_sms, blocks, s);
+    return launch_grad_rows<T, kVec, 512, 16 / kVec, true>(a, num_sms, blocks, s);
 }
 
 template <typename T, int kVec>
-cudaError_t launch_backward_wide(const LayerNormGradArgs &a, int64_t blocks, cudaStream_t s) {
+cudaError_t launch_backward_wide(const LayerNormGradArgs &a, int num_sms, cudaStream_t s) {
     const int pieces = a.H / kVec;
-    if (pieces <= 2048) return launch_grad_rows<T, kVec, 512, 4, false>(a, blocks, s);
-    if (pieces <= 4096) return launch_grad_rows<T, kVec, 1024, 4, false>(a, blocks, s);
-    if (pieces <= 8192) return launch_grad_rows<T, kVec, 1024, 8, false>(a, blocks, s);
+    int blocks;
+    if (pieces <= 2048) return launch_grad_rows<T, kVec, 512, 4, false>(a, num_sms, &blocks, s);
+    if (pieces <= 4096) return launch_grad_rows<T, kVec, 1024, 4, false>(a, num_sms, &blocks, s);
+    if (pieces <= 8192) return launch_grad_rows<T, kVec, 1024, 8, false>(a, num_sms, &blocks, s);
     if constexpr (kVec <= 4) {
-        if (pieces <= 16384) return launch_grad_rows<T, kVec, 1024, 16, false>(a, blocks, s);
+        if (pieces <= 16384)
+            return launch_grad_rows<T, kVec, 1024, 16, false>(a, num_sms, &blocks, s);
     }
-    if constexpr (kVec == 1) return launch_grad_rows<T, kVec, 1024, 64, false>(a, blocks, s);
+    if constexpr (kVec == 1)
+        return launch_grad_rows<T, kVec, 1024, 64, false>(a, num_sms, &blocks, s);
     return cudaErrorInvalidValue;
 }
 
@@ -497,19 +531,12 @@ bool vectors(int H, int bf16, std::initializer_list<const void *> arrays) {
     return true;
 }
 
-int rows_a_block(int H) {
-    // what launch_backward takes: 256 threads, 16 columns a thread (8 up to 256)
-    const int threads = H <= 512 ? 32 : H <= 1024 ? 64 : H <= 2048 ? 128 : 256;
-    return 256 / threads;
-}
-
 }  // namespace
 
 int layernorm_grad_blocks(int64_t N, int H, int num_sms) {
     if (H <= kSumColumnsH) {
-        const int64_t rows = rows_a_block(H), blocks = (N + rows - 1) / rows;
         const int64_t most = 2 * static_cast<int64_t>(num_sms);
-        return static_cast<int>(blocks < most ? blocks : most);
+        return static_cast<int>(N < most ? N : most);
     }
     const int64_t columns = (H + kColumnThreads - 1) / kColumnThreads;
     int64_t runs = 4 * static_cast<int64_t>(num_sms) / columns;
@@ -528,16 +555,16 @@ cudaError_t launch_layernorm(const LayerNormArgs &a, int bf16, int num_sms, cuda
 cudaError_t launch_layernorm_grad(const LayerNormGradArgs &a, int bf16, int num_sms, int *launches,
                                   cudaStream_t s) {
     const bool vec = vectors(a.H, bf16, {a.dout, a.x, a.weight, a.dresidual, a.dx});
-    const int blocks = layernorm_grad_blocks(a.N, a.H, num_sms);
+    int blocks = layernorm_grad_blocks(a.N, a.H, num_sms);  // at most
     const bool sums = a.dweight || a.dbias;
     cudaError_t err = cudaSuccess;
     if (a.H <= kSumColumnsH) {
         if (bf16)
-            err = vec ? launch_backward<__nv_bfloat16, 8>(a, blocks, s)
-                      : launch_backward<__nv_bfloat16, 1>(a, blocks, s);
+            err = vec ? launch_backward<__nv_bfloat16, 8>(a, num_sms, &blocks, s)
+                      : launch_backward<__nv_bfloat16, 1>(a, num_sms, &blocks, s);
         else
-            err = vec ? launch_backward<float, 4>(a, blocks, s)
-                      : launch_backward<float, 1>(a, blocks, s);
+            err = vec ? launch_backward<float, 4>(a, num_sms, &blocks, s)
+                      : launch_backward<float, 1>(a, num_sms, &blocks, s);
         *launches += 1;
     } else {
         if (sums) {  // first: dx may be one of the inputs
@@ -550,13 +577,12 @@ cudaError_t launch_layernorm_grad(const LayerNormGradArgs &a, int bf16, int num_
             *launches += 1;
         }
         if (err == cudaSuccess && a.dx) {
-            const int64_t most = 4 * static_cast<int64_t>(num_sms);
             if (bf16)
-                err = vec ? launch_backward_wide<__nv_bfloat16, 8>(a, most, s)
-                          : launch_backward_wide<__nv_bfloat16, 1>(a, most, s);
+                err = vec ? launch_backward_wide<__nv_bfloat16, 8>(a, num_sms, s)
+                          : launch_backward_wide<__nv_bfloat16, 1>(a, num_sms, s);
             else
-                err = vec ? launch_backward_wide<float, 4>(a, most, s)
-                          : launch_backward_wide<float, 1>(a, most, s);
+                err = vec ? launch_backward_wide<float, 4>(a, num_sms, s)
+                          : launch_backward_wide<float, 1>(a, num_sms, s);
             *launches += 1;
         }
     }
