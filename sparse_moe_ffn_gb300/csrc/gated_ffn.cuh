@@ -26,7 +26,6 @@ enum FfnOp { kFfnGateUp = 0, kFfnDown = 1, kFfnDh = 2, kFfnDx = 3, kFfnDw = 4 };
 // two tiles a pair.
 constexpr int kFfnMaxPairs = 76;
 constexpr int kFfnTile = 256;  // rows of a tile
-constexpr size_t kFfnPartFloats = static_cast<size_t>(kFfnTile) * 256;
 
 // How a launch's tiles go to the pairs: whole waves of tiles, then, where the
 // last wave is partial and K long, its tiles' K slices in `parts` equal runs,
@@ -36,6 +35,7 @@ struct FfnPlan {
     int whole;   // tiles that one pair computes from end to end
     int parts;   // > 0: pairs that share the other tiles' slices
     int nk;      // K slices of a tile
+    int bn;      // accumulator columns of a tile: 256 or 128
     int pairs;   // launched
 };
 
@@ -47,15 +47,16 @@ struct FfnArgs {
     const uint16_t *gate, *up;  // kFfnDh
     const uint16_t *residual;   // kFfnDown, nullable
     uint16_t *out[3];           // h, gate, up; h, dgate, dup; dWg, dWu, dWd; or one
-    float *part;                // [2 pairs][kFfnPartFloats]
+    float *part;                // [2 pairs][256 x bn]
     int32_t *status;
     int reset_status;
     FfnPlan plan;
 };
 
 // The operands' tensor maps: a: the M side's, b: the N side's.  A K-major
-// operand ([rows, K]) comes in boxes of 64 values of K x 128 rows, an MN-major
-// one ([K, rows]) in boxes of 64 rows x 64 values of K.
+// operand ([rows, K]) comes in boxes of 64 values of K x the rows of a CTA (128,
+// or on the N side half a tile's columns), an MN-major one ([K, rows]) in boxes
+// of 64 rows x 64 values of K.
 struct FfnMaps {
     CUtensorMap a[3], b[3];
 };
@@ -64,6 +65,8 @@ FfnPlan ffn_plan(FfnOp op, int64_t N, int H, int I, int num_sms);
 size_t ffn_part_bytes(const FfnPlan &p);
 cudaError_t launch_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, int *launches,
                        cudaStream_t s);
+// Adds the partial sums, where the plan has any.
+cudaError_t launch_ffn_join(FfnOp op, const FfnArgs &a, int *launches, cudaStream_t s);
 
 
 // A decode batch (ffn_split.cu): kFfnGateUp and kFfnDown with the weights' rows
