@@ -6,9 +6,14 @@ biased projection MLP (linear, SiLU, linear) read from the e4m3 copy.
 ``router_step`` is the training signal of its router: logits in fp32, the load
 balance and log-sum-exp losses over the tokens that a mask leaves in, and the
 gradient of the router's weights.
+``DenseBlock`` is the FFN half of a decoder block without experts: residual add +
+layer norm and the gated feed-forward block onto the residual stream, for
+serving and, with what ``forward(..., keep=True)`` keeps, for training.
+``clip_step`` scales a set of gradients to a largest norm.
 
-``python -m sparse_moe_ffn_gb300.block`` runs a block and then balances a
-skewed router by gradient steps, printing the load before and after.
+``python -m sparse_moe_ffn_gb300.block`` runs a block, balances a skewed router
+by gradient steps, printing the load before and after, and takes steps of a
+dense block.
 """
 from __future__ import annotations
 
@@ -73,6 +78,82 @@ def router_step(normed, router, k: int, balance_weight: float = 0.01, z_weight: 
     return losses, counts, dlogits.t() @ hidden
 
 
+class DenseBlock:
+    """r = x + residual, out = FFN(layernorm(r)) + r: norm_weight [H], norm_bias
+    [H] or None, w_gate and w_up [I, H], w_down [H, I], all bf16; activation as
+    moe_gated_ffn takes it."""
+
+    def __init__(self, norm_weight, norm_bias, w_gate, w_up, w_down, activation: str = "silu",
+                 eps: float = 1e-5):
+        self.norm_weight, self.norm_bias = norm_weight, norm_bias
+        self.w_gate, self.w_up, self.w_down = w_gate, w_up, w_down
+        self.activation, self.eps = activation, eps
+
+    def __call__(self, x, residual, keep: bool = False, workspace=None):
+        """out [N, H], the residual stream behind the block; with ``keep`` also
+        what ``backward`` needs.  residual becomes r."""
+        normed, mean, rstd = binding.moe_layernorm(x, self.norm_weight, self.norm_bias, residual,
+                                                   self.eps)
+        out, gate, up = binding.moe_gated_ffn(normed, self.w_gate, self.w_up, self.w_down,
+                                              self.activation, residual=residual, keep=keep,
+                                              workspace=workspace)
+        return (out, (residual, normed, mean, rstd, gate, up)) if keep else out
+
+    def backward(self, dout, kept, workspace=None):
+        """(the gradient of r, which is x's and the residual's, {name: gradient}
+        of the weights) for the gradient dout of out: bf16 for the projections,
+        fp32 for the norm."""
+        r, normed, mean, rstd, gate, up = kept
+        dnormed, dw_gate, dw_up, dw_down = binding.moe_gated_ffn_backward(
+            dout, normed, self.w_gate, self.w_up, self.w_down, gate, up, self.activation,
+            workspace=workspace)
+        dr, dweight, dbias = binding.moe_layernorm_backward(
+            dnormed, r, self.norm_weight, mean, rstd, dresidual=dout,
+            want_dbias=self.norm_bias is not None)
+        grads = {"w_gate": dw_gate, "w_up": dw_up, "w_down": dw_down, "norm_weight": dweight}
+        if dbias is not None:
+            grads["norm_bias"] = dbias
+        return dr, grads
+
+
+def clip_step(grads: dict, max_norm: float):
+    """Scales the gradients in place so that the norm of all of them together is
+    max_norm at most; returns the norm before (fp32 [1], on the device)."""
+    kept = binding.GradSet(grads.values())
+    norm = binding.moe_grad_norm(kept)
+    binding.moe_clip_grads(kept, norm, max_norm)
+    return norm
+
+
+def dense_steps(N: int = 1000, H: int = 256, I: int = 512, steps: int = 20, max_norm: float = 1.0):
+    """Gradient steps of a DenseBlock towards a random target, the gradients
+    clipped; returns the norms before clipping."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+
+    def normal(*s, std):
+        return torch.randn(s, generator=g, device="cuda") * std
+
+    master = {"norm_weight": torch.ones(H, device="cuda"),
+              "norm_bias": torch.zeros(H, device="cuda"), "w_gate": normal(I, H, std=H ** -0.5),
+              "w_up": normal(I, H, std=H ** -0.5), "w_down": normal(H, I, std=I ** -0.5)}
+    x, residual = (normal(N, H, std=1.0).to(torch.bfloat16) for _ in range(2))
+    target = normal(N, H, std=1.0)
+    norms = []
+    for step in range(steps):
+        block = DenseBlock(**{n: t.to(torch.bfloat16) for n, t in master.items()})
+        out, kept = block(x, residual.clone(), keep=True)
+        diff = out.float() - target
+        _, grads = block.backward((2.0 / N * diff).to(torch.bfloat16), kept)
+        norms.append(float(clip_step(grads, max_norm)))
+        for name, t in master.items():
+            t -= 0.1 * grads[name].float()
+        if step in (0, steps - 1):
+            print(f"dense step {step}: loss {float(diff.square().sum() / N):.4f}, gradient norm "
+                  f"{norms[-1]:.4f}")
+    return norms
+
+
 def main(N: int = 2048, H: int = 512, E: int = 32, k: int = 4, I: int = 256, steps: int = 60):
     from .inputs import MoEShape, make_inputs, to_device
     shape = MoEShape("block", N=N, H=H, E=E, k=k, I=I, skew=True)
@@ -99,6 +180,7 @@ def main(N: int = 2048, H: int = 512, E: int = 32, k: int = 4, I: int = 256, ste
                   f"{int(counts.max())} of {N * k} slots, experts without one "
                   f"{int((counts == 0).sum())}")
         master -= 2.0 * grad
+    dense_steps()
     return losses
 
 

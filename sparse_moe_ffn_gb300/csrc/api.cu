@@ -1650,6 +1650,8 @@ moe_status_t moe_gated_ffn(const moe_bf16_t *x, const moe_bf16_t *w_gate, const 
     MOE_TRY(check_ffn(N, H, I, act));
     if ((gate == nullptr) != (up == nullptr))
         return fail(MOE_ERR_INVALID_ARG, "gate and up are kept both or neither");
+    if (gate && (gate == up || gate == out || up == out))
+        return fail(MOE_ERR_INVALID_ARG, "gate, up and out must be three arrays");
     if (N == 0) return MOE_OK;
     if (!x || !w_gate || !w_up || !w_down || !out)
         return fail(MOE_ERR_INVALID_ARG, "x, w_gate, w_up, w_down and out must be non-null");
@@ -1728,6 +1730,9 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
     const int weights = (dw_gate ? 1 : 0) + (dw_up ? 1 : 0) + (dw_down ? 1 : 0);
     if (weights != 0 && weights != 3)
         return fail(MOE_ERR_INVALID_ARG, "dw_gate, dw_up and dw_down are wanted all or none");
+    if (weights && (dw_gate == dw_up || dw_gate == dw_down || dw_up == dw_down || dw_gate == dx ||
+                    dw_up == dx || dw_down == dx))
+        return fail(MOE_ERR_INVALID_ARG, "the gradients must be arrays of their own");
     if (!aligned16(dx) || !aligned16(dw_gate) || !aligned16(dw_up) || !aligned16(dw_down))
         return fail(MOE_ERR_INVALID_ARG, "matrices must be 16-byte aligned");
     if (N == 0) {  // sums over no tokens
@@ -1830,6 +1835,8 @@ moe_status_t moe_layernorm(const void *x, const void *residual, const void *weig
     if (N == 0) return MOE_OK;
     if (!x || !weight || !out)
         return fail(MOE_ERR_INVALID_ARG, "x, weight and out must be non-null");
+    if (out == residual_out)
+        return fail(MOE_ERR_INVALID_ARG, "out and residual_out must be two arrays");
     const uintptr_t size = bf16 ? 2 : 4;
     if (!aligned_to(x, size) || !aligned_to(residual, size) || !aligned_to(weight, size) ||
         !aligned_to(bias, size) || !aligned_to(residual_out, size) || !aligned_to(out, size) ||

@@ -7,9 +7,10 @@
 // steps are in flight; a step's registers are asked for again as soon as it is
 // used, across outputs too, and the blocks stay (two an SM), so that the memory
 // always has more than a step of every warp.  (One step of twice the size a
-// block, blocks that come and go: one token of 2048 x 8192 took 21.6 us,
-// so 19.5 with the prefetch below.)  The warps of a block share long rows where there are few; their sums are
-// added in a fixed order.  The tokens lie in shared memory.
+// block, blocks that come and go: one token of 2048 x 8192 took 21.6 us, so
+// 21.0, and 19.5 with the first weights fetched to L2 ahead.)  The warps of a
+// block share long rows where there are few; their sums are added in a fixed
+// order.  The tokens lie in shared memory.
 //
 // The down step's first weights are asked for before the kernel waits for the
 // gate/up step (programmatic dependent launch): its blocks start where the

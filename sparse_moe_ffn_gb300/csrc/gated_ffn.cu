@@ -208,7 +208,8 @@ struct Row32 {
 // whole 32-byte sectors.  Tensor-map stores of 32 x 32 values would take the
 // TMA unit's time from the operands, which keep it busy (a row of a box, of up
 // to 128 bytes, costs it about two cycles): with them dh of 8192 x 2048 x 8192
-// took 236 us and gate/up 270 instead of @DH and @GU.
+// took 236 us instead of 216, and the forward pass that keeps gate and up 472
+// instead of 459.
 __device__ __forceinline__ void store_row(uint16_t *p, const float (&v)[32], int left, bool wide) {
     if (wide && left >= 32) {
 #pragma unroll
