@@ -1323,14 +1323,15 @@ moe_status_t moe_quantize_fp8(const moe_bf16_t *x, int64_t N, int H, moe_e4m3_t 
 
 namespace {
 
-// Dense rows of `cols` values, in boxes of box_rows rows x box_cols values;
-// what lies outside reads 0 and is not written.
+// Rows of `cols` values (dense, or `ld` values apart), in boxes of box_rows rows
+// x box_cols values; what lies outside reads 0 and is not written.
 moe_status_t make_rows_map(CUtensorMap *m, CUtensorMapDataType type, int size, const void *base,
-                           int cols, int64_t rows, int box_cols, int box_rows, const char *what) {
+                           int cols, int64_t rows, int box_cols, int box_rows, const char *what,
+                           int64_t ld = 0) {
     auto fn = encode_tiled();
     if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * size};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld > 0 ? ld : cols) * size};
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols),
                                static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t estr[2] = {1, 1};
@@ -1585,7 +1586,7 @@ struct FfnLayout {
 
 FfnLayout ffn_layout(int64_t N, int H, int I, bool backward, int sms) {
     FfnLayout L = {};
-    const size_t rows = round_up(2 * static_cast<size_t>(N) * I, kAlign);
+    const size_t rows = round_up(2 * static_cast<size_t>(N) * round_up64(I, kFfnLd), kAlign);
     L.h = kAlign;
     L.dgate = L.h + rows;
     L.dup = L.dgate + (backward ? rows : 0);
@@ -1605,9 +1606,12 @@ FfnLayout ffn_layout(int64_t N, int H, int I, bool backward, int sms) {
 // The map of an operand: `base` [rows, cols], K-major (K along the rows) in
 // boxes of 64 values of K x `box` rows; MN-major in boxes of 64 x 64.
 moe_status_t ffn_operand(CUtensorMap *m, const void *base, int64_t rows, int cols, int box,
-                         const char *what) {
-    return make_rows_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, 64, box, what);
+                         const char *what, int64_t ld = 0) {
+    return make_rows_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, 64, box, what,
+                         ld);
 }
+
+int64_t ffn_ld(int I) { return round_up64(I, kFfnLd); }
 
 moe_status_t run_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, cudaStream_t stream,
                      const char *what) {
@@ -1669,6 +1673,7 @@ moe_status_t moe_gated_ffn(const moe_bf16_t *x, const moe_bf16_t *w_gate, const 
     a.I = I;
     a.act = act;
     a.keep = gate ? 1 : 0;
+    a.ld = ffn_ld(I);
     a.part = reinterpret_cast<float *>(ws + L.part);
     a.status = reinterpret_cast<int32_t *>(ws);
     a.reset_status = 1;
@@ -1692,7 +1697,7 @@ moe_status_t moe_gated_ffn(const moe_bf16_t *x, const moe_bf16_t *w_gate, const 
     MOE_TRY(ffn_operand(&m.a[0], x, N, H, su.bn ? su.bn : 128, "x"));
     MOE_TRY(ffn_operand(&m.b[0], w_gate, I, H, box_u, "w_gate"));
     MOE_TRY(ffn_operand(&m.b[1], w_up, I, H, box_u, "w_up"));
-    MOE_TRY(ffn_operand(&d.a[0], h, N, I, sd.bn ? sd.bn : 128, "h"));
+    MOE_TRY(ffn_operand(&d.a[0], h, N, I, sd.bn ? sd.bn : 128, "h", a.ld));
     MOE_TRY(ffn_operand(&d.b[0], w_down, H, I, sd.bn ? 128 : pd.bn / 2, "w_down"));
     a.out[0] = h;
     a.out[1] = gate;
@@ -1764,6 +1769,7 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
     a.act = act;
     a.gate = gate;
     a.up = up;
+    a.ld = ffn_ld(I);
     a.part = reinterpret_cast<float *>(ws + L.part);
     a.status = reinterpret_cast<int32_t *>(ws);
     a.reset_status = 1;
@@ -1786,16 +1792,16 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
     MOE_TRY(ffn_operand(&m.a[0], dout, N, H, 128, "dout"));
     MOE_TRY(ffn_operand(&m.b[0], w_down, H, I, 64, "w_down"));
     if (weights) {
-        MOE_TRY(ffn_operand(&w.a[0], dgate, N, I, 64, "dgate"));
-        MOE_TRY(ffn_operand(&w.a[1], dup, N, I, 64, "dup"));
+        MOE_TRY(ffn_operand(&w.a[0], dgate, N, I, 64, "dgate", a.ld));
+        MOE_TRY(ffn_operand(&w.a[1], dup, N, I, 64, "dup", a.ld));
         MOE_TRY(ffn_operand(&w.a[2], dout, N, H, 64, "dout"));
         MOE_TRY(ffn_operand(&w.b[0], x, N, H, 64, "x"));
         w.b[1] = w.b[0];
-        MOE_TRY(ffn_operand(&w.b[2], h, N, I, 64, "h"));
+        MOE_TRY(ffn_operand(&w.b[2], h, N, I, 64, "h", a.ld));
     }
     if (dx) {
-        MOE_TRY(ffn_operand(&d.a[0], dgate, N, I, 128, "dgate"));
-        MOE_TRY(ffn_operand(&d.a[1], dup, N, I, 128, "dup"));
+        MOE_TRY(ffn_operand(&d.a[0], dgate, N, I, 128, "dgate", a.ld));
+        MOE_TRY(ffn_operand(&d.a[1], dup, N, I, 128, "dup", a.ld));
         MOE_TRY(ffn_operand(&d.b[0], w_gate, I, H, 64, "w_gate"));
         MOE_TRY(ffn_operand(&d.b[1], w_up, I, H, 64, "w_up"));
     }

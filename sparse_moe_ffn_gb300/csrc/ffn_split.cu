@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 const float2 x = unpack_bf16x2(res.x), y = unpack_bf16x2(res.y);
                 v[0] += x.x, v[1] += x.y, v[2] += y.x, v[3] += y.y;
             }
-            store4(a.out[0] + at, v);
+            store4(a.out[0] + (kGated ? (first + t) * a.ld + o : at), v);
         }
     }
     __syncthreads();

@@ -231,14 +231,16 @@ __device__ __forceinline__ void store_row(uint16_t *p, const float (&v)[32], int
                            pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
 }
 
-// Whether the rows that the epilogue reads and writes start on 32 bytes.
+// Whether the caller's arrays that the epilogue reads and writes have rows that
+// start on 32 bytes (those of the workspace do: kFfnLd).
+template <FfnOp kOp>
 __device__ __forceinline__ bool all_wide(const FfnArgs &a, int cols) {
-    return cols % 16 == 0 &&
-           (reinterpret_cast<uintptr_t>(a.gate) | reinterpret_cast<uintptr_t>(a.up) |
-            reinterpret_cast<uintptr_t>(a.residual) | reinterpret_cast<uintptr_t>(a.out[0]) |
-            reinterpret_cast<uintptr_t>(a.out[1]) | reinterpret_cast<uintptr_t>(a.out[2])) %
-                   32 ==
-               0;
+    uintptr_t p = reinterpret_cast<uintptr_t>(a.gate) | reinterpret_cast<uintptr_t>(a.up) |
+                  reinterpret_cast<uintptr_t>(a.residual);
+    if (kOp != kFfnDh)
+        p |= reinterpret_cast<uintptr_t>(a.out[0]) | reinterpret_cast<uintptr_t>(a.out[1]) |
+             reinterpret_cast<uintptr_t>(a.out[2]);
+    return cols % 16 == 0 && p % 32 == 0;
 }
 
 // a = act(v) and d = act'(v).  The logistic function s is exactly 0 where 2^t
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             const int64_t r = r0 + lane;
             // columns of this warp that exist (warp-uniform)
             const int cols = r0 < rows ? min(kCols, all_cols - c0) : 0;
-            const bool wide = all_wide(a, all_cols);
+            const bool wide = all_wide<kOp>(a, all_cols);
             // operands of the elementwise part, read 32 columns ahead
             Row32 e0 = {}, e1 = {};
             auto fetch = [&](int c) {
@@ -562,11 +564,19 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                     fetch(c + 32);
                     if (r < rows) {
                         const int64_t at = r * all_cols + c0 + c;
-                        constexpr bool kThree = kOp == kFfnGateUp || kOp == kFfnDh;
-                        store_row(a.out[t.prod] + at, kThree ? x : v, cols - c, wide);
-                        if (kOp == kFfnDh || (kOp == kFfnGateUp && a.keep)) {
-                            store_row(a.out[1] + at, v, cols - c, wide);
-                            store_row(a.out[2] + at, w, cols - c, wide);
+                        const int64_t own = r * a.ld + c0 + c;  // in the workspace
+                        if (kOp == kFfnGateUp) {
+                            store_row(a.out[0] + own, x, cols - c, true);
+                            if (a.keep) {
+                                store_row(a.out[1] + at, v, cols - c, wide);
+                                store_row(a.out[2] + at, w, cols - c, wide);
+                            }
+                        } else if (kOp == kFfnDh) {
+                            store_row(a.out[0] + own, x, cols - c, true);
+                            store_row(a.out[1] + own, v, cols - c, true);
+                            store_row(a.out[2] + own, w, cols - c, true);
+                        } else {
+                            store_row(a.out[t.prod] + at, v, cols - c, wide);
                         }
                     }
                 }

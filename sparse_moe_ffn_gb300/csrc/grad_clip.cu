@@ -332,8 +332,12 @@ GradTable<kMax> table_of(const GradSet &g, int64_t at, int chunk = kChunk) {
     return t;
 }
 
+// Four blocks an SM are what fits at once; sets of more than 128 chunks an SM
+// take 32, eight after one another, which evens out who ends last (50 M values:
+// 55.4 us for norm and clipping with 4, 63.6 with 16; 604 M: 776 us with 4, 747
+// with 16, 738 with 32).
 int blocks_for(int chunks, int num_sms) {
-    const int most = num_sms * kGradBlocksPerSm;
+    const int most = num_sms * (chunks > 128 * num_sms ? kGradBlocksPerSm : 4);
     return chunks < most ? (chunks > 0 ? chunks : 1) : most;
 }
 

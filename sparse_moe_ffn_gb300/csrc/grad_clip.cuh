@@ -8,7 +8,7 @@ namespace moe {
 
 // Tensors that one launch takes: their table is a kernel parameter.
 constexpr int kGradTable = 512;
-constexpr int kGradBlocksPerSm = 8;
+constexpr int kGradBlocksPerSm = 32;  // at most, see blocks_for
 
 struct GradSet {
     const void *const *grads;
