@@ -754,7 +754,7 @@ double plan_tiles(FfnOp op, int64_t N, int H, int I, int bn, int P, FfnPlan *pla
 // Tiles of 256 columns, or of 128 where those are so few that the half ones
 // take less time: the constants (a slice, an epilogue, the join) are measured.
 FfnPlan ffn_plan(FfnOp op, int64_t N, int H, int I, int num_sms) {
-    const int P = num_sms / 2 < kFfnMaxPairs ? num_sms / 2 : kFfnMaxPairs;
+    const int P = num_sms < 4 ? 1 : num_sms / 2 < kFfnMaxPairs ? num_sms / 2 : kFfnMaxPairs;
     FfnPlan wide, narrow;
     const double a = plan_tiles(op, N, H, I, 256, P, &wide);
     const double b = plan_tiles(op, N, H, I, 128, P, &narrow);

@@ -152,6 +152,13 @@ def test_forward_activations(N, act):
     check_forward(N, 328, 456, act, residual=True, keep=N == 300)
 
 
+@pytest.mark.parametrize("N,H,I", [(1, 512, 5000), (2, 5000, 512), (1, 20000, 64), (2, 264, 16384),
+                                   (1, 40000, 72), (3, 72, 40000), (128, 1000, 5000)])
+def test_forward_rows_shared_by_warps_or_clusters(N, H, I):
+    """Few long rows: steps of K that do not divide evenly among warps or CTAs."""
+    check_forward(N, H, I, "gelu", residual=True, keep=N != 2)
+
+
 @pytest.mark.parametrize("N,H,I", [(1, 2048, 8192), (300, 256, 8192), (2048, 512, 4096)])
 def test_forward_long_sums(N, H, I):
     """Long K: the slices of the last wave are shared."""

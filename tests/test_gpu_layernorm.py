@@ -203,6 +203,14 @@ def test_outputs_in_place_of_inputs(H):
         assert torch.equal(ins[which], dx) and torch.equal(got[1], dw) and torch.equal(got[2], db)
 
 
+@pytest.mark.parametrize("H", [64, 100])
+def test_sum_stored_without_a_residual(H):
+    x, w = normal(gen(H), 7, H), normal(gen(1), H)
+    copy = torch.empty_like(x)
+    out, _, _ = binding.moe_layernorm(x, w, residual_out=copy)
+    assert torch.equal(copy, x) and torch.equal(out, binding.moe_layernorm(x, w)[0])
+
+
 def test_no_rows():
     x = torch.empty(0, 64, dtype=BF16, device="cuda")
     w = torch.ones(64, dtype=BF16, device="cuda")
