@@ -304,21 +304,37 @@ cudaError_t launch_tokens(const FfnMaps &m, const FfnArgs &a, const FfnSplit &t,
 // the weights have so few rows that clusters of 8 still fit at once: the rows
 // are then read again, from L2, and twice as many CTAs do so (128 tokens of 2048
 // x 8192: 34.2 us with 128 tokens a tile in the down step, 28.8 with 64).
-// Beyond 128 tokens the pair kernel takes over (4096 x 12288, 256 tokens in two
-// tiles of 128: 98 us against 82; 2048 x 8192 38.8 against 40).
+// Beyond 128 tokens the pair kernel takes over (gate/up of 2048 x 8192, 256
+// tokens: 45 us and more in all with tiles of 128, 40 with pairs), but for a down
+// step of up to 512 tokens whose long K four CTAs or more can share at once:
+// pairs would share it through memory and a second kernel (256 tokens: 33.8 us
+// against 40.0, 512 tokens of 1024 x 2816 19.1 against 25.0; with two CTAs a tile
+// 512 tokens of 4096 x 12288 take 112 either way, with 12 slices of K 512 tokens
+// of 2048 x 768 take 18.6 against 15.7).
 FfnSplit ffn_split(FfnOp op, int64_t N, int H, int I, int num_sms) {
     FfnSplit t = {0, 1};
-    if (N > 128) return t;
+    if (N > 512) return t;
     const int n = static_cast<int>(N);
     const int O = op == kFfnGateUp ? I : H, K = op == kFfnGateUp ? H : I;
     const int outs = op == kFfnGateUp ? kM / 2 : kM;
     const int64_t rows = (O + outs - 1) / outs;
     const int nk = (K + kSliceValues - 1) / kSliceValues;
     const int64_t fit = 2 * static_cast<int64_t>(num_sms);
+    const auto share = [&](int bn) {  // CTAs that can share a tile of bn tokens
+        const int64_t tiles = rows * ((n + bn - 1) / bn);
+        int split = 1;
+        while (split < 8 && 2 * split <= nk && 2 * split * tiles <= fit) split *= 2;
+        return split;
+    };
+    if (n > 128) {
+        if (op != kFfnDown || nk < 32) return t;
+        for (const int bn : {64, 128})
+            if (share(bn) >= 4) return {bn, share(bn)};
+        return t;
+    }
     t.bn = n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : 128;
     while (t.bn > 16 && 8 * rows * ((n + t.bn / 2 - 1) / (t.bn / 2)) <= fit) t.bn /= 2;
-    const int64_t tiles = rows * ((n + t.bn - 1) / t.bn);
-    while (t.split < 8 && 2 * t.split <= nk && 2 * t.split * tiles <= fit) t.split *= 2;
+    t.split = share(t.bn);
     return t;
 }
 

@@ -74,7 +74,7 @@ cudaError_t launch_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, int *lau
 cudaError_t launch_ffn_join(FfnOp op, const FfnArgs &a, int *launches, cudaStream_t s);
 
 
-// A decode batch (ffn_split.cu): kFfnGateUp and kFfnDown with the weights' rows
+// A decode batch, or a down step of some more tokens (ffn_split.cu): with the weights' rows
 // in boxes of 64 (gate, up) or 128, x's in boxes of `bn`; bn 0: not for this
 // batch.
 struct FfnSplit {
