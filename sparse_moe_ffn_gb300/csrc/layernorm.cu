@@ -141,41 +141,59 @@ __global__ void __launch_bounds__(row_threads<kRow>())
     const float inv_h = 1.f / static_cast<float>(a.H);
     const T *x = static_cast<const T *>(a.x), *residual = static_cast<const T *>(a.residual);
     const T *weight = static_cast<const T *>(a.weight), *bias = static_cast<const T *>(a.bias);
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kRows; base < a.N;
-         base += static_cast<int64_t>(gridDim.x) * kRows) {
+    // the gain and the bias are read once, the next row before this one's sums,
+    // where registers are left for that
+    constexpr bool kHold = kVec * kChunks <= 16 && kRow <= 512;
+    constexpr bool kAhead = kHold;
+    Piece<T, kVec> hw[kHold ? kChunks : 1], hb[kHold ? kChunks : 1];
+    if constexpr (kHold) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            hw[c].zero();
+            hb[c].zero();
+            if (t + c * kRow < pieces) {
+                hw[c].load(weight + kVec * (t + c * kRow));
+                if (bias) hb[c].load(bias + kVec * (t + c * kRow));
+            }
+        }
+    }
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows;
+    auto load = [&](int64_t n, Piece<T, kVec>(&px)[kChunks], Piece<T, kVec>(&pr)[kChunks]) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            px[c].zero();
+            pr[c].zero();
+            if (n < a.N && t + c * kRow < pieces) {
+                const int64_t at = n * a.H + kVec * (t + c * kRow);
+                px[c].load(x + at);
+                if (residual) pr[c].load(residual + at);
+            }
+        }
+    };
+    Piece<T, kVec> nx[kChunks], nr[kChunks];
+    if (kAhead) load(first + sub, nx, nr);
+    for (int64_t base = first; base < a.N; base += stride) {
         const int64_t n = base + sub;
         const bool row = n < a.N;
         const int64_t at = n * a.H;
+        if (!kAhead) load(n, nx, nr);
         Piece<T, kVec> r[kChunks];
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-            r[c].zero();
-            if (row && t + c * kRow < pieces) r[c].load(x + at + kVec * (t + c * kRow));
-        }
-        if (residual) {
-            Piece<T, kVec> b[kChunks];
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                b[c].zero();
-                if (row && t + c * kRow < pieces) b[c].load(residual + at + kVec * (t + c * kRow));
-            }
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
+            r[c] = nx[c];
+            if (residual) {
                 float u[kVec], v[kVec];
                 r[c].get(u);
-                b[c].get(v);
+                nr[c].get(v);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) u[i] += v[i];
                 r[c].set(u);
-                if (a.residual_out && row && t + c * kRow < pieces)
-                    r[c].store(static_cast<T *>(a.residual_out) + at + kVec * (t + c * kRow));
             }
-        } else if (a.residual_out) {
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-                if (row && t + c * kRow < pieces)
-                    r[c].store(static_cast<T *>(a.residual_out) + at + kVec * (t + c * kRow));
+            if (a.residual_out && row && t + c * kRow < pieces)
+                r[c].store(static_cast<T *>(a.residual_out) + at + kVec * (t + c * kRow));
         }
+        if (kAhead) load(n + stride, nx, nr);
         float s[1] = {0.f};
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
@@ -207,16 +225,18 @@ __global__ void __launch_bounds__(row_threads<kRow>())
             if (t + c * kRow >= pieces) break;
             const int h = kVec * (t + c * kRow);
             Piece<T, kVec> w, b;
-            w.load(weight + h);
+            if constexpr (kHold) {
+                w = hw[c];
+                b = hb[c];
+            } else {
+                w.load(weight + h);
+                b.zero();
+                if (bias) b.load(bias + h);
+            }
             float v[kVec], g[kVec], z[kVec];
             r[c].get(v);
             w.get(g);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) z[i] = 0.f;
-            if (bias) {
-                b.load(bias + h);
-                b.get(z);
-            }
+            b.get(z);
 #pragma unroll
             for (int i = 0; i < kVec; ++i) v[i] = fmaf((v[i] - mean) * rstd, g[i], z[i]);
             r[c].set(v);
@@ -228,7 +248,8 @@ __global__ void __launch_bounds__(row_threads<kRow>())
 // kSumColumns: the block keeps its columns' sums (dweight, dbias) and stores
 // them as part blockIdx.x.
 template <typename T, int kVec, int kRow, int kChunks, bool kSumColumns>
-__global__ void __launch_bounds__(row_threads<kRow>(), kSumColumns ? 512 / row_threads<kRow>() : 1)
+__global__ void __launch_bounds__(row_threads<kRow>(),
+                                  kSumColumns && kRow <= 256 ? 2 : 1)
     layernorm_grad_kernel(const LayerNormGradArgs a) {
     constexpr int kThreads = row_threads<kRow>();
     constexpr int kRows = kThreads / kRow;
@@ -368,33 +389,55 @@ __global__ void __launch_bounds__(row_threads<kRow>(), kSumColumns ? 512 / row_t
     }
 }
 
-// Rows too long for their sums in registers: a thread a column, a block a run
+// Rows too long for their sums in registers: a thread kVec columns, a block a run
 // of rows (part blockIdx.y).
 constexpr int kColumnThreads = 256;
+constexpr int kColumnRows = 4;  // at a time
 
-template <typename T>
+template <typename T, int kVec>
 __global__ void __launch_bounds__(kColumnThreads)
     layernorm_columns_kernel(const LayerNormGradArgs a) {
     griddep_launch_dependents();
     griddep_wait();
-    const int h = blockIdx.x * kColumnThreads + threadIdx.x;
+    const int h = (blockIdx.x * kColumnThreads + threadIdx.x) * kVec;
     if (h >= a.H) return;
     const int64_t first = a.N * blockIdx.y / gridDim.y, end = a.N * (blockIdx.y + 1) / gridDim.y;
-    float dw = 0.f, db = 0.f;
-#pragma unroll 8
-    for (int64_t n = first; n < end; ++n) {
-        Piece<T, 1> r, d;
-        r.load(static_cast<const T *>(a.x) + n * a.H + h);
-        d.load(static_cast<const T *>(a.dout) + n * a.H + h);
-        float v[1], y[1];
-        r.get(v);
-        d.get(y);
-        dw = fmaf(y[0], (v[0] - __ldcg(a.mean + n)) * __ldcg(a.rstd + n), dw);
-        db += y[0];
+    const T *x = static_cast<const T *>(a.x) + h, *dout = static_cast<const T *>(a.dout) + h;
+    float dw[kVec] = {}, db[kVec] = {};
+    for (int64_t n = first; n < end; n += kColumnRows) {
+        Piece<T, kVec> r[kColumnRows], d[kColumnRows];
+        float mean[kColumnRows], rstd[kColumnRows];
+#pragma unroll
+        for (int j = 0; j < kColumnRows; ++j) {
+            r[j].zero();
+            d[j].zero();
+            mean[j] = rstd[j] = 0.f;
+            if (n + j < end) {
+                r[j].load(x + (n + j) * a.H);
+                d[j].load(dout + (n + j) * a.H);
+                mean[j] = __ldcg(a.mean + n + j);
+                rstd[j] = __ldcg(a.rstd + n + j);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kColumnRows; ++j) {
+            if (n + j >= end) break;
+            float v[kVec], y[kVec];
+            r[j].get(v);
+            d[j].get(y);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                dw[i] = fmaf(y[i], (v[i] - mean[j]) * rstd[j], dw[i]);
+                db[i] += y[i];
+            }
+        }
     }
-    float *out = a.part + static_cast<int64_t>(blockIdx.y) * 2 * a.H;
-    __stcg(out + h, dw);
-    __stcg(out + a.H + h, db);
+    float *out = a.part + static_cast<int64_t>(blockIdx.y) * 2 * a.H + h;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        __stcg(out + i, dw[i]);
+        __stcg(out + a.H + i, db[i]);
+    }
 }
 
 // The parts' sum, in order: 32 columns a block, its warps taking the parts in
@@ -452,7 +495,7 @@ cudaError_t launch_rows(const LayerNormArgs &a, int num_sms, cudaStream_t s) {
     auto kern = layernorm_kernel<T, kVec, kRow, kChunks>;
     static const int fit = resident(kern, row_threads<kRow>(), 1);
     int64_t blocks = (a.N + kRows - 1) / kRows;
-    const int64_t limit = static_cast<int64_t>(fit) * num_sms * 4;
+    const int64_t limit = static_cast<int64_t>(fit) * num_sms * 2;
     if (blocks > limit) blocks = limit;
     return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(row_threads<kRow>()), 0, s, 1,
                       a);
@@ -484,14 +527,14 @@ cudaError_t launch_grad_rows(const LayerNormGradArgs &a, int num_sms, int *block
                              cudaStream_t s) {
     constexpr int kThreads = row_threads<kRow>(), kRows = kThreads / kRow;
     const int64_t most = (a.N + kRows - 1) / kRows;
-    const int64_t fit = static_cast<int64_t>(num_sms) * (kSum ? 512 / kThreads : 4);
+    const int64_t fit = static_cast<int64_t>(num_sms) * (kSum ? (kThreads == 256 ? 2 : 1) : 4);
     *blocks = static_cast<int>(most < fit ? most : fit);
     return launch_pdl(layernorm_grad_kernel<T, kVec, kRow, kChunks, kSum>,
                       dim3(static_cast<unsigned>(*blocks)), dim3(kThreads), 0, s, 1, a);
 }
 
-// 16 columns a thread in vectors of eight bf16 values (8 in rows of up to 256),
-// else 8 (16 in rows over 4096): more leave no registers for the row ahead.
+// 16 columns a thread in vectors of eight bf16 values (8 in rows of up to 256
+// values), else 8: more leave no registers for the row ahead.
 template <typename T, int kVec>
 cudaError_t launch_backward(const LayerNormGradArgs &a, int num_sms, int *blocks, cudaStream_t s) {
     constexpr int kC = kVec == 8 ? 2 : 8 / kVec;  // pieces a thread
@@ -502,14 +545,23 @@ cudaError_t launch_backward(const LayerNormGradArgs &a, int num_sms, int *blocks
     if (threads <= 64) return launch_grad_rows<T, kVec, 64, kC, true>(a, num_sms, blocks, s);
     if (threads <= 128) return launch_grad_rows<T, kVec, 128, kC, true>(a, num_sms, blocks, s);
     if (threads <= 256) return launch_grad_rows<T, kVec, 256, kC, true>(a, num_sms, blocks, s);
-    if (threads <= 512) return launch_grad_rows<T, kVec, 512, kC, true>(a, num_sms, blocks, s);
-    return launch_grad_rows<T, kVec, 512, 16 / kVec, true>(a, num_sms, blocks, s);
+    if constexpr (kVec < 8) return launch_grad_rows<T, kVec, 512, kC, true>(a, num_sms, blocks, s);
+    return cudaErrorInvalidValue;
+}
+
+template <typename T, int kVec>
+cudaError_t launch_columns(const LayerNormGradArgs &a, int blocks, cudaStream_t s) {
+    constexpr int kColumns = kColumnThreads * kVec;
+    const dim3 grid(static_cast<unsigned>((a.H + kColumns - 1) / kColumns),
+                    static_cast<unsigned>(blocks));
+    return launch_pdl(layernorm_columns_kernel<T, kVec>, grid, dim3(kColumnThreads), 0, s, 1, a);
 }
 
 template <typename T, int kVec>
 cudaError_t launch_backward_wide(const LayerNormGradArgs &a, int num_sms, cudaStream_t s) {
     const int pieces = a.H / kVec;
     int blocks;
+    if (pieces <= 1024) return launch_grad_rows<T, kVec, 256, 4, false>(a, num_sms, &blocks, s);
     if (pieces <= 2048) return launch_grad_rows<T, kVec, 512, 4, false>(a, num_sms, &blocks, s);
     if (pieces <= 4096) return launch_grad_rows<T, kVec, 1024, 4, false>(a, num_sms, &blocks, s);
     if (pieces <= 8192) return launch_grad_rows<T, kVec, 1024, 8, false>(a, num_sms, &blocks, s);
@@ -522,7 +574,10 @@ cudaError_t launch_backward_wide(const LayerNormGradArgs &a, int num_sms, cudaSt
     return cudaErrorInvalidValue;
 }
 
-constexpr int kSumColumnsH = 8192;  // longest row whose sums stay in registers
+// The longest rows whose sums stay in registers.  Beyond, a block would be alone
+// on its SM with one row at a time: 4096 x 8192 took 98 us with 512 threads and
+// 111 with 1024, and takes @W with a second pass for the sums.
+constexpr int kSumColumnsH = 4096;
 
 bool vectors(int H, int bf16, std::initializer_list<const void *> arrays) {
     if (H % (bf16 ? 8 : 4)) return false;
@@ -534,14 +589,12 @@ bool vectors(int H, int bf16, std::initializer_list<const void *> arrays) {
 }  // namespace
 
 int layernorm_grad_blocks(int64_t N, int H, int num_sms) {
-    if (H <= kSumColumnsH) {
-        const int64_t most = 2 * static_cast<int64_t>(num_sms);
-        return static_cast<int>(N < most ? N : most);
-    }
-    const int64_t columns = (H + kColumnThreads - 1) / kColumnThreads;
-    int64_t runs = 4 * static_cast<int64_t>(num_sms) / columns;
-    if (runs > (N + 15) / 16) runs = (N + 15) / 16;
-    return static_cast<int>(runs > 1 ? runs : 1);
+    // of whichever kernel the arrays' types and alignment choose (a block of
+    // layernorm_columns_kernel covers 2048 columns at most)
+    const int64_t rows = H <= kSumColumnsH ? 2 * static_cast<int64_t>(num_sms) : 0;
+    const int64_t columns = 4 * static_cast<int64_t>(num_sms) / ((H + 2047) / 2048);
+    const int64_t most = rows > columns ? rows : columns;
+    return static_cast<int>(N < most ? N : most > 1 ? most : 1);
 }
 
 cudaError_t launch_layernorm(const LayerNormArgs &a, int bf16, int num_sms, cudaStream_t s) {
@@ -555,9 +608,9 @@ cudaError_t launch_layernorm(const LayerNormArgs &a, int bf16, int num_sms, cuda
 cudaError_t launch_layernorm_grad(const LayerNormGradArgs &a, int bf16, int num_sms, int *launches,
                                   cudaStream_t s) {
     const bool vec = vectors(a.H, bf16, {a.dout, a.x, a.weight, a.dresidual, a.dx});
-    int blocks = layernorm_grad_blocks(a.N, a.H, num_sms);  // at most
     const bool sums = a.dweight || a.dbias;
     cudaError_t err = cudaSuccess;
+    int blocks = 0;
     if (a.H <= kSumColumnsH) {
         if (bf16)
             err = vec ? launch_backward<__nv_bfloat16, 8>(a, num_sms, &blocks, s)
@@ -568,12 +621,17 @@ cudaError_t launch_layernorm_grad(const LayerNormGradArgs &a, int bf16, int num_
         *launches += 1;
     } else {
         if (sums) {  // first: dx may be one of the inputs
-            const dim3 grid(static_cast<unsigned>((a.H + kColumnThreads - 1) / kColumnThreads),
-                            static_cast<unsigned>(blocks));
-            err = bf16 ? launch_pdl(layernorm_columns_kernel<__nv_bfloat16>, grid,
-                                    dim3(kColumnThreads), 0, s, 1, a)
-                       : launch_pdl(layernorm_columns_kernel<float>, grid, dim3(kColumnThreads), 0,
-                                    s, 1, a);
+            // runs of 16 rows and more
+            const int columns = kColumnThreads * (!vec ? 1 : bf16 ? 8 : 4);
+            const int64_t fit = 4 * static_cast<int64_t>(num_sms) / ((a.H + columns - 1) / columns);
+            const int64_t most = (a.N + 15) / 16 < fit ? (a.N + 15) / 16 : fit;
+            blocks = static_cast<int>(most > 1 ? most : 1);
+            if (bf16)
+                err = vec ? launch_columns<__nv_bfloat16, 8>(a, blocks, s)
+                          : launch_columns<__nv_bfloat16, 1>(a, blocks, s);
+            else
+                err = vec ? launch_columns<float, 4>(a, blocks, s)
+                          : launch_columns<float, 1>(a, blocks, s);
             *launches += 1;
         }
         if (err == cudaSuccess && a.dx) {
