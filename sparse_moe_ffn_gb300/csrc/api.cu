@@ -1787,9 +1787,10 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
     aw.out[0] = dw_gate;
     aw.out[1] = dw_up;
     aw.out[2] = dw_down;
+    const FfnSplit sh = ffn_split(kFfnDh, N, H, I, sms), sx = ffn_split(kFfnDx, N, H, I, sms);
     // each step's maps first, so that nothing is enqueued if one is refused
     FfnMaps m = {}, w = {}, d = {};
-    MOE_TRY(ffn_operand(&m.a[0], dout, N, H, 128, "dout"));
+    MOE_TRY(ffn_operand(&m.a[0], dout, N, H, sh.bn ? sh.bn : 128, "dout"));
     MOE_TRY(ffn_operand(&m.b[0], w_down, H, I, 64, "w_down"));
     if (weights) {
         MOE_TRY(ffn_operand(&w.a[0], dgate, N, I, 64, "dgate", a.ld));
@@ -1800,17 +1801,25 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
         MOE_TRY(ffn_operand(&w.b[2], h, N, I, 64, "h", a.ld));
     }
     if (dx) {
-        MOE_TRY(ffn_operand(&d.a[0], dgate, N, I, 128, "dgate", a.ld));
-        MOE_TRY(ffn_operand(&d.a[1], dup, N, I, 128, "dup", a.ld));
+        MOE_TRY(ffn_operand(&d.a[0], dgate, N, I, sx.bn ? sx.bn : 128, "dgate", a.ld));
+        MOE_TRY(ffn_operand(&d.a[1], dup, N, I, sx.bn ? sx.bn : 128, "dup", a.ld));
         MOE_TRY(ffn_operand(&d.b[0], w_gate, I, H, 64, "w_gate"));
         MOE_TRY(ffn_operand(&d.b[1], w_up, I, H, 64, "w_up"));
     }
-    MOE_TRY(run_ffn(kFfnDh, m, a, stream, "dh kernel launch"));
+    if (sh.bn) {
+        MOE_CUDA(launch_ffn_split(kFfnDh, m, a, sh, stream), "dh kernel launch");
+        g_launches += 1;
+    } else {
+        MOE_TRY(run_ffn(kFfnDh, m, a, stream, "dh kernel launch"));
+    }
     if (weights) {
         MOE_TRY(run_ffn(kFfnDw, w, aw, stream, "weight gradients kernel launch"));
         MOE_TRY(join_ffn(kFfnDw, aw, stream, "weight gradients join kernel launch"));
     }
-    if (dx) {
+    if (dx && sx.bn) {
+        MOE_CUDA(launch_ffn_split(kFfnDx, d, ax, sx, stream), "dx kernel launch");
+        g_launches += 1;
+    } else if (dx) {
         MOE_TRY(run_ffn(kFfnDx, d, ax, stream, "dx kernel launch"));
         MOE_TRY(join_ffn(kFfnDx, ax, stream, "dx join kernel launch"));
     }

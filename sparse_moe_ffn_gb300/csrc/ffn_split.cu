@@ -1,7 +1,8 @@
-// ffn_split.cu -- the gated feed-forward block for a decode batch: the weights
-// on the MMA's M side (128 rows, in the gate/up step 64 of Wg and the 64 of Wu
-// that belong to them), up to 128 tokens on its N side, and K shared by the CTAs
-// of a cluster.
+// ffn_split.cu -- the gated feed-forward block and its backward pass for a decode
+// batch: the weights on the MMA's M side (128 rows, in the gate/up step 64 of Wg
+// and the 64 of Wu that belong to them; in dh and dx 128 columns of the weights
+// as they lie, MN-major), up to 128 tokens on its N side, and K shared by the
+// CTAs of a cluster (in dx the K of both products, one after the other).
 //
 // Each CTA writes its partial sums straight into the shared memory of the CTA
 // that owns the token (tokens are dealt out in equal runs); one cluster barrier
@@ -14,14 +15,14 @@
 //
 // A CTA takes half an SM's shared memory, so that the down step's CTAs start
 // while the gate/up step's still run: their first weights are asked for before
-// they wait for that step (programmatic dependent launch).  The weights may be
-// read that early because the gate/up kernel lets its dependents start only
-// after its own wait: whatever wrote them has ended then.
+// they wait for that step (programmatic dependent launch), and so are those of dx
+// while dh or the weights' gradients are made.  The weights may be read that
+// early because the block's first kernel lets its dependents start only after its
+// own wait: whatever wrote them has ended then.
 // Every wait is bounded; a CTA that gives up records MOE_ERR_DEVICE_TIMEOUT and
 // still takes part in the cluster's barriers.
+#include "ffn_epilogue.cuh"
 #include "gated_ffn.cuh"
-#include "linear_epilogue.cuh"
-#include "linear_gemm.cuh"
 
 namespace moe {
 
@@ -59,13 +60,36 @@ __device__ __forceinline__ void store4(uint16_t *p, const float (&v)[4]) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
-template <bool kGated, int kBN>
+__device__ __forceinline__ void load4(const uint16_t *p, float (&v)[4]) {
+    const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(p));
+    const float2 x = unpack_bf16x2(u.x), y = unpack_bf16x2(u.y);
+    v[0] = x.x, v[1] = x.y, v[2] = y.x, v[3] = y.y;
+}
+
+template <int ACT>
+__device__ __forceinline__ void gate_grads4(float (&dh)[4], const float (&g)[4],
+                                            const float (&u)[4], float (&dup)[4], float (&h)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v, d;
+        act_slope<ACT>(g[i], &v, &d);
+        dup[i] = dh[i] * v;
+        h[i] = v * u[i];
+        dh[i] *= u[i] * d;
+    }
+}
+
+template <FfnOp kOp, int kBN>
 __global__ void __launch_bounds__(kSplitThreads, 2)
-    ffn_split_kernel(const __grid_constant__ CUtensorMap tm_x,
+    ffn_split_kernel(const __grid_constant__ CUtensorMap tm_x0,
+                     const __grid_constant__ CUtensorMap tm_x1,
                      const __grid_constant__ CUtensorMap tm_w0,
                      const __grid_constant__ CUtensorMap tm_w1, const FfnArgs a,
                      const int split_log) {
     using T = Tile<kBN>;
+    constexpr bool kGated = kOp == kFfnGateUp;
+    constexpr bool kAMn = kOp == kFfnDh || kOp == kFfnDx;
+    constexpr bool kEarly = kOp == kFfnDown || kOp == kFfnDx;  // weights before the wait
     constexpr int kBNLog = kBN == 16 ? 4 : kBN == 32 ? 5 : kBN == 64 ? 6 : 7;
     constexpr int kStages = T::kStages;
     constexpr int kOuts = kGated ? kM / 2 : kM;  // outputs of a tile
@@ -78,7 +102,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     SplitShared *sm = reinterpret_cast<SplitShared *>(behind + (T::kInPlace ? 0 : T::kPartBytes));
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = static_cast<int>(cluster_ctarank());
-    const int K = kGated ? a.H : a.I, O = kGated ? a.I : a.H;
+    const int K = kGated || kOp == kFfnDh ? a.H : a.I;
+    const int O = kGated || kOp == kFfnDh ? a.I : a.H;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -88,7 +113,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         mbar_init(&sm->acc_full, 1);
         sm->abort_flag = 0;
         fence_barrier_init();
-        prefetch_tensor_map(&tm_x);
+        prefetch_tensor_map(&tm_x0);
         prefetch_tensor_map(&tm_w0);
     }
     if (warp == 1) {
@@ -106,7 +131,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 
     const int o0 = (blockIdx.x >> split_log) * kOuts;
     const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kBN;
-    const int nk = (K + kSliceValues - 1) / kSliceValues;
+    const int each = (K + kSliceValues - 1) / kSliceValues;  // of a product
+    const int nk = kOp == kFfnDx ? 2 * each : each;
     const int k_first = static_cast<int>(static_cast<int64_t>(nk) * rank >> split_log);
     const int k_end = static_cast<int>(static_cast<int64_t>(nk) * (rank + 1) >> split_log);
     const int slices = k_end - k_first;
@@ -114,17 +140,24 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     auto load_weights = [&](int g) {
         uint8_t *st = tiles + g % kStages * T::kStageBytes;
         uint64_t *bar = &sm->full[g % kStages];
-        const int k = (k_first + g) * kSliceValues;
+        const bool second = kOp == kFfnDx && k_first + g >= each;
+        const int k = (k_first + g - (second ? each : 0)) * kSliceValues;
         mbar_arrive_expect_tx(bar, T::kStageBytes);
-        tma_load_2d(st, &tm_w0, bar, k, o0);
-        if (kGated) tma_load_2d(st + kRowsBytes128 / 2, &tm_w1, bar, k, o0);
+        if (kAMn) {
+            const CUtensorMap *w = second ? &tm_w1 : &tm_w0;
+            tma_load_2d(st, w, bar, o0, k);
+            tma_load_2d(st + kMnChunk, w, bar, o0 + 64, k);
+        } else {
+            tma_load_2d(st, &tm_w0, bar, k, o0);
+            if (kGated) tma_load_2d(st + kRowsBytes128 / 2, &tm_w1, bar, k, o0);
+        }
     };
-    const int early = kGated ? 0 : min(slices, kStages);
-    if (kGated) griddep_wait();
-    if (!kGated && warp == 0 && elect_one())
+    const int early = kEarly ? min(slices, kStages) : 0;
+    if (!kEarly) griddep_wait();
+    if (kEarly && warp == 0 && elect_one())
         for (int g = 0; g < early; ++g) load_weights(g);
     griddep_launch_dependents();
-    if (!kGated) griddep_wait();
+    if (kEarly) griddep_wait();
     if (a.reset_status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
         *a.status = MOE_OK;
 
@@ -143,8 +176,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             }
             if (issues) {
                 if (g >= early) load_weights(g);
-                tma_load_2d(tiles + s * T::kStageBytes + kRowsBytes128, &tm_x, &sm->full[s],
-                            (k_first + g) * kSliceValues, static_cast<int>(n0));
+                const bool second = kOp == kFfnDx && k_first + g >= each;
+                tma_load_2d(tiles + s * T::kStageBytes + kRowsBytes128, second ? &tm_x1 : &tm_x0,
+                            &sm->full[s], (k_first + g - (second ? each : 0)) * kSliceValues,
+                            static_cast<int>(n0));
             }
         }
         // no copy may be in flight when the CTA ends
@@ -156,8 +191,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         // the whole warp runs the loop and one lane issues: descriptors and
         // barriers stay in uniform registers
         const bool issues = elect_one();
-        constexpr uint32_t idesc = idesc_bf16_f32(kM, kBN);
-        const uint64_t desc0 = sw128_kmajor_desc(smem_addr(tiles));
+        constexpr uint32_t idesc = idesc_bf16_f32(kM, kBN) | (kAMn ? kIdescAMn : 0);
+        constexpr int kStepA = kAMn ? kStepMnMajor : kStepKMajor;
+        const uint32_t base = smem_addr(tiles);
+        const uint64_t desc_a = kAMn ? sw128_mnmajor_desc(base) : sw128_kmajor_desc(base);
+        const uint64_t desc_b = sw128_kmajor_desc(base + kRowsBytes128);
         for (int g = 0; g < slices; ++g) {
             const int s = g % kStages;
             if (!warp_wait(&sm->full[s], (g / kStages) & 1, abort_flag)) {
@@ -169,11 +207,12 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             }
             tc_fence_after_sync();
             if (issues) {
-                const uint64_t da = desc0 + s * (T::kStageBytes >> 4);
-                const uint64_t db = da + (kRowsBytes128 >> 4);
+                const uint64_t da = desc_a + s * (T::kStageBytes >> 4);
+                const uint64_t db = desc_b + s * (T::kStageBytes >> 4);
 #pragma unroll
                 for (int kk = 0; kk < kSliceBytes / kMmaBytes; ++kk)
-                    mma_f16kind(tmem, da + 2 * kk, db + 2 * kk, idesc, (g | kk) != 0);
+                    mma_f16kind(tmem, da + kStepA * kk, db + kStepKMajor * kk, idesc,
+                                (g | kk) != 0);
                 mma_commit(&sm->empty[s]);
             }
         }
@@ -190,6 +229,21 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     const int own_log = kBNLog - split_log;
     const int mine = min(1 << own_log, tokens - (rank << own_log));  // may be <= 0
     const int64_t first = n0 + (rank << own_log);
+    // four outputs a thread; a thread keeps its outputs from token to token
+    constexpr int kLanes = kOuts / 4;                // threads a token
+    constexpr int kStep = kSplitThreads / kLanes;    // tokens in one go
+    const int ch = threadIdx.x % kLanes * 4;
+    const int o = o0 + ch;
+    const int t0 = threadIdx.x / kLanes;
+    // (dh) gate and up of the first go, before the accumulator is waited for
+    float gate[4] = {}, up[4] = {};
+    auto fetch = [&](int t) {
+        if (kOp == kFfnDh && o < O && t < mine) {
+            load4(a.gate + (first + t) * O + o, gate);
+            load4(a.up + (first + t) * O + o, up);
+        }
+    };
+    fetch(t0);
     // the accumulator, then the parts of all ranks
     bool ok = true;
     if (lane == 0) ok = mbar_wait(&sm->acc_full, 0, abort_flag);
@@ -226,19 +280,15 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     }
     cluster_barrier();
 
-    // four outputs a thread; a thread keeps its outputs from token to token
-    constexpr int kLanes = kOuts / 4;                // threads a token
-    constexpr int kStep = kSplitThreads / kLanes;    // tokens in one go
-    const int ch = threadIdx.x % kLanes * 4;
-    const int o = o0 + ch;
     const int split = 1 << split_log;
     if (o < O && !*abort_flag) {
-        for (int t = threadIdx.x / kLanes; t < mine; t += kStep) {
+        for (int t = t0; t < mine; t += kStep) {
             const int64_t at = (first + t) * O + o;
-            uint2 res = make_uint2(0, 0);
-            if (!kGated && a.residual)
-                res = __ldcg(reinterpret_cast<const uint2 *>(a.residual + at));
-            float v[4] = {}, w[4] = {};
+            const int64_t own = (first + t) * a.ld + o;  // in the workspace
+            float res[4] = {};
+            if (kOp == kFfnDown && a.residual) load4(a.residual + at, res);
+            if (t != t0) fetch(t);
+            float v[4] = {}, w[4] = {}, h[4];
             for (int r = 0; r < split; ++r) {
                 const float *p = part + ((r << own_log) + t) * kM + ch;
                 const float4 f = *reinterpret_cast<const float4 *>(p);
@@ -256,11 +306,25 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 act_all(a.act, v);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] *= w[i];
+                store4(a.out[0] + own, v);
+            } else if (kOp == kFfnDh) {
+                switch (a.act) {
+                    case MOE_ACT_SILU: gate_grads4<MOE_ACT_SILU>(v, gate, up, w, h); break;
+                    case MOE_ACT_GELU: gate_grads4<MOE_ACT_GELU>(v, gate, up, w, h); break;
+                    case MOE_ACT_GELU_TANH:
+                        gate_grads4<MOE_ACT_GELU_TANH>(v, gate, up, w, h);
+                        break;
+                    case MOE_ACT_RELU: gate_grads4<MOE_ACT_RELU>(v, gate, up, w, h); break;
+                    default: gate_grads4<MOE_ACT_NONE>(v, gate, up, w, h); break;
+                }
+                store4(a.out[0] + own, h);
+                store4(a.out[1] + own, v);
+                store4(a.out[2] + own, w);
             } else {
-                const float2 x = unpack_bf16x2(res.x), y = unpack_bf16x2(res.y);
-                v[0] += x.x, v[1] += x.y, v[2] += y.x, v[3] += y.y;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += res[i];
+                store4(a.out[0] + at, v);
             }
-            store4(a.out[0] + (kGated ? (first + t) * a.ld + o : at), v);
         }
     }
     __syncthreads();
@@ -271,30 +335,34 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     }
 }
 
-template <bool kGated, int kBN>
+int split_outs(FfnOp op) { return op == kFfnGateUp ? kM / 2 : kM; }
+int split_o(FfnOp op, int H, int I) { return op == kFfnGateUp || op == kFfnDh ? I : H; }
+
+template <FfnOp kOp, int kBN>
 cudaError_t launch_one(const FfnMaps &m, const FfnArgs &a, int split, cudaStream_t s) {
     int split_log = 0;
     while ((1 << split_log) < split) ++split_log;
     using T = Tile<kBN>;
     const size_t smem = T::kShared;
-    auto kern = ffn_split_kernel<kGated, kBN>;
+    auto kern = ffn_split_kernel<kOp, kBN>;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t err = allow_shared(kern, smem, allowed);
     if (err != cudaSuccess) return err;
-    const int outs = kGated ? kM / 2 : kM, O = kGated ? a.I : a.H;
+    const int outs = split_outs(kOp), O = split_o(kOp, a.H, a.I);
     const dim3 grid(static_cast<unsigned>((O + outs - 1) / outs * split),
                     static_cast<unsigned>((a.N + kBN - 1) / kBN));
     return launch_pdl(kern, grid, dim3(kSplitThreads), smem, s, static_cast<unsigned>(split),
-                      m.a[0], m.b[0], m.b[kGated ? 1 : 0], a, split_log);
+                      m.a[0], m.a[kOp == kFfnDx ? 1 : 0], m.b[0],
+                      m.b[kOp == kFfnGateUp || kOp == kFfnDx ? 1 : 0], a, split_log);
 }
 
-template <bool kGated>
+template <FfnOp kOp>
 cudaError_t launch_tokens(const FfnMaps &m, const FfnArgs &a, const FfnSplit &t, cudaStream_t s) {
     switch (t.bn) {
-        case 16: return launch_one<kGated, 16>(m, a, t.split, s);
-        case 32: return launch_one<kGated, 32>(m, a, t.split, s);
-        case 64: return launch_one<kGated, 64>(m, a, t.split, s);
-        default: return launch_one<kGated, 128>(m, a, t.split, s);
+        case 16: return launch_one<kOp, 16>(m, a, t.split, s);
+        case 32: return launch_one<kOp, 32>(m, a, t.split, s);
+        case 64: return launch_one<kOp, 64>(m, a, t.split, s);
+        default: return launch_one<kOp, 128>(m, a, t.split, s);
     }
 }
 
@@ -315,10 +383,10 @@ FfnSplit ffn_split(FfnOp op, int64_t N, int H, int I, int num_sms) {
     FfnSplit t = {0, 1};
     if (N > 512) return t;
     const int n = static_cast<int>(N);
-    const int O = op == kFfnGateUp ? I : H, K = op == kFfnGateUp ? H : I;
-    const int outs = op == kFfnGateUp ? kM / 2 : kM;
+    const int outs = split_outs(op), O = split_o(op, H, I);
+    const int K = op == kFfnGateUp || op == kFfnDh ? H : I;
     const int64_t rows = (O + outs - 1) / outs;
-    const int nk = (K + kSliceValues - 1) / kSliceValues;
+    const int nk = (K + kSliceValues - 1) / kSliceValues * (op == kFfnDx ? 2 : 1);
     const int64_t fit = 2 * static_cast<int64_t>(num_sms);
     const auto share = [&](int bn) {  // CTAs that can share a tile of bn tokens
         const int64_t tiles = rows * ((n + bn - 1) / bn);
@@ -340,7 +408,12 @@ FfnSplit ffn_split(FfnOp op, int64_t N, int H, int I, int num_sms) {
 
 cudaError_t launch_ffn_split(FfnOp op, const FfnMaps &m, const FfnArgs &a, const FfnSplit &t,
                              cudaStream_t s) {
-    return op == kFfnGateUp ? launch_tokens<true>(m, a, t, s) : launch_tokens<false>(m, a, t, s);
+    switch (op) {
+        case kFfnGateUp: return launch_tokens<kFfnGateUp>(m, a, t, s);
+        case kFfnDown: return launch_tokens<kFfnDown>(m, a, t, s);
+        case kFfnDh: return launch_tokens<kFfnDh>(m, a, t, s);
+        default: return launch_tokens<kFfnDx>(m, a, t, s);
+    }
 }
 
 }  // namespace moe

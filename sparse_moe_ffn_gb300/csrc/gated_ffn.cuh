@@ -74,9 +74,10 @@ cudaError_t launch_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, int *lau
 cudaError_t launch_ffn_join(FfnOp op, const FfnArgs &a, int *launches, cudaStream_t s);
 
 
-// A decode batch, or a down step of some more tokens (ffn_split.cu): with the weights' rows
-// in boxes of 64 (gate, up) or 128, x's in boxes of `bn`; bn 0: not for this
-// batch.
+// A decode batch, or a down step of some more tokens (ffn_split.cu; not the
+// weights' gradients): with the tokens' operands (maps.a) in boxes of `bn` rows,
+// the weights in boxes of 64 rows (gate, up), 128 (down), or, MN-major, of 64 x
+// 64; bn 0: not for this batch.
 struct FfnSplit {
     int bn;     // tokens of a tile
     int split;  // CTAs of a cluster that share a tile's K
