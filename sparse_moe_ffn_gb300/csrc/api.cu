@@ -1799,6 +1799,12 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
         MOE_TRY(ffn_operand(&w.b[0], x, N, H, 64, "x"));
         w.b[1] = w.b[0];
         MOE_TRY(ffn_operand(&w.b[2], h, N, I, 64, "h", a.ld));
+        aw.boxes = aw.plan.nk <= kFfnBoxSlices ? 1 : 0;
+        if (aw.boxes) {
+            MOE_TRY(ffn_operand(&w.out[0], dw_gate, I, H, 32, "dw_gate"));
+            MOE_TRY(ffn_operand(&w.out[1], dw_up, I, H, 32, "dw_up"));
+            MOE_TRY(ffn_operand(&w.out[2], dw_down, H, I, 32, "dw_down"));
+        }
     }
     if (dx) {
         MOE_TRY(ffn_operand(&d.a[0], dgate, N, I, sx.bn ? sx.bn : 128, "dgate", a.ld));

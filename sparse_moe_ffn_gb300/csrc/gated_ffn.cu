@@ -42,6 +42,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kFfnThreads = 64 + 32 * kEpiWarps;
 constexpr int kMostStages = 6;
 constexpr int kSliceK = 64;            // values of K in a slice
+constexpr int kBoxBytes = 32 * 128;    // 32 rows x 64 values of an output
 constexpr int kMinSlices = 8;          // of a part of a tile
 constexpr double kJoinUs = 12.0;
 
@@ -63,9 +64,11 @@ struct FfnTraits {
     static constexpr int kColsPerTile = kOp == kFfnGateUp ? kBN / 2 : kBN;  // of the output
     static constexpr int kBBytes = kBN / 2 * kSliceBytes;  // a CTA's share of a slice
     static constexpr int kStageBytes = kRowsBytes128 + kBBytes;
-    static constexpr int kStages = kOp == kFfnDh ? 5 : kMostStages;  // dh: 211 us, 216 with six
-    static constexpr size_t kShared =
-        1024 + static_cast<size_t>(kStages) * kStageBytes + sizeof(FfnShared);
+    // dh: 211 us, 216 with six; dw: room for its outputs on their way
+    static constexpr int kStages = kOp == kFfnDh || kOp == kFfnDw ? 5 : kMostStages;
+    static constexpr int kOutBytes = kOp == kFfnDw ? kEpiWarps * 2 * kBoxBytes : 0;
+    static constexpr size_t kShared = 1024 + static_cast<size_t>(kStages) * kStageBytes +
+                                      kOutBytes + sizeof(FfnShared);
     static constexpr int kPartFloats = kFfnTile * kBN;
 };
 
@@ -188,7 +191,8 @@ struct Row32 {
 };
 
 // 32 values to a bf16 row, as Row32 reads them.  Each lane stores its own row's
-// whole 32-byte sectors.  Tensor-map stores of 32 x 32 values would take the
+// whole 32-byte sectors (but for the weights' gradients of few tokens, whose
+// tiles are mostly stores: FfnArgs::boxes).  Tensor-map stores of 32 x 32 values would take the
 // TMA unit's time from the operands, which keep it busy (a row of a box, of up
 // to 128 bytes, costs it about two cycles): with them dh of 8192 x 2048 x 8192
 // took 236 us instead of 216, and the forward pass that keeps gate and up 472
@@ -212,6 +216,28 @@ __device__ __forceinline__ void store_row(uint16_t *p, const float (&v)[32], int
                            pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
                            pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
                            pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+}
+
+// This lane's 64 values (a row of a 32 x 64 box), as a tensor-map store with
+// 128-byte swizzled rows reads them.
+__device__ __forceinline__ void write_box_row(uint8_t *buf, int lane, const float (&v)[32],
+                                              const float (&w)[32]) {
+    uint8_t *row = buf + lane * 128;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float *f = j < 4 ? v + 8 * j : w + 8 * (j - 4);
+        *reinterpret_cast<uint4 *>(row + 16 * (j ^ (lane & 7))) =
+            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                       pack_bf16x2(f[6], f[7]));
+    }
+}
+
+__device__ __forceinline__ void tma_store_box(const CUtensorMap *map, const void *src, int c0,
+                                              int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
+                 ::"l"(map), "r"(smem_addr(src)), "r"(c0), "r"(c1)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
 // Whether the caller's arrays that the epilogue reads and writes have rows that
@@ -254,7 +280,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *tiles = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    FfnShared *sm = reinterpret_cast<FfnShared *>(tiles + kStages * kStageBytes);
+    uint8_t *out_bufs = tiles + kStages * kStageBytes;
+    FfnShared *sm = reinterpret_cast<FfnShared *>(out_bufs + T::kOutBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = static_cast<int>(cluster_ctarank());
     const bool leader = rank == 0;
@@ -421,7 +448,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(a.up + r * a.I + c));
                 }
         }
-        int n = 0;
+        int n = 0, boxes = 0;
         for (; walk.next(it); ++n) {
             const FfnTile t = ffn_tile<kOp, kBN>(a, it.tile);
             int64_t rows;
@@ -461,7 +488,26 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             tc_fence_after_sync();
             const uint32_t taddr =
                 tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * kBN + half * kCols;
-            if (it.slot >= 0) {  // (kFfnDown, kFfnDx, kFfnDw)
+            if (kOp == kFfnDw && a.boxes && it.slot < 0) {
+#pragma unroll 1
+                for (int c = 0; c < cols; c += 64, ++boxes) {
+                    float v[32], w[32];
+                    __syncwarp();  // TMEM wants whole warps
+                    tmem_load32(taddr + c, v);
+                    __syncwarp();
+                    tmem_load32(taddr + c + 32, w);
+                    tmem_load_wait();
+                    // the buffer in turn has left
+                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    __syncwarp();
+                    uint8_t *b = out_bufs + ((warp - 2) * 2 + (boxes & 1)) * kBoxBytes;
+                    write_box_row(b, lane, v, w);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0)
+                        tma_store_box(&maps.out[t.prod], b, c0 + c, static_cast<int>(r0));
+                }
+            } else if (it.slot >= 0) {  // (kFfnDown, kFfnDx, kFfnDw)
                 float *part = a.part + static_cast<int64_t>(it.slot) * T::kPartFloats +
                               ((rank * 4 + quarter) * 2 + half) * (kBN / 64) * 1024 + 4 * lane;
 #pragma unroll 1
@@ -529,6 +575,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) arrive_remote_relaxed(acc ? empty1 : empty0);
+        }
+        if (kOp == kFfnDw) {
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // stores have landed
+            __syncwarp();
         }
     }
 
@@ -703,6 +753,7 @@ FfnPlan ffn_plan(FfnOp op, int64_t N, int H, int I, int num_sms) {
     FfnPlan wide, narrow;
     const double a = plan_tiles(op, N, H, I, 256, P, &wide);
     const double b = plan_tiles(op, N, H, I, 128, P, &narrow);
+    if (op == kFfnDw && wide.nk <= kFfnBoxSlices) return wide;
     return b < a ? narrow : wide;
 }
 

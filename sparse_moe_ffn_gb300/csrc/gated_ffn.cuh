@@ -50,6 +50,7 @@ struct FfnArgs {
     int keep;                   // gate and up are stored
     const uint16_t *gate, *up;  // kFfnDh
     const uint16_t *residual;   // kFfnDown, nullable
+    int boxes;                  // kFfnDw: the outputs leave by tensor-map stores
     int64_t ld;                 // row stride of h, dgate and dup (see kFfnLd)
     uint16_t *out[3];           // h, gate, up; h, dgate, dup; dWg, dWu, dWd; or one
     float *part;                // [2 pairs][256 x bn]
@@ -64,10 +65,16 @@ struct FfnArgs {
 // of 64 rows x 64 values of K.
 struct FfnMaps {
     CUtensorMap a[3], b[3];
+    CUtensorMap out[3];  // kFfnDw with FfnArgs::boxes: boxes of 32 rows x 64 values
 };
 
 FfnPlan ffn_plan(FfnOp op, int64_t N, int H, int I, int num_sms);
 size_t ffn_part_bytes(const FfnPlan &p);
+// The weights' gradients of up to this many slices of tokens leave by tensor-map
+// stores, from tiles of 256 columns: the TMA unit has the time for them then (8
+// tokens of 2048 x 8192: 25 us instead of 31, 256 tokens 33.6 and 36.7, 512 tokens
+// 43.7 and 42.0, 1024 tokens 65 and 61).
+constexpr int kFfnBoxSlices = 4;
 cudaError_t launch_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, int *launches,
                        cudaStream_t s);
 // Adds the partial sums, where the plan has any.
