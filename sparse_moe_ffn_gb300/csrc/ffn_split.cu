@@ -373,12 +373,17 @@ cudaError_t launch_tokens(const FfnMaps &m, const FfnArgs &a, const FfnSplit &t,
 // are then read again, from L2, and twice as many CTAs do so (128 tokens of 2048
 // x 8192: 34.2 us with 128 tokens a tile in the down step, 28.8 with 64).
 // Beyond 128 tokens the pair kernel takes over (gate/up of 2048 x 8192, 256
-// tokens: 45 us and more in all with tiles of 128, 40 with pairs), but for a down
-// step of up to 512 tokens whose long K four CTAs or more can share at once:
-// pairs would share it through memory and a second kernel (256 tokens: 33.8 us
-// against 40.0, 512 tokens of 1024 x 2816 19.1 against 25.0; with two CTAs a tile
-// 512 tokens of 4096 x 12288 take 112 either way, with 12 slices of K 512 tokens
-// of 2048 x 768 take 18.6 against 15.7).
+// tokens: 45 us and more in all with tiles of 128, 40 with pairs), but for
+//  - down and dx of up to 512 tokens whose long K four CTAs or more can share at
+//    once: pairs would share it through memory and a second kernel (down of 256
+//    tokens of 2048 x 8192: 33.8 us against 40.0, of 512 of 1024 x 2816 19.1
+//    against 25.0; both ways, with dx, 256 of 1024 x 2816: 45.6 against 51.1.  With
+//    two CTAs a tile 512 tokens of 4096 x 12288 take 112 either way, with 12
+//    slices of K 512 tokens of 2048 x 768 18.6 against 15.7, dx with 256 slices
+//    114 against 111.5);
+//  - dh and gate/up of up to 256 tokens whose tiles are so few that two or four
+//    CTAs share one (both ways, dh of 256 tokens of 2048 x 768: 40.0 against 46.2,
+//    without sharing of 2048 x 8192 118 against 114).
 FfnSplit ffn_split(FfnOp op, int64_t N, int H, int I, int num_sms) {
     FfnSplit t = {0, 1};
     if (N > 512) return t;
@@ -395,7 +400,11 @@ FfnSplit ffn_split(FfnOp op, int64_t N, int H, int I, int num_sms) {
         return split;
     };
     if (n > 128) {
-        if (op != kFfnDown || nk < 32) return t;
+        if (op == kFfnGateUp || op == kFfnDh) {
+            if (n <= 256 && share(64) >= (op == kFfnDh ? 2 : 4)) return {64, share(64)};
+            return t;
+        }
+        if (nk < 32 || (op == kFfnDx && nk > 128)) return t;
         for (const int bn : {64, 128})
             if (share(bn) >= 4) return {bn, share(bn)};
         return t;

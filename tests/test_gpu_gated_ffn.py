@@ -213,6 +213,17 @@ def test_backward_activations(N, act):
     check_backward(N, 328, 456, act)
 
 
+BETWEEN = [(130, 768, 2048), (160, 2048, 768), (200, 264, 2056), (256, 512, 4096), (257, 520, 2816),
+           (400, 1024, 2816), (512, 72, 2056), (513, 256, 2048)]
+
+
+@pytest.mark.parametrize("N,H,I", BETWEEN)
+def test_sizes_between_the_kernels_both_ways(N, H, I):
+    """Batches that take one kernel for some products and another for the rest."""
+    check_forward(N, H, I, "silu", residual=True, keep=True)
+    check_backward(N, H, I, "silu")
+
+
 @pytest.mark.parametrize("N,H,I", [(5000, 256, 256), (300, 256, 8192), (9001, 72, 520)])
 def test_backward_long_sums(N, H, I):
     """Long K: the slices of the last wave are shared."""
