@@ -1788,6 +1788,9 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
     aw.out[1] = dw_up;
     aw.out[2] = dw_down;
     const FfnSplit sh = ffn_split(kFfnDh, N, H, I, sms), sx = ffn_split(kFfnDx, N, H, I, sms);
+    // dx and the weights' gradients need the same
+    FfnPlan both;
+    const bool together = dx && weights && !sx.bn && ffn_grads_plan(N, H, I, sms, &both);
     // each step's maps first, so that nothing is enqueued if one is refused
     FfnMaps m = {}, w = {}, d = {};
     MOE_TRY(ffn_operand(&m.a[0], dout, N, H, sh.bn ? sh.bn : 128, "dout"));
@@ -1799,6 +1802,14 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
         MOE_TRY(ffn_operand(&w.b[0], x, N, H, 64, "x"));
         w.b[1] = w.b[0];
         MOE_TRY(ffn_operand(&w.b[2], h, N, I, 64, "h", a.ld));
+        if (together) {
+            aw.plan = both;
+            aw.out[3] = dx;
+            MOE_TRY(ffn_operand(&w.a[3], dgate, N, I, 128, "dgate", a.ld));
+            MOE_TRY(ffn_operand(&w.a[4], dup, N, I, 128, "dup", a.ld));
+            MOE_TRY(ffn_operand(&w.b[3], w_gate, I, H, 64, "w_gate"));
+            MOE_TRY(ffn_operand(&w.b[4], w_up, I, H, 64, "w_up"));
+        }
         aw.boxes = aw.plan.nk <= kFfnBoxSlices ? 1 : 0;
         if (aw.boxes) {
             MOE_TRY(ffn_operand(&w.out[0], dw_gate, I, H, 32, "dw_gate"));
@@ -1806,7 +1817,7 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
             MOE_TRY(ffn_operand(&w.out[2], dw_down, H, I, 32, "dw_down"));
         }
     }
-    if (dx) {
+    if (dx && !together) {
         MOE_TRY(ffn_operand(&d.a[0], dgate, N, I, sx.bn ? sx.bn : 128, "dgate", a.ld));
         MOE_TRY(ffn_operand(&d.a[1], dup, N, I, sx.bn ? sx.bn : 128, "dup", a.ld));
         MOE_TRY(ffn_operand(&d.b[0], w_gate, I, H, 64, "w_gate"));
@@ -1817,6 +1828,10 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
         g_launches += 1;
     } else {
         MOE_TRY(run_ffn(kFfnDh, m, a, stream, "dh kernel launch"));
+    }
+    if (together) {
+        MOE_TRY(run_ffn(kFfnGrads, w, aw, stream, "gradients kernel launch"));
+        return MOE_OK;
     }
     if (weights) {
         MOE_TRY(run_ffn(kFfnDw, w, aw, stream, "weight gradients kernel launch"));

@@ -13,7 +13,8 @@
 //             rows of Wu: a pair's accumulator is 128 columns of gate next to
 //             the 128 of up that belong to them
 //   dx        dgate Wg + dup Wu is one product whose K is the two in a row
-//   dW        the three weights' tiles are one list
+//   dW        the three weights' tiles are one list, and where both are of few
+//             tiles dx's join them: one launch instead of two
 //
 //   warp 0     producer: TMA copies; the even CTA's barrier counts both CTAs'
 //              bytes
@@ -45,6 +46,7 @@ constexpr int kSliceK = 64;            // values of K in a slice
 constexpr int kBoxBytes = 32 * 128;    // 32 rows x 64 values of an output
 constexpr int kMinSlices = 8;          // of a part of a tile
 constexpr double kJoinUs = 12.0;
+constexpr double kLaunchUs = 2.0;
 
 struct FfnShared {
     uint64_t full[kMostStages];   // even CTA: both CTAs' bytes of a stage landed
@@ -59,8 +61,8 @@ struct FfnShared {
 // kBN: accumulator columns of a tile, 256 or 128
 template <FfnOp kOp, int kBN>
 struct FfnTraits {
-    static constexpr bool kAMn = kOp == kFfnDw;
-    static constexpr bool kBMn = kOp == kFfnDh || kOp == kFfnDx || kOp == kFfnDw;
+    static constexpr bool kBMn = kOp == kFfnDh || kOp == kFfnDx || kOp == kFfnDw ||
+                                 kOp == kFfnGrads;
     static constexpr int kColsPerTile = kOp == kFfnGateUp ? kBN / 2 : kBN;  // of the output
     static constexpr int kBBytes = kBN / 2 * kSliceBytes;  // a CTA's share of a slice
     static constexpr int kStageBytes = kRowsBytes128 + kBBytes;
@@ -78,7 +80,21 @@ struct FfnItem {
     int tile, k0, k1, slot;
 };
 
-// The pieces of pair `pair`, in order.
+// Whether a tile of kFfnGrads is one of dx.
+__device__ __forceinline__ bool is_dx(const FfnPlan &p, int tile) {
+    return p.dx_first ? tile < p.dx_tiles : tile >= p.tiles - p.dx_tiles;
+}
+
+// Whether a tile's M side lies MN-major.
+template <FfnOp kOp>
+__device__ __forceinline__ bool a_is_mn(const FfnPlan &p, int tile) {
+    return kOp == kFfnDw || (kOp == kFfnGrads && !is_dx(p, tile));
+}
+
+// The pieces of pair `pair`, in order.  kFfnGrads deals its tiles out forth and
+// back, the long ones first, so that a pair that got one more long one gets one
+// short one less.
+template <FfnOp kOp>
 struct FfnWalk {
     const FfnPlan &p;
     int pair, tile, turn;
@@ -92,6 +108,13 @@ struct FfnWalk {
         }
     }
     __device__ __forceinline__ bool next(FfnItem &it) {
+        if (kOp == kFfnGrads) {
+            const int i = turn * p.pairs + (turn % 2 ? p.pairs - 1 - pair : pair);
+            if (i >= p.tiles) return false;
+            it = {i, 0, is_dx(p, i) ? p.dx_nk : p.nk, -1};
+            ++turn;
+            return true;
+        }
         if (tile < p.whole) {
             it = {tile, 0, p.nk, -1};
             tile += p.pairs;
@@ -119,7 +142,7 @@ struct FfnTile {
 
 template <FfnOp kOp>
 __device__ __forceinline__ void ffn_dims(const FfnArgs &a, int prod, int64_t *rows, int *cols) {
-    if (kOp == kFfnDw) {
+    if (kOp == kFfnDw || (kOp == kFfnGrads && prod < 3)) {
         *rows = prod == 2 ? a.H : a.I;
         *cols = prod == 2 ? a.I : a.H;
     } else {
@@ -131,7 +154,13 @@ __device__ __forceinline__ void ffn_dims(const FfnArgs &a, int prod, int64_t *ro
 template <FfnOp kOp, int kBN>
 __device__ __forceinline__ FfnTile ffn_tile(const FfnArgs &a, int tile) {
     FfnTile t = {0, 0, 0};
-    if (kOp == kFfnDw) {
+    if (kOp == kFfnGrads) {
+        const FfnPlan &p = a.plan;
+        if (is_dx(p, tile)) t.prod = 3;
+        if (t.prod == 3 ? !p.dx_first : p.dx_first)
+            tile -= t.prod == 3 ? p.tiles - p.dx_tiles : p.dx_tiles;
+    }
+    if (kOp == kFfnDw || (kOp == kFfnGrads && t.prod == 0)) {
         const int each = (a.I + kFfnTile - 1) / kFfnTile * ((a.H + kBN - 1) / kBN);
         t.prod = min(tile / each, 2);
         tile -= t.prod * each;
@@ -192,11 +221,11 @@ struct Row32 {
 
 // 32 values to a bf16 row, as Row32 reads them.  Each lane stores its own row's
 // whole 32-byte sectors (but for the weights' gradients of few tokens, whose
-// tiles are mostly stores: FfnArgs::boxes).  Tensor-map stores of 32 x 32 values would take the
-// TMA unit's time from the operands, which keep it busy (a row of a box, of up
-// to 128 bytes, costs it about two cycles): with them dh of 8192 x 2048 x 8192
-// took 236 us instead of 216, and the forward pass that keeps gate and up 472
-// instead of 459.
+// tiles are mostly stores: FfnArgs::boxes).  Tensor-map stores of 32 x 32 values
+// would take the TMA unit's time from the operands, which keep it busy (a row of a
+// box, of up to 128 bytes, costs it about two cycles): with them dh of 8192 x 2048
+// x 8192 took 236 us instead of 216, and the forward pass that keeps gate and up
+// 472 instead of 459.
 __device__ __forceinline__ void store_row(uint16_t *p, const float (&v)[32], int left, bool wide) {
     if (wide && left >= 32) {
 #pragma unroll
@@ -248,7 +277,7 @@ __device__ __forceinline__ bool all_wide(const FfnArgs &a, int cols) {
                   reinterpret_cast<uintptr_t>(a.residual);
     if (kOp != kFfnDh)
         p |= reinterpret_cast<uintptr_t>(a.out[0]) | reinterpret_cast<uintptr_t>(a.out[1]) |
-             reinterpret_cast<uintptr_t>(a.out[2]);
+             reinterpret_cast<uintptr_t>(a.out[2]) | reinterpret_cast<uintptr_t>(a.out[3]);
     return cols % 16 == 0 && p % 32 == 0;
 }
 
@@ -314,7 +343,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     if (a.reset_status && blockIdx.x == 0 && threadIdx.x == 0 && a.status) *a.status = MOE_OK;
 
     const int pair = blockIdx.x / 2;
-    FfnWalk walk(a.plan, pair);
+    FfnWalk<kOp> walk(a.plan, pair);
     FfnItem it;
 
     if (warp == 0) {
@@ -328,7 +357,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             const FfnTile t = ffn_tile<kOp, kBN>(a, it.tile);
             const int row = t.m * kFfnTile + rank * 128;
             const int col = t.n * T::kColsPerTile + (kOp == kFfnGateUp ? 0 : rank * (kBN / 2));
-            const int half = a.plan.nk / 2;  // dx: slices of the first product
+            // dx: slices of its first product
+            const bool dx = kOp == kFfnDx || (kOp == kFfnGrads && t.prod == 3);
+            const int half = (kOp == kFfnGrads ? a.plan.dx_nk : a.plan.nk) / 2;
+            const bool a_mn = a_is_mn<kOp>(a.plan, it.tile);
             for (int kc = it.k0; kc < it.k1; ++kc, ++g) {
                 if (g >= kStages && !warp_wait(&sm->empty[s], parity, abort_flag)) {
                     if (issues) {
@@ -343,13 +375,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                     uint8_t *sb = st + kRowsBytes128;
                     const uint32_t bar = map_to_rank(smem_addr(&sm->full[s]), 0);
                     if (leader) mbar_arrive_expect_tx(&sm->full[s], 2 * kStageBytes);
-                    const int second = kOp == kFfnDx && kc >= half ? 1 : 0;
+                    const int second = dx && kc >= half ? 1 : 0;
                     const int k = (kc - second * half) * kSliceK;
-                    const CUtensorMap *ma = &maps.a[kOp == kFfnDw ? t.prod : second];
-                    const CUtensorMap *mb = &maps.b[kOp == kFfnGateUp ? rank
-                                                    : kOp == kFfnDw   ? t.prod
-                                                                      : second];
-                    if (T::kAMn) {
+                    const CUtensorMap *ma = &maps.a[t.prod + second];
+                    const CUtensorMap *mb = &maps.b[kOp == kFfnGateUp ? rank : t.prod + second];
+                    if (a_mn) {
                         tma_load_2d_pair(st, ma, bar, row, k);
                         tma_load_2d_pair(st + kMnChunk, ma, bar, row + 64, k);
                     } else {
@@ -378,12 +408,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             // The whole warp runs the loop and one lane of it issues, so that
             // the compiler keeps descriptors and barriers in uniform registers.
             const bool issues = elect_one();
-            constexpr uint32_t idesc = idesc_bf16_f32(kFfnTile, kBN) |
-                                       (T::kAMn ? kIdescAMn : 0) | (T::kBMn ? kIdescBMn : 0);
-            constexpr int kStepA = T::kAMn ? kStepMnMajor : kStepKMajor;
             constexpr int kStepB = T::kBMn ? kStepMnMajor : kStepKMajor;
             const uint32_t base = smem_addr(tiles);
-            const uint64_t desc_a = T::kAMn ? sw128_mnmajor_desc(base) : sw128_kmajor_desc(base);
             const uint64_t desc_b = T::kBMn ? sw128_mnmajor_desc(base + kRowsBytes128)
                                             : sw128_kmajor_desc(base + kRowsBytes128);
             int s = 0, n = 0;
@@ -398,6 +424,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 }
                 tc_fence_after_sync();
                 const uint32_t d = tmem + acc * kBN;
+                const bool a_mn = a_is_mn<kOp>(a.plan, it.tile);
+                const uint32_t idesc = idesc_bf16_f32(kFfnTile, kBN) | (a_mn ? kIdescAMn : 0) |
+                                       (T::kBMn ? kIdescBMn : 0);
+                const uint64_t desc_a = a_mn ? sw128_mnmajor_desc(base) : sw128_kmajor_desc(base);
+                const int step_a = a_mn ? kStepMnMajor : kStepKMajor;
                 for (int kc = it.k0; kc < it.k1; ++kc) {
                     if (!warp_wait(&sm->full[s], phase, abort_flag)) {
                         failed = true;
@@ -409,7 +440,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                         const uint64_t db = desc_b + s * (kStageBytes >> 4);
 #pragma unroll
                         for (int kk = 0; kk < kSliceK / 16; ++kk)
-                            linear_mma_pair<false>(d, da + kStepA * kk, db + kStepB * kk, idesc,
+                            linear_mma_pair<false>(d, da + step_a * kk, db + kStepB * kk, idesc,
                                                    kk == 0 ? kc != it.k0 : 1);
                         commit_2cta(&sm->empty[s], 3);
                     }
@@ -691,6 +722,10 @@ cudaError_t launch_join(const FfnArgs &a, int *launches, cudaStream_t s) {
 
 int64_t up_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Measured times in us: a slice of a tile, and its epilogue on its own.
+double slice_us(int bn) { return bn == 256 ? 0.29 : 0.21; }
+double epilogue_us(FfnOp op, int bn) { return (op == kFfnDh ? 4.0 : 2.5) * bn / 256; }
+
 // The plan for tiles of bn columns, and its time in us.
 double plan_tiles(FfnOp op, int64_t N, int H, int I, int bn, int P, FfnPlan *plan) {
     FfnPlan p;
@@ -722,8 +757,8 @@ double plan_tiles(FfnOp op, int64_t N, int H, int I, int bn, int P, FfnPlan *pla
     p.whole = p.tiles;
     p.parts = 0;
     p.pairs = p.tiles < P ? p.tiles : P;
-    const double slice = bn == 256 ? 0.29 : 0.21;
-    const double epilogue = (op == kFfnDh ? 4.0 : 2.5) * bn / 256;
+    p.dx_tiles = p.dx_nk = p.dx_first = 0;
+    const double slice = slice_us(bn), epilogue = epilogue_us(op, bn);
     const double waves = static_cast<double>(up_div(tiles, P));
     double us = waves * (p.nk * slice > epilogue ? p.nk * slice : epilogue) + epilogue;
     if (op != kFfnGateUp && op != kFfnDh) {  // theirs need whole sums
@@ -746,15 +781,73 @@ double plan_tiles(FfnOp op, int64_t N, int H, int I, int bn, int P, FfnPlan *pla
 
 }  // namespace
 
+namespace {
+
+int most_pairs(int num_sms) {
+    return num_sms < 4 ? 1 : num_sms / 2 < kFfnMaxPairs ? num_sms / 2 : kFfnMaxPairs;
+}
+
+// The better of the two widths' plans, and its time.
+double best_plan(FfnOp op, int64_t N, int H, int I, int P, FfnPlan *plan) {
+    FfnPlan narrow;
+    const double a = plan_tiles(op, N, H, I, 256, P, plan);
+    const double b = plan_tiles(op, N, H, I, 128, P, &narrow);
+    if (b >= a || (op == kFfnDw && plan->nk <= kFfnBoxSlices)) return a;
+    *plan = narrow;
+    return b;
+}
+
+}  // namespace
+
 // Tiles of 256 columns, or of 128 where those are so few that the half ones
 // take less time: the constants (a slice, an epilogue, the join) are measured.
 FfnPlan ffn_plan(FfnOp op, int64_t N, int H, int I, int num_sms) {
-    const int P = num_sms < 4 ? 1 : num_sms / 2 < kFfnMaxPairs ? num_sms / 2 : kFfnMaxPairs;
-    FfnPlan wide, narrow;
-    const double a = plan_tiles(op, N, H, I, 256, P, &wide);
-    const double b = plan_tiles(op, N, H, I, 128, P, &narrow);
-    if (op == kFfnDw && wide.nk <= kFfnBoxSlices) return wide;
-    return b < a ? narrow : wide;
+    FfnPlan p;
+    best_plan(op, N, H, I, most_pairs(num_sms), &p);
+    return p;
+}
+
+// A launch less, with its start, first copies, last epilogue and hand-over, takes
+// kLaunchUs off; the tiles of both have to go evenly to the pairs, which they are
+// dealt out to here as the kernel does it.
+bool ffn_grads_plan(int64_t N, int H, int I, int num_sms, FfnPlan *plan) {
+    const int P = most_pairs(num_sms);
+    FfnPlan x, w;
+    const double apart = best_plan(kFfnDx, N, H, I, P, &x) + best_plan(kFfnDw, N, H, I, P, &w);
+    if (w.nk <= kFfnBoxSlices) return false;
+    double best = apart + kLaunchUs;
+    bool found = false;
+    for (const int bn : {256, 128}) {
+        FfnPlan px, pw;
+        plan_tiles(kFfnDx, N, H, I, bn, P, &px);
+        plan_tiles(kFfnDw, N, H, I, bn, P, &pw);
+        if (static_cast<int64_t>(px.tiles) + pw.tiles > 8 * P) continue;
+        FfnPlan p = pw;
+        p.dx_tiles = px.tiles;
+        p.dx_nk = px.nk;
+        p.dx_first = px.nk > pw.nk ? 1 : 0;
+        p.tiles = p.whole = px.tiles + pw.tiles;
+        p.parts = 0;
+        p.pairs = p.tiles < P ? p.tiles : P;
+        int longest = 0;
+        for (int pair = 0; pair < p.pairs; ++pair) {
+            int slices = 0;
+            for (int turn = 0;; ++turn) {
+                const int i = turn * p.pairs + (turn % 2 ? p.pairs - 1 - pair : pair);
+                if (i >= p.tiles) break;
+                slices += (p.dx_first ? i < p.dx_tiles : i >= p.tiles - p.dx_tiles) ? p.dx_nk
+                                                                                      : p.nk;
+            }
+            longest = slices > longest ? slices : longest;
+        }
+        const double us = longest * slice_us(bn) + epilogue_us(kFfnDw, bn);
+        if (us < best) {
+            best = us;
+            *plan = p;
+            found = true;
+        }
+    }
+    return found;
 }
 
 size_t ffn_part_bytes(const FfnPlan &p) {
@@ -768,7 +861,8 @@ cudaError_t launch_ffn(FfnOp op, const FfnMaps &maps, const FfnArgs &a, int *lau
         case kFfnDown: return launch_op<kFfnDown>(maps, a, launches, s);
         case kFfnDh: return launch_op<kFfnDh>(maps, a, launches, s);
         case kFfnDx: return launch_op<kFfnDx>(maps, a, launches, s);
-        default: return launch_op<kFfnDw>(maps, a, launches, s);
+        case kFfnDw: return launch_op<kFfnDw>(maps, a, launches, s);
+        default: return launch_op<kFfnGrads>(maps, a, launches, s);
     }
 }
 

@@ -20,7 +20,14 @@
 
 namespace moe {
 
-enum FfnOp { kFfnGateUp = 0, kFfnDown = 1, kFfnDh = 2, kFfnDx = 3, kFfnDw = 4 };
+enum FfnOp {
+    kFfnGateUp = 0,
+    kFfnDown = 1,
+    kFfnDh = 2,
+    kFfnDx = 3,
+    kFfnDw = 4,
+    kFfnGrads = 5  // kFfnDx and kFfnDw in one launch
+};
 
 // Pairs of CTAs that run at once at most; a launch's partial sums have room for
 // two tiles a pair.
@@ -41,6 +48,9 @@ struct FfnPlan {
     int nk;      // K slices of a tile
     int bn;      // accumulator columns of a tile: 256 or 128
     int pairs;   // launched
+    // kFfnGrads: dx's tiles and their slices, and whether they come before the
+    // weights'; no tile is shared
+    int dx_tiles, dx_nk, dx_first;
 };
 
 struct FfnArgs {
@@ -52,7 +62,7 @@ struct FfnArgs {
     const uint16_t *residual;   // kFfnDown, nullable
     int boxes;                  // kFfnDw: the outputs leave by tensor-map stores
     int64_t ld;                 // row stride of h, dgate and dup (see kFfnLd)
-    uint16_t *out[3];           // h, gate, up; h, dgate, dup; dWg, dWu, dWd; or one
+    uint16_t *out[4];           // h, gate, up; h, dgate, dup; dWg, dWu, dWd (, dx); or one
     float *part;                // [2 pairs][256 x bn]
     int32_t *status;
     int reset_status;
@@ -64,11 +74,13 @@ struct FfnArgs {
 // or on the N side half a tile's columns), an MN-major one ([K, rows]) in boxes
 // of 64 rows x 64 values of K.
 struct FfnMaps {
-    CUtensorMap a[3], b[3];
+    CUtensorMap a[5], b[5];  // kFfnGrads: kFfnDw's, then kFfnDx's
     CUtensorMap out[3];  // kFfnDw with FfnArgs::boxes: boxes of 32 rows x 64 values
 };
 
 FfnPlan ffn_plan(FfnOp op, int64_t N, int H, int I, int num_sms);
+// Whether kFfnGrads takes less time than the two one after the other, and its plan.
+bool ffn_grads_plan(int64_t N, int H, int I, int num_sms, FfnPlan *plan);
 size_t ffn_part_bytes(const FfnPlan &p);
 // The weights' gradients of up to this many slices of tokens leave by tensor-map
 // stores, from tiles of 256 columns: the TMA unit has the time for them then (8

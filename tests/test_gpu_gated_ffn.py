@@ -135,7 +135,7 @@ def check_forward(N, H, I, act, residual, keep, seed=0):
     assert_close(out.t, y, rounded(y, ey), "out", 2)
 
 
-SIZES = [(1, 8, 8), (1, 64, 64), (2, 72, 200), (7, 1000, 136), (16, 512, 1024), (33, 264, 520),
+SIZES = [(1, 8, 8), (3, 8, 8), (20, 8, 72), (300, 8, 8), (1, 64, 64), (2, 72, 200), (7, 1000, 136), (16, 512, 1024), (33, 264, 520),
          (64, 2048, 768), (100, 128, 2056), (129, 640, 640), (256, 256, 256), (257, 1000, 1400),
          (500, 64, 4096), (1021, 1000, 1400), (1300, 2056, 72), (4099, 136, 264)]
 
@@ -222,6 +222,13 @@ def test_sizes_between_the_kernels_both_ways(N, H, I):
     """Batches that take one kernel for some products and another for the rest."""
     check_forward(N, H, I, "silu", residual=True, keep=True)
     check_backward(N, H, I, "silu")
+
+
+@pytest.mark.parametrize("N,H,I", [(600, 1024, 1400), (1500, 2048, 768), (2500, 520, 264), (3000, 72, 72),
+                                   (1030, 776, 3000)])
+def test_gradients_in_one_launch(N, H, I):
+    """Batches whose dx and weights' gradients share a launch."""
+    check_backward(N, H, I, "gelu")
 
 
 @pytest.mark.parametrize("N,H,I", [(5000, 256, 256), (300, 256, 8192), (9001, 72, 520)])
