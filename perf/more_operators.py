@@ -306,7 +306,8 @@ def _own_layernorm(s):
         x = s["x"] if s["residual"] is None else s["residual_out"]
         r["dx"], r["dweight"], r["dbias"] = b.moe_layernorm_backward(
             s["dout"], x, s["weight"], mean, rstd, dresidual=s["dresidual"], dx=s["dx"],
-            dweight=s["dweight"], dbias=s["dbias"], workspace=s["workspace"])
+            dweight=s["dweight"], dbias=s["dbias"], want_dbias=c["bias"],
+            workspace=s["workspace"])
     return r
 
 
