@@ -110,10 +110,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) ffn_rows_kernel(const FfnRows
     if (!kGated) {
         // the next two steps on their way to L2
         int g = load_group, q = load_step;
-        for (int i = 0; i < 2; ++i) {
+        for (int j = 0; j < 2; ++j) {
             const int64_t o = static_cast<int64_t>(g) * per_block + warp / a.per_row;
             const int n = min(kStep, a.K - q * kStep);
-            if (lane == i && g < groups && o < a.O && n > 0)
+            if (lane == j && g < groups && o < a.O && n > 0)
                 prefetch_l2_bulk(a.w0 + o * a.K + q * kStep, 2 * n);
             q += a.per_row;
             if (q >= steps) {

@@ -504,6 +504,20 @@ cudaError_t launch_rows(const LayerNormArgs &a, int num_sms, cudaStream_t s) {
 template <typename T, int kVec>
 cudaError_t launch_forward(const LayerNormArgs &a, int num_sms, cudaStream_t s) {
     const int pieces = a.H / kVec;
+    if constexpr (kVec == 1) {
+        // Single values: eight (sixteen) on their way a thread and row, twice with
+        // the row ahead.  With two and four 100000 x 151 in bf16 took 67 us instead
+        // of 39, 4000 x 4099 118 instead of 51, 1021 x 1111 in fp32 7 and 4.
+        if (pieces <= 128) return launch_rows<T, 1, 32, 4>(a, num_sms, s);
+        if (pieces <= 256) return launch_rows<T, 1, 32, 8>(a, num_sms, s);
+        if (pieces <= 512) return launch_rows<T, 1, 64, 8>(a, num_sms, s);
+        if (pieces <= 1024) return launch_rows<T, 1, 128, 8>(a, num_sms, s);
+        if (pieces <= 2048) return launch_rows<T, 1, 256, 8>(a, num_sms, s);
+        if (pieces <= 4096) return launch_rows<T, 1, 512, 8>(a, num_sms, s);
+        if (pieces <= 8192) return launch_rows<T, 1, 512, 16>(a, num_sms, s);
+        if (pieces <= 16384) return launch_rows<T, 1, 1024, 16>(a, num_sms, s);
+        return launch_rows<T, 1, 1024, 64>(a, num_sms, s);
+    }
     if (pieces <= 32) return launch_rows<T, kVec, 32, 1>(a, num_sms, s);
     if (pieces <= 64) return launch_rows<T, kVec, 32, 2>(a, num_sms, s);
     if (pieces <= 128) return launch_rows<T, kVec, 64, 2>(a, num_sms, s);
@@ -513,10 +527,9 @@ cudaError_t launch_forward(const LayerNormArgs &a, int num_sms, cudaStream_t s) 
     if (pieces <= 2048) return launch_rows<T, kVec, 512, 4>(a, num_sms, s);
     if (pieces <= 4096) return launch_rows<T, kVec, 1024, 4>(a, num_sms, s);
     if (pieces <= 8192) return launch_rows<T, kVec, 1024, 8>(a, num_sms, s);
-    if constexpr (kVec <= 4) {
+    if constexpr (kVec == 4) {
         if (pieces <= 16384) return launch_rows<T, kVec, 1024, 16>(a, num_sms, s);
     }
-    if constexpr (kVec == 1) return launch_rows<T, kVec, 1024, 64>(a, num_sms, s);
     return cudaErrorInvalidValue;
 }
 
