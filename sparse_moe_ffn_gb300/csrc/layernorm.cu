@@ -481,19 +481,19 @@ __global__ void __launch_bounds__(kFinishThreads)
 
 // ---------------------------------------------------------------- launchers
 
-// Blocks of a kernel that fit at once.
+// Blocks of a kernel that fit on an SM at once.
 template <typename Kernel>
-int resident(Kernel kern, int threads, int num_sms) {
+int resident(Kernel kern, int threads) {
     int n = 0;
     cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0);
-    return (n > 0 ? n : 1) * num_sms;
+    return n > 0 ? n : 1;
 }
 
 template <typename T, int kVec, int kRow, int kChunks>
 cudaError_t launch_rows(const LayerNormArgs &a, int num_sms, cudaStream_t s) {
     constexpr int kRows = row_threads<kRow>() / kRow;
     auto kern = layernorm_kernel<T, kVec, kRow, kChunks>;
-    static const int fit = resident(kern, row_threads<kRow>(), 1);
+    static const int fit = resident(kern, row_threads<kRow>());
     int64_t blocks = (a.N + kRows - 1) / kRows;
     const int64_t limit = static_cast<int64_t>(fit) * num_sms * 2;
     if (blocks > limit) blocks = limit;
@@ -570,15 +570,21 @@ cudaError_t launch_columns(const LayerNormGradArgs &a, int blocks, cudaStream_t 
     return launch_pdl(layernorm_columns_kernel<T, kVec>, grid, dim3(kColumnThreads), 0, s, 1, a);
 }
 
+// dx alone, of rows over kSumColumnsH.
 template <typename T, int kVec>
 cudaError_t launch_backward_wide(const LayerNormGradArgs &a, int num_sms, cudaStream_t s) {
     const int pieces = a.H / kVec;
     int blocks;
-    if (pieces <= 1024) return launch_grad_rows<T, kVec, 256, 4, false>(a, num_sms, &blocks, s);
-    if (pieces <= 2048) return launch_grad_rows<T, kVec, 512, 4, false>(a, num_sms, &blocks, s);
-    if (pieces <= 4096) return launch_grad_rows<T, kVec, 1024, 4, false>(a, num_sms, &blocks, s);
+    if constexpr (kVec == 8) {
+        if (pieces <= 1024) return launch_grad_rows<T, kVec, 256, 4, false>(a, num_sms, &blocks, s);
+    }
+    if constexpr (kVec > 1) {
+        if (pieces <= 2048) return launch_grad_rows<T, kVec, 512, 4, false>(a, num_sms, &blocks, s);
+        if (pieces <= 4096)
+            return launch_grad_rows<T, kVec, 1024, 4, false>(a, num_sms, &blocks, s);
+    }
     if (pieces <= 8192) return launch_grad_rows<T, kVec, 1024, 8, false>(a, num_sms, &blocks, s);
-    if constexpr (kVec <= 4) {
+    if constexpr (kVec < 8) {
         if (pieces <= 16384)
             return launch_grad_rows<T, kVec, 1024, 16, false>(a, num_sms, &blocks, s);
     }
