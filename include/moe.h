@@ -629,8 +629,8 @@ moe_status_t moe_dense_mlp_prepared(const moe_bf16_t *x, const moe_bf16_t *w_gat
  *   workspace >= the *_workspace_bytes of the sizes (on the device of the
  *            call), 256-byte aligned; its status word as everywhere.  Neither
  *            call needs what an earlier one left in it.
- * out may be residual itself; no other output may overlap an input or another
- * output.  With N = 0 the weights' gradients are 0.
+ * out may be residual or x itself; no other output may overlap an input or
+ * another output (such a call is refused).  With N = 0 the weights' gradients are 0.
  * Precision: products and sums in fp32 on the tensor cores; gate, up, dgate, dup
  * and h are rounded to bf16 once each (they are operands of the next product,
  * or kept), each output once.  h comes from the unrounded gate and up in the
@@ -676,8 +676,8 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
  *            the call), 256-byte aligned; NULL if neither dweight nor dbias is
  *            wanted.  It holds no status word: nothing here waits.
  * residual_out and out may each be x or residual (not the same one), dx may be
- * dout, x or dresidual; nothing else may overlap.  With N = 0 dweight and dbias
- * are 0.
+ * dout, x or dresidual; no other output may overlap an input or another output
+ * (such a call is refused).  With N = 0 dweight and dbias are 0.
  * Precision: the sums in fp32 (the variance from the squared deviations),
  * one rounding of each output; the gradients' sums over rows in fp32 a block of
  * rows, then in 64 bits, in a fixed order.  A row with a NaN or an infinity

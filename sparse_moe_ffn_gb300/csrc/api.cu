@@ -10,6 +10,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
@@ -1580,6 +1581,31 @@ moe_status_t check_workspace(const void *workspace, size_t bytes, size_t need, c
     return MOE_OK;
 }
 
+struct Span {
+    const void *p;  // NULL: an array that this call does not have
+    size_t bytes;
+};
+
+bool overlap(const Span &a, const Span &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+}
+
+// An output may be one of the first `in_place` inputs, as a whole; apart from
+// that none overlaps an input or another output.
+moe_status_t check_overlaps(std::initializer_list<Span> outs, std::initializer_list<Span> ins,
+                            int in_place = 0) {
+    for (const Span &o : outs) {
+        for (const Span &other : outs)
+            if (&other != &o && overlap(o, other))
+                return fail(MOE_ERR_INVALID_ARG, "two outputs overlap");
+        for (const Span &in : ins)
+            if (overlap(o, in) && !(&in - ins.begin() < in_place && o.p == in.p))
+                return fail(MOE_ERR_INVALID_ARG, "an output overlaps an input");
+    }
+    return MOE_OK;
+}
+
 struct FfnLayout {
     size_t h, dgate, dup, part, total;  // the status word comes first
 };
@@ -1665,6 +1691,13 @@ moe_status_t moe_gated_ffn(const moe_bf16_t *x, const moe_bf16_t *w_gate, const 
     const int sms = num_sms_of_current_device();
     const FfnLayout L = ffn_layout(N, H, I, false, sms);
     MOE_TRY(check_workspace(workspace, workspace_bytes, L.total, "gated feed-forward"));
+    const size_t rows = 2 * static_cast<size_t>(N), xb = rows * H, ib = rows * I,
+                 wb = 2 * static_cast<size_t>(H) * I;
+    // x has been read when out is written
+    MOE_TRY(check_overlaps({{out, xb}}, {{x, xb}, {residual, xb}, {w_gate, wb}, {w_up, wb},
+                                         {w_down, wb}, {gate, ib}, {up, ib}}, 2));
+    MOE_TRY(check_overlaps({{gate, ib}, {up, ib}}, {{x, xb}, {residual, xb}, {w_gate, wb},
+                                                    {w_up, wb}, {w_down, wb}}));
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h);
     FfnArgs a = {};
@@ -1758,6 +1791,11 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
     const int sms = num_sms_of_current_device();
     const FfnLayout L = ffn_layout(N, H, I, true, sms);
     MOE_TRY(check_workspace(workspace, workspace_bytes, L.total, "gated feed-forward backward"));
+    const size_t rows = 2 * static_cast<size_t>(N), xb = rows * H, ib = rows * I,
+                 wb = 2 * static_cast<size_t>(H) * I;
+    MOE_TRY(check_overlaps({{dx, xb}, {dw_gate, wb}, {dw_up, wb}, {dw_down, wb}},
+                           {{dout, xb}, {x, xb}, {w_gate, wb}, {w_up, wb}, {w_down, wb},
+                            {gate, ib}, {up, ib}}));
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     uint16_t *h = reinterpret_cast<uint16_t *>(ws + L.h);
     uint16_t *dgate = reinterpret_cast<uint16_t *>(ws + L.dgate);
@@ -1878,6 +1916,12 @@ moe_status_t moe_layernorm(const void *x, const void *residual, const void *weig
         !aligned_to(bias, size) || !aligned_to(residual_out, size) || !aligned_to(out, size) ||
         !aligned_to(mean, 4) || !aligned_to(rstd, 4))
         return fail(MOE_ERR_INVALID_ARG, "arrays must be aligned to their types");
+    const size_t row = H * size, all = row * N, each = 4 * static_cast<size_t>(N);
+    MOE_TRY(check_overlaps({{out, all}, {residual_out, all}},
+                           {{x, all}, {residual, all}, {weight, row}, {bias, row}}, 2));
+    MOE_TRY(check_overlaps({{mean, each}, {rstd, each}},
+                           {{x, all}, {residual, all}, {weight, row}, {bias, row}, {out, all},
+                            {residual_out, all}}));
     MOE_CUDA(launch_layernorm({x, residual, weight, bias, N, H, eps, residual_out, out, mean, rstd},
                               bf16 ? 1 : 0, num_sms_of_current_device(), stream),
              "layer norm kernel launch");
@@ -1918,6 +1962,14 @@ moe_status_t moe_layernorm_backward(const void *dout, const void *x, const void 
             static_cast<size_t>(layernorm_grad_blocks(N, H, sms)) * 2 * H * sizeof(float), kAlign);
         MOE_TRY(check_workspace(workspace, workspace_bytes, need, "layer norm backward"));
     }
+    const size_t row = H * size, all = row * N, each = 4 * static_cast<size_t>(N),
+                 grad = 4 * static_cast<size_t>(H);
+    MOE_TRY(check_overlaps({{dx, all}},
+                           {{dout, all}, {x, all}, {dresidual, all}, {weight, row}, {mean, each},
+                            {rstd, each}}, 3));
+    MOE_TRY(check_overlaps({{dweight, grad}, {dbias, grad}},
+                           {{dout, all}, {x, all}, {dresidual, all}, {weight, row}, {mean, each},
+                            {rstd, each}, {dx, all}}));
     int launches = 0;
     MOE_CUDA(launch_layernorm_grad({dout, x, weight, dresidual, mean, rstd, N, H, dx, dweight,
                                     dbias, static_cast<float *>(workspace)},

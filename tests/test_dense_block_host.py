@@ -344,3 +344,57 @@ def test_clipped_gradients_lie_in_their_own_only():
         binding.GradSet([At(torch.float16, 8, P)])
     with pytest.raises(ValueError, match="out tensors already"):
         binding.moe_clip_grads(binding.GradSet([a]), None, 1.0, out=[a])
+
+
+def test_outputs_that_overlap_are_refused(L):
+    """Each array 256 KB from the next, 300 x 64 and 300 x 128 of them used."""
+    at = {n: (i + 1) << 18 for i, n in enumerate(
+        "x wg wu wd r gate up out dy dx dg du dd w b ro m s dr dw db ws".split())}
+    need = L.moe_gated_ffn_backward_workspace_bytes(300, 64, 128)
+
+    def refused(function, names, **change):
+        p = {**at, **{n: at[v] if isinstance(v, str) else v for n, v in change.items()}}
+        status = getattr(L, function)(*(p.get(n, n) if isinstance(n, str) else n for n in names),
+                                      None)
+        return status == INVALID and b"overlap" in L.moe_last_error()
+
+    def forward(**change):
+        return refused("moe_gated_ffn", ["x", "wg", "wu", "wd", "r", 300, 64, 128, 1, "gate", "up",
+                                         "out", "ws", need], **change)
+
+    for name in ("wg", "wu", "wd"):
+        assert forward(out=name), name
+    for name in ("x", "wg", "wu", "wd", "r"):
+        assert forward(gate=name) and forward(up=name), name
+        assert forward(up=at[name] - 16), name
+    assert forward(out=at["r"] + 128) and forward(out=at["x"] - 128)
+    assert forward(up=at["gate"] + 300 * 128 * 2 - 16) and forward(out=at["up"] + 16)
+
+    def backward(**change):
+        return refused("moe_gated_ffn_backward", ["dy", "x", "wg", "wu", "wd", "gate", "up", 300,
+                                                  64, 128, 1, "dx", "dg", "du", "dd", "ws", need],
+                       **change)
+
+    for name in ("dy", "x", "wg", "wu", "wd", "gate", "up"):
+        for out in ("dx", "dg", "du", "dd"):
+            assert backward(**{out: name}), (out, name)
+    assert backward(dx=at["dy"] + 128) and backward(du=at["dg"] + 16)
+
+    def norm(**change):
+        return refused("moe_layernorm", ["x", "r", "w", "b", 1, 300, 64, 1e-5, "ro", "out", "m",
+                                         "s"], **change)
+
+    for out in ("out", "ro", "m", "s"):
+        assert norm(**{out: "w"}) and norm(**{out: "b"}), out
+    assert norm(out=at["x"] + 128) and norm(ro=at["r"] - 128) and norm(out=at["ro"] + 2)
+    assert norm(m="x") and norm(s="m")
+
+    def norm_backward(**change):
+        return refused("moe_layernorm_backward", ["dy", "x", "w", "m", "s", "dr", 1, 300, 64, "dx",
+                                                  "dw", "db", "ws", need], **change)
+
+    for name in ("w", "m", "s"):
+        assert norm_backward(dx=name), name
+    for name in ("dy", "x", "dr", "w", "m", "s", "dx"):
+        assert norm_backward(dw=name) and norm_backward(db=name), name
+    assert norm_backward(dx=at["dy"] + 128) and norm_backward(db="dw")

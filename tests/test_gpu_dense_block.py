@@ -214,6 +214,21 @@ def test_arrays_on_16_bytes_only(N, H, I):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("N", [1, 40, 300, 700])
+def test_out_in_place_of_x(N):
+    """out = x + FFN(x), written over x."""
+    H, I = 512, 1024
+    g = gen(N)
+    wg, wu, wd = weights(g, H, I)
+    x = normal(g, N, H)
+    want, _, _ = binding.moe_gated_ffn(x, wg, wu, wd, residual=x)
+    got, _, _ = binding.moe_gated_ffn(x, wg, wu, wd, residual=x, out=x)
+    assert got is x and torch.equal(got, want)
+    want, _, _ = binding.moe_gated_ffn(x, wg, wu, wd)
+    binding.moe_gated_ffn(x, wg, wu, wd, out=x)
+    assert torch.equal(x, want)
+
+
 def step(block, x, residual, dout, bufs):
     """A training step into given buffers, without an allocation."""
     normed, mean, rstd = binding.moe_layernorm(
