@@ -681,8 +681,9 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
  * Precision: the sums in fp32 (the variance from the squared deviations),
  * one rounding of each output; the gradients' sums over rows in fp32 a block of
  * rows, then in 64 bits, in a fixed order.  A row with a NaN or an infinity
- * gives NaN.  Limits: 1 <= H <= 65536; arrays aligned to their types (16-byte
- * accesses are taken where H and all arrays allow them).
+ * gives NaN, and the squares of values beyond 1e16 may leave fp32's range.
+ * Limits: 1 <= H <= 65536; arrays aligned to their types (16-byte accesses are
+ * taken where H and all arrays allow them).
  * ---------------------------------------------------------------------- */
 moe_status_t moe_layernorm(const void *x, const void *residual, const void *weight,
                            const void *bias, int bf16, int64_t N, int H, float eps,
@@ -717,8 +718,8 @@ moe_status_t moe_layernorm_backward(const void *dout, const void *x, const void 
  * Precision: the squares are summed in fp32 over at most 32 values, in 64 bits
  * beyond that, and in 64 bits from the start where fp32 would overflow or lose
  * them (the norm is infinite only where it passes 3.4e38 itself); the sums have
- * a fixed order.  The factor in fp32, one rounding of each output.  No tensors, or empty ones, have norm 0.  Arrays aligned to their
- * types; any sizes.
+ * a fixed order.  The factor in fp32, one rounding of each output.  No tensors,
+ * or empty ones, have norm 0.  Arrays aligned to their types; any sizes.
  * ---------------------------------------------------------------------- */
 size_t moe_grad_norm_workspace_bytes(int64_t n);
 moe_status_t moe_grad_norm(const void *const *grads, const int64_t *sizes, const uint8_t *bf16,

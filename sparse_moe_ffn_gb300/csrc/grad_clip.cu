@@ -373,11 +373,12 @@ int64_t grad_norm_parts(int64_t n, int num_sms) {
 cudaError_t launch_grad_norm(const GradSet &g, double *parts, float *norm, int num_sms,
                              int *launches, cudaStream_t s) {
     if (g.n <= kSmallTable) {
-        const GradTable<kSmallTable> t = table_of<kSmallTable>(g, 0, kPiece);
-        if (t.first[t.n] <= kSmallPieces) {
+        int64_t pieces = 0;  // a table counts them in 32 bits
+        for (int64_t i = 0; i < g.n; ++i) pieces += (g.sizes[i] + kPiece - 1) / kPiece;
+        if (pieces <= kSmallPieces) {
             *launches += 1;
             return launch_pdl(grad_norm_small_kernel, dim3(kSmallBlocks), dim3(kSmallThreads), 0, s,
-                              kSmallBlocks, t, norm);
+                              kSmallBlocks, table_of<kSmallTable>(g, 0, kPiece), norm);
         }
     }
     int64_t used = 0;
