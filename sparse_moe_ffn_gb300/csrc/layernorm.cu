@@ -389,6 +389,87 @@ __global__ void __launch_bounds__(row_threads<kRow>(),
     }
 }
 
+// dx of rows too long for registers, which are read again, from L2, for their
+// second pass; the blocks that fit instead hide each other's waits.  By single
+// values 4000 x 4099 in bf16 took 74 us, held in registers 117 (2000 x 16383: 131
+// and 200, 300 x 65535: 128 and 350); in vectors 1024 x 16384 in fp32 59 and 70,
+// 1000 x 32768 in bf16 63 and 84, but 4096 x 8192 66 and 50, which stay there.
+constexpr int kLongThreads = 512;
+constexpr int long_blocks(int vec) { return vec == 1 ? 4 : 2; }  // an SM
+
+template <typename T, int kVec>
+__global__ void __launch_bounds__(kLongThreads, long_blocks(kVec))
+    layernorm_grad_long_kernel(const LayerNormGradArgs a) {
+    constexpr int kAt = kVec == 1 ? 4 : 2;  // pieces on their way
+    __shared__ RowSums<kLongThreads, 1, 2> sums;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int t = threadIdx.x, pieces = a.H / kVec;
+    const float inv_h = 1.f / static_cast<float>(a.H);
+    int turn = 0;
+    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x, turn ^= 1) {
+        const int64_t at = n * a.H;
+        const T *x = static_cast<const T *>(a.x) + at, *dout = static_cast<const T *>(a.dout) + at;
+        const T *weight = static_cast<const T *>(a.weight);
+        const T *dres = a.dresidual ? static_cast<const T *>(a.dresidual) + at : nullptr;
+        T *dx = static_cast<T *>(a.dx) + at;
+        const float mean = __ldcg(a.mean + n), rstd = __ldcg(a.rstd + n);
+        Piece<T, kVec> r[kAt], d[kAt], w[kAt], e[kAt];
+        auto load = [&](int first, bool all) {
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+                const int i = kVec * (first + j * kLongThreads);
+                e[j].zero();
+                if (i < a.H) {
+                    r[j].load(x + i);
+                    d[j].load(dout + i);
+                    w[j].load(weight + i);
+                    if (all && dres) e[j].load(dres + i);
+                }
+            }
+        };
+        float s[2] = {0.f, 0.f};
+        for (int first = t; first < pieces; first += kAt * kLongThreads) {
+            load(first, false);
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+                if (first + j * kLongThreads >= pieces) break;
+                float v[kVec], g[kVec], y[kVec];
+                r[j].get(v);
+                d[j].get(y);
+                w[j].get(g);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    const float u = y[i] * g[i];
+                    s[0] += u;
+                    s[1] = fmaf(u, (v[i] - mean) * rstd, s[1]);
+                }
+            }
+        }
+        row_sums(sums, turn, t, 0, s);
+        const float m1 = s[0] * inv_h, m2 = s[1] * inv_h;
+        for (int first = t; first < pieces; first += kAt * kLongThreads) {
+            load(first, true);
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+                if (first + j * kLongThreads >= pieces) break;
+                float v[kVec], g[kVec], y[kVec], z[kVec];
+                r[j].get(v);
+                d[j].get(y);
+                w[j].get(g);
+                e[j].get(z);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    const float m = (v[i] - mean) * rstd;
+                    v[i] = fmaf(rstd, fmaf(-m, m2, fmaf(y[i], g[i], -m1)), z[i]);
+                }
+                r[j].set(v);
+                r[j].store(dx + kVec * (first + j * kLongThreads));
+            }
+        }
+    }
+}
+
 // Rows too long for their sums in registers: a thread kVec columns, a block a run
 // of rows (part blockIdx.y).
 constexpr int kColumnThreads = 256;
@@ -580,17 +661,11 @@ cudaError_t launch_backward_wide(const LayerNormGradArgs &a, int num_sms, cudaSt
     }
     if constexpr (kVec > 1) {
         if (pieces <= 2048) return launch_grad_rows<T, kVec, 512, 4, false>(a, num_sms, &blocks, s);
-        if (pieces <= 4096)
-            return launch_grad_rows<T, kVec, 1024, 4, false>(a, num_sms, &blocks, s);
     }
-    if (pieces <= 8192) return launch_grad_rows<T, kVec, 1024, 8, false>(a, num_sms, &blocks, s);
-    if constexpr (kVec < 8) {
-        if (pieces <= 16384)
-            return launch_grad_rows<T, kVec, 1024, 16, false>(a, num_sms, &blocks, s);
-    }
-    if constexpr (kVec == 1)
-        return launch_grad_rows<T, kVec, 1024, 64, false>(a, num_sms, &blocks, s);
-    return cudaErrorInvalidValue;
+    const int64_t fit = static_cast<int64_t>(num_sms) * long_blocks(kVec);
+    return launch_pdl(layernorm_grad_long_kernel<T, kVec>,
+                      dim3(static_cast<unsigned>(a.N < fit ? a.N : fit)), dim3(kLongThreads), 0, s,
+                      1, a);
 }
 
 // The longest rows whose sums stay in registers.  Beyond, a block would be alone
