@@ -245,6 +245,116 @@ __global__ void __launch_bounds__(row_threads<kRow>())
     }
 }
 
+// Rows too long for registers: the sum, the deviations' squares and the result
+// each read them again, from L2; the blocks that fit instead hide each other's
+// waits (300 x 65536 in fp32 81 us, 214 with registers that spill; 300 x 65535 in
+// bf16 156 and 293).
+constexpr int kLongThreads = 512;
+constexpr int long_blocks(int vec) { return vec == 1 ? 4 : 2; }  // an SM
+
+template <typename T, int kVec>
+__global__ void __launch_bounds__(kLongThreads, long_blocks(kVec))
+    layernorm_long_kernel(const LayerNormArgs a) {
+    constexpr int kAt = 4;  // pieces on their way
+    __shared__ RowSums<kLongThreads, 1, 1> sums;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int t = threadIdx.x, pieces = a.H / kVec;
+    const float inv_h = 1.f / static_cast<float>(a.H);
+    const T *weight = static_cast<const T *>(a.weight), *bias = static_cast<const T *>(a.bias);
+    for (int64_t n = blockIdx.x; n < a.N; n += gridDim.x) {
+        const int64_t at = n * a.H;
+        const T *x = static_cast<const T *>(a.x) + at;
+        const T *residual = a.residual ? static_cast<const T *>(a.residual) + at : nullptr;
+        T *kept = a.residual_out ? static_cast<T *>(a.residual_out) + at : nullptr;
+        Piece<T, kVec> r[kAt], other[kAt];
+        // pieces first, first + kLongThreads, ... of r = x + residual
+        auto load = [&](int first) {
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+                const int i = kVec * (first + j * kLongThreads);
+                r[j].zero();
+                other[j].zero();
+                if (i < a.H) {
+                    r[j].load(x + i);
+                    if (residual) other[j].load(residual + i);
+                }
+            }
+            if (!residual) return;
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+                float u[kVec], v[kVec];
+                r[j].get(u);
+                other[j].get(v);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) u[i] += v[i];
+                r[j].set(u);
+            }
+        };
+        float s[1] = {0.f};
+        for (int first = t; first < pieces; first += kAt * kLongThreads) {
+            load(first);
+            float part = 0.f;  // sums of sums: fewer roundings in a row
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+                float v[kVec];
+                r[j].get(v);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) part += v[i];
+                if (kept && first + j * kLongThreads < pieces)
+                    r[j].store(kept + kVec * (first + j * kLongThreads));
+            }
+            s[0] += part;
+        }
+        if (kept) {  // x and residual may have been written over
+            x = kept;
+            residual = nullptr;
+        }
+        row_sums(sums, 0, t, 0, s);
+        const float mean = s[0] * inv_h;
+        s[0] = 0.f;
+        for (int first = t; first < pieces; first += kAt * kLongThreads) {
+            load(first);
+            float part = 0.f;
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+                if (first + j * kLongThreads >= pieces) break;
+                float v[kVec];
+                r[j].get(v);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) part = fmaf(v[i] - mean, v[i] - mean, part);
+            }
+            s[0] += part;
+        }
+        row_sums(sums, 1, t, 0, s);
+        const float rstd = 1.f / sqrtf(fmaf(s[0], inv_h, a.eps));
+        if (t == 0) {
+            if (a.mean) a.mean[n] = mean;
+            if (a.rstd) a.rstd[n] = rstd;
+        }
+        for (int first = t; first < pieces; first += kAt * kLongThreads) {
+            load(first);
+#pragma unroll
+            for (int j = 0; j < kAt; ++j) {
+                const int h = kVec * (first + j * kLongThreads);
+                if (h >= a.H) break;
+                Piece<T, kVec> w, b;
+                w.load(weight + h);
+                b.zero();
+                if (bias) b.load(bias + h);
+                float v[kVec], g[kVec], z[kVec];
+                r[j].get(v);
+                w.get(g);
+                b.get(z);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) v[i] = fmaf((v[i] - mean) * rstd, g[i], z[i]);
+                r[j].set(v);
+                r[j].store(static_cast<T *>(a.out) + at + h);
+            }
+        }
+    }
+}
+
 // kSumColumns: the block keeps its columns' sums (dweight, dbias) and stores
 // them as part blockIdx.x.
 template <typename T, int kVec, int kRow, int kChunks, bool kSumColumns>
@@ -394,9 +504,6 @@ __global__ void __launch_bounds__(row_threads<kRow>(),
 // values 4000 x 4099 in bf16 took 74 us, held in registers 117 (2000 x 16383: 131
 // and 200, 300 x 65535: 128 and 350); in vectors 1024 x 16384 in fp32 59 and 70,
 // 1000 x 32768 in bf16 63 and 84, but 4096 x 8192 66 and 50, which stay there.
-constexpr int kLongThreads = 512;
-constexpr int long_blocks(int vec) { return vec == 1 ? 4 : 2; }  // an SM
-
 template <typename T, int kVec>
 __global__ void __launch_bounds__(kLongThreads, long_blocks(kVec))
     layernorm_grad_long_kernel(const LayerNormGradArgs a) {
@@ -431,6 +538,7 @@ __global__ void __launch_bounds__(kLongThreads, long_blocks(kVec))
         float s[2] = {0.f, 0.f};
         for (int first = t; first < pieces; first += kAt * kLongThreads) {
             load(first, false);
+            float part[2] = {0.f, 0.f};  // sums of sums: fewer roundings in a row
 #pragma unroll
             for (int j = 0; j < kAt; ++j) {
                 if (first + j * kLongThreads >= pieces) break;
@@ -441,10 +549,12 @@ __global__ void __launch_bounds__(kLongThreads, long_blocks(kVec))
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) {
                     const float u = y[i] * g[i];
-                    s[0] += u;
-                    s[1] = fmaf(u, (v[i] - mean) * rstd, s[1]);
+                    part[0] += u;
+                    part[1] = fmaf(u, (v[i] - mean) * rstd, part[1]);
                 }
             }
+            s[0] += part[0];
+            s[1] += part[1];
         }
         row_sums(sums, turn, t, 0, s);
         const float m1 = s[0] * inv_h, m2 = s[1] * inv_h;
@@ -583,6 +693,14 @@ cudaError_t launch_rows(const LayerNormArgs &a, int num_sms, cudaStream_t s) {
 }
 
 template <typename T, int kVec>
+cudaError_t launch_long(const LayerNormArgs &a, int num_sms, cudaStream_t s) {
+    const int64_t fit = static_cast<int64_t>(num_sms) * long_blocks(kVec);
+    return launch_pdl(layernorm_long_kernel<T, kVec>,
+                      dim3(static_cast<unsigned>(a.N < fit ? a.N : fit)), dim3(kLongThreads), 0, s,
+                      1, a);
+}
+
+template <typename T, int kVec>
 cudaError_t launch_forward(const LayerNormArgs &a, int num_sms, cudaStream_t s) {
     const int pieces = a.H / kVec;
     if constexpr (kVec == 1) {
@@ -596,8 +714,12 @@ cudaError_t launch_forward(const LayerNormArgs &a, int num_sms, cudaStream_t s) 
         if (pieces <= 2048) return launch_rows<T, 1, 256, 8>(a, num_sms, s);
         if (pieces <= 4096) return launch_rows<T, 1, 512, 8>(a, num_sms, s);
         if (pieces <= 8192) return launch_rows<T, 1, 512, 16>(a, num_sms, s);
-        if (pieces <= 16384) return launch_rows<T, 1, 1024, 16>(a, num_sms, s);
-        return launch_rows<T, 1, 1024, 64>(a, num_sms, s);
+        // 2000 x 16383 in fp32: 126 us from registers and 153 read again, in bf16
+        // 208 and 141
+        if constexpr (sizeof(T) == 4) {
+            if (pieces <= 16384) return launch_rows<T, 1, 1024, 16>(a, num_sms, s);
+        }
+        return launch_long<T, 1>(a, num_sms, s);
     }
     if (pieces <= 32) return launch_rows<T, kVec, 32, 1>(a, num_sms, s);
     if (pieces <= 64) return launch_rows<T, kVec, 32, 2>(a, num_sms, s);
@@ -608,10 +730,7 @@ cudaError_t launch_forward(const LayerNormArgs &a, int num_sms, cudaStream_t s) 
     if (pieces <= 2048) return launch_rows<T, kVec, 512, 4>(a, num_sms, s);
     if (pieces <= 4096) return launch_rows<T, kVec, 1024, 4>(a, num_sms, s);
     if (pieces <= 8192) return launch_rows<T, kVec, 1024, 8>(a, num_sms, s);
-    if constexpr (kVec == 4) {
-        if (pieces <= 16384) return launch_rows<T, kVec, 1024, 16>(a, num_sms, s);
-    }
-    return cudaErrorInvalidValue;
+    return launch_long<T, kVec>(a, num_sms, s);
 }
 
 // As many blocks as fit at once: two of 256 threads an SM with the sums in

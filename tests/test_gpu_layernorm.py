@@ -203,6 +203,32 @@ def test_outputs_in_place_of_inputs(H):
         assert torch.equal(ins[which], dx) and torch.equal(got[1], dw) and torch.equal(got[2], db)
 
 
+@pytest.mark.parametrize("H", [10001, 20000, 40001, 65536])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "fp32"])
+def test_long_rows(H, dtype):
+    """More rows than blocks, and the outputs in place of the inputs: rows that
+    are read again find what they had."""
+    N = 701
+    check(N, H, dtype, residual=H % 2 == 0)
+    g = gen(H)
+    x, res, w, b = (normal(g, *s, dtype=dtype) for s in ((N, H), (N, H), (H,), (H,)))
+    ro = torch.empty_like(x)
+    out, mean, rstd = binding.moe_layernorm(x, w, b, res, residual_out=ro)
+    for sum_in in (0, 1):  # r over x, out over the residual, and the other way round
+        ins = [x.clone(), res.clone()]
+        got = binding.moe_layernorm(ins[0], w, b, ins[1], out=ins[1 - sum_in],
+                                    residual_out=ins[sum_in])
+        assert torch.equal(ins[sum_in], ro) and torch.equal(ins[1 - sum_in], out)
+        assert torch.equal(got[1], mean) and torch.equal(got[2], rstd)
+    dy, dr = normal(g, N, H, dtype=dtype), normal(g, N, H, dtype=dtype)
+    want = binding.moe_layernorm_backward(dy, ro, w, mean, rstd, dr)
+    for which in range(3):
+        ins = [dy.clone(), ro.clone(), dr.clone()]
+        got = binding.moe_layernorm_backward(ins[0], ins[1], w, mean, rstd, ins[2], dx=ins[which])
+        for a, e in zip(got, want):
+            assert torch.equal(a, e)
+
+
 @pytest.mark.parametrize("H", [64, 100])
 def test_sum_stored_without_a_residual(H):
     x, w = normal(gen(H), 7, H), normal(gen(1), H)
