@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kLongThreads, long_blocks(kVec))
 }
 
 // kSumColumns: the block keeps its columns' sums (dweight, dbias) and stores
-// them as part blockIdx.x.
+// them as part blockIdx.x, unless a.part is NULL (dx alone is wanted).
 template <typename T, int kVec, int kRow, int kChunks, bool kSumColumns>
 __global__ void __launch_bounds__(row_threads<kRow>(),
                                   kSumColumns && kRow <= 256 ? 2 : 1)
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(row_threads<kRow>(),
             rstd = nrstd;
         }
     }
-    if (!kSumColumns) return;
+    if (!kSumColumns || !a.part) return;
     // the rows of the block side by side, then the block's part
     float *out = a.part + static_cast<int64_t>(blockIdx.x) * 2 * a.H;
     if constexpr (kRows > 1) {
@@ -818,10 +818,13 @@ cudaError_t launch_layernorm(const LayerNormArgs &a, int bf16, int num_sms, cuda
     return vec ? launch_forward<float, 4>(a, num_sms, s) : launch_forward<float, 1>(a, num_sms, s);
 }
 
-cudaError_t launch_layernorm_grad(const LayerNormGradArgs &a, int bf16, int num_sms, int *launches,
-                                  cudaStream_t s) {
+cudaError_t launch_layernorm_grad(const LayerNormGradArgs &args, int bf16, int num_sms,
+                                  int *launches, cudaStream_t s) {
+    LayerNormGradArgs a = args;
     const bool vec = vectors(a.H, bf16, {a.dout, a.x, a.weight, a.dresidual, a.dx});
     const bool sums = a.dweight || a.dbias;
+    // without sums there need be no workspace, or one of any size: no part is stored
+    if (!sums) a.part = nullptr;
     cudaError_t err = cudaSuccess;
     int blocks = 0;
     if (a.H <= kSumColumnsH) {

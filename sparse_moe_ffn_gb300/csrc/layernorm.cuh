@@ -25,7 +25,7 @@ struct LayerNormGradArgs {
     int H;
     void *dx;                       // nullable
     float *dweight, *dbias;         // nullable
-    float *part;                    // [blocks][2][H]
+    float *part;                    // [blocks][2][H]; for dweight and dbias alone
 };
 
 // The sums over tokens of the weight's and the bias's gradients come in this
