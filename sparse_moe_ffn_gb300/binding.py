@@ -669,17 +669,19 @@ def moe_layernorm_backward_workspace_bytes(N, H) -> int:
 
 
 def moe_layernorm_backward(dout, x, weight, mean, rstd, dresidual=None, dx=None, dweight=None,
-                           dbias=None, want_dbias: bool = True, workspace=None):
-    """(dx [N, H], dweight fp32 [H], dbias fp32 [H] or None) for the gradient
-    dout of moe_layernorm's out; x is what was normalised (the residual_out
-    where there was a residual), dresidual the gradient that reaches it by the
-    residual stream and is added to dx."""
+                           dbias=None, want_dbias: bool = True, workspace=None,
+                           want_dx: bool = True, want_dweight: bool = True):
+    """(dx [N, H], dweight fp32 [H], dbias fp32 [H]) for the gradient dout of
+    moe_layernorm's out; those not wanted are None (without dweight and dbias no
+    workspace is needed and none made).  x is what was normalised (the
+    residual_out where there was a residual), dresidual the gradient that
+    reaches it by the residual stream and is added to dx."""
     dtype = _bf16_or_fp32(x, "x")
     shape = N, H = x.shape
     dev = x.get_device()
-    if dx is None:
+    if dx is None and want_dx:
         dx = torch.empty(shape, dtype=dtype, device=x.device)
-    if dweight is None:
+    if dweight is None and want_dweight:
         dweight = torch.empty(H, dtype=_F32, device=x.device)
     if dbias is None and want_dbias:
         dbias = torch.empty(H, dtype=_F32, device=x.device)
@@ -687,11 +689,14 @@ def moe_layernorm_backward(dout, x, weight, mean, rstd, dresidual=None, dx=None,
               _typed(weight, "weight", dtype, (H,), dev), _typed(mean, "mean", _F32, (N,), dev),
               _typed(rstd, "rstd", _F32, (N,), dev),
               None if dresidual is None else _typed(dresidual, "dresidual", dtype, shape, dev))
-    outputs = (_typed(dx, "dx", dtype, shape, dev), _typed(dweight, "dweight", _F32, (H,), dev),
+    outputs = (None if dx is None else _typed(dx, "dx", dtype, shape, dev),
+               None if dweight is None else _typed(dweight, "dweight", _F32, (H,), dev),
                None if dbias is None else _typed(dbias, "dbias", _F32, (H,), dev))
     stream = _stream_of(dev)
-    workspace, ws, bytes_ = _scratch(
-        workspace, lambda: _layernorm_backward_workspace_bytes(N, H, dev), x.device, dev)
+    ws, bytes_ = None, 0
+    if workspace is not None or dweight is not None or dbias is not None:
+        workspace, ws, bytes_ = _scratch(
+            workspace, lambda: _layernorm_backward_workspace_bytes(N, H, dev), x.device, dev)
     status = lib().moe_layernorm_backward(*inputs, dtype is _BF16, N, H, *outputs, ws, bytes_,
                                           stream)
     if status:

@@ -82,3 +82,23 @@ def test_dx_alone_in_place_and_captured():
             call(ins, got, None, None, None, 0)
         graph.replay()
         assert torch.equal(got, dx)
+
+
+@pytest.mark.parametrize("H", [100, 2048, 8192])
+def test_parts_by_the_wrapper(H):
+    ins = inputs(77, H, BF16)
+    both = binding.moe_layernorm_backward(*ins)
+    for want in range(8):
+        which = [bool(want & 1), bool(want & 2), bool(want & 4)]
+        before = torch.cuda.memory_stats()["allocation.all.allocated"]
+        got = binding.moe_layernorm_backward(*ins, want_dx=which[0], want_dweight=which[1],
+                                             want_dbias=which[2])
+        made = torch.cuda.memory_stats()["allocation.all.allocated"] - before
+        for g, b, w in zip(got, both, which):
+            assert torch.equal(g, b) if w else g is None
+        # the outputs, and a workspace where sums are wanted
+        assert made == sum(which) + (which[1] or which[2])
+    dw = torch.zeros_like(both[1])
+    got = binding.moe_layernorm_backward(*ins, dweight=dw, want_dx=False, want_dweight=False,
+                                         want_dbias=False)
+    assert got[0] is None and got[1] is dw and got[2] is None and torch.equal(dw, both[1])
