@@ -704,13 +704,13 @@ moe_status_t moe_layernorm_backward(const void *dout, const void *x, const void 
  *   out[i] = grads[i] * factor
  *
  *   grads, out  n device pointers each (host arrays, read before the call
- *               returns); out[i] may be grads[i] itself, and overlaps nothing
- *               else
+ *               returns); out[i] may be grads[i] itself (in its type), and
+ *               overlaps nothing else (such a call is refused)
  *   sizes       n int64: values of each tensor (0: none, its pointers are not
  *               looked at)
  *   bf16        n bytes: 1: grads[i] is bf16, 0: fp32;  out_bf16: the same of out
- *   norm        [1] fp32 on the device: written by moe_grad_norm, read by
- *               moe_clip_grads
+ *   norm        [1] fp32 on the device, in none of the tensors: written by
+ *               moe_grad_norm, read by moe_clip_grads
  *   workspace >= moe_grad_norm_workspace_bytes(n), 256-byte aligned.  It holds
  *               no status word: nothing here waits.
  * A norm that is NaN makes every output NaN, an infinite one 0 (and what was
