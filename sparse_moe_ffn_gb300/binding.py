@@ -704,13 +704,18 @@ def moe_layernorm_backward(dout, x, weight, mean, rstd, dresidual=None, dx=None,
     return dx, dweight, dbias
 
 
+_data_ptr = torch.Tensor.data_ptr
+
+
 class GradSet:
     """Gradient tensors as moe_grad_norm and moe_clip_grads take them, for a
     program that keeps its gradients where they are: checked once, here, instead
     of on every call.  ``grads``: contiguous bf16 and fp32 CUDA tensors of one
     device; ``out``: where the clipped ones go, as many tensors of the same
     numbers of values (either type), or None: in place.  The set keeps the
-    tensors; they keep their storage as long as it is used."""
+    tensors; they keep their storage, size and type as long as it is used.  Every
+    call looks where they are (4 us for 60 tensors) and refuses a set of which
+    one has moved."""
 
     def __init__(self, grads, out=None):
         self.grads = list(grads)
@@ -730,6 +735,8 @@ class GradSet:
                                      f"got {o.numel()}")
             self._dst, self._dst_bf16 = self._pointers(self.out, "out")
         self._check_overlaps()
+        self._places = self._src.tolist()
+        self._out_places = self._dst.tolist()
         n = len(self.grads)
         self._norm_args = (self._src.buffer_info()[0], self._sizes.buffer_info()[0],
                            self._src_bf16, n)
@@ -745,6 +752,22 @@ class GradSet:
                     f"{t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
         return (array.array("Q", [t.data_ptr() for t in tensors]),
                 bytes([t.dtype is _BF16 for t in tensors]))
+
+    def _check_places(self, out):
+        """The gradients, and with `out` the clipped ones, are where they were."""
+        if list(map(_data_ptr, self.grads)) != self._places:
+            self._moved(self.grads, self._places, "grads")
+        if (out and self.out is not self.grads
+                and list(map(_data_ptr, self.out)) != self._out_places):
+            self._moved(self.out, self._out_places, "out")
+
+    def _moved(self, tensors, places, name):
+        if len(tensors) != len(places):
+            raise ValueError(f"{name} has {len(tensors)} tensors instead of {len(places)}: make a "
+                             "new GradSet")
+        i = next(i for i, (t, p) in enumerate(zip(tensors, places)) if _data_ptr(t) != p)
+        raise ValueError(f"{name}[{i}] has another storage than when the GradSet was made: make a "
+                         "new one")
 
     def _check_overlaps(self):
         """No output may lie in another tensor (its own gradient apart)."""
@@ -769,10 +792,11 @@ class GradSet:
                 far_out = s
 
 
-def _grad_set(grads, out=None):
+def _grad_set(grads, clips, out=None):
     if isinstance(grads, GradSet):
         if out is not None:
             raise ValueError("a GradSet has its out tensors already")
+        grads._check_places(clips)
         return grads
     return GradSet(grads, out)
 
@@ -789,7 +813,7 @@ def _grad_norm_workspace_bytes(n, device):
 def moe_grad_norm(grads, norm=None, workspace=None):
     """sqrt of the sum of squares of all values of the tensors (a GradSet, or a
     sequence of bf16 and fp32 CUDA tensors): norm fp32 [1], on the device."""
-    g = _grad_set(grads)
+    g = _grad_set(grads, False)
     if not g.grads:
         raise ValueError("grads must have at least one tensor")
     if norm is None:
@@ -809,7 +833,7 @@ def moe_clip_grads(grads, norm, max_norm: float, out=None):
     """The tensors scaled by max_norm / norm where norm (moe_grad_norm's, on the
     device) is above max_norm, in place or to ``out`` (bf16 or fp32, whatever the
     gradients are); returns the list of scaled tensors."""
-    g = _grad_set(grads, out)
+    g = _grad_set(grads, True, out)
     if not g.grads:
         return []
     status = lib().moe_clip_grads(*g._norm_args, _typed(norm, "norm", _F32, (1,), g.index),
