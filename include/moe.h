@@ -679,8 +679,9 @@ moe_status_t moe_gated_ffn_backward(const moe_bf16_t *dout, const moe_bf16_t *x,
  * dout, x or dresidual; no other output may overlap an input or another output
  * (such a call is refused).  With N = 0 dweight and dbias are 0.
  * Precision: the sums in fp32 (the variance from the squared deviations),
- * one rounding of each output; the gradients' sums over rows in fp32 a block of
- * rows, then in 64 bits, in a fixed order.  A row with a NaN or an infinity
+ * one rounding of each output; the gradients' sums over rows in fp32 over at most
+ * 128 rows, those sums in fp32 within a block and by eights, then in 64 bits, in a
+ * fixed order.  A row with a NaN or an infinity
  * gives NaN, and the squares of values beyond 1e16 may leave fp32's range.
  * Limits: 1 <= H <= 65536; arrays aligned to their types (16-byte accesses are
  * taken where H and all arrays allow them).

@@ -30,7 +30,7 @@ struct LayerNormGradArgs {
 
 // The sums over tokens of the weight's and the bias's gradients come in this
 // many parts at most.
-int layernorm_grad_blocks(int64_t N, int H, int num_sms);
+int64_t layernorm_grad_blocks(int64_t N, int H, int num_sms);
 // bf16: the type of all arrays but the statistics and dweight, dbias; else fp32
 cudaError_t launch_layernorm(const LayerNormArgs &a, int bf16, int num_sms, cudaStream_t s);
 cudaError_t launch_layernorm_grad(const LayerNormGradArgs &a, int bf16, int num_sms, int *launches,
