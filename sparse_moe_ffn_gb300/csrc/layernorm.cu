@@ -745,8 +745,11 @@ cudaError_t launch_forward(const LayerNormArgs &a, int num_sms, cudaStream_t s) 
     if (pieces <= 1024) return launch_rows<T, kVec, 256, 4>(a, num_sms, s);
     if (pieces <= 2048) return launch_rows<T, kVec, 512, 4>(a, num_sms, s);
     if (pieces <= 4096) return launch_rows<T, kVec, 1024, 4>(a, num_sms, s);
-    if (pieces <= 8192) return launch_rows<T, kVec, 1024, 8>(a, num_sms, s);
-    return launch_long<T, kVec>(a, num_sms, s);
+    // the longest rows of bf16 values are 8192 pieces
+    if constexpr (kVec == 4) {
+        if (pieces > 8192) return launch_long<T, kVec>(a, num_sms, s);
+    }
+    return launch_rows<T, kVec, 1024, 8>(a, num_sms, s);
 }
 
 // As many blocks as fit at once: two of 256 threads an SM with the sums in
