@@ -593,8 +593,11 @@ moe_status_t moe_balance_loss_backward(const void *logits, int logits_bf16,
  *   x [N, H], w_gate / w_up [I, H], w_down [H, I], out [N, H]: bf16
  *   (moe_dense_mlp_prepared: w_down_f16 [H, I] fp16)
  *   workspace >= moe_dense_mlp_workspace_bytes(N, H, I), 256-byte aligned
- * Precision as moe_forward (moe_forward_prepared).  Limits: H % 8 == 0,
- * I % 8 == 0, N < 2^30.
+ * Precision as moe_forward (moe_forward_prepared): the product of gate and up in
+ * two bf16 parts (in fp16).  moe_gated_ffn rounds it to bf16 once, as a training
+ * step does, takes a seventh to four fifths of the time, and has other activations
+ * and a residual: it is the one to take unless the output has to round like the
+ * sparse layer's.  Limits: H % 8 == 0, I % 8 == 0, N < 2^30.
  * ---------------------------------------------------------------------- */
 size_t moe_dense_mlp_workspace_bytes(int64_t N, int H, int I);
 moe_status_t moe_dense_mlp(const moe_bf16_t *x, const moe_bf16_t *w_gate,
@@ -628,7 +631,9 @@ moe_status_t moe_dense_mlp_prepared(const moe_bf16_t *x, const moe_bf16_t *w_gat
  *   dw_gate, dw_up [I, H], dw_down [H, I] bf16 out: all or none NULL
  *   workspace >= the *_workspace_bytes of the sizes (on the device of the
  *            call), 256-byte aligned; its status word as everywhere.  Neither
- *            call needs what an earlier one left in it.
+ *            call needs what an earlier one left in it.  Fewer tokens may need
+ *            more (for partial sums that larger batches do without): one that
+ *            several N share has the largest of their values.
  * out may be residual or x itself; no other output may overlap an input or
  * another output (such a call is refused).  With N = 0 the weights' gradients are 0.
  * Precision: products and sums in fp32 on the tensor cores; gate, up, dgate, dup

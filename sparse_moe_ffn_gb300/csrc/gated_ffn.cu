@@ -45,6 +45,13 @@ constexpr int kMostStages = 6;
 constexpr int kSliceK = 64;            // values of K in a slice
 constexpr int kBoxBytes = 32 * 128;    // 32 rows x 64 values of an output
 constexpr int kMinSlices = 8;          // of a part of a tile
+// Sharing the last wave has to take this much off the time that the constants below
+// give, for the second epilogue and the join.  Measured, unshared and shared, where
+// they say 5.9 us: down of 2048 x 2048 x 8192 115 and 132; 8.8: of 1200 x 2048 x 4096
+// 55 and 60; 9.4: dx of 3000 x 1024 x 2816 58 and 66; 13.7: down of 1536 x 2048 x
+// 8192 104 and 114, of 3000 x 2048 x 4096 112 and 107; 16.2: of 5000 x 1024 x 4096 91
+// and 85, the weights' gradients of 4096 x 2048 x 4096 186 and 178; 20.6: of 5000 x
+// 2048 x 4096 233 and 222.
 constexpr double kJoinUs = 12.0;
 constexpr double kLaunchUs = 2.0;
 

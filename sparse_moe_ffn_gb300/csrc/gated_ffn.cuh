@@ -33,9 +33,10 @@ enum FfnOp {
 // two tiles a pair.
 constexpr int kFfnMaxPairs = 76;
 constexpr int kFfnTile = 256;  // rows of a tile
-// The workspace's rows of h, dgate and dup start on whole lines of 128 bytes.
-// (With rows of I values, 1021 x 1000 x 1400 had 16-byte stores to half sectors
-// and lines in two: a training step took 69.6 us instead of 65.0.)
+// The workspace's rows of h, dgate and dup start on whole lines of 128 bytes, so
+// that their 32-byte stores are whole sectors.  (1021 x 1000 x 1400 with rows of I
+// values and 16-byte stores: 4.6 us more of a training step; with rows on 32 bytes
+// 54.0 us as with lines.)
 constexpr int kFfnLd = 64;
 
 // How a launch's tiles go to the pairs: whole waves of tiles, then, where the

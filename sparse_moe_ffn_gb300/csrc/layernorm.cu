@@ -9,10 +9,13 @@
 //   dx = rstd (t - mean(t) - n mean(t n)) + dresidual
 //   dw = sum over rows of dout n,  db = sum over rows of dout
 //
-// The row stays in registers, so the variance is the sum of the squared
-// deviations themselves, whatever the mean is.  In the backward pass a thread
-// keeps its columns' two sums over the block's rows in registers as well; the
-// blocks' sums are added in 64 bits, in a fixed order, by a second kernel.
+// The variance is the sum of the squared deviations themselves, whatever the mean
+// is: a row stays in registers, or, where it is too long for them, is read again
+// from L2 for the deviations and for the result (the launchers say from which
+// length on).  In the backward pass a thread keeps its columns' two sums over up to
+// kRunRows rows in registers as well; in rows over kSumColumnsH values a kernel of
+// its own makes them, from a second reading of x and dout.  The blocks' sums are
+// added in 64 bits, in a fixed order, by a last kernel.
 //
 // Rows whose length or arrays allow 16-byte accesses take them, others go value
 // by value.

@@ -6,7 +6,7 @@
 
 namespace moe {
 
-constexpr int kMaxNormH = 65536;  // longest row that stays in one block's registers
+constexpr int kMaxNormH = 65536;  // the longest rows that the operators take
 
 struct LayerNormArgs {
     const void *x, *residual;      // residual nullable
